@@ -2,6 +2,7 @@
 
 The compute path lives in ``libsignmuon.so`` (built from ``csrc/``); the
 Python side only marshals arguments (see ``binding``); ``optim`` is a
-torch.optim front end over it.  ``workloads`` holds seeded synthetic inputs.
+torch.optim front end over it and ``layers`` the layer norm and embedding of the
+models it trains.  ``workloads`` holds seeded synthetic inputs.
 """
-__all__ = ["binding", "optim", "workloads"]
+__all__ = ["binding", "layers", "optim", "workloads"]

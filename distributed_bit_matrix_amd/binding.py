@@ -8,6 +8,7 @@ library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -25,6 +26,7 @@ NS_F32, NS_BF16, NS_BF16X3 = 0, 1, 2
 SCALE_FRO, SCALE_SPECTRAL = 0, 1
 SIGNS_PACKED, SIGNS_TERNARY = 0, 1
 MAX_WORKERS = 32767
+_NO_SIZE = ctypes.c_size_t(-1).value    # a workspace query refused its arguments
 
 EXPORTS = (
     "signmuon_strerror", "signmuon_abi_version", "signmuon_momentum",
@@ -34,6 +36,12 @@ EXPORTS = (
     "signmuon_worker_pipeline", "signmuon_sign_ternary", "signmuon_majority_vote_ternary",
     "signmuon_executor_create", "signmuon_executor_destroy", "signmuon_reset_status",
     "signmuon_polar_ns_static",
+)
+# include/signmuon_layers.h
+LAYER_EXPORTS = (
+    "signmuon_layer_norm", "signmuon_layer_norm_backward",
+    "signmuon_layer_norm_backward_workspace", "signmuon_embedding",
+    "signmuon_embedding_backward", "signmuon_embedding_backward_workspace",
 )
 PHASES = {0: "start", 1: "momentum", 2: "prescale", 3: "gemm", 4: "pack", 5: "vote",
           6: "gram", 7: "square", 8: "update", 9: "gap"}
@@ -129,6 +137,15 @@ def lib():
             "signmuon_executor_create": (i32, [ctypes.POINTER(vp)]),
             "signmuon_executor_destroy": (i32, [vp]),
             "signmuon_reset_status": (i32, [vp, vp]),
+            "signmuon_layer_norm": (i32, [vp, i32, i64, vp, vp, i32, i64, i64, f32, vp, vp, vp,
+                                          vp]),
+            "signmuon_layer_norm_backward_workspace": (sz, [i64, i64]),
+            "signmuon_layer_norm_backward": (i32, [vp, i64, vp, i32, i64, vp, i32, vp, vp, i64,
+                                                   i64, vp, vp, vp, i32, i32, vp, sz, vp]),
+            "signmuon_embedding": (i32, [vp, i32, i64, i64, vp, i32, i64, f32, vp, i32, vp]),
+            "signmuon_embedding_backward_workspace": (sz, [i64, i64, i64]),
+            "signmuon_embedding_backward": (i32, [vp, i32, i64, vp, i32, i64, i64, f32, vp, i32,
+                                                  i64, i64, i32, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -306,6 +323,250 @@ def apply(W, eta: float, D=None, Df=None, stream=None):
     _check("signmuon_apply", lib().signmuon_apply(
         _ptr(W), _wdtype(W), _ptr(D), _ptr(Df), eta, n, _stream(stream)))
     return W
+
+
+# ---------------------------------------------------------------------------
+# Layers (include/signmuon_layers.h).  Calls run on the device of their first
+# tensor, on `stream` (default: that device's current stream); what they
+# allocate belongs to that stream.
+# ---------------------------------------------------------------------------
+def _elsewhere(t, stream) -> bool:
+    import torch
+    if not t.is_cuda:
+        raise TypeError("tensors must be on a GPU")
+    return stream is not None or t.device.index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _placed(t, stream):
+    import torch
+    if stream is not None and stream.device != t.device:
+        raise ValueError("the stream is not on the tensors' device")
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        yield
+
+
+def _dtype(t, name) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return SM_F32
+    if t.dtype == torch.bfloat16:
+        return SM_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16")
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is not on the device of the first tensor")
+
+
+def _rows(t, name) -> Tuple[int, int, int]:
+    """(rows, cols, row stride) of a tensor whose last dimension is dense:
+    any contiguous one, or a 2-D one with longer row strides."""
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = t.shape[-1]
+    rows = t.numel() // cols if cols else 0
+    if t.is_contiguous():
+        return rows, cols, cols
+    if t.dim() == 2 and (cols == 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols):
+        return rows, cols, t.stride(0) if rows > 1 else cols
+    raise TypeError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
+
+
+def _vector(t, cols, dtype, name):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {cols} entries")
+
+
+def _result(t, shape, dtype, name):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _workspace(ws, nbytes, like):
+    import torch
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if not ws.is_contiguous():
+        raise TypeError("ws must be contiguous")
+    return ws
+
+
+def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, want_stats: bool = False, Y=None,
+               mean=None, rstd=None, stream=None):
+    """Layer norm over the last dimension of X (float32 or bfloat16): Y, or
+    with want_stats (Y, mean, rstd), the latter float32 of X's leading shape.
+    weight and bias: float32 or bfloat16, one dtype for both; None stands for
+    ones and zeros.  Y may be X."""
+    import torch
+    if _elsewhere(X, stream):
+        with _placed(X, stream):
+            return layer_norm(X, weight, bias, eps, want_stats, Y, mean, rstd)
+    rows, cols, xs = _rows(X, "X")
+    xd = _dtype(X, "X")
+    wd = xd
+    first = weight if weight is not None else bias
+    if first is not None:
+        wd = _dtype(first, "weight")
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t is not None:
+                _vector(t, cols, first.dtype, name)
+    if Y is None:
+        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    else:
+        _result(Y, X.shape, X.dtype, "Y")
+    lead = X.shape[:-1]
+    if want_stats:
+        mean = torch.empty(lead, dtype=torch.float32, device=X.device) if mean is None else mean
+        rstd = torch.empty(lead, dtype=torch.float32, device=X.device) if rstd is None else rstd
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None:
+            _result(t, lead, torch.float32, name)
+    _same_device(X, weight=weight, bias=bias, Y=Y, mean=mean, rstd=rstd)
+    _check("signmuon_layer_norm", lib().signmuon_layer_norm(
+        X.data_ptr(), xd, xs, _ptr(weight), _ptr(bias), wd, rows, cols, eps, Y.data_ptr(),
+        _ptr(mean), _ptr(rstd), _stream()))
+    return (Y, mean, rstd) if want_stats else Y
+
+
+def layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    n = int(lib().signmuon_layer_norm_backward_workspace(rows, cols))
+    if n == _NO_SIZE:
+        raise SignMuonError("signmuon_layer_norm_backward_workspace", SM_EINVAL,
+                            strerror(SM_EINVAL))
+    return n
+
+
+def layer_norm_backward(dY, X, weight, mean, rstd, want_x: bool = True, want_weight: bool = True,
+                        want_bias: bool = True, dX=None, dweight=None, dbias=None, dtype=None,
+                        accumulate: bool = False, ws=None, stream=None):
+    """(dX, dweight, dbias) of layer_norm, None in the place of one that is
+    not wanted.  mean and rstd are the forward pass's; dX may be dY.  dtype:
+    that of dweight and dbias (default: what dweight or dbias has, else
+    float32).  accumulate adds to the dweight and dbias passed in (float32);
+    X and dX are never accumulated."""
+    import torch
+    if _elsewhere(dY, stream):
+        with _placed(dY, stream):
+            return layer_norm_backward(dY, X, weight, mean, rstd, want_x, want_weight, want_bias,
+                                       dX, dweight, dbias, dtype, accumulate, ws)
+    rows, cols, dys = _rows(dY, "dY")
+    xd = _dtype(X, "X")
+    if X.dtype != dY.dtype or X.shape != dY.shape:
+        raise TypeError("dY must have X's dtype and shape")
+    xs = _rows(X, "X")[2]
+    wd = xd
+    if weight is not None:
+        wd = _dtype(weight, "weight")
+        _vector(weight, cols, weight.dtype, "weight")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous float32 tensor of {rows} entries")
+    if not want_x:
+        dX = None
+    elif dX is None:
+        dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    else:
+        _result(dX, X.shape, X.dtype, "dX")
+    dweight = dweight if want_weight else None
+    dbias = dbias if want_bias else None
+    if accumulate and ((want_weight and dweight is None) or (want_bias and dbias is None)):
+        raise ValueError("accumulate needs dweight and dbias to add to")
+    if dtype is None:
+        given = dweight if dweight is not None else dbias
+        dtype = torch.float32 if given is None else given.dtype
+    if want_weight and dweight is None:
+        dweight = torch.empty(cols, dtype=dtype, device=X.device)
+    if want_bias and dbias is None:
+        dbias = torch.empty(cols, dtype=dtype, device=X.device)
+    dwd = SM_F32
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None:
+            dwd = _dtype(t, name)
+            _vector(t, cols, dtype, name)
+    ws = _workspace(ws, layer_norm_backward_workspace(rows, cols), X)
+    _same_device(dY, X=X, weight=weight, mean=mean, rstd=rstd, dX=dX, dweight=dweight,
+                 dbias=dbias, ws=ws)
+    _check("signmuon_layer_norm_backward", lib().signmuon_layer_norm_backward(
+        dY.data_ptr(), dys, X.data_ptr(), xd, xs, _ptr(weight), wd, mean.data_ptr(),
+        rstd.data_ptr(), rows, cols, _ptr(dX), _ptr(dweight), _ptr(dbias), dwd, int(accumulate),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _stream()))
+    return dX, dweight, dbias
+
+
+def _tokens(t) -> int:
+    import torch
+    if t.dtype not in (torch.int32, torch.int64) or not t.is_contiguous():
+        raise TypeError("tokens must be a contiguous int32 or int64 tensor")
+    return 64 if t.dtype == torch.int64 else 32
+
+
+def embedding(tokens, weight, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """scale * weight[tokens], of shape tokens.shape + (dim,), in out_dtype
+    (default: weight's).  A token outside the table makes its row NaN."""
+    import torch
+    if _elsewhere(tokens, stream):
+        with _placed(tokens, stream):
+            return embedding(tokens, weight, scale, out, out_dtype)
+    bits = _tokens(tokens)
+    if weight.dim() != 2 or not weight.is_contiguous():
+        raise TypeError("weight must be a contiguous 2-D tensor")
+    vocab, dim = weight.shape
+    wd = _dtype(weight, "weight")
+    shape = tokens.shape + (dim,)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or weight.dtype, device=tokens.device)
+    else:
+        _result(out, shape, out_dtype or out.dtype, "out")
+    yd = _dtype(out, "out")
+    _same_device(tokens, weight=weight, out=out)
+    _check("signmuon_embedding", lib().signmuon_embedding(
+        weight.data_ptr(), wd, vocab, dim, tokens.data_ptr(), bits, tokens.numel(), scale,
+        out.data_ptr(), yd, _stream()))
+    return out
+
+
+def embedding_backward_workspace(n: int, vocab: int, dim: int) -> int:
+    nbytes = int(lib().signmuon_embedding_backward_workspace(n, vocab, dim))
+    if nbytes == _NO_SIZE:
+        raise SignMuonError("signmuon_embedding_backward_workspace", SM_EINVAL,
+                            strerror(SM_EINVAL))
+    return nbytes
+
+
+def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Optional[int] = None,
+                       dW=None, dtype=None, accumulate: bool = False, ws=None, stream=None):
+    """Gradient of the table: dW[v] = scale * the sum of dY's rows whose token
+    is v, for all v < vocab, in dtype (default: dW's, else float32).  Tokens
+    equal to padding or outside the table add nothing.  accumulate adds to
+    the float32 dW passed in, and touches only the rows of present tokens."""
+    import torch
+    if _elsewhere(dY, stream):
+        with _placed(dY, stream):
+            return embedding_backward(dY, tokens, vocab, scale, padding, dW, dtype, accumulate,
+                                      ws)
+    bits = _tokens(tokens)
+    n = tokens.numel()
+    rows, dim, dys = _rows(dY, "dY")
+    if dY.shape[:-1].numel() != n:
+        raise ValueError("dY must have one row for each token")
+    dyd = _dtype(dY, "dY")
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dW to add to")
+        dW = torch.empty((vocab, dim), dtype=dtype or torch.float32, device=dY.device)
+    else:
+        _result(dW, (vocab, dim), dtype or dW.dtype, "dW")
+    dwd = _dtype(dW, "dW")
+    ws = _workspace(ws, embedding_backward_workspace(n, vocab, dim), dY)
+    _same_device(dY, tokens=tokens, dW=dW, ws=ws)
+    _check("signmuon_embedding_backward", lib().signmuon_embedding_backward(
+        dY.data_ptr(), dyd, dys, tokens.data_ptr(), bits, n,
+        -1 if padding is None else int(padding), scale, dW.data_ptr(), dwd, vocab, dim,
+        int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _stream()))
+    return dW
 
 
 def step_workspace(mats, hp: HParams, post_vote: int) -> int:

@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsignmuon.so")
 OBJDIR = os.path.join(PKG, "_build")
-SOURCES = ["sm_api.cpp", "sm_gemm.hip", "sm_elementwise.hip"]
+SOURCES = ["sm_api.cpp", "sm_gemm.hip", "sm_elementwise.hip", "sm_layers_api.cpp",
+           "sm_norm.hip", "sm_embed.hip"]
 ARCH = "gfx950"
 
 

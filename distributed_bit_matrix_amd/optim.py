@@ -9,7 +9,9 @@ update is the sign of its momentum.  The pages define the method for
 matrices and say nothing of other parameters; this is the reading taken
 here.  Parameters of one group must share a device and a dtype (float32 or
 bfloat16): at the first step they are moved into one flat buffer (each
-parameter becomes a view of it), which the library updates in place.
+parameter becomes a view of it), which the library updates in place.  A
+sparse gradient of a 2-D parameter (torch.nn.Embedding(sparse=True)) is summed
+straight into its rows, in an order that the tokens alone decide.
 
 Single process: the local worker is worker 0 of M.  With workers = 1 the
 vote is over the local buffer alone (Algorithm 1).  With workers > 1,
@@ -19,6 +21,7 @@ exchange; the step then votes over all M.
 """
 from __future__ import annotations
 
+import weakref
 from typing import Callable, Optional
 
 import torch
@@ -40,8 +43,37 @@ def matrix_shape(shape) -> tuple:
     return (rows, cols)
 
 
+class GradSlot:
+    """Where a parameter's gradient goes under ``direct_grads``: its place in
+    the group's flat float32 array.  ``open`` and ``close`` enclose a write on the
+    current stream, in order with other writes and with the step, on whatever
+    streams those run."""
+
+    __slots__ = ("grad", "filled", "_state")
+
+    def __init__(self, state, grad):
+        self.grad = grad
+        self.filled = False          # holds a gradient that no step has used
+        self._state = weakref.ref(state)
+
+    def alive(self) -> bool:
+        return self._state() is not None
+
+    def open(self, add: bool):
+        """The float32 array to write: to be overwritten, or with `add` to be
+        added to (cleared here if it holds nothing yet)."""
+        self._state().wait()
+        if add and not self.filled:
+            self.grad.zero_()
+        return self.grad
+
+    def close(self):
+        self.filled = True
+        self._state().mark()
+
+
 class _GroupState:
-    def __init__(self, params, group, post_vote, workers, encoding):
+    def __init__(self, params, group, post_vote, workers, encoding, direct=False):
         dev = params[0].device
         dtype = params[0].dtype
         for p in params:
@@ -73,6 +105,42 @@ class _GroupState:
                             tie_value=group["tie_value"], encoding=encoding)
         with torch.cuda.device(dev):
             self.plan = B.StepPlan(self.layout, self.hp, post_vote, device=dev)
+            self.event = torch.cuda.Event()
+            self.mark()
+        self.slots = []
+        for p, (_, _, off, _) in zip(params, self.layout):
+            p.__dict__.pop("_signmuon_slot", None)     # of an earlier optimizer
+            if direct:
+                p._signmuon_slot = GradSlot(self, self.G[off:off + p.numel()].view_as(p))
+                self.slots.append(p._signmuon_slot)
+
+    def wait(self):
+        torch.cuda.current_stream(self.G.device).wait_event(self.event)
+
+    def mark(self):
+        self.event.record(torch.cuda.current_stream(self.G.device))
+
+    def gather(self, i):
+        """Parameter i's gradient into its place in the flat array."""
+        p, (rows, cols, off, _) = self.params[i], self.layout[i]
+        g = p.grad
+        dst = self.G[off:off + p.numel()]
+        filled = bool(self.slots) and self.slots[i].filled
+        if g is None:
+            if not filled:
+                dst.zero_()
+        elif g.layout == torch.sparse_coo and p.dim() == 2 and g.sparse_dim() == 1 and \
+                g.dtype in (torch.float32, torch.bfloat16):
+            # rows of the table with their tokens, not yet summed
+            B.embedding_backward(g._values().contiguous(), g._indices()[0].contiguous(), rows,
+                                 dW=dst.view(rows, cols), accumulate=filled)
+        else:
+            if g.layout != torch.strided:
+                g = g.to_dense()
+            if filled:
+                dst.add_(g.reshape(-1))
+            else:
+                dst.copy_(g.reshape(-1))
 
 
 class SignMuon(torch.optim.Optimizer):
@@ -84,14 +152,22 @@ class SignMuon(torch.optim.Optimizer):
     tie_value are Algorithm 1's inputs and the library's hyper-parameters
     (per parameter group).  post_vote: 0 Algorithm 2, 1 polar step after the
     vote, 2 both, 3 the normalized sign step.  encoding: "packed" (1-bit
-    buffers) or "ternary" (int8 signs)."""
+    buffers) or "ternary" (int8 signs).
+
+    direct_grads: the layers of ``layers`` write their parameters' gradients in
+    float32 straight into the flat array that the step reads, neither rounded
+    to a bfloat16 parameter's dtype nor copied.  The parameters have to be on
+    their GPU already: they move into the flat buffer here.  Such a gradient
+    is the sum since the last step or zero_grad of this optimizer; p.grad
+    stays None for it, and what other operators put there is added to it (a
+    table shared with the output product)."""
 
     def __init__(self, params, lr: float = 0.02, beta: float = 0.9,
                  weight_decay: float = 0.0, eps: float = 1e-7, K: int = 5,
                  scale: str = "spectral", P: int = 5, coeffs=(1.5, -0.5, 0.0),
                  ns_precision: str = "bf16", tie_value: int = 0, post_vote: int = 0,
                  encoding: str = "packed", workers: int = 1,
-                 fill_other_workers: Optional[Callable] = None):
+                 fill_other_workers: Optional[Callable] = None, direct_grads: bool = False):
         if workers < 1:
             raise ValueError("workers must be >= 1")
         if workers > 1 and fill_other_workers is None:
@@ -105,12 +181,18 @@ class SignMuon(torch.optim.Optimizer):
         self.workers = int(workers)
         self.fill_other_workers = fill_other_workers
         self._groups = {}
+        self.direct_grads = bool(direct_grads)
+        if self.direct_grads:
+            for gi, group in enumerate(self.param_groups):
+                if group["params"]:
+                    self._state(gi, group)
 
     def _state(self, gi, group):
         st = self._groups.get(gi)
         if st is None:
             params = [p for p in group["params"]]
-            st = _GroupState(params, group, self.post_vote, self.workers, self.encoding)
+            st = _GroupState(params, group, self.post_vote, self.workers, self.encoding,
+                             self.direct_grads)
             self._groups[gi] = st
         return st
 
@@ -124,17 +206,25 @@ class SignMuon(torch.optim.Optimizer):
             if not group["params"]:
                 continue
             st = self._state(gi, group)
-            for p, (_, _, off, _) in zip(st.params, st.layout):
-                n = p.numel()
-                if p.grad is None:
-                    st.G[off:off + n].zero_()
-                else:
-                    st.G[off:off + n].copy_(p.grad.reshape(-1))
+            if st.slots:
+                st.wait()
+            for i in range(len(st.params)):
+                st.gather(i)
             st.plan.set_eta(float(group["lr"]))
             if self.workers > 1:
                 self.fill_other_workers(st.bits, st.stride, self.workers)
             st.plan(st.G, st.W, st.Mom, st.bits, st.stride, self.workers, 0)
+            for slot in st.slots:
+                slot.filled = False
+            if st.slots:
+                st.mark()
         return loss
+
+    def zero_grad(self, set_to_none: bool = True):
+        super().zero_grad(set_to_none)
+        for st in self._groups.values():
+            for slot in st.slots:
+                slot.filled = False
 
     def nonfinite(self) -> bool:
         """Whether the last step of any group met a non-finite value (and
