@@ -328,13 +328,17 @@ def apply(W, eta: float, D=None, Df=None, stream=None):
 # ---------------------------------------------------------------------------
 # Layers (include/signmuon_layers.h).  Calls run on the device of their first
 # tensor, on `stream` (default: that device's current stream); what they
-# allocate belongs to that stream.
+# allocate belongs to that stream.  The checks are written for speed: small
+# calls take as long as their host side.
 # ---------------------------------------------------------------------------
-def _elsewhere(t, stream) -> bool:
+def _here(t, stream) -> int:
+    """The device of t if a call can go straight to its current stream, -1 if
+    device and stream have to be set first."""
     import torch
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise TypeError("tensors must be on a GPU")
-    return stream is not None or t.device.index != torch.cuda.current_device()
+    return dev if stream is None and dev == torch.cuda.current_device() else -1
 
 
 @contextlib.contextmanager
@@ -346,6 +350,14 @@ def _placed(t, stream):
         yield
 
 
+def _raw_stream(dev: int) -> int:
+    """Handle of the device's current stream (0.1 us; building a torch Stream
+    object for it takes 2 us)."""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev) if get else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _dtype(t, name) -> int:
     import torch
     if t.dtype == torch.float32:
@@ -355,43 +367,40 @@ def _dtype(t, name) -> int:
     raise TypeError(f"{name} must be float32 or bfloat16")
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is not on the device of the first tensor")
-
-
 def _rows(t, name) -> Tuple[int, int, int]:
     """(rows, cols, row stride) of a tensor whose last dimension is dense:
     any contiguous one, or a 2-D one with longer row strides."""
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    cols = t.shape[-1]
-    rows = t.numel() // cols if cols else 0
+    cols = shape[-1]
     if t.is_contiguous():
-        return rows, cols, cols
-    if t.dim() == 2 and (cols == 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols):
-        return rows, cols, t.stride(0) if rows > 1 else cols
+        return (t.numel() // cols if cols else 0), cols, cols
+    if len(shape) == 2 and (cols == 1 or t.stride(1) == 1):
+        if shape[0] == 1:
+            return 1, cols, cols
+        if t.stride(0) >= cols:
+            return shape[0], cols, t.stride(0)
     raise TypeError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
 
 
-def _vector(t, cols, dtype, name):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {cols} entries")
-
-
-def _result(t, shape, dtype, name):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+def _check_arg(t, shape, dtype, dev, name):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is not on the first tensor's device")
 
 
-def _workspace(ws, nbytes, like):
+def _workspace(ws, nbytes, like, dev):
+    """(pointer, bytes) of the workspace: ws, or a new one."""
     import torch
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    if not ws.is_contiguous():
+        ws = like.new_empty(nbytes, dtype=torch.uint8)
+    elif not ws.is_contiguous():
         raise TypeError("ws must be contiguous")
-    return ws
+    elif ws.get_device() != dev:
+        raise ValueError("ws is not on the first tensor's device")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, want_stats: bool = False, Y=None,
@@ -401,41 +410,42 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, want_stats: bool = 
     weight and bias: float32 or bfloat16, one dtype for both; None stands for
     ones and zeros.  Y may be X."""
     import torch
-    if _elsewhere(X, stream):
+    dev = _here(X, stream)
+    if dev < 0:
         with _placed(X, stream):
             return layer_norm(X, weight, bias, eps, want_stats, Y, mean, rstd)
     rows, cols, xs = _rows(X, "X")
-    xd = _dtype(X, "X")
-    wd = xd
-    first = weight if weight is not None else bias
-    if first is not None:
-        wd = _dtype(first, "weight")
-        for t, name in ((weight, "weight"), (bias, "bias")):
-            if t is not None:
-                _vector(t, cols, first.dtype, name)
+    xd = wd = _dtype(X, "X")
+    if weight is not None:
+        wd = _dtype(weight, "weight")
+        _check_arg(weight, (cols,), weight.dtype, dev, "weight")
+        if bias is not None:
+            _check_arg(bias, (cols,), weight.dtype, dev, "bias")
+    elif bias is not None:
+        wd = _dtype(bias, "bias")
+        _check_arg(bias, (cols,), bias.dtype, dev, "bias")
     if Y is None:
-        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        Y = X.new_empty(X.shape)
     else:
-        _result(Y, X.shape, X.dtype, "Y")
-    lead = X.shape[:-1]
-    if want_stats:
-        mean = torch.empty(lead, dtype=torch.float32, device=X.device) if mean is None else mean
-        rstd = torch.empty(lead, dtype=torch.float32, device=X.device) if rstd is None else rstd
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t is not None:
-            _result(t, lead, torch.float32, name)
-    _same_device(X, weight=weight, bias=bias, Y=Y, mean=mean, rstd=rstd)
+        _check_arg(Y, X.shape, X.dtype, dev, "Y")
+    if mean is not None:
+        _check_arg(mean, X.shape[:-1], torch.float32, dev, "mean")
+    elif want_stats:
+        mean = X.new_empty(X.shape[:-1], dtype=torch.float32)
+    if rstd is not None:
+        _check_arg(rstd, X.shape[:-1], torch.float32, dev, "rstd")
+    elif want_stats:
+        rstd = torch.empty_like(mean)
     _check("signmuon_layer_norm", lib().signmuon_layer_norm(
         X.data_ptr(), xd, xs, _ptr(weight), _ptr(bias), wd, rows, cols, eps, Y.data_ptr(),
-        _ptr(mean), _ptr(rstd), _stream()))
+        _ptr(mean), _ptr(rstd), _raw_stream(dev)))
     return (Y, mean, rstd) if want_stats else Y
 
 
 def layer_norm_backward_workspace(rows: int, cols: int) -> int:
-    n = int(lib().signmuon_layer_norm_backward_workspace(rows, cols))
+    n = lib().signmuon_layer_norm_backward_workspace(rows, cols)
     if n == _NO_SIZE:
-        raise SignMuonError("signmuon_layer_norm_backward_workspace", SM_EINVAL,
-                            strerror(SM_EINVAL))
+        _check("signmuon_layer_norm_backward_workspace", SM_EINVAL)
     return n
 
 
@@ -446,93 +456,103 @@ def layer_norm_backward(dY, X, weight, mean, rstd, want_x: bool = True, want_wei
     not wanted.  mean and rstd are the forward pass's; dX may be dY.  dtype:
     that of dweight and dbias (default: what dweight or dbias has, else
     float32).  accumulate adds to the dweight and dbias passed in (float32);
-    X and dX are never accumulated."""
+    dX is overwritten."""
     import torch
-    if _elsewhere(dY, stream):
+    dev = _here(dY, stream)
+    if dev < 0:
         with _placed(dY, stream):
             return layer_norm_backward(dY, X, weight, mean, rstd, want_x, want_weight, want_bias,
                                        dX, dweight, dbias, dtype, accumulate, ws)
     rows, cols, dys = _rows(dY, "dY")
-    xd = _dtype(X, "X")
+    xd = wd = _dtype(X, "X")
     if X.dtype != dY.dtype or X.shape != dY.shape:
         raise TypeError("dY must have X's dtype and shape")
+    if X.get_device() != dev:
+        raise ValueError("X is not on the first tensor's device")
     xs = _rows(X, "X")[2]
-    wd = xd
     if weight is not None:
         wd = _dtype(weight, "weight")
-        _vector(weight, cols, weight.dtype, "weight")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous float32 tensor of {rows} entries")
+        _check_arg(weight, (cols,), weight.dtype, dev, "weight")
+    _check_arg(mean, X.shape[:-1], torch.float32, dev, "mean")
+    _check_arg(rstd, X.shape[:-1], torch.float32, dev, "rstd")
     if not want_x:
         dX = None
     elif dX is None:
-        dX = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+        dX = X.new_empty(X.shape)
     else:
-        _result(dX, X.shape, X.dtype, "dX")
-    dweight = dweight if want_weight else None
-    dbias = dbias if want_bias else None
+        _check_arg(dX, X.shape, X.dtype, dev, "dX")
+    if not want_weight:
+        dweight = None
+    if not want_bias:
+        dbias = None
     if accumulate and ((want_weight and dweight is None) or (want_bias and dbias is None)):
-        raise ValueError("accumulate needs dweight and dbias to add to")
+        raise ValueError("accumulate needs the dweight and dbias to add to")
     if dtype is None:
-        given = dweight if dweight is not None else dbias
-        dtype = torch.float32 if given is None else given.dtype
-    if want_weight and dweight is None:
-        dweight = torch.empty(cols, dtype=dtype, device=X.device)
-    if want_bias and dbias is None:
-        dbias = torch.empty(cols, dtype=dtype, device=X.device)
+        dtype = (dweight.dtype if dweight is not None else
+                 dbias.dtype if dbias is not None else torch.float32)
     dwd = SM_F32
-    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
-        if t is not None:
-            dwd = _dtype(t, name)
-            _vector(t, cols, dtype, name)
-    ws = _workspace(ws, layer_norm_backward_workspace(rows, cols), X)
-    _same_device(dY, X=X, weight=weight, mean=mean, rstd=rstd, dX=dX, dweight=dweight,
-                 dbias=dbias, ws=ws)
+    if want_weight:
+        if dweight is None:
+            dweight = X.new_empty(cols, dtype=dtype)
+        else:
+            _check_arg(dweight, (cols,), dtype, dev, "dweight")
+        dwd = _dtype(dweight, "dweight")
+    if want_bias:
+        if dbias is None:
+            dbias = X.new_empty(cols, dtype=dtype)
+        else:
+            _check_arg(dbias, (cols,), dtype, dev, "dbias")
+        dwd = _dtype(dbias, "dbias")
+    ws, wsp, nbytes = _workspace(ws, layer_norm_backward_workspace(rows, cols), X, dev)
     _check("signmuon_layer_norm_backward", lib().signmuon_layer_norm_backward(
         dY.data_ptr(), dys, X.data_ptr(), xd, xs, _ptr(weight), wd, mean.data_ptr(),
-        rstd.data_ptr(), rows, cols, _ptr(dX), _ptr(dweight), _ptr(dbias), dwd, int(accumulate),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _stream()))
+        rstd.data_ptr(), rows, cols, _ptr(dX), _ptr(dweight), _ptr(dbias), dwd, accumulate,
+        wsp, nbytes, _raw_stream(dev)))
     return dX, dweight, dbias
 
 
-def _tokens(t) -> int:
+def _token_bits(t) -> int:
     import torch
-    if t.dtype not in (torch.int32, torch.int64) or not t.is_contiguous():
-        raise TypeError("tokens must be a contiguous int32 or int64 tensor")
-    return 64 if t.dtype == torch.int64 else 32
+    if t.dtype == torch.int64:
+        bits = 64
+    elif t.dtype == torch.int32:
+        bits = 32
+    else:
+        raise TypeError("tokens must be int32 or int64")
+    if not t.is_contiguous():
+        raise TypeError("tokens must be contiguous")
+    return bits
 
 
 def embedding(tokens, weight, scale: float = 1.0, out=None, out_dtype=None, stream=None):
     """scale * weight[tokens], of shape tokens.shape + (dim,), in out_dtype
     (default: weight's).  A token outside the table makes its row NaN."""
-    import torch
-    if _elsewhere(tokens, stream):
+    dev = _here(tokens, stream)
+    if dev < 0:
         with _placed(tokens, stream):
             return embedding(tokens, weight, scale, out, out_dtype)
-    bits = _tokens(tokens)
-    if weight.dim() != 2 or not weight.is_contiguous():
+    bits = _token_bits(tokens)
+    shape = weight.shape
+    if len(shape) != 2 or not weight.is_contiguous():
         raise TypeError("weight must be a contiguous 2-D tensor")
-    vocab, dim = weight.shape
+    if weight.get_device() != dev:
+        raise ValueError("weight is not on the first tensor's device")
+    vocab, dim = shape
     wd = _dtype(weight, "weight")
-    shape = tokens.shape + (dim,)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or weight.dtype, device=tokens.device)
+        out = weight.new_empty(tokens.shape + (dim,), dtype=out_dtype)
     else:
-        _result(out, shape, out_dtype or out.dtype, "out")
-    yd = _dtype(out, "out")
-    _same_device(tokens, weight=weight, out=out)
+        _check_arg(out, tokens.shape + (dim,), out_dtype or out.dtype, dev, "out")
     _check("signmuon_embedding", lib().signmuon_embedding(
         weight.data_ptr(), wd, vocab, dim, tokens.data_ptr(), bits, tokens.numel(), scale,
-        out.data_ptr(), yd, _stream()))
+        out.data_ptr(), _dtype(out, "out"), _raw_stream(dev)))
     return out
 
 
 def embedding_backward_workspace(n: int, vocab: int, dim: int) -> int:
-    nbytes = int(lib().signmuon_embedding_backward_workspace(n, vocab, dim))
+    nbytes = lib().signmuon_embedding_backward_workspace(n, vocab, dim)
     if nbytes == _NO_SIZE:
-        raise SignMuonError("signmuon_embedding_backward_workspace", SM_EINVAL,
-                            strerror(SM_EINVAL))
+        _check("signmuon_embedding_backward_workspace", SM_EINVAL)
     return nbytes
 
 
@@ -543,29 +563,30 @@ def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Opti
     equal to padding or outside the table add nothing.  accumulate adds to
     the float32 dW passed in, and touches only the rows of present tokens."""
     import torch
-    if _elsewhere(dY, stream):
+    dev = _here(dY, stream)
+    if dev < 0:
         with _placed(dY, stream):
             return embedding_backward(dY, tokens, vocab, scale, padding, dW, dtype, accumulate,
                                       ws)
-    bits = _tokens(tokens)
+    bits = _token_bits(tokens)
     n = tokens.numel()
     rows, dim, dys = _rows(dY, "dY")
-    if dY.shape[:-1].numel() != n:
+    if rows != n and dim:
         raise ValueError("dY must have one row for each token")
+    if tokens.get_device() != dev:
+        raise ValueError("tokens are not on the first tensor's device")
     dyd = _dtype(dY, "dY")
     if dW is None:
         if accumulate:
             raise ValueError("accumulate needs the dW to add to")
-        dW = torch.empty((vocab, dim), dtype=dtype or torch.float32, device=dY.device)
+        dW = dY.new_empty((vocab, dim), dtype=dtype or torch.float32)
     else:
-        _result(dW, (vocab, dim), dtype or dW.dtype, "dW")
-    dwd = _dtype(dW, "dW")
-    ws = _workspace(ws, embedding_backward_workspace(n, vocab, dim), dY)
-    _same_device(dY, tokens=tokens, dW=dW, ws=ws)
+        _check_arg(dW, (vocab, dim), dtype or dW.dtype, dev, "dW")
+    ws, wsp, nbytes = _workspace(ws, embedding_backward_workspace(n, vocab, dim), dY, dev)
     _check("signmuon_embedding_backward", lib().signmuon_embedding_backward(
         dY.data_ptr(), dyd, dys, tokens.data_ptr(), bits, n,
-        -1 if padding is None else int(padding), scale, dW.data_ptr(), dwd, vocab, dim,
-        int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size(), _stream()))
+        -1 if padding is None else int(padding), scale, dW.data_ptr(), _dtype(dW, "dW"), vocab,
+        dim, accumulate, wsp, nbytes, _raw_stream(dev)))
     return dW
 
 

@@ -1,44 +1,149 @@
 // Layer norm of the rows of a matrix, forward and backward
 // (signmuon_layers.h).  No floating-point atomics: every sum has an order
 // that the sizes alone decide.
+//
+// Rows live in registers: a group of LANES threads holds one row as NV pieces
+// of 16 bytes a thread, so a row is read from memory once, the squares are
+// taken of deviations from the finished mean (a difference of squares would
+// lose a large mean's variance), and the result is written from registers.
+// Both passes are bound by HBM.
+#include <algorithm>
+
 #include "sm_layers.h"
 #include "sm_rows.h"
 
 namespace sm {
 
-// Sum over a block of B threads in a fixed order; valid in every thread.
-template <int B>
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);   // entries of a 16-byte piece
+
+// Sums of K values each over groups of LANES threads, in a fixed order; valid
+// in every thread of the group.  Groups wider than a wave meet in LDS, where
+// `turn` alternates between two buffers: one barrier a sum is enough, since a
+// buffer is written again only after the barrier of the sum in between.
+template <int LANES, int K>
+__device__ __forceinline__ void group_sums(float (&v)[K], int& turn) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = lanes_sum<(LANES < 64 ? LANES : 64)>(v[k]);
+  if constexpr (LANES > 64) {
+    constexpr int W = LANES / 64, G = 512 / LANES > 0 ? 512 / LANES : 1;
+    __shared__ float sh[2][G][K][W];
+    const int g = threadIdx.x / LANES, w = threadIdx.x % LANES >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) sh[turn][g][k][w] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float t = sh[turn][g][k][0];
+#pragma unroll
+      for (int j = 1; j < W; ++j) t += sh[turn][g][k][j];
+      v[k] = t;
+    }
+    turn ^= 1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+template <typename T, typename TW, int LANES, int NV>
+__global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_norm(
+    const T* X, int64_t xs, const TW* gamma, const TW* beta, int64_t rows, int cols, float eps,
+    T* Y, float* mean, float* rstd) {
+  constexpr int V = kVec<T>, GROUPS = LANES > 256 ? 1 : 256 / LANES;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const float inv = 1.0f / cols;
+  int turn = 0;
+  // rows of a block run together: barriers are met by all its threads
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < rows; r0 += (int64_t)gridDim.x * GROUPS) {
+    const int64_t r = r0 + group;
+    const bool live = r < rows;
+    float x[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + lane) * V;
+      load_part<V>(X + r * xs + c, live ? cols - c : 0, x[j]);
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < V; ++k) s[0] += x[j][k];
+    group_sums<LANES, 1>(s, turn);
+    const float mu = s[0] / cols;
+    s[0] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int have = cols - (j * LANES + lane) * V;
+      if (have >= V) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          x[j][k] -= mu;
+          s[0] += x[j][k] * x[j][k];
+        }
+      } else if (have > 0) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          x[j][k] = k < have ? x[j][k] - mu : 0.f;
+          s[0] += x[j][k] * x[j][k];
+        }
+      }
+    }
+    group_sums<LANES, 1>(s, turn);
+    const float rs = 1.0f / sqrtf(s[0] * inv + eps);
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + lane) * V, have = cols - c;
+      if (have <= 0) continue;
+      float g[V], b[V];
+      if (gamma) load_part<V>(gamma + c, have, g);
+      if (beta) load_part<V>(beta + c, have, b);
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        x[j][k] = x[j][k] * rs * (gamma ? g[k] : 1.f) + (beta ? b[k] : 0.f);
+      store_part<V>(Y + r * cols + c, have, x[j]);
+    }
+    if (lane == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
+  }
+}
+
+// Sum over a block of 1024 threads in a fixed order; valid in every thread.
 __device__ __forceinline__ float block_total(float v) {
-  __shared__ float sh[B / 64];
+  __shared__ float sh[16];
   v = lanes_sum<64>(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
   __syncthreads();
   float t = 0.f;
 #pragma unroll
-  for (int k = 0; k < B / 64; ++k) t += sh[k];
+  for (int k = 0; k < 16; ++k) t += sh[k];
   return t;
 }
 
-// One block per row, which is read once for the mean, once for the squared
-// deviations from it and once for the result.
+// Rows too long for registers: one block per row, which is read once for the
+// mean, once for the squared deviations from it and once for the result.
 template <typename T, typename TW>
-__global__ __launch_bounds__(256) void k_norm_loop(const T* X, int64_t xs, const TW* gamma,
-                                                   const TW* beta, int64_t rows, int cols,
-                                                   float eps, T* Y, float* mean, float* rstd) {
+__global__ __launch_bounds__(1024) void k_norm_long(const T* X, int64_t xs, const TW* gamma,
+                                                    const TW* beta, int64_t rows, int cols,
+                                                    float eps, T* Y, float* mean, float* rstd) {
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* x = X + r * xs;
     T* y = Y + r * cols;
     float s = 0.f;
-    for (int c = threadIdx.x; c < cols; c += 256) s += to_f32(x[c]);
-    const float mu = block_total<256>(s) / cols;
+    for (int c = threadIdx.x; c < cols; c += 1024) s += to_f32(x[c]);
+    const float mu = block_total(s) / cols;
     float q = 0.f;
-    for (int c = threadIdx.x; c < cols; c += 256) {
+    for (int c = threadIdx.x; c < cols; c += 1024) {
       const float d = to_f32(x[c]) - mu;
       q += d * d;
     }
-    const float rs = 1.0f / sqrtf(block_total<256>(q) / cols + eps);
-    for (int c = threadIdx.x; c < cols; c += 256)
+    const float rs = 1.0f / sqrtf(block_total(q) / cols + eps);
+    for (int c = threadIdx.x; c < cols; c += 1024)
       put(y + c, (to_f32(x[c]) - mu) * rs * (gamma ? to_f32(gamma[c]) : 1.f) +
                      (beta ? to_f32(beta[c]) : 0.f));
     if (threadIdx.x == 0) {
@@ -48,8 +153,100 @@ __global__ __launch_bounds__(256) void k_norm_loop(const T* X, int64_t xs, const
   }
 }
 
+// ---------------------------------------------------------------------------
+// Backward.  One pass over dY and X: a block takes every gridDim-th set of
+// rows, writes their dX, and adds dY * xhat and dY of its columns up in
+// registers; its groups' sums meet in LDS at the end, and k_norm_join adds the
+// blocks' (part[block][2][cols]).
+// ---------------------------------------------------------------------------
+template <typename T, typename TW, int LANES, int NV>
+__global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
+    const T* dY, int64_t dys, const T* X, int64_t xs, const TW* gamma, const float* mean,
+    const float* rstd, int64_t rows, int cols, T* dX, float* part) {
+  constexpr int V = kVec<T>, THREADS = LANES > 512 ? LANES : 512, GROUPS = THREADS / LANES;
+  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const float inv = 1.0f / cols;
+  int turn = 0;
+  float w[NV][V], ag[NV][V], ab[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * LANES + lane) * V;
+    if (gamma) load_part<V>(gamma + c, cols - c, w[j]);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      if (!gamma) w[j][k] = 1.f;
+      ag[j][k] = ab[j][k] = 0.f;
+    }
+  }
+  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < rows; r0 += (int64_t)gridDim.x * GROUPS) {
+    const int64_t r = r0 + group;
+    const bool live = r < rows;
+    float dy[NV][V], xh[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + lane) * V, have = live ? cols - c : 0;
+      load_part<V>(dY + r * dys + c, have, dy[j]);
+      load_part<V>(X + r * xs + c, have, xh[j]);
+    }
+    const float mu = live ? mean[r] : 0.f, rs = live ? rstd[r] : 0.f;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        // past the row's end dy is 0, and so is all that follows from it
+        xh[j][k] = (xh[j][k] - mu) * rs;
+        ag[j][k] += dy[j][k] * xh[j][k];
+        ab[j][k] += dy[j][k];
+        dy[j][k] *= w[j][k];
+        s[0] += dy[j][k];
+        s[1] += dy[j][k] * xh[j][k];
+      }
+    if (!dX) continue;
+    group_sums<LANES, 2>(s, turn);
+    const float c1 = s[0] * inv, c2 = s[1] * inv;
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + lane) * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) dy[j][k] = rs * (dy[j][k] - c1 - xh[j][k] * c2);
+      if (cols - c > 0) store_part<V>(dX + r * cols + c, cols - c, dy[j]);
+    }
+  }
+  if (!part) return;
+  float* out = part + (int64_t)blockIdx.x * 2 * cols;
+  if constexpr (GROUPS == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LANES + lane) * V;
+      if (cols - c <= 0) continue;
+      store_part<V>(out + c, cols - c, ag[j]);
+      store_part<V>(out + cols + c, cols - c, ab[j]);
+    }
+  } else {
+    constexpr int SPAN = LANES * NV * V;
+    __shared__ float sh[GROUPS * SPAN];
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        store_vec<V>(sh + group * SPAN + (j * LANES + lane) * V, pass ? ab[j] : ag[j]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < cols; c += THREADS) {
+        float t = sh[c];
+#pragma unroll 8
+        for (int g = 1; g < GROUPS; ++g) t += sh[g * SPAN + c];
+        out[pass * cols + c] = t;
+      }
+    }
+  }
+}
+
+// dX of rows too long for registers.
 template <typename T, typename TW>
-__global__ __launch_bounds__(256) void k_norm_grad_loop(
+__global__ __launch_bounds__(1024) void k_norm_grad_long(
     const T* dY, int64_t dys, const T* X, int64_t xs, const TW* gamma, const float* mean,
     const float* rstd, int64_t rows, int cols, T* dX) {
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -58,13 +255,13 @@ __global__ __launch_bounds__(256) void k_norm_grad_loop(
     T* dx = dX + r * cols;
     const float mu = mean[r], rs = rstd[r];
     float s1 = 0.f, s2 = 0.f;
-    for (int c = threadIdx.x; c < cols; c += 256) {
+    for (int c = threadIdx.x; c < cols; c += 1024) {
       const float g = to_f32(dy[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
       s1 += g;
       s2 += g * ((to_f32(x[c]) - mu) * rs);
     }
-    const float c1 = block_total<256>(s1) / cols, c2 = block_total<256>(s2) / cols;
-    for (int c = threadIdx.x; c < cols; c += 256) {
+    const float c1 = block_total(s1) / cols, c2 = block_total(s2) / cols;
+    for (int c = threadIdx.x; c < cols; c += 1024) {
       const float g = to_f32(dy[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
       const float xh = (to_f32(x[c]) - mu) * rs;
       put(dx + c, rs * (g - c1 - xh * c2));
@@ -72,8 +269,8 @@ __global__ __launch_bounds__(256) void k_norm_grad_loop(
   }
 }
 
-// Column sums of dY * xhat and of dY over one run of rows: 64 columns by 4
-// row lanes a block, partial sums to part[run][2][cols].
+// Column sums of dY * xhat and of dY over one run of such rows: 64 columns by
+// 4 row lanes a block, to part[run][2][cols].
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_cols(const T* dY, int64_t dys, const T* X,
                                                    int64_t xs, const float* mean,
@@ -99,17 +296,26 @@ __global__ __launch_bounds__(256) void k_norm_cols(const T* dY, int64_t dys, con
         ((sh[w][0][lane] + sh[w][1][lane]) + sh[w][2][lane]) + sh[w][3][lane];
 }
 
-// dgamma and dbeta from the partial sums (or, with none, from nothing).
+// dgamma (blockIdx.y = 0) and dbeta (1) from the blocks' sums: 32 columns by
+// 32 lanes over the blocks.
 template <typename TO>
-__global__ __launch_bounds__(256) void k_norm_join(const float* part, int runs, int cols,
-                                                   TO* dgamma, TO* dbeta, int accumulate) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= cols) return;
-  for (int k = 0; k < 2; ++k) {
-    TO* out = k ? dbeta : dgamma;
-    if (!out) continue;
-    float s = 0.f;
-    for (int b = 0; b < runs; ++b) s += part[((int64_t)b * 2 + k) * cols + c];
+__global__ __launch_bounds__(1024) void k_norm_join(const float* part, int blocks, int cols,
+                                                    TO* dgamma, TO* dbeta, int accumulate) {
+  __shared__ float sh[32][33];
+  TO* out = blockIdx.y ? dbeta : dgamma;
+  if (!out) return;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + x;
+  const float* p = part + (int64_t)blockIdx.y * cols + c;
+  float s = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int b = y; b < blocks; b += 32) s += p[(int64_t)b * 2 * cols];
+  }
+  sh[y][x] = s;
+  __syncthreads();
+  if (y == 0 && c < cols) {
+    for (int k = 1; k < 32; ++k) s += sh[k][x];
     put(out + c, accumulate ? to_f32(out[c]) + s : s);
   }
 }
@@ -117,50 +323,133 @@ __global__ __launch_bounds__(256) void k_norm_join(const float* part, int runs, 
 namespace {
 
 constexpr int64_t kMaxBlocks = 1 << 16;   // larger grids loop
+constexpr int kGradBlocks = 512;          // two blocks of 512 threads a CU
 
-int64_t runs_of(int64_t rows) {
-  int64_t n = (rows + 63) / 64;
-  return n < 64 ? n : 64;
+// Threads a row: the fewest that hold it in at most `most` pieces each.  0: too long.
+int lanes_for(int64_t cols, int vec, int most) {
+  for (int lanes : {8, 16, 32})
+    if (cols <= lanes * vec) return lanes;
+  for (int lanes : {64, 256, 1024})
+    if (cols <= (int64_t)lanes * vec * most) return lanes;
+  return 0;
+}
+int vec_of(int32_t dtype) { return dtype == SM_BF16 ? 8 : 4; }
+// The backward pass holds five values an entry: 16 entries a thread.
+int grad_lanes(int64_t cols, int32_t dtype) {
+  return lanes_for(cols, vec_of(dtype), 16 / vec_of(dtype));
+}
+
+// Blocks whose partial sums k_norm_join adds.
+int64_t grad_blocks(int64_t rows, int64_t cols, int32_t dtype) {
+  const int lanes = grad_lanes(cols, dtype);
+  if (lanes == 0) return std::min<int64_t>((rows + 63) / 64, 64);
+  const int groups = lanes > 512 ? 1 : 512 / lanes;
+  return std::min<int64_t>((rows + groups - 1) / groups, lanes > 512 ? 256 : kGradBlocks);
+}
+
+template <typename T, typename TW, int LANES, int NV>
+void norm_go(const NormArgs& a, hipStream_t s) {
+  constexpr int THREADS = LANES > 256 ? LANES : 256, GROUPS = THREADS / LANES;
+  const int64_t grid = std::min<int64_t>((a.rows + GROUPS - 1) / GROUPS, kMaxBlocks);
+  hipLaunchKernelGGL((k_norm<T, TW, LANES, NV>), dim3((unsigned)grid), dim3(THREADS), 0, s,
+                     (const T*)a.X, a.x_stride, (const TW*)a.gamma, (const TW*)a.beta, a.rows,
+                     (int)a.cols, a.eps, (T*)a.Y, a.mean, a.rstd);
+}
+
+template <typename T, typename TW, int LANES>
+void norm_pieces(const NormArgs& a, hipStream_t s) {
+  const int64_t per = (int64_t)LANES * kVec<T>;
+  switch ((a.cols + per - 1) / per) {
+    case 1: return norm_go<T, TW, LANES, 1>(a, s);
+    case 2: return norm_go<T, TW, LANES, 2>(a, s);
+    case 3: return norm_go<T, TW, LANES, 3>(a, s);
+    default: return norm_go<T, TW, LANES, 4>(a, s);
+  }
 }
 
 template <typename T, typename TW>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
-  const int64_t grid = a.rows < kMaxBlocks ? a.rows : kMaxBlocks;
-  hipLaunchKernelGGL((k_norm_loop<T, TW>), dim3((unsigned)grid), dim3(256), 0, s,
-                     (const T*)a.X, a.x_stride, (const TW*)a.gamma, (const TW*)a.beta, a.rows,
-                     (int)a.cols, a.eps, (T*)a.Y, a.mean, a.rstd);
+  switch (lanes_for(a.cols, kVec<T>, 4)) {
+    case 8: norm_go<T, TW, 8, 1>(a, s); break;
+    case 16: norm_go<T, TW, 16, 1>(a, s); break;
+    case 32: norm_go<T, TW, 32, 1>(a, s); break;
+    case 64: norm_pieces<T, TW, 64>(a, s); break;
+    case 256: norm_pieces<T, TW, 256>(a, s); break;
+    case 1024: norm_pieces<T, TW, 1024>(a, s); break;
+    default:
+      hipLaunchKernelGGL((k_norm_long<T, TW>), dim3((unsigned)std::min(a.rows, kMaxBlocks)),
+                         dim3(1024), 0, s, (const T*)a.X, a.x_stride, (const TW*)a.gamma,
+                         (const TW*)a.beta, a.rows, (int)a.cols, a.eps, (T*)a.Y, a.mean, a.rstd);
+  }
   return hipGetLastError();
+}
+
+template <typename T, typename TW, int LANES, int NV>
+void norm_grad_go(const NormGradArgs& a, int64_t grid, float* part, hipStream_t s) {
+  hipLaunchKernelGGL((k_norm_grad<T, TW, LANES, NV>), dim3((unsigned)grid),
+                     dim3(LANES > 512 ? LANES : 512), 0, s, (const T*)a.dY, a.dy_stride,
+                     (const T*)a.X, a.x_stride, (const TW*)a.gamma, a.mean, a.rstd, a.rows,
+                     (int)a.cols, (T*)a.dX, part);
+}
+
+template <typename T, typename TW, int LANES>
+void norm_grad_pieces(const NormGradArgs& a, int64_t grid, float* part, hipStream_t s) {
+  const int64_t per = (int64_t)LANES * kVec<T>;
+  const int64_t nv = (a.cols + per - 1) / per;
+  if constexpr (kVec<T> == 8) {
+    if (nv == 1) norm_grad_go<T, TW, LANES, 1>(a, grid, part, s);
+    else norm_grad_go<T, TW, LANES, 2>(a, grid, part, s);
+  } else {
+    switch (nv) {
+      case 1: return norm_grad_go<T, TW, LANES, 1>(a, grid, part, s);
+      case 2: return norm_grad_go<T, TW, LANES, 2>(a, grid, part, s);
+      case 3: return norm_grad_go<T, TW, LANES, 3>(a, grid, part, s);
+      default: return norm_grad_go<T, TW, LANES, 4>(a, grid, part, s);
+    }
+  }
 }
 
 template <typename T, typename TW>
 hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
-  hipError_t e;
-  const int cols = (int)a.cols;
-  // the column sums first: dX may be dY
   const bool sums = a.dgamma || a.dbeta;
-  const int64_t runs = runs_of(a.rows);
-  if (sums && runs > 0) {
-    const int64_t run = (a.rows + runs - 1) / runs;
-    hipLaunchKernelGGL((k_norm_cols<T>), dim3((cols + 63) / 64, (unsigned)runs), dim3(256), 0, s,
-                       (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride, a.mean, a.rstd,
-                       a.rows, cols, run, (float*)a.ws);
+  const int64_t blocks = grad_blocks(a.rows, a.cols, a.x_dtype);
+  float* part = sums ? (float*)a.ws : nullptr;
+  hipError_t e;
+  if (a.rows > 0) {
+    switch (grad_lanes(a.cols, a.x_dtype)) {
+      case 8: norm_grad_go<T, TW, 8, 1>(a, blocks, part, s); break;
+      case 16: norm_grad_go<T, TW, 16, 1>(a, blocks, part, s); break;
+      case 32: norm_grad_go<T, TW, 32, 1>(a, blocks, part, s); break;
+      case 64: norm_grad_pieces<T, TW, 64>(a, blocks, part, s); break;
+      case 256: norm_grad_pieces<T, TW, 256>(a, blocks, part, s); break;
+      case 1024: norm_grad_pieces<T, TW, 1024>(a, blocks, part, s); break;
+      default:
+        // the column sums first: dX may be dY
+        if (sums) {
+          const int64_t run = (a.rows + blocks - 1) / blocks;
+          hipLaunchKernelGGL((k_norm_cols<T>),
+                             dim3((unsigned)((a.cols + 63) / 64), (unsigned)blocks), dim3(256),
+                             0, s, (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride,
+                             a.mean, a.rstd, a.rows, (int)a.cols, run, part);
+          if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        if (a.dX)
+          hipLaunchKernelGGL((k_norm_grad_long<T, TW>),
+                             dim3((unsigned)std::min(a.rows, kMaxBlocks)), dim3(1024), 0, s,
+                             (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride,
+                             (const TW*)a.gamma, a.mean, a.rstd, a.rows, (int)a.cols,
+                             (T*)a.dX);
+    }
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (sums && !(runs == 0 && a.accumulate)) {
-    dim3 grid((cols + 255) / 256);
+  if (sums && !(a.rows == 0 && a.accumulate)) {
+    const dim3 grid((unsigned)((a.cols + 31) / 32), 2);
     if (a.dw_dtype == SM_BF16)
-      hipLaunchKernelGGL((k_norm_join<bf16_t>), grid, dim3(256), 0, s, (const float*)a.ws,
-                         (int)runs, cols, (bf16_t*)a.dgamma, (bf16_t*)a.dbeta, a.accumulate);
+      hipLaunchKernelGGL((k_norm_join<bf16_t>), grid, dim3(1024), 0, s, part, (int)blocks,
+                         (int)a.cols, (bf16_t*)a.dgamma, (bf16_t*)a.dbeta, a.accumulate);
     else
-      hipLaunchKernelGGL((k_norm_join<float>), grid, dim3(256), 0, s, (const float*)a.ws,
-                         (int)runs, cols, (float*)a.dgamma, (float*)a.dbeta, a.accumulate);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (a.dX && a.rows > 0) {
-    const int64_t grid = a.rows < kMaxBlocks ? a.rows : kMaxBlocks;
-    hipLaunchKernelGGL((k_norm_grad_loop<T, TW>), dim3((unsigned)grid), dim3(256), 0, s,
-                       (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride,
-                       (const TW*)a.gamma, a.mean, a.rstd, a.rows, cols, (T*)a.dX);
+      hipLaunchKernelGGL((k_norm_join<float>), grid, dim3(1024), 0, s, part, (int)blocks,
+                         (int)a.cols, (float*)a.dgamma, (float*)a.dbeta, a.accumulate);
     return hipGetLastError();
   }
   return hipSuccess;
@@ -169,7 +458,8 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t norm_grad_workspace(int64_t rows, int64_t cols) {
-  return ((size_t)runs_of(rows) * 2 * cols * 4 + 255) / 256 * 256;
+  const int64_t blocks = std::max(grad_blocks(rows, cols, SM_F32), grad_blocks(rows, cols, SM_BF16));
+  return ((size_t)blocks * 2 * cols * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {

@@ -76,7 +76,7 @@ sm_status signmuon_layer_norm_backward(
  * contiguous vocab x dim of w_dtype; Y: contiguous n x dim of y_dtype.
  * tokens: n integers of token_bits (32 or 64) bits.  A token outside
  * [0, vocab) reads nothing and makes its row NaN, which the optimizer step
- * reports as a non-finite gradient.  0 <= n < 2^31, 1 <= vocab, dim <= 2^20,
+ * reports as a non-finite gradient.  0 <= n <= 2^30, 1 <= vocab, dim <= 2^20,
  * scale finite.  n = 0 is a no-op.
  */
 sm_status signmuon_embedding(const void *W, int32_t w_dtype, int64_t vocab,
