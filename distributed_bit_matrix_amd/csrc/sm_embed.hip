@@ -31,57 +31,70 @@ __global__ __launch_bounds__(256) void k_embed(const TW* __restrict__ W, int64_t
 #pragma unroll 2
     for (int c0 = lane * V; c0 < dim; c0 += LANES * V) {
       const int c = c0 + V <= dim ? c0 : dim - V;
+      Piece<TW, V> p;
+      p.load(w + c);
       float v[V];
-      if constexpr (V == 1) v[0] = to_f32(w[c]);
-      else load_vec<V>(w + c, v);
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = ok ? scale * v[k] : __builtin_nanf("");
-      if constexpr (V == 1) put(y + c, v[0]);
-      else store_vec<V>(y + c, v);
+      for (int k = 0; k < V; ++k) v[k] = ok ? scale * p[k] : __builtin_nanf("");
+      store_vec<V>(y + c, v);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Sort.  Block b owns the tokens lo <= t < lo + range and reads the whole
-// batch, so the blocks need nothing of each other: tokens below lo are counted
-// on the way, which gives the block's place in the sorted order.  Each of its
-// 16 waves reads one run of consecutive positions and lists the positions it
-// finds in range, in order; the list is counted by token, the counts are
-// scanned over tokens and waves, and the list is placed.  A wave whose list
-// overflows counts it and starts it anew, and reads its run again to place.
-// Equal tokens among 64 listed ones are found by one ballot per bit of t - lo.
-// Between counting and placing the block clears the rows of the table that no
-// token names (unless the caller accumulates), while placing goes on.
+// Sort.  Equal tokens have to be neighbours, in the order of the batch; the
+// tokens themselves may come in any fixed order.  Block b of B = 2^shift takes
+// the tokens t with t % B = b, so that frequent tokens, which vocabularies
+// number next to each other, spread over the blocks.  Every block reads the
+// whole batch and needs nothing of the others: it counts the tokens of the
+// blocks before it on the way, which gives its place in the order.  Each of
+// its 16 waves reads one run of consecutive positions and lists its own; the
+// list is counted by token, the counts are scanned over tokens and waves, and
+// the list is placed.  A wave whose list overflows counts it and starts it
+// anew, and reads its run again to place.  When placing, equal tokens among 64
+// listed ones are found by one ballot per bit of t / B.  Between counting and
+// placing the block clears the rows of the table that no token names (unless
+// the caller accumulates): those stores drain while placing goes on.
 //   order[p], sorted[p]: batch position and token of the p-th in sorted order
-//   start[v]: the first p of token v; start[vocab]: how many tokens count
-// One launch.  Every block reading all tokens costs n / 64 loads a wave run
-// (n = 65536: 8 us) and grows with n; a sort by digits would read each token
-// once a pass but takes two launches a pass.
+//   total: how many tokens count
+// Reading all tokens in every block costs 7 vector instructions for 64 of them
+// in each CU; a sort by digits would read them once a pass, but takes two
+// launches a pass.
 // ---------------------------------------------------------------------------
 constexpr int kSortWaves = 16;
-constexpr int kMaxRange = 512;   // 32 KB of counts
-constexpr int kList = 256;       // listed positions a wave
+constexpr int kMaxRange = 512;   // tokens a block
+constexpr int kBatch = 8;        // loads of 64 tokens in flight a wave
+constexpr int kList = 64 * kBatch;   // listed positions a wave
+constexpr int kRunBits = 23;     // a listed position: bin << 23 | place in the run
+
+typedef volatile __attribute__((address_space(3))) int32_t lds_i32;
+typedef volatile __attribute__((address_space(3))) uint32_t lds_u32;
+
+__device__ __forceinline__ uint32_t token_key(const int32_t* t) { return (uint32_t)*t; }
+__device__ __forceinline__ uint32_t token_key(const int64_t* t) {
+  const uint64_t v = (uint64_t)*t;
+  return (uint32_t)(v >> 32) == 0 ? (uint32_t)v : ~0u;
+}
 
 template <typename TI, typename TO>
 __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
-    const TI* __restrict__ tokens, int64_t n, int64_t vocab, int64_t padding, int range, int bits,
-    int32_t* __restrict__ order, int32_t* __restrict__ sorted, int32_t* __restrict__ start,
-    TO* __restrict__ dW, int dim) {
-  extern __shared__ int32_t counts[];   // [kSortWaves][range]
-  __shared__ int32_t list_pos[kSortWaves][kList];
-  __shared__ uint16_t list_bin[kSortWaves][kList];
+    const TI* __restrict__ tokens, int64_t n, uint32_t vocab, uint32_t padding, int shift,
+    int range, int bits, int32_t* __restrict__ order, int32_t* __restrict__ sorted,
+    int32_t* __restrict__ total, TO* __restrict__ dW, int dim) {
+  __shared__ int32_t counts[kSortWaves * kMaxRange];   // [kSortWaves][range]
+  __shared__ uint32_t lists[kSortWaves][kList];
   __shared__ int32_t below[kSortWaves], wave_total[kSortWaves];
   __shared__ uint8_t empty[kMaxRange];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t before = ((uint64_t)1 << lane) - 1;
-  const int64_t lo = (int64_t)blockIdx.x * range;
+  const uint32_t block = blockIdx.x, mask = (1u << shift) - 1;
   const int64_t share = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
-  const int64_t i0 = w * share, i1 = i0 + share < n ? i0 + share : n;
-  volatile int32_t* mine = counts + w * range;
-  volatile int32_t* pos = list_pos[w];
-  volatile uint16_t* bin = list_bin[w];
+  const int64_t i0 = w * share;
+  const int run = (int)(i0 + share < n ? share : n > i0 ? n - i0 : 0);   // < 2^kRunBits
+  const TI* mine = tokens + i0;
+  lds_i32* count = (lds_i32*)(counts + w * range);
+  lds_u32* list = (lds_u32*)lists[w];
   for (int k = threadIdx.x; k < kSortWaves * range; k += 64 * kSortWaves) counts[k] = 0;
   __syncthreads();
 
@@ -89,22 +102,38 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
   auto settle = [&](int len, bool place) {
     for (int k = 0; k < len; k += 64) {
       const bool in = k + lane < len;
-      const int b = in ? bin[k + lane] : 0;
-      uint64_t peers = __ballot(in);
-      for (int d = 0; d < bits; ++d) {
-        const bool set = (b >> d) & 1;
-        const uint64_t v = __ballot(set);
-        peers &= set ? v : ~v;
+      const uint32_t entry = in ? list[k + lane] : 0;
+      const int b = (int)(entry >> kRunBits);
+      const uint64_t live = __ballot(in);
+      const int b0 = __builtin_amdgcn_readfirstlane(b);
+      uint64_t peers = live & __ballot(b == b0);
+      const bool one = peers == live;       // all of them the same token
+      if (!place) {
+        if (one) {
+          if (lane == 0) count[b0] = count[b0] + __popcll(live);
+        } else if (in) {
+          __hip_atomic_fetch_add(&counts[w * range + b], 1, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+        continue;
+      }
+      if (!one) {
+        uint32_t lo = (uint32_t)live, hi = (uint32_t)(live >> 32);
+        for (int d = 0; d < bits; ++d) {
+          const int32_t set = (int32_t)((uint32_t)b << (31 - d)) >> 31;
+          const uint64_t v = __ballot(set != 0);
+          lo &= ~((uint32_t)v ^ set);
+          hi &= ~((uint32_t)(v >> 32) ^ set);
+        }
+        peers = ((uint64_t)hi << 32) | lo;
       }
       if (in) {
-        const int32_t c = mine[b];
-        if (place) {
-          const int32_t p = c + __popcll(peers & before);
-          order[p] = pos[k + lane];
-          sorted[p] = (int32_t)(lo + b);
-        }
+        const int32_t c = count[b];
+        const int32_t p = c + __popcll(peers & before);
+        order[p] = (int32_t)(i0 + (entry & ((1u << kRunBits) - 1)));
+        sorted[p] = (int32_t)(((uint32_t)b << shift) + block);
         __builtin_amdgcn_wave_barrier();
-        if ((peers & before) == 0) mine[b] = c + __popcll(peers);
+        if ((peers & before) == 0) count[b] = c + __popcll(peers);
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -114,33 +143,38 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
   int32_t under = 0;
   auto scan = [&](bool place) {
     int len = 0;
-    constexpr int U = 8;      // loads in flight
-    for (int64_t i = i0; i < i1; i += 64 * U) {
-      int64_t t[U];
+    for (int i = 0; i < run; i += kList) {
+      uint32_t t[kBatch];
+      if (i + kList <= run) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t at = i + 64 * u + lane;
-        t[u] = at < i1 ? (int64_t)tokens[at] : -1;
+        for (int u = 0; u < kBatch; ++u) t[u] = token_key(mine + (i + 64 * u + lane));
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          t[u] = i + 64 * u + lane < run ? token_key(mine + (i + 64 * u + lane)) : ~0u;
+      }
+      uint64_t m[kBatch];
+      int more = 0;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const uint64_t valid = __ballot(t[u] < vocab) & ~__ballot(t[u] == padding);
+        const uint32_t b = t[u] & mask;
+        under += __popcll(valid & __ballot(b < block));
+        m[u] = valid & __ballot(b == block);
+        more += __popcll(m[u]);
+      }
+      if (more == 0) continue;
+      if (len + more > kList) {
+        settle(len, place);
+        whole = false;
+        len = 0;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool valid = t[u] >= 0 && t[u] < vocab && t[u] != padding;
-        const bool in = valid && t[u] >= lo && t[u] < lo + range;
-        under += __popcll(__ballot(valid && t[u] < lo));
-        const uint64_t m = __ballot(in);
-        if (m == 0) continue;
-        const int more = __popcll(m);
-        if (len + more > kList) {
-          settle(len, place);
-          whole = false;
-          len = 0;
-        }
-        if (in) {
-          const int at = len + __popcll(m & before);
-          pos[at] = (int32_t)(i + 64 * u + lane);
-          bin[at] = (uint16_t)(t[u] - lo);
-        }
-        len += more;
+      for (int u = 0; u < kBatch; ++u) {
+        if (m[u] >> lane & 1)
+          list[len + __popcll(m[u] & before)] =
+              (t[u] >> shift) << kRunBits | (uint32_t)(i + 64 * u + lane);
+        len += __popcll(m[u]);
       }
     }
     return len;
@@ -150,14 +184,14 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
   settle(len, false);
   if (lane == 0) below[w] = under;
   __syncthreads();
-  // thread k holds token lo + k (range <= the threads of the block)
-  const int mybin = threadIdx.x;
+  // thread k holds bin k (range <= the threads of the block)
+  const int k = threadIdx.x;
   int32_t base = 0;
-  for (int k = 0; k < kSortWaves; ++k) base += below[k];
-  int32_t total = 0;
-  if (mybin < range)
-    for (int k = 0; k < kSortWaves; ++k) total += counts[k * range + mybin];
-  int32_t incl = total;
+  for (int j = 0; j < kSortWaves; ++j) base += below[j];
+  int32_t sum = 0;
+  if (k < range)
+    for (int j = 0; j < kSortWaves; ++j) sum += counts[j * range + k];
+  int32_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int32_t up = __shfl_up(incl, o);
@@ -165,17 +199,16 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
   }
   if (lane == 63) wave_total[w] = incl;
   __syncthreads();
-  for (int k = 0; k < w; ++k) base += wave_total[k];
-  if (mybin < range) {
-    int32_t at = base + incl - total;
-    if (lo + mybin < vocab) start[lo + mybin] = at;
-    if (lo + mybin == vocab - 1) start[vocab] = at + total;
-    empty[mybin] = total == 0 && lo + mybin < vocab;
-    for (int k = 0; k < kSortWaves; ++k) {
-      const int32_t c = counts[k * range + mybin];
-      counts[k * range + mybin] = at;
+  for (int j = 0; j < w; ++j) base += wave_total[j];
+  if (k < range) {
+    int32_t at = base + incl - sum;
+    empty[k] = sum == 0 && ((uint32_t)k << shift) + block < vocab;
+    for (int j = 0; j < kSortWaves; ++j) {
+      const int32_t c = counts[j * range + k];
+      counts[j * range + k] = at;
       at += c;
     }
+    if (k == range - 1 && block == gridDim.x - 1) *total = at;
   }
   __syncthreads();
   if (dW) {
@@ -187,8 +220,12 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
     const int rows = 64 / lanes;
     for (int r = w * rows + lane / lanes; r < range; r += kSortWaves * rows)
       if (empty[r]) {
-        TO* row = dW + (lo + r) * dim;
-        for (int c = lane % lanes * V; c < dim; c += lanes * V) store_part<V>(row + c, dim - c, zero);
+        TO* row = dW + (((int64_t)r << shift) + block) * dim;
+        for (int c = lane % lanes * V; c < dim; c += lanes * V) {
+          if (c + V <= dim) store_vec<V>(row + c, zero);
+          else
+            for (int j = c; j < dim; ++j) put(row + j, 0.f);
+        }
       }
   }
   if (!whole) len = scan(true);
@@ -196,157 +233,169 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
 }
 
 // ---------------------------------------------------------------------------
-// Sums.  The sorted positions are cut into units of `span` positions, one wave
-// each (and each slice of 64 V columns).  A unit finishes the tokens that
-// begin in it, even past its end, unless a token has more than kLong rows:
-// of those every unit sums its own positions only, to part[2 u] where the
-// token began before the unit and part[2 u + 1] where it begins in it, and
-// k_embed_join adds the parts.  So work is even however often a token occurs
-// (a unit adds at most span + kLong rows) and most rows need no second pass.
+// Sums.  The sorted positions are cut evenly, however often a token occurs:
+// `span` positions a wave, kSumWaves waves a block (and 64 V columns).  A wave
+// writes the rows of the tokens that lie inside its positions.  The rows that
+// a wave adds up for a token begun before it go to LDS, and the wave in which
+// the token begins collects them; what a block adds up for tokens that cross
+// its own borders goes to part[2 block] (begun before the block) and
+// part[2 block + 1] (begun in it), and k_embed_join adds those.  Only
+// neighbours in sorted[] are looked at, so nothing is loaded but order[] and
+// sorted[], and then the rows.
 // ---------------------------------------------------------------------------
-constexpr int kLong = 64;    // at least the span
+constexpr int kSumWaves = 8;
 
-template <int V, typename T>
-__device__ __forceinline__ void read_cols(const T* p, float (&v)[V]) {
-  if constexpr (V == 1) v[0] = to_f32(*p);
-  else load_vec<V>(p, v);
+// out = scale * acc, or += where the caller accumulates.
+template <int V, typename TO>
+__device__ __forceinline__ void write_row(TO* out, const float (&acc)[V], int skip, float scale,
+                                          int accumulate) {
+  float v[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) v[k] = scale * acc[k];
+  if (accumulate) {
+    Piece<TO, V> old;
+    old.load(out);
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] += old[k];
+  }
+  store_own<V>(out, skip, v);
 }
 
 template <typename T, typename TO, int V>
-__global__ __launch_bounds__(256) void k_embed_sum(
+__global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
     const T* __restrict__ dY, int64_t dys, const int32_t* __restrict__ order,
-    const int32_t* __restrict__ sorted, const int32_t* __restrict__ start, int64_t vocab, int dim,
-    int slices, int span, float scale, TO* __restrict__ dW, int accumulate,
-    float* __restrict__ part) {
+    const int32_t* __restrict__ sorted, const int32_t* __restrict__ total, int dim, int span,
+    int slices, float scale, TO* __restrict__ dW, int accumulate, float* __restrict__ part) {
   constexpr int U = 8;      // rows in flight
+  const int block = blockIdx.x / slices, slice = blockIdx.x - block * slices;
+  __shared__ float heads[kSumWaves][64 * V];
+  __shared__ int through[kSumWaves];
   const int lane = threadIdx.x & 63;
-  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t unit = wave / slices;
-  const int64_t p0 = unit * span, n = start[vocab];
-  if (p0 >= n) return;
-  const int64_t p1 = p0 + span < n ? p0 + span : n;
-  // columns; a lane that would pass the row's end starts earlier and leaves
-  // the `skip` entries before its own to the lane that has them
-  int c = ((int)(wave - unit * slices) * 64 + lane) * V, skip = 0;
-  if (c >= dim) skip = V;
-  else if (c + V > dim) skip = c + V - dim;
-  c = c + V <= dim ? c : dim - V;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n = *total;
+  const int64_t p0 = ((int64_t)block * kSumWaves + w) * span;
+  if (p0 - w * span >= n) return;       // the whole block
+  const Place<V> at((slice * 64 + lane) * V, dim);
 
-  int64_t p = p0, end = p1;
-  const int32_t first = sorted[p0], last = sorted[p1 - 1];
-  const int32_t s1 = start[first], e1 = start[first + 1];
-  const int32_t s2 = start[last], e2 = start[last + 1];
-  bool head = false, tail = false;      // the first / last token's rows are a part
-  if (s1 < p0) {
-    if (e1 - s1 > kLong) head = true;
-    else p = e1;
-  }
-  if (e2 > p1) {
-    if (e2 - s2 > kLong) tail = true;
-    else end = e2;
-  }
-  if (p >= end) return;
+  const int have = (int)(n - p0 < span ? (n > p0 ? n - p0 : 0) : span);
+  // lane i: the token at p0 + i - 1, and the batch position at p0 + i
+  const int64_t q = p0 + lane - 1;
+  const int32_t tok = lane <= span + 1 && q >= 0 && q < n ? sorted[q] : -1;
+  const int32_t row = lane < have ? order[p0 + lane] : 0;
+  // bit i: the token at p0 + i is not the one before it
+  const uint64_t changes = __ballot(tok != __shfl_up(tok, 1)) >> 1;
+  int32_t cur = __builtin_amdgcn_readlane(tok, 1);
+  bool head = have > 0 && !(changes & 1);   // the first token began before this wave
+  const bool begun = head;
   float acc[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) acc[k] = 0.f;
-  int32_t cur = __builtin_amdgcn_readfirstlane(sorted[p]);
-  auto flush = [&](bool is_last) {
-    if (skip < V) {
-      if (head || (is_last && tail)) {
-        float* out = part + (2 * unit + (head ? 0 : 1)) * dim + c;
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (k >= skip) out[k] = acc[k];
-      } else {
-        TO* out = dW + (int64_t)cur * dim + c;
-        float v[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = scale * acc[k];
-        if (accumulate) {
-          float old[V];
-          read_cols<V>(out, old);
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[k] += old[k];
-        }
-        if constexpr (V > 1) {
-          if (skip == 0) store_vec<V>(out, v);
-        }
-        if (V == 1 || skip > 0)
-#pragma unroll
-          for (int k = 0; k < V; ++k)
-            if (k >= skip) put(out + k, v[k]);
-      }
-    }
+  // The sum of a token that ends here, or of the first one's rows.
+  auto flush = [&]() {
+    if (head) store_vec<V>(&heads[w][lane * V], acc);
+    else write_row<V>(dW + (int64_t)cur * dim + at.c, acc, at.skip, scale, accumulate);
     head = false;
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
   };
-  for (; p < end; p += 64) {
-    const int have = (int)(end - p < 64 ? end - p : 64);
-    const int32_t row = lane < have ? order[p + lane] : 0;
-    const int32_t tok = lane < have ? sorted[p + lane] : 0;
-    for (int i = 0; i < have; i += U) {
-      float v[U][V];
+  for (int i = 0; i < have; i += U) {
+    Piece<T, V> v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t r = __builtin_amdgcn_readlane(row, i + u < have ? i + u : i);
-        read_cols<V>(dY + r * dys + c, v[u]);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = __builtin_amdgcn_readlane(row, i + u < have ? i + u : i);
+      v[u].load(dY + r * dys + at.c);
+    }
+    const uint32_t turns = (uint32_t)(changes >> i) & ((1u << U) - 1) & (i == 0 ? ~1u : ~0u);
+    if (turns == 0 && i + U <= have) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] += v[u][k];
+    } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (i + u < have) {
-          const int32_t t = __builtin_amdgcn_readlane(tok, i + u);
-          if (t != cur) {
-            flush(false);
-            cur = t;
+          if (turns >> u & 1) {
+            flush();
+            cur = __builtin_amdgcn_readlane(tok, i + u + 1);
           }
 #pragma unroll
           for (int k = 0; k < V; ++k) acc[k] += v[u][k];
         }
     }
   }
-  flush(true);
+  // does the last token go on after this wave?
+  const bool on = have > 0 && !(changes >> have & 1);
+  const bool tail = on && !head;        // ... having begun in it
+  if (lane == 0) through[w] = on && head;
+  if (have > 0 && !tail) flush();
+  __syncthreads();
+  // Adds the heads of waves j.. to acc while the token goes on; whether it
+  // leaves the block.
+  auto collect = [&](int j) {
+    for (; j < kSumWaves; ++j) {
+      Piece<float, V> v;
+      v.load(&heads[j][lane * V]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] += v[k];
+      if (!through[j]) return false;
+    }
+    return true;
+  };
+  if (tail) {
+    if (collect(w + 1))
+      store_own<V>(part + (2 * (int64_t)block + 1) * dim + at.c, at.skip, acc);
+    else
+      write_row<V>(dW + (int64_t)cur * dim + at.c, acc, at.skip, scale, accumulate);
+  }
+  if (w == 0 && begun) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+    collect(0);
+    store_own<V>(part + 2 * (int64_t)block * dim + at.c, at.skip, acc);
+  }
 }
 
-// Adds the parts of long tokens.  A block looks for the long tokens that begin
-// in its kJoinUnits units; its 8 waves each add a run of consecutive parts
-// (64 columns), and meet in LDS.
-constexpr int kJoinUnits = 16, kJoinWaves = 8;
-
+// Adds the parts of a token that begins in block b of the sums (blockIdx.x)
+// and goes on in the next, for 128 columns by 4 lanes over consecutive parts.
 template <typename TO>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_embed_join(
-    const float* __restrict__ part, const int32_t* __restrict__ sorted,
-    const int32_t* __restrict__ start, int64_t vocab, int dim, int span, float scale,
-    TO* __restrict__ dW, int accumulate) {
-  __shared__ float sh[kJoinWaves][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = blockIdx.y * 64 + lane;
-  const int64_t n = start[vocab];
-  for (int k = 0; k < kJoinUnits; ++k) {
-    const int64_t u = (int64_t)blockIdx.x * kJoinUnits + k, p0 = u * span;
-    if (p0 + span >= n) return;           // nothing goes on past this unit
-    const int32_t t = sorted[p0 + span - 1];
-    const int32_t s = start[t], e = start[t + 1];
-    if (s < p0 || e <= p0 + span || e - s <= kLong) continue;
-    // part 2u + 1, then 2j for the units j after u up to the token's end
-    const int64_t parts = (e - 1) / span - u + 1;
-    const int64_t run = (parts + kJoinWaves - 1) / kJoinWaves;
-    const int64_t j1 = (w + 1) * run < parts ? (w + 1) * run : parts;
-    float a = 0.f;
-    if (c < dim) {
+__global__ __launch_bounds__(512) void k_embed_join(const float* __restrict__ part,
+                                                     const int32_t* __restrict__ sorted,
+                                                     const int32_t* __restrict__ total,
+                                                     int64_t blocks, int dim, int positions,
+                                                     float scale, TO* __restrict__ dW,
+                                                     int accumulate) {
+  __shared__ float sh[4][128];
+  const int64_t b = blockIdx.x, p0 = b * positions, p1 = p0 + positions;
+  const int64_t n = *total;
+  if (p1 >= n) return;
+  const int32_t t = sorted[p1 - 1];
+  if (sorted[p1] != t || (b > 0 && sorted[p0 - 1] == t)) return;
+  // the blocks after b that begin with t: equal tokens are neighbours
+  const int lane = threadIdx.x & 63;
+  int64_t more = 0;
+  for (int64_t j = b + 1;; j += 64) {
+    const int64_t at = (j + lane) * positions;
+    const int found = __popcll(__ballot(at < n && sorted[at < n ? at : 0] == t));
+    more += found;
+    if (found < 64) break;
+  }
+  // parts: 2b + 1, then 2j for each of those
+  const int x = threadIdx.x & 127, y = threadIdx.x >> 7;
+  const int c = blockIdx.y * 128 + x;
+  const int64_t run = (more + 4) / 4;
+  const int64_t j1 = (y + 1) * run < more + 1 ? (y + 1) * run : more + 1;
+  float a = 0.f;
+  if (c < dim) {
 #pragma unroll 8
-      for (int64_t j = w * run; j < j1; ++j)
-        a += part[(2 * (u + j) + (j == 0)) * dim + c];
-    }
-    sh[w][lane] = a;
-    __syncthreads();
-    if (w == 0 && c < dim) {
-#pragma unroll
-      for (int q = 1; q < kJoinWaves; ++q) a += sh[q][lane];
-      TO* out = dW + (int64_t)t * dim + c;
-      put(out, accumulate ? to_f32(*out) + scale * a : scale * a);
-    }
-    __syncthreads();
+    for (int64_t j = y * run; j < j1; ++j) a += part[(2 * (b + j) + (j == 0)) * dim + c];
+  }
+  sh[y][x] = a;
+  __syncthreads();
+  if (y == 0 && c < dim) {
+    a = ((a + sh[1][x]) + sh[2][x]) + sh[3][x];
+    TO* out = dW + (int64_t)t * dim + c;
+    put(out, accumulate ? to_f32(*out) + scale * a : scale * a);
   }
 }
 
@@ -356,24 +405,25 @@ constexpr int64_t kMaxBlocks = 1 << 16;   // larger grids loop
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Positions a unit.
-int span_of(int64_t n) { return n <= 32768 ? 16 : 32; }
+// Positions a wave of the sums.
+int span_of(int64_t n) { return n <= 32768 ? 8 : n <= 131072 ? 16 : 32; }
 
 struct GradPlan {
-  int span, range, bits;
-  int64_t units;
-  size_t order, sorted, start, part, total;
+  int shift, range, bits, span;
+  int64_t blocks;       // of the sums
+  size_t order, sorted, count, part, total;
   GradPlan(int64_t n, int64_t vocab, int64_t dim) {
-    range = (int)std::min<int64_t>((vocab + 255) / 256, kMaxRange);
+    for (shift = 8; (vocab - 1) >> shift >= kMaxRange;) ++shift;
+    range = (int)((vocab - 1) >> shift) + 1;
     for (bits = 0; (1 << bits) < range;) ++bits;
     span = span_of(n);
-    units = (n + span - 1) / span;
+    blocks = (n + span * kSumWaves - 1) / (span * kSumWaves);
     order = 0;
     sorted = order + align256((size_t)n * 4);
-    start = sorted + align256((size_t)n * 4);
-    part = start + align256((size_t)(vocab + 1) * 4);
-    // no token has more than kLong rows in a batch of kLong
-    total = part + (n > kLong ? align256((size_t)units * 2 * dim * 4) : 0);
+    count = sorted + align256((size_t)n * 4);
+    part = count + 256;
+    // one block has no neighbours
+    total = part + (blocks > 1 ? align256((size_t)blocks * 2 * dim * 4) : 0);
   }
 };
 
@@ -403,22 +453,22 @@ hipError_t embed(const EmbedArgs& a, hipStream_t s) {
 
 template <typename TI, typename TO>
 hipError_t token_sort(const EmbedGradArgs& a, const GradPlan& pl, int32_t* order, int32_t* sorted,
-                      int32_t* start, hipStream_t s) {
-  const int64_t grid = (a.vocab + pl.range - 1) / pl.range;
+                      int32_t* total, hipStream_t s) {
+  const int64_t grid = std::min<int64_t>((int64_t)1 << pl.shift, a.vocab);
   hipLaunchKernelGGL((k_token_sort<TI, TO>), dim3((unsigned)grid), dim3(64 * kSortWaves),
-                     (size_t)kSortWaves * pl.range * 4, s, (const TI*)a.tokens, a.n, a.vocab,
-                     a.padding, pl.range, pl.bits, order, sorted, start,
-                     a.accumulate ? nullptr : (TO*)a.dW, (int)a.dim);
+                     0, s, (const TI*)a.tokens, a.n,
+                     (uint32_t)a.vocab, (uint32_t)a.padding, pl.shift, pl.range, pl.bits, order,
+                     sorted, total, a.accumulate ? nullptr : (TO*)a.dW, (int)a.dim);
   return hipGetLastError();
 }
 
 template <typename T, typename TO, int V>
 void embed_sum(const EmbedGradArgs& a, const GradPlan& pl, const int32_t* order,
-               const int32_t* sorted, const int32_t* start, float* part, hipStream_t s) {
+               const int32_t* sorted, const int32_t* total, float* part, hipStream_t s) {
   const int64_t slices = (a.dim + 64 * V - 1) / (64 * V);
-  hipLaunchKernelGGL((k_embed_sum<T, TO, V>), dim3((unsigned)((pl.units * slices + 3) / 4)),
-                     dim3(256), 0, s, (const T*)a.dY, a.dy_stride, order, sorted, start, a.vocab,
-                     (int)a.dim, (int)slices, pl.span, a.scale, (TO*)a.dW, a.accumulate, part);
+  hipLaunchKernelGGL((k_embed_sum<T, TO, V>), dim3((unsigned)(pl.blocks * slices)),
+                     dim3(64 * kSumWaves), 0, s, (const T*)a.dY, a.dy_stride, order, sorted, total,
+                     (int)a.dim, pl.span, (int)slices, a.scale, (TO*)a.dW, a.accumulate, part);
 }
 
 template <typename T, typename TO>
@@ -427,23 +477,22 @@ hipError_t embed_grad(const EmbedGradArgs& a, hipStream_t s) {
   char* ws = (char*)a.ws;
   int32_t* order = (int32_t*)(ws + pl.order);
   int32_t* sorted = (int32_t*)(ws + pl.sorted);
-  int32_t* start = (int32_t*)(ws + pl.start);
+  int32_t* total = (int32_t*)(ws + pl.count);
   float* part = (float*)(ws + pl.part);
-  hipError_t e = a.token_bits == 64 ? token_sort<int64_t, TO>(a, pl, order, sorted, start, s)
-                                    : token_sort<int32_t, TO>(a, pl, order, sorted, start, s);
+  hipError_t e = a.token_bits == 64 ? token_sort<int64_t, TO>(a, pl, order, sorted, total, s)
+                                    : token_sort<int32_t, TO>(a, pl, order, sorted, total, s);
   if (e != hipSuccess || a.n == 0) return e;
   if (sizeof(T) == 2 && a.dim >= 512)
-    embed_sum<T, TO, 8>(a, pl, order, sorted, start, part, s);
+    embed_sum<T, TO, 8>(a, pl, order, sorted, total, part, s);
   else if (a.dim >= 4)
-    embed_sum<T, TO, 4>(a, pl, order, sorted, start, part, s);
+    embed_sum<T, TO, 4>(a, pl, order, sorted, total, part, s);
   else
-    embed_sum<T, TO, 1>(a, pl, order, sorted, start, part, s);
-  if ((e = hipGetLastError()) != hipSuccess || a.n <= kLong) return e;
+    embed_sum<T, TO, 1>(a, pl, order, sorted, total, part, s);
+  if ((e = hipGetLastError()) != hipSuccess || pl.blocks <= 1) return e;
   hipLaunchKernelGGL((k_embed_join<TO>),
-                     dim3((unsigned)((pl.units + kJoinUnits - 1) / kJoinUnits),
-                          (unsigned)((a.dim + 63) / 64)),
-                     dim3(64 * kJoinWaves), 0, s, part, sorted, start, a.vocab, (int)a.dim,
-                     pl.span, a.scale, (TO*)a.dW, a.accumulate);
+                     dim3((unsigned)pl.blocks, (unsigned)((a.dim + 127) / 128)), dim3(512), 0, s,
+                     part, sorted, total, pl.blocks, (int)a.dim, pl.span * kSumWaves, a.scale,
+                     (TO*)a.dW, a.accumulate);
   return hipGetLastError();
 }
 

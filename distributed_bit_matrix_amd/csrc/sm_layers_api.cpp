@@ -10,7 +10,8 @@ namespace {
 
 constexpr int64_t kMaxDim = 1 << 20;                 // cols, dim, vocab
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
-constexpr int64_t kMaxTokens = (int64_t)1 << 30;      // a launch has below 2^32 threads
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxSorted = (int64_t)1 << 27;      // a 16th of it has a 23-bit place
 
 bool dtype_ok(int32_t d) { return d == SM_F32 || d == SM_BF16; }
 bool aligned(const void* p, int32_t dtype) {
@@ -90,7 +91,7 @@ sm_status signmuon_embedding(const void* W, int32_t w_dtype, int64_t vocab, int6
 }
 
 size_t signmuon_embedding_backward_workspace(int64_t n, int64_t vocab, int64_t dim) {
-  if (!in(n, 0, kMaxTokens) || !in(vocab, 1, kMaxDim) || !in(dim, 1, kMaxDim)) return SIZE_MAX;
+  if (!in(n, 0, kMaxSorted) || !in(vocab, 1, kMaxDim) || !in(dim, 1, kMaxDim)) return SIZE_MAX;
   return embed_grad_workspace(n, vocab, dim);
 }
 
@@ -101,7 +102,7 @@ sm_status signmuon_embedding_backward(const void* dY, int32_t dy_dtype, int64_t 
                                       size_t ws_bytes, hipStream_t stream) {
   if (!dtype_ok(dy_dtype) || !dtype_ok(dw_dtype)) return SM_EINVAL;
   if (token_bits != 32 && token_bits != 64) return SM_EINVAL;
-  if (!in(n, 0, kMaxTokens) || !in(vocab, 1, kMaxDim) || !in(dim, 1, kMaxDim)) return SM_EINVAL;
+  if (!in(n, 0, kMaxSorted) || !in(vocab, 1, kMaxDim) || !in(dim, 1, kMaxDim)) return SM_EINVAL;
   if (!in(padding, -1, vocab - 1) || !std::isfinite(scale)) return SM_EINVAL;
   if (!in(accumulate, 0, 1) || (accumulate && dw_dtype != SM_F32)) return SM_EINVAL;
   if (n == 0 && accumulate) return SM_OK;

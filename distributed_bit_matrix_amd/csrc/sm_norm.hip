@@ -14,9 +14,6 @@
 
 namespace sm {
 
-template <typename T>
-constexpr int kVec = 16 / (int)sizeof(T);   // entries of a 16-byte piece
-
 // Sums of K values each over groups of LANES threads, in a fixed order; valid
 // in every thread of the group.  Groups wider than a wave meet in LDS, where
 // `turn` alternates between two buffers: one barrier a sum is enough, since a
@@ -47,63 +44,56 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int& turn) {
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
-template <typename T, typename TW, int LANES, int NV>
+template <typename T, typename TW, int V, int LANES, int NV>
 __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void k_norm(
     const T* X, int64_t xs, const TW* gamma, const TW* beta, int64_t rows, int cols, float eps,
     T* Y, float* mean, float* rstd) {
-  constexpr int V = kVec<T>, GROUPS = LANES > 256 ? 1 : 256 / LANES;
-  const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  constexpr int GROUPS = LANES > 256 ? 1 : 256 / LANES;
+  const int lane = threadIdx.x % LANES;
+  const Place<V> last(((NV - 1) * LANES + lane) * V, cols);   // only the last piece can be cut
   const float inv = 1.0f / cols;
   int turn = 0;
-  // rows of a block run together: barriers are met by all its threads
-  for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < rows; r0 += (int64_t)gridDim.x * GROUPS) {
-    const int64_t r = r0 + group;
-    const bool live = r < rows;
-    float x[NV][V];
+  for (int64_t r = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES; r < rows;
+       r += (int64_t)gridDim.x * GROUPS) {
+    Piece<T, V> in[NV];
+    Piece<TW, V> g[NV], b[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      in[j].load(X + r * xs + (j < NV - 1 ? (j * LANES + lane) * V : last.c));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * LANES + lane) * V;
-      load_part<V>(X + r * xs + c, live ? cols - c : 0, x[j]);
+      const int c = j < NV - 1 ? (j * LANES + lane) * V : last.c;
+      if (gamma) g[j].load(gamma + c);
+      if (beta) b[j].load(beta + c);
     }
+    float x[NV][V];
     float s[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int k = 0; k < V; ++k) s[0] += x[j][k];
+      for (int k = 0; k < V; ++k) {
+        x[j][k] = in[j][k];
+        s[0] += j < NV - 1 || k >= last.skip ? x[j][k] : 0.f;
+      }
     group_sums<LANES, 1>(s, turn);
     const float mu = s[0] / cols;
     s[0] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int have = cols - (j * LANES + lane) * V;
-      if (have >= V) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          x[j][k] -= mu;
-          s[0] += x[j][k] * x[j][k];
-        }
-      } else if (have > 0) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          x[j][k] = k < have ? x[j][k] - mu : 0.f;
-          s[0] += x[j][k] * x[j][k];
-        }
+      for (int k = 0; k < V; ++k) {
+        x[j][k] = j < NV - 1 || k >= last.skip ? x[j][k] - mu : 0.f;
+        s[0] += x[j][k] * x[j][k];
       }
-    }
     group_sums<LANES, 1>(s, turn);
     const float rs = 1.0f / sqrtf(s[0] * inv + eps);
-    if (!live) continue;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * LANES + lane) * V, have = cols - c;
-      if (have <= 0) continue;
-      float g[V], b[V];
-      if (gamma) load_part<V>(gamma + c, have, g);
-      if (beta) load_part<V>(beta + c, have, b);
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        x[j][k] = x[j][k] * rs * (gamma ? g[k] : 1.f) + (beta ? b[k] : 0.f);
-      store_part<V>(Y + r * cols + c, have, x[j]);
+        x[j][k] = x[j][k] * rs * (gamma ? g[j][k] : 1.f) + (beta ? b[j][k] : 0.f);
+      if (j < NV - 1) store_vec<V>(Y + r * cols + (j * LANES + lane) * V, x[j]);
+      else store_own<V>(Y + r * cols + last.c, last.skip, x[j]);
     }
     if (lane == 0) {
       if (mean) mean[r] = mu;
@@ -159,59 +149,68 @@ __global__ __launch_bounds__(1024) void k_norm_long(const T* X, int64_t xs, cons
 // registers; its groups' sums meet in LDS at the end, and k_norm_join adds the
 // blocks' (part[block][2][cols]).
 // ---------------------------------------------------------------------------
-template <typename T, typename TW, int LANES, int NV>
+template <typename T, typename TW, int V, int LANES, int NV>
 __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
     const T* dY, int64_t dys, const T* X, int64_t xs, const TW* gamma, const float* mean,
     const float* rstd, int64_t rows, int cols, T* dX, float* part) {
-  constexpr int V = kVec<T>, THREADS = LANES > 512 ? LANES : 512, GROUPS = THREADS / LANES;
+  constexpr int THREADS = LANES > 512 ? LANES : 512, GROUPS = THREADS / LANES;
   const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const Place<V> last(((NV - 1) * LANES + lane) * V, cols);   // only the last piece can be cut
   const float inv = 1.0f / cols;
   int turn = 0;
   float w[NV][V], ag[NV][V], ab[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = (j * LANES + lane) * V;
-    if (gamma) load_part<V>(gamma + c, cols - c, w[j]);
+    Piece<TW, V> g;
+    if (gamma) g.load(gamma + (j < NV - 1 ? (j * LANES + lane) * V : last.c));
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      if (!gamma) w[j][k] = 1.f;
+      w[j][k] = gamma ? g[k] : 1.f;
       ag[j][k] = ab[j][k] = 0.f;
     }
   }
+  // where groups meet in barriers, all of a block's go through the same turns
   for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < rows; r0 += (int64_t)gridDim.x * GROUPS) {
     const int64_t r = r0 + group;
     const bool live = r < rows;
-    float dy[NV][V], xh[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * LANES + lane) * V, have = live ? cols - c : 0;
-      load_part<V>(dY + r * dys + c, have, dy[j]);
-      load_part<V>(X + r * xs + c, have, xh[j]);
-    }
-    const float mu = live ? mean[r] : 0.f, rs = live ? rstd[r] : 0.f;
     float s[2] = {0.f, 0.f};
+    float g[NV][V], xh[NV][V];
+    float rs = 0.f;
+    if (live) {
+      Piece<T, V> pd[NV], px[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        // past the row's end dy is 0, and so is all that follows from it
-        xh[j][k] = (xh[j][k] - mu) * rs;
-        ag[j][k] += dy[j][k] * xh[j][k];
-        ab[j][k] += dy[j][k];
-        dy[j][k] *= w[j][k];
-        s[0] += dy[j][k];
-        s[1] += dy[j][k] * xh[j][k];
+      for (int j = 0; j < NV; ++j) {
+        const int c = j < NV - 1 ? (j * LANES + lane) * V : last.c;
+        pd[j].load(dY + r * dys + c);
+        px[j].load(X + r * xs + c);
       }
+      const float mu = mean[r];
+      rs = rstd[r];
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          // what is not the lane's own counts as dY = 0, X = mean
+          const bool own = j < NV - 1 || k >= last.skip;
+          const float dy = own ? pd[j][k] : 0.f;
+          xh[j][k] = own ? (px[j][k] - mu) * rs : 0.f;
+          ag[j][k] += dy * xh[j][k];
+          ab[j][k] += dy;
+          g[j][k] = dy * w[j][k];
+          s[0] += g[j][k];
+          s[1] += g[j][k] * xh[j][k];
+        }
+    }
     if (!dX) continue;
     group_sums<LANES, 2>(s, turn);
-    const float c1 = s[0] * inv, c2 = s[1] * inv;
     if (!live) continue;
+    const float c1 = s[0] * inv, c2 = s[1] * inv;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * LANES + lane) * V;
 #pragma unroll
-      for (int k = 0; k < V; ++k) dy[j][k] = rs * (dy[j][k] - c1 - xh[j][k] * c2);
-      if (cols - c > 0) store_part<V>(dX + r * cols + c, cols - c, dy[j]);
+      for (int k = 0; k < V; ++k) g[j][k] = rs * (g[j][k] - c1 - xh[j][k] * c2);
+      if (j < NV - 1) store_vec<V>(dX + r * cols + (j * LANES + lane) * V, g[j]);
+      else store_own<V>(dX + r * cols + last.c, last.skip, g[j]);
     }
   }
   if (!part) return;
@@ -219,12 +218,14 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
   if constexpr (GROUPS == 1) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * LANES + lane) * V;
-      if (cols - c <= 0) continue;
-      store_part<V>(out + c, cols - c, ag[j]);
-      store_part<V>(out + cols + c, cols - c, ab[j]);
+      const int c = j < NV - 1 ? (j * LANES + lane) * V : last.c;
+      const int skip = j < NV - 1 ? 0 : last.skip;
+      store_own<V>(out + c, skip, ag[j]);
+      store_own<V>(out + cols + c, skip, ab[j]);
     }
   } else {
+    // one column after the other of a piece, so that neighbouring lanes write
+    // neighbouring words
     constexpr int SPAN = LANES * NV * V;
     __shared__ float sh[GROUPS * SPAN];
 #pragma unroll
@@ -232,13 +233,18 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        store_vec<V>(sh + group * SPAN + (j * LANES + lane) * V, pass ? ab[j] : ag[j]);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          sh[group * SPAN + (j * V + k) * LANES + lane] = pass ? ab[j][k] : ag[j][k];
       __syncthreads();
-      for (int c = threadIdx.x; c < cols; c += THREADS) {
-        float t = sh[c];
+      for (int q = threadIdx.x; q < SPAN; q += THREADS) {
+        const int l = q % LANES, jk = q / LANES, j = jk / V, k = jk % V;
+        const Place<V> at((j * LANES + l) * V, cols);
+        if (k < at.skip) continue;
+        float t = sh[q];
 #pragma unroll 8
-        for (int g = 1; g < GROUPS; ++g) t += sh[g * SPAN + c];
-        out[pass * cols + c] = t;
+        for (int g = 1; g < GROUPS; ++g) t += sh[g * SPAN + q];
+        out[pass * cols + at.c + k] = t;
       }
     }
   }
@@ -326,6 +332,7 @@ constexpr int64_t kMaxBlocks = 1 << 16;   // larger grids loop
 constexpr int kGradBlocks = 512;          // two blocks of 512 threads a CU
 
 // Threads a row: the fewest that hold it in at most `most` pieces each.  0: too long.
+// Rows shorter than a piece go entry by entry (8 threads).
 int lanes_for(int64_t cols, int vec, int most) {
   for (int lanes : {8, 16, 32})
     if (cols <= lanes * vec) return lanes;
@@ -347,32 +354,37 @@ int64_t grad_blocks(int64_t rows, int64_t cols, int32_t dtype) {
   return std::min<int64_t>((rows + groups - 1) / groups, lanes > 512 ? 256 : kGradBlocks);
 }
 
-template <typename T, typename TW, int LANES, int NV>
+template <typename T, typename TW, int V, int LANES, int NV>
 void norm_go(const NormArgs& a, hipStream_t s) {
   constexpr int THREADS = LANES > 256 ? LANES : 256, GROUPS = THREADS / LANES;
   const int64_t grid = std::min<int64_t>((a.rows + GROUPS - 1) / GROUPS, kMaxBlocks);
-  hipLaunchKernelGGL((k_norm<T, TW, LANES, NV>), dim3((unsigned)grid), dim3(THREADS), 0, s,
+  hipLaunchKernelGGL((k_norm<T, TW, V, LANES, NV>), dim3((unsigned)grid), dim3(THREADS), 0, s,
                      (const T*)a.X, a.x_stride, (const TW*)a.gamma, (const TW*)a.beta, a.rows,
                      (int)a.cols, a.eps, (T*)a.Y, a.mean, a.rstd);
 }
 
 template <typename T, typename TW, int LANES>
 void norm_pieces(const NormArgs& a, hipStream_t s) {
-  const int64_t per = (int64_t)LANES * kVec<T>;
+  constexpr int V = 16 / (int)sizeof(T);
+  const int64_t per = (int64_t)LANES * V;
   switch ((a.cols + per - 1) / per) {
-    case 1: return norm_go<T, TW, LANES, 1>(a, s);
-    case 2: return norm_go<T, TW, LANES, 2>(a, s);
-    case 3: return norm_go<T, TW, LANES, 3>(a, s);
-    default: return norm_go<T, TW, LANES, 4>(a, s);
+    case 1: return norm_go<T, TW, V, LANES, 1>(a, s);
+    case 2: return norm_go<T, TW, V, LANES, 2>(a, s);
+    case 3: return norm_go<T, TW, V, LANES, 3>(a, s);
+    default: return norm_go<T, TW, V, LANES, 4>(a, s);
   }
 }
 
 template <typename T, typename TW>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
-  switch (lanes_for(a.cols, kVec<T>, 4)) {
-    case 8: norm_go<T, TW, 8, 1>(a, s); break;
-    case 16: norm_go<T, TW, 16, 1>(a, s); break;
-    case 32: norm_go<T, TW, 32, 1>(a, s); break;
+  constexpr int V = 16 / (int)sizeof(T);
+  switch (lanes_for(a.cols, V, 4)) {
+    case 8:
+      if (a.cols < V) norm_go<T, TW, 1, 8, 1>(a, s);
+      else norm_go<T, TW, V, 8, 1>(a, s);
+      break;
+    case 16: norm_go<T, TW, V, 16, 1>(a, s); break;
+    case 32: norm_go<T, TW, V, 32, 1>(a, s); break;
     case 64: norm_pieces<T, TW, 64>(a, s); break;
     case 256: norm_pieces<T, TW, 256>(a, s); break;
     case 1024: norm_pieces<T, TW, 1024>(a, s); break;
@@ -384,9 +396,9 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, typename TW, int LANES, int NV>
+template <typename T, typename TW, int V, int LANES, int NV>
 void norm_grad_go(const NormGradArgs& a, int64_t grid, float* part, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_grad<T, TW, LANES, NV>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((k_norm_grad<T, TW, V, LANES, NV>), dim3((unsigned)grid),
                      dim3(LANES > 512 ? LANES : 512), 0, s, (const T*)a.dY, a.dy_stride,
                      (const T*)a.X, a.x_stride, (const TW*)a.gamma, a.mean, a.rstd, a.rows,
                      (int)a.cols, (T*)a.dX, part);
@@ -394,32 +406,37 @@ void norm_grad_go(const NormGradArgs& a, int64_t grid, float* part, hipStream_t 
 
 template <typename T, typename TW, int LANES>
 void norm_grad_pieces(const NormGradArgs& a, int64_t grid, float* part, hipStream_t s) {
-  const int64_t per = (int64_t)LANES * kVec<T>;
+  constexpr int V = 16 / (int)sizeof(T);
+  const int64_t per = (int64_t)LANES * V;
   const int64_t nv = (a.cols + per - 1) / per;
-  if constexpr (kVec<T> == 8) {
-    if (nv == 1) norm_grad_go<T, TW, LANES, 1>(a, grid, part, s);
-    else norm_grad_go<T, TW, LANES, 2>(a, grid, part, s);
+  if constexpr (V == 8) {
+    if (nv == 1) norm_grad_go<T, TW, V, LANES, 1>(a, grid, part, s);
+    else norm_grad_go<T, TW, V, LANES, 2>(a, grid, part, s);
   } else {
     switch (nv) {
-      case 1: return norm_grad_go<T, TW, LANES, 1>(a, grid, part, s);
-      case 2: return norm_grad_go<T, TW, LANES, 2>(a, grid, part, s);
-      case 3: return norm_grad_go<T, TW, LANES, 3>(a, grid, part, s);
-      default: return norm_grad_go<T, TW, LANES, 4>(a, grid, part, s);
+      case 1: return norm_grad_go<T, TW, V, LANES, 1>(a, grid, part, s);
+      case 2: return norm_grad_go<T, TW, V, LANES, 2>(a, grid, part, s);
+      case 3: return norm_grad_go<T, TW, V, LANES, 3>(a, grid, part, s);
+      default: return norm_grad_go<T, TW, V, LANES, 4>(a, grid, part, s);
     }
   }
 }
 
 template <typename T, typename TW>
 hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
+  constexpr int V = 16 / (int)sizeof(T);
   const bool sums = a.dgamma || a.dbeta;
   const int64_t blocks = grad_blocks(a.rows, a.cols, a.x_dtype);
   float* part = sums ? (float*)a.ws : nullptr;
   hipError_t e;
   if (a.rows > 0) {
     switch (grad_lanes(a.cols, a.x_dtype)) {
-      case 8: norm_grad_go<T, TW, 8, 1>(a, blocks, part, s); break;
-      case 16: norm_grad_go<T, TW, 16, 1>(a, blocks, part, s); break;
-      case 32: norm_grad_go<T, TW, 32, 1>(a, blocks, part, s); break;
+      case 8:
+        if (a.cols < V) norm_grad_go<T, TW, 1, 8, 1>(a, blocks, part, s);
+        else norm_grad_go<T, TW, V, 8, 1>(a, blocks, part, s);
+        break;
+      case 16: norm_grad_go<T, TW, V, 16, 1>(a, blocks, part, s); break;
+      case 32: norm_grad_go<T, TW, V, 32, 1>(a, blocks, part, s); break;
       case 64: norm_grad_pieces<T, TW, 64>(a, blocks, part, s); break;
       case 256: norm_grad_pieces<T, TW, 256>(a, blocks, part, s); break;
       case 1024: norm_grad_pieces<T, TW, 1024>(a, blocks, part, s); break;

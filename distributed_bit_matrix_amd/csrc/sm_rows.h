@@ -1,10 +1,15 @@
-// Device helpers shared by the row operators (layer norm, embedding): wide
-// loads and stores at any element alignment, and sums within lane groups.
+// Device helpers shared by the row operators (layer norm, embedding): pieces of
+// rows at any element alignment, and sums within lane groups.
 #pragma once
 
 #include "sm_internal.h"
 
 namespace sm {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
 // A row of odd length starts at an address that is a multiple of its element
 // size only.  Global memory instructions of 16 bytes take such addresses, so
@@ -12,57 +17,68 @@ namespace sm {
 // length move in 16-byte pieces.
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(bf16_t v) { return bf16_to_f32(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
-
-template <int V>
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[V]) {
-  static_assert(V % 4 == 0, "pieces of 4");
+// V consecutive entries as they lie in memory (V = 1, or 8 bytes or a multiple
+// of 16).  Loading and widening are apart, so that a kernel can have all its
+// loads under way before the first value is looked at.
+template <typename T, int V>
+struct Piece {
+  static constexpr int kWords = V * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 2) {
+      const u32x2_a2 t = *reinterpret_cast<const u32x2_a2*>(p);
+      w[0] = t[0];
+      w[1] = t[1];
+    } else {
 #pragma unroll
-  for (int k = 0; k < V; k += 4) {
-    f32x4_a4 t = *reinterpret_cast<const f32x4_a4*>(p + k);
+      for (int k = 0; k < kWords; k += 4) {
+        uint32_t t[4];
+        if constexpr (sizeof(T) == 4) {
+          const u32x4_a4 v = *reinterpret_cast<const u32x4_a4*>(p + k);
+          t[0] = v[0], t[1] = v[1], t[2] = v[2], t[3] = v[3];
+        } else {
+          const u32x4_a2 v = *reinterpret_cast<const u32x4_a2*>(p + 2 * k);
+          t[0] = v[0], t[1] = v[1], t[2] = v[2], t[3] = v[3];
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[k + j] = t[j];
-  }
-}
-template <int V>
-__device__ __forceinline__ void load_vec(const bf16_t* p, float (&v)[V]) {
-  static_assert(V == 4 || V % 8 == 0, "pieces of 4 or 8");
-  if constexpr (V == 4) {
-    u32x2_a2 t = *reinterpret_cast<const u32x2_a2*>(p);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      v[2 * j] = __uint_as_float(t[j] << 16);
-      v[2 * j + 1] = __uint_as_float(t[j] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; k += 8) {
-      u32x4_a2 t = *reinterpret_cast<const u32x4_a2*>(p + k);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[k + 2 * j] = __uint_as_float(t[j] << 16);
-        v[k + 2 * j + 1] = __uint_as_float(t[j] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) w[k + j] = t[j];
       }
     }
   }
-}
-template <int V>
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
-#pragma unroll
-  for (int k = 0; k < V; k += 4)
-    *reinterpret_cast<f32x4_a4*>(p + k) = f32x4_a4{v[k], v[k + 1], v[k + 2], v[k + 3]};
-}
+  __device__ __forceinline__ float operator[](int k) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+    else return __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+  }
+};
+template <typename T>
+struct Piece<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ float operator[](int) const { return to_f32(v); }
+};
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
 }
 template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = v[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4)
+      *reinterpret_cast<u32x4_a4*>(p + k) =
+          u32x4_a4{__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]),
+                   __float_as_uint(v[k + 3])};
+  }
+}
+template <int V>
 __device__ __forceinline__ void store_vec(bf16_t* p, const float (&v)[V]) {
-  if constexpr (V == 4) {
+  if constexpr (V == 1) {
+    *p = f32_to_bf16(v[0]);
+  } else if constexpr (V == 4) {
     *reinterpret_cast<u32x2_a2*>(p) = u32x2_a2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
   } else {
 #pragma unroll
@@ -72,25 +88,30 @@ __device__ __forceinline__ void store_vec(bf16_t* p, const float (&v)[V]) {
                    pack_bf16(v[k + 4], v[k + 5]), pack_bf16(v[k + 6], v[k + 7])};
   }
 }
-// The first `have` of V elements (all, when have >= V); the rest read as 0.
-template <int V, typename T>
-__device__ __forceinline__ void load_part(const T* p, int have, float (&v)[V]) {
-  if (have >= V) {
-    load_vec<V>(p, v);
-    return;
+
+// Where a lane's piece of a row of `cols` >= V entries lies if it would begin
+// at c: a piece that would pass the row's end begins earlier, and its first
+// `skip` entries belong to the lane before it (all V: the piece has none).
+// So every lane loads a whole piece inside the row.
+template <int V>
+struct Place {
+  int c, skip;
+  __device__ __forceinline__ Place(int at, int cols) {
+    const int over = at + V - cols;
+    skip = over <= 0 ? 0 : over < V ? over : V;
+    c = over <= 0 ? at : cols - V;
   }
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] = k < have ? to_f32(p[k]) : 0.f;
-}
+};
+// The entries of v that are the lane's own, to p.
 template <int V, typename T>
-__device__ __forceinline__ void store_part(T* p, int have, const float (&v)[V]) {
-  if (have >= V) {
+__device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[V]) {
+  if (skip == 0) {
     store_vec<V>(p, v);
-    return;
-  }
+  } else if (skip < V) {
 #pragma unroll
-  for (int k = 0; k < V; ++k)
-    if (k < have) put(p + k, v[k]);
+    for (int k = 1; k < V; ++k)
+      if (k >= skip) put(p + k, v[k]);
+  }
 }
 
 // Sum over aligned groups of W lanes (W a power of two, at most 64), in a

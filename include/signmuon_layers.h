@@ -91,8 +91,8 @@ sm_status signmuon_embedding(const void *W, int32_t w_dtype, int64_t vocab,
  * rows untouched.  Tokens equal to padding (-1: none) and tokens outside
  * [0, vocab) add nothing.  Row i of dY starts at element i * dy_stride
  * (dy_stride >= dim).  The rows of one token are added in an order that n
- * and the tokens alone decide.  Limits as for signmuon_embedding; padding is
- * -1 or in [0, vocab).
+ * and the tokens alone decide.  n <= 2^27, other limits as for
+ * signmuon_embedding; padding is -1 or in [0, vocab).
  * ws: signmuon_embedding_backward_workspace() bytes, 256-byte aligned; its
  * contents on entry do not matter.  The query returns SIZE_MAX for arguments
  * outside the limits.

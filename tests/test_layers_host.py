@@ -97,7 +97,7 @@ def _embed_grad(dY=P, dyd=0, dys=8, t=Q, bits=64, n=5, pad=-1, scale=1.0, dW=S, 
 @built
 def test_embedding_grad_refusals():
     assert _embed_grad(n=0, acc=1, dW=None, ws=None) == B.SM_OK
-    for bad in (dict(dyd=2), dict(dwd=2), dict(bits=8), dict(n=-1), dict(n=(1 << 30) + 1),
+    for bad in (dict(dyd=2), dict(dwd=2), dict(bits=8), dict(n=-1), dict(n=(1 << 27) + 1),
                 dict(vocab=0), dict(dim=0), dict(pad=-2), dict(pad=9), dict(scale=NAN),
                 dict(acc=2), dict(acc=1, dwd=1), dict(dW=None), dict(dW=ODD), dict(dY=None),
                 dict(t=None), dict(dys=7), dict(dY=ODD), dict(t=ctypes.c_void_p((1 << 20) + 4))):
@@ -107,7 +107,7 @@ def test_embedding_grad_refusals():
     assert _embed_grad(nbytes=need - 1) == B.SM_EWORKSPACE
     assert _embed_grad(ws=None) == B.SM_EWORKSPACE
     assert _embed_grad(ws=ctypes.c_void_p((1 << 20) + 64)) == B.SM_EWORKSPACE
-    for args in ((-1, 9, 8), (5, 0, 8), (5, 9, 0), ((1 << 30) + 1, 9, 8), (5, (1 << 20) + 1, 8)):
+    for args in ((-1, 9, 8), (5, 0, 8), (5, 9, 0), ((1 << 27) + 1, 9, 8), (5, (1 << 20) + 1, 8)):
         with pytest.raises(B.SignMuonError) as e:
             B.embedding_backward_workspace(*args)
         assert e.value.status == B.SM_EINVAL
