@@ -392,8 +392,11 @@ def _check_arg(t, shape, dtype, dev, name):
 
 
 def _workspace(ws, nbytes, like, dev):
-    """(pointer, bytes) of the workspace: ws, or a new one."""
+    """(ws, pointer, bytes) of the workspace: the caller's, or a new one where
+    one is needed."""
     import torch
+    if nbytes == 0:
+        return None, None, 0
     if ws is None:
         ws = like.new_empty(nbytes, dtype=torch.uint8)
     elif not ws.is_contiguous():

@@ -115,11 +115,28 @@ __device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[V]) {
 }
 
 // Sum over aligned groups of W lanes (W a power of two, at most 64), in a
-// fixed order; the result reaches every lane of the group.
+// fixed order; the result reaches every lane of the group.  Up to 16 lanes meet
+// by data-parallel moves within a row of 16 (a shuffle would take a round trip
+// to LDS); four rows of 16 meet through scalars.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF,
+                                                        false));
+}
 template <int W>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if constexpr (W >= 2) v = dpp_add<0xB1>(v);     // quad_perm 1,0,3,2
+  if constexpr (W >= 4) v = dpp_add<0x4E>(v);     // quad_perm 2,3,0,1
+  if constexpr (W >= 8) v = dpp_add<0x141>(v);    // row_half_mirror
+  if constexpr (W >= 16) v = dpp_add<0x140>(v);   // row_mirror
+  if constexpr (W == 32) v += __shfl_xor(v, 16);
+  if constexpr (W == 64) {
+    const int i = __float_as_int(v);
+    v = (__int_as_float(__builtin_amdgcn_readlane(i, 0)) +
+         __int_as_float(__builtin_amdgcn_readlane(i, 16))) +
+        (__int_as_float(__builtin_amdgcn_readlane(i, 32)) +
+         __int_as_float(__builtin_amdgcn_readlane(i, 48)));
+  }
   return v;
 }
 

@@ -93,9 +93,9 @@ sm_status signmuon_embedding(const void *W, int32_t w_dtype, int64_t vocab,
  * (dy_stride >= dim).  The rows of one token are added in an order that n
  * and the tokens alone decide.  n <= 2^27, other limits as for
  * signmuon_embedding; padding is -1 or in [0, vocab).
- * ws: signmuon_embedding_backward_workspace() bytes, 256-byte aligned; its
- * contents on entry do not matter.  The query returns SIZE_MAX for arguments
- * outside the limits.
+ * ws: signmuon_embedding_backward_workspace() bytes, 256-byte aligned; NULL
+ * where that is 0 (small batches).  Its contents on entry do not matter.  The
+ * query returns SIZE_MAX for arguments outside the limits.
  */
 size_t signmuon_embedding_backward_workspace(int64_t n, int64_t vocab,
                                              int64_t dim);

@@ -110,6 +110,35 @@ def test_norm_backward(rows, cols, x_dtype):
         assert torch.equal(bits(one[k]), bits(both[k]))
 
 
+# rows times columns past what one launch serves, at the boundaries of the
+# kernels' row widths
+LARGE = [(1030, c) for c in (1, 3, 4, 7, 8, 31, 33, 63, 65, 127, 129, 255, 257, 511, 513, 767,
+                             1001, 1023, 1025, 2047, 2049, 4071)] + \
+    [(1025, 4097), (513, 8191), (512, 8193), (350, 12287), (340, 12289), (257, 16383),
+     (70, 16385)]
+
+
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", LARGE)
+def test_norm_backward_large(rows, cols, x_dtype):
+    print(f"norm grad large {rows}x{cols} {x_dtype}", flush=True)
+    rng = np.random.default_rng(rows + cols)
+    x, dy = values(rng, (rows, cols), x_dtype, 1.5, 0.4), values(rng, (rows, cols), x_dtype)
+    g = values(rng, cols, "f32", 0.3, 1.0)
+    _, m, r = R.norm(x, None, None, EPS)
+    m, r = m.astype(np.float32), r.astype(np.float32)
+    d2 = dev(dy, x_dtype)
+    got = B.layer_norm_backward(d2, dev(x, x_dtype), dev(g), dev(m), dev(r))
+    for a, w, e, name in zip(got, R.norm_grad(dy, x, g, m, r),
+                             R.norm_grad_bounds(dy, x, g, m, r, x_dtype, "f32"),
+                             ("dx", "dgamma", "dbeta")):
+        within(host(a), w, e, name)
+    inplace = B.layer_norm_backward(d2, dev(x, x_dtype), dev(g), dev(m), dev(r), dX=d2)
+    for a, b in zip(got, inplace):
+        assert torch.equal(bits(a), bits(b))
+    assert B.layer_norm_backward_workspace(rows, cols) > 0 or rows * cols <= 1 << 22
+
+
 @pytest.mark.parametrize("rows,cols", [(12289, 768), (70000, 24), (3001, 4096), (300, 16384),
                                        (140000, 3)])
 def test_norm_many_rows(rows, cols):
@@ -288,6 +317,8 @@ def _tokens(rng, kind, n, vocab):
         return np.arange(n) % vocab
     if kind == "falling":
         return (vocab - 1 - np.arange(n) % vocab)
+    if kind == "skew":                  # many tokens of one residue
+        return 5 + 256 * rng.integers(0, vocab // 256, n)
     if kind == "zipf":
         return np.minimum((vocab ** rng.random(n)).astype(np.int64) - 1, vocab - 1)
     return rng.integers(0, vocab, n)
@@ -299,7 +330,9 @@ GRADS = [(1, 1, 1, "uniform"), (2, 3, 5, "same"), (63, 7, 4, "uniform"), (64, 64
          (5000, 131073, 4, "uniform"), (6000, 257, 100, "falling"), (1025, 5000, 768, "zipf"),
          (900, 1024, 1001, "same"), (300, 600000, 2, "last"), (20000, 513, 12, "zipf"),
          (50000, 4096, 3, "zipf"), (70000, 100, 1, "uniform"), (33000, 70000, 2, "zipf"),
-         (150000, 30000, 2, "zipf"), (131073, 3, 5, "same"), (4000, 64, 2048, "zipf")]
+         (150000, 30000, 2, "zipf"), (131073, 3, 5, "same"), (4000, 64, 2048, "zipf"),
+         (20000, 70000, 8, "skew"), (800, 70000, 40, "skew"), (896, 300, 30, "zipf"),
+         (897, 300, 30, "zipf"), (896, 513, 5, "same"), (40000, 200000, 3, "skew")]
 
 
 @pytest.mark.parametrize("dy_dtype,dw_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"),

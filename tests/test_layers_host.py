@@ -63,11 +63,13 @@ def test_norm_grad_refusals():
                 dict(dg=ODD), dict(db=ODD), dict(dY=ODD), dict(X=ODD), dict(g=ODD),
                 dict(m=ODD), dict(r=ODD)):
         assert _norm_grad(**bad) == B.SM_EINVAL, bad
-    need = B.layer_norm_backward_workspace(4, 8)
+    need = B.layer_norm_backward_workspace(5000, 8)
     assert need > 0 and need % 256 == 0
-    assert _norm_grad(nbytes=need - 1) == B.SM_EWORKSPACE
-    assert _norm_grad(ws=None) == B.SM_EWORKSPACE
-    assert _norm_grad(ws=ctypes.c_void_p((1 << 20) + 16)) == B.SM_EWORKSPACE
+    assert _norm_grad(rows=5000, nbytes=need - 1) == B.SM_EWORKSPACE
+    assert _norm_grad(rows=5000, ws=None, nbytes=need) == B.SM_EWORKSPACE
+    assert _norm_grad(rows=5000, ws=ctypes.c_void_p((1 << 20) + 16),
+                      nbytes=need) == B.SM_EWORKSPACE
+    assert B.layer_norm_backward_workspace(4, 8) == 0           # one launch
     for rows, cols in ((-1, 8), (4, 0), (1 << 31, 8), (4, (1 << 20) + 1)):
         with pytest.raises(B.SignMuonError) as e:
             B.layer_norm_backward_workspace(rows, cols)
@@ -102,11 +104,13 @@ def test_embedding_grad_refusals():
                 dict(acc=2), dict(acc=1, dwd=1), dict(dW=None), dict(dW=ODD), dict(dY=None),
                 dict(t=None), dict(dys=7), dict(dY=ODD), dict(t=ctypes.c_void_p((1 << 20) + 4))):
         assert _embed_grad(**bad) == B.SM_EINVAL, bad
-    need = B.embedding_backward_workspace(5, 9, 8)
-    assert need > 0 and need % 256 == 0
-    assert _embed_grad(nbytes=need - 1) == B.SM_EWORKSPACE
-    assert _embed_grad(ws=None) == B.SM_EWORKSPACE
-    assert _embed_grad(ws=ctypes.c_void_p((1 << 20) + 64)) == B.SM_EWORKSPACE
+    big = dict(n=5000, vocab=900, dim=8)
+    need = B.embedding_backward_workspace(5000, 900, 8)
+    assert need > 2 * 5000 * 4 and need % 256 == 0
+    assert _embed_grad(**big, nbytes=need - 1) == B.SM_EWORKSPACE
+    assert _embed_grad(**big, ws=None) == B.SM_EWORKSPACE
+    assert _embed_grad(**big, ws=ctypes.c_void_p((1 << 20) + 64)) == B.SM_EWORKSPACE
+    assert B.embedding_backward_workspace(5, 9, 8) == 0         # one launch
     for args in ((-1, 9, 8), (5, 0, 8), (5, 9, 0), ((1 << 27) + 1, 9, 8), (5, (1 << 20) + 1, 8)):
         with pytest.raises(B.SignMuonError) as e:
             B.embedding_backward_workspace(*args)
