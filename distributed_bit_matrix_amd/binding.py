@@ -358,12 +358,12 @@ def _raw_stream(dev: int) -> int:
     return get(dev) if get else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _dtype(t, name) -> int:
+def _code(dtype, name) -> int:
     import torch
-    if t.dtype == torch.float32:
-        return SM_F32
-    if t.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return SM_BF16
+    if dtype is torch.float32:
+        return SM_F32
     raise TypeError(f"{name} must be float32 or bfloat16")
 
 
@@ -385,10 +385,15 @@ def _rows(t, name) -> Tuple[int, int, int]:
 
 
 def _check_arg(t, shape, dtype, dev, name):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is not on the first tensor's device")
+
+
+def _dense_like(t):
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def _workspace(ws, nbytes, like, dev):
@@ -418,17 +423,17 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, want_stats: bool = 
         with _placed(X, stream):
             return layer_norm(X, weight, bias, eps, want_stats, Y, mean, rstd)
     rows, cols, xs = _rows(X, "X")
-    xd = wd = _dtype(X, "X")
+    xd = wd = _code(X.dtype, "X")
     if weight is not None:
-        wd = _dtype(weight, "weight")
+        wd = _code(weight.dtype, "weight")
         _check_arg(weight, (cols,), weight.dtype, dev, "weight")
         if bias is not None:
             _check_arg(bias, (cols,), weight.dtype, dev, "bias")
     elif bias is not None:
-        wd = _dtype(bias, "bias")
+        wd = _code(bias.dtype, "bias")
         _check_arg(bias, (cols,), bias.dtype, dev, "bias")
     if Y is None:
-        Y = X.new_empty(X.shape)
+        Y = _dense_like(X)
     else:
         _check_arg(Y, X.shape, X.dtype, dev, "Y")
     if mean is not None:
@@ -467,21 +472,21 @@ def layer_norm_backward(dY, X, weight, mean, rstd, want_x: bool = True, want_wei
             return layer_norm_backward(dY, X, weight, mean, rstd, want_x, want_weight, want_bias,
                                        dX, dweight, dbias, dtype, accumulate, ws)
     rows, cols, dys = _rows(dY, "dY")
-    xd = wd = _dtype(X, "X")
+    xd = wd = _code(X.dtype, "X")
     if X.dtype != dY.dtype or X.shape != dY.shape:
         raise TypeError("dY must have X's dtype and shape")
     if X.get_device() != dev:
         raise ValueError("X is not on the first tensor's device")
     xs = _rows(X, "X")[2]
     if weight is not None:
-        wd = _dtype(weight, "weight")
+        wd = _code(weight.dtype, "weight")
         _check_arg(weight, (cols,), weight.dtype, dev, "weight")
     _check_arg(mean, X.shape[:-1], torch.float32, dev, "mean")
     _check_arg(rstd, X.shape[:-1], torch.float32, dev, "rstd")
     if not want_x:
         dX = None
     elif dX is None:
-        dX = X.new_empty(X.shape)
+        dX = _dense_like(X)
     else:
         _check_arg(dX, X.shape, X.dtype, dev, "dX")
     if not want_weight:
@@ -499,13 +504,13 @@ def layer_norm_backward(dY, X, weight, mean, rstd, want_x: bool = True, want_wei
             dweight = X.new_empty(cols, dtype=dtype)
         else:
             _check_arg(dweight, (cols,), dtype, dev, "dweight")
-        dwd = _dtype(dweight, "dweight")
+        dwd = _code(dweight.dtype, "dweight")
     if want_bias:
         if dbias is None:
             dbias = X.new_empty(cols, dtype=dtype)
         else:
             _check_arg(dbias, (cols,), dtype, dev, "dbias")
-        dwd = _dtype(dbias, "dbias")
+        dwd = _code(dbias.dtype, "dbias")
     ws, wsp, nbytes = _workspace(ws, layer_norm_backward_workspace(rows, cols), X, dev)
     _check("signmuon_layer_norm_backward", lib().signmuon_layer_norm_backward(
         dY.data_ptr(), dys, X.data_ptr(), xd, xs, _ptr(weight), wd, mean.data_ptr(),
@@ -541,14 +546,14 @@ def embedding(tokens, weight, scale: float = 1.0, out=None, out_dtype=None, stre
     if weight.get_device() != dev:
         raise ValueError("weight is not on the first tensor's device")
     vocab, dim = shape
-    wd = _dtype(weight, "weight")
+    wd = _code(weight.dtype, "weight")
     if out is None:
         out = weight.new_empty(tokens.shape + (dim,), dtype=out_dtype)
     else:
         _check_arg(out, tokens.shape + (dim,), out_dtype or out.dtype, dev, "out")
     _check("signmuon_embedding", lib().signmuon_embedding(
         weight.data_ptr(), wd, vocab, dim, tokens.data_ptr(), bits, tokens.numel(), scale,
-        out.data_ptr(), _dtype(out, "out"), _raw_stream(dev)))
+        out.data_ptr(), _code(out.dtype, "out"), _raw_stream(dev)))
     return out
 
 
@@ -578,7 +583,7 @@ def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Opti
         raise ValueError("dY must have one row for each token")
     if tokens.get_device() != dev:
         raise ValueError("tokens are not on the first tensor's device")
-    dyd = _dtype(dY, "dY")
+    dyd = _code(dY.dtype, "dY")
     if dW is None:
         if accumulate:
             raise ValueError("accumulate needs the dW to add to")
@@ -588,7 +593,7 @@ def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Opti
     ws, wsp, nbytes = _workspace(ws, embedding_backward_workspace(n, vocab, dim), dY, dev)
     _check("signmuon_embedding_backward", lib().signmuon_embedding_backward(
         dY.data_ptr(), dyd, dys, tokens.data_ptr(), bits, n,
-        -1 if padding is None else int(padding), scale, dW.data_ptr(), _dtype(dW, "dW"), vocab,
+        -1 if padding is None else int(padding), scale, dW.data_ptr(), _code(dW.dtype, "dW"), vocab,
         dim, accumulate, wsp, nbytes, _raw_stream(dev)))
     return dW
 
