@@ -295,9 +295,10 @@ __device__ __forceinline__ void write_row(TO* out, const float (&acc)[V], int sk
 
 // The sums of a block of WAVES waves, each over `have` sorted positions.  Lane
 // i's tok: the token at the wave's position i - 1 (-1 outside the order), row:
-// the batch position at its position i.  parts: where the two sums go that
+// the batch position at its position i.  ONCE: dY is read with the
+// non-temporal hint.  parts: where the two sums go that
 // cross the block's borders (null where none does).
-template <int WAVES, int V, typename T, typename TO>
+template <int WAVES, int V, bool ONCE, typename T, typename TO>
 __device__ __forceinline__ void sum_block(const T* __restrict__ dY, int64_t dys, int32_t tok,
                                           int32_t row, int have, const Place<V>& at, int w,
                                           float (&heads)[WAVES][64 * V], int (&through)[WAVES],
@@ -326,7 +327,7 @@ __device__ __forceinline__ void sum_block(const T* __restrict__ dY, int64_t dys,
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = __builtin_amdgcn_readlane(row, i + u < have ? i + u : i);
-      v[u].load(dY + r * dys + at.c);
+      v[u].template load<ONCE>(dY + r * dys + at.c);
     }
     const uint32_t turns = (uint32_t)(changes >> i) & ((1u << U) - 1) & (i == 0 ? ~1u : ~0u);
     if (turns == 0 && i + U <= have) {
@@ -378,11 +379,12 @@ __device__ __forceinline__ void sum_block(const T* __restrict__ dY, int64_t dys,
   }
 }
 
-template <typename T, typename TO, int V>
+template <typename T, typename TO, int V, bool ONCE>
 __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
     const T* __restrict__ dY, int64_t dys, const int32_t* __restrict__ order,
     const int32_t* __restrict__ sorted, const int32_t* __restrict__ total, int dim, int span,
-    int slices, float scale, TO* __restrict__ dW, int accumulate, float* __restrict__ part) {
+    int slices, float scale, TO* __restrict__ dW, int accumulate,
+    float* __restrict__ part) {
   __shared__ float heads[kSumWaves][64 * V];
   __shared__ int through[kSumWaves];
   const int block = blockIdx.x / slices, slice = blockIdx.x - block * slices;
@@ -395,7 +397,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
   const int64_t q = p0 + lane - 1;
   const int32_t tok = lane <= span + 1 && q >= 0 && q < n ? sorted[q] : -1;
   const int32_t row = lane < have ? order[p0 + lane] : 0;
-  sum_block<kSumWaves, V>(dY, dys, tok, row, have, Place<V>((slice * 64 + lane) * V, dim), w,
+  sum_block<kSumWaves, V, ONCE>(dY, dys, tok, row, have, Place<V>((slice * 64 + lane) * V, dim), w,
                           heads, through, dW, dim, scale, accumulate,
                           part + 2 * (int64_t)block * dim);
 }
@@ -483,7 +485,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_embed_small(
   const int q = p0 + lane - 1;
   const int32_t tok = lane <= span + 1 && q >= 0 && q < count ? sorted[q] : -1;
   const int32_t row = lane < have ? order[p0 + lane] : 0;
-  sum_block<kSmallWaves, V>(dY, dys, tok, row, have, at, w, heads, through, dW, dim, scale,
+  sum_block<kSmallWaves, V, false>(dY, dys, tok, row, have, at, w, heads, through, dW, dim, scale,
                             accumulate, (float*)nullptr);
 }
 
@@ -621,9 +623,12 @@ template <typename T, typename TO, int V>
 hipError_t embed_sum(const EmbedGradArgs& a, const GradPlan& pl, const int32_t* order,
                      const int32_t* sorted, const int32_t* total, float* part, hipStream_t s) {
   const int64_t slices = (a.dim + 64 * V - 1) / (64 * V);
-  hipLaunchKernelGGL((k_embed_sum<T, TO, V>), dim3((unsigned)(pl.blocks * slices)),
-                     dim3(64 * kSumWaves), 0, s, (const T*)a.dY, a.dy_stride, order, sorted, total,
-                     (int)a.dim, pl.span, (int)slices, a.scale, (TO*)a.dW, a.accumulate, part);
+  const bool once = a.n * a.dim * (int64_t)sizeof(T) + a.vocab * a.dim * (int64_t)sizeof(TO) >
+                    kCacheBytes;
+  hipLaunchKernelGGL((once ? k_embed_sum<T, TO, V, true> : k_embed_sum<T, TO, V, false>),
+                     dim3((unsigned)(pl.blocks * slices)), dim3(64 * kSumWaves), 0, s,
+                     (const T*)a.dY, a.dy_stride, order, sorted, total, (int)a.dim, pl.span,
+                     (int)slices, a.scale, (TO*)a.dW, a.accumulate, part);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.blocks <= 1) return e;
   hipLaunchKernelGGL((k_embed_join<TO, V>), dim3((unsigned)pl.blocks, (unsigned)slices), dim3(256),

@@ -44,7 +44,7 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int& turn) {
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
-template <typename T, typename TW, int V, int LANES, int NV>
+template <typename T, typename TW, int V, int LANES, int NV, bool ONCE>
 __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_norm(
     const T* X, int64_t xs, const TW* gamma, const TW* beta, int64_t rows, int cols, float eps,
     T* Y, float* mean, float* rstd) {
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_norm(
     Piece<TW, V> g[NV], b[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      in[j].load(X + r * xs + (j < NV - 1 ? (j * LANES + lane) * V : last.c));
+      in[j].template load<ONCE>(X + r * xs + (j < NV - 1 ? (j * LANES + lane) * V : last.c));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = j < NV - 1 ? (j * LANES + lane) * V : last.c;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(1024) void k_norm_long(const T* X, int64_t xs, cons
 // One row of the backward pass: g = dY gamma, xhat, and the lane's shares of
 // the sums of g and g xhat; `each` sees every entry's dY and xhat.  Contraction
 // is spelled out, so that the kernels that share this give dX the same bits.
-template <int V, int LANES, int NV, typename T, typename TW, typename F>
+template <int V, int LANES, int NV, bool ONCE, typename T, typename TW, typename F>
 __device__ __forceinline__ void grad_row(const T* dY, const T* X, const Piece<TW, V> (&w)[NV],
                                          bool weighted, const Place<V>& last, float mu, float rs,
                                          float (&g)[NV][V], float (&xh)[NV][V], float (&s)[2],
@@ -164,8 +164,8 @@ __device__ __forceinline__ void grad_row(const T* dY, const T* X, const Piece<TW
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = j < NV - 1 ? (j * LANES + lane) * V : last.c;
-    pd[j].load(dY + c);
-    px[j].load(X + c);
+    pd[j].template load<ONCE>(dY + c);
+    px[j].template load<ONCE>(X + c);
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j)
@@ -197,7 +197,7 @@ __device__ __forceinline__ void grad_store(T* dX, const Place<V>& last, float rs
   }
 }
 
-template <typename T, typename TW, int V, int LANES, int NV>
+template <typename T, typename TW, int V, int LANES, int NV, bool ONCE>
 __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
     const T* dY, int64_t dys, const T* X, int64_t xs, const TW* gamma, const float* mean,
     const float* rstd, int64_t rows, int cols, T* dX, float* part) {
@@ -223,7 +223,7 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
     float rs = 0.f;
     if (live) {
       rs = rstd[r];
-      grad_row<V, LANES, NV>(dY + r * dys, X + r * xs, w, gamma != nullptr, last, mean[r], rs, g,
+      grad_row<V, LANES, NV, ONCE>(dY + r * dys, X + r * xs, w, gamma != nullptr, last, mean[r], rs, g,
                              xh, s, [&](int j, int k, float dy, float x) {
                                ag[j][k] = __builtin_fmaf(dy, x, ag[j][k]);
                                ab[j][k] += dy;
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512) void k_norm_grad_few(
     const float rs = rstd[at], inv = 1.0f / cols;
     float s[2] = {0.f, 0.f};
     float g[NV][V], xh[NV][V];
-    grad_row<V, LANES, NV>(dY + at * dys, X + at * xs, w, gamma != nullptr, last, mean[at], rs, g,
+    grad_row<V, LANES, NV, false>(dY + at * dys, X + at * xs, w, gamma != nullptr, last, mean[at], rs, g,
                            xh, s, [](int, int, float, float) {});
     group_sums<LANES, 2>(s, turn);
     if (r < rows)
@@ -462,9 +462,12 @@ template <typename T, typename TW, int V, int LANES, int NV>
 void norm_go(const NormArgs& a, hipStream_t s) {
   constexpr int THREADS = LANES > 64 ? LANES : 256, GROUPS = THREADS / LANES;
   const int64_t grid = std::min<int64_t>((a.rows + GROUPS - 1) / GROUPS, kMaxBlocks);
-  hipLaunchKernelGGL((k_norm<T, TW, V, LANES, NV>), dim3((unsigned)grid), dim3(THREADS), 0, s,
-                     (const T*)a.X, a.x_stride, (const TW*)a.gamma, (const TW*)a.beta, a.rows,
-                     (int)a.cols, a.eps, (T*)a.Y, a.mean, a.rstd);
+  const auto kernel = 2 * a.rows * a.cols * (int64_t)sizeof(T) > kCacheBytes
+                          ? k_norm<T, TW, V, LANES, NV, true>
+                          : k_norm<T, TW, V, LANES, NV, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, (const T*)a.X,
+                     a.x_stride, (const TW*)a.gamma, (const TW*)a.beta, a.rows, (int)a.cols,
+                     a.eps, (T*)a.Y, a.mean, a.rstd);
 }
 
 template <typename T, typename TW, int LANES>
@@ -504,10 +507,12 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
 
 template <typename T, typename TW, int V, int LANES, int NV>
 void norm_grad_go(const NormGradArgs& a, int64_t grid, float* part, hipStream_t s) {
-  hipLaunchKernelGGL((k_norm_grad<T, TW, V, LANES, NV>), dim3((unsigned)grid),
-                     dim3(LANES > 512 ? LANES : 512), 0, s, (const T*)a.dY, a.dy_stride,
-                     (const T*)a.X, a.x_stride, (const TW*)a.gamma, a.mean, a.rstd, a.rows,
-                     (int)a.cols, (T*)a.dX, part);
+  const auto kernel = 3 * a.rows * a.cols * (int64_t)sizeof(T) > kCacheBytes
+                          ? k_norm_grad<T, TW, V, LANES, NV, true>
+                          : k_norm_grad<T, TW, V, LANES, NV, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(LANES > 512 ? LANES : 512), 0, s,
+                     (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride, (const TW*)a.gamma,
+                     a.mean, a.rstd, a.rows, (int)a.cols, (T*)a.dX, part);
 }
 
 template <typename T, typename TW, int LANES>
