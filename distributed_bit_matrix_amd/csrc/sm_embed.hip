@@ -44,33 +44,40 @@ __global__ __launch_bounds__(256) void k_embed(const TW* __restrict__ W, int64_t
 
 // ---------------------------------------------------------------------------
 // Sort.  Equal tokens have to be neighbours, in the order of the batch; the
-// tokens themselves may come in any fixed order.  Block b of B = 2^shift takes
-// the tokens t with t % B = b, so that frequent tokens, which vocabularies
-// number next to each other, spread over the blocks.  Every block reads the
-// whole batch and needs nothing of the others: it counts the tokens of the
-// blocks before it on the way, which gives its place in the order.  Each of
-// its 16 waves reads one run of consecutive positions and lists its own; the
-// list is counted by token, the counts are scanned over tokens and waves, and
-// the list is placed.  A wave whose list overflows counts it and starts it
-// anew, and reads its run again to place.  When placing, equal tokens among 64
-// listed ones are found by one ballot per bit of t / B.  Between counting and
-// placing the block clears the rows of the table that no token names (unless
-// the caller accumulates): those stores drain while placing goes on.
+// tokens themselves may come in any fixed order.  Of B = 2^shift sets of
+// blocks, set b takes the tokens t with t % B = b, so that frequent tokens,
+// which vocabularies number next to each other, spread over the sets.
+//
+// Small batches (SPLIT = false): one block a set and one launch.  Every block
+// reads the whole batch and needs nothing of the others: it counts the tokens
+// of the sets before it on the way, which gives its place in the order.
+// Larger ones: a set has a block for each of S runs of the batch; a first
+// launch (k_token_count) counts every block's tokens, the second one knows
+// from these counts where each token of each run goes.
+//
+// Each of a block's 16 waves reads a part of its run and lists the positions
+// that are the set's; the list is counted by token, the counts are scanned
+// over tokens and waves, and the list is placed.  A wave whose list overflows
+// counts it and starts it anew, and reads its part again to place.  When
+// placing, equal tokens among 64 listed ones are found by one ballot per bit
+// of t / B.  Between counting and placing the block clears the rows of the
+// table that no token names (unless the caller accumulates): those stores
+// drain while placing goes on.
 //   order[p], sorted[p]: batch position and token of the p-th in sorted order
 //   total: how many tokens count
-// Reading all tokens in every block costs 7 vector instructions for 64 of them
-// in each CU; a sort by digits would read them once a pass, but takes two
-// launches a pass.
+// Bound by the reading: every token is read by B blocks, with 5 to 7 vector
+// instructions for 64 of them.
 // ---------------------------------------------------------------------------
 constexpr int kSortWaves = 16;
-constexpr int kMaxRange = 512;   // tokens a block
-constexpr int kMinShift = 8;     // at least 256 blocks: one a CU
 constexpr int kBatch = 8;        // loads of 64 tokens in flight a wave
 constexpr int kList = 64 * kBatch;   // listed positions a wave
-constexpr int kRunBits = 23;     // a listed position: bin << 23 | place in the run
+constexpr int kRunBits = 16;     // a listed position: bin << 16 | place in the part
+constexpr int kOneRange = 512, kOneShift = 8;   // one launch: tokens a block, fewest sets
+constexpr int kSplitRange = 2048;               // two launches
 
 typedef volatile __attribute__((address_space(3))) int32_t lds_i32;
 typedef volatile __attribute__((address_space(3))) uint32_t lds_u32;
+typedef volatile __attribute__((address_space(3))) uint16_t lds_u16;
 
 // A token as loaded: its low word, and whether that is all of it (a negative
 // or larger token is no token of the table).
@@ -93,30 +100,129 @@ struct Token64 {
 template <typename TI>
 using Token = std::conditional_t<sizeof(TI) == 8, Token64, Token32>;
 
-template <typename TI, typename TO, int SHIFT, bool PAD>
+// Reads `run` tokens, 64 kBatch at a time, the next ones under way: f gets the
+// place of the first, the tokens, the lanes whose tokens are the set's, for
+// each 64, and how many those are.  under: how many tokens of the sets before.
+template <typename TI, int SHIFT, bool PAD, typename F>
+__device__ __forceinline__ void each_batch(const TI* __restrict__ tokens, int run, uint32_t vocab,
+                                           uint32_t padding, int shift, uint32_t set,
+                                           int32_t& under, const F& f) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t mask = (1u << (SHIFT ? SHIFT : shift)) - 1;
+  Token<TI> next[kBatch];
+  auto fetch = [&](int i) {
+    const TI* at = tokens + i;
+    if (i + kList <= run) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) next[u].load(at + 64 * u + lane);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = 64 * u + lane;
+        next[u].load(at + (i + k < run ? k : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (i + 64 * u + lane >= run) next[u].drop();
+    }
+  };
+  if (run > 0) fetch(0);
+  for (int i = 0; i < run; i += kList) {
+    uint64_t m[kBatch];
+    uint32_t t[kBatch];
+    int more = 0;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      t[u] = next[u].lo;
+      uint64_t valid = __ballot(t[u] < vocab);
+      if (sizeof(TI) == 8) valid &= __ballot(next[u].whole());
+      if (PAD) valid &= ~__ballot(t[u] == padding);
+      const uint32_t b = t[u] & mask;
+      under += __popcll(valid & __ballot(b < set));
+      m[u] = valid & __ballot(b == set);
+      more += __popcll(m[u]);
+    }
+    if (i + kList < run) fetch(i + kList);
+    if (more > 0) f(i, t, m, more);
+  }
+}
+
+// Tokens of set blockIdx.x in run blockIdx.y: table[run][set][bin], and their
+// sum, sums[run][set].
+template <typename TI, bool PAD>
+__global__ __launch_bounds__(64 * kSortWaves) void k_token_count(
+    const TI* __restrict__ tokens, int64_t n, int chunk, uint32_t vocab, uint32_t padding,
+    int shift, int range, int32_t* __restrict__ table, int32_t* __restrict__ sums) {
+  __shared__ int32_t counts[kSplitRange], wave_total[kSortWaves];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c0 = (int64_t)blockIdx.y * chunk;
+  const int size = (int)(n - c0 < chunk ? n - c0 : chunk);
+  const int share = ((size + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+  const int left = size - w * share, run = left < 0 ? 0 : left < share ? left : share;
+  for (int k = threadIdx.x; k < range; k += 64 * kSortWaves) counts[k] = 0;
+  __syncthreads();
+  int32_t under = 0, mine = 0;
+  each_batch<TI, 0, PAD>(
+      tokens + c0 + w * share, run, vocab, padding, shift, blockIdx.x, under,
+      [&](int, const uint32_t(&t)[kBatch], const uint64_t(&m)[kBatch], int more) {
+        mine += more;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (m[u] == 0) continue;
+          const uint32_t b = t[u] >> shift;
+          const uint32_t b0 = __builtin_amdgcn_readlane(b, __builtin_ctzll(m[u]));
+          // one token many times over would meet itself in the atomics
+          if ((m[u] & __ballot(b == b0)) == m[u]) {
+            if (lane == 0)
+              __hip_atomic_fetch_add(&counts[b0], __popcll(m[u]), __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_WORKGROUP);
+          } else if (m[u] >> lane & 1) {
+            __hip_atomic_fetch_add(&counts[b], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+          }
+        }
+      });
+  if (lane == 0) wave_total[w] = mine;
+  __syncthreads();
+  const int64_t at = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  for (int k = threadIdx.x; k < range; k += 64 * kSortWaves) table[at * range + k] = counts[k];
+  if (threadIdx.x == 0) {
+    int32_t all = 0;
+    for (int j = 0; j < kSortWaves; ++j) all += wave_total[j];
+    sums[at] = all;
+  }
+}
+
+template <typename TI, typename TO, int SHIFT, bool PAD, bool SPLIT>
 __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
-    const TI* __restrict__ tokens, int64_t n, uint32_t vocab, uint32_t padding, int shift,
-    int range, int bits, int32_t* __restrict__ order, int32_t* __restrict__ sorted,
+    const TI* __restrict__ tokens, int64_t n, int chunk, uint32_t vocab, uint32_t padding,
+    int shift, int range, int bits, const int32_t* __restrict__ table,
+    const int32_t* __restrict__ sums, int32_t* __restrict__ order, int32_t* __restrict__ sorted,
     int32_t* __restrict__ total, TO* __restrict__ dW, int dim) {
-  __shared__ int32_t counts[kSortWaves * kMaxRange];   // [kSortWaves][range]
+  constexpr int RANGE = SPLIT ? kSplitRange : kOneRange;
+  constexpr int BINS = RANGE > 64 * kSortWaves ? RANGE / (64 * kSortWaves) : 1;   // a thread
+  __shared__ uint32_t counts[kSortWaves][RANGE / 2];   // two 16-bit counts a word
+  __shared__ int32_t place[RANGE];
   __shared__ uint32_t lists[kSortWaves][kList];
   __shared__ int32_t below[kSortWaves], wave_total[kSortWaves];
-  __shared__ uint8_t empty[kMaxRange];
+  __shared__ uint8_t empty[RANGE];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t before = ((uint64_t)1 << lane) - 1;
-  const uint32_t block = blockIdx.x, mask = (1u << shift) - 1;
-  const int64_t share = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
-  const int64_t i0 = w * share;
-  const int run = (int)(i0 + share < n ? share : n > i0 ? n - i0 : 0);   // < 2^kRunBits
-  const TI* mine = tokens + i0;
-  lds_i32* count = (lds_i32*)(counts + w * range);
+  const uint32_t set = blockIdx.x;
+  const int64_t c0 = (int64_t)blockIdx.y * chunk;
+  const int size = (int)(n - c0 < chunk ? n - c0 : chunk);
+  const int share = ((size + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;   // < 2^kRunBits
+  const int left = size - w * share, run = left < 0 ? 0 : left < share ? left : share;
+  const int64_t i0 = c0 + w * share;
+  lds_u16* count = (lds_u16*)counts[w];
   lds_u32* list = (lds_u32*)lists[w];
-  for (int k = threadIdx.x; k < kSortWaves * range; k += 64 * kSortWaves) counts[k] = 0;
+  for (int k = threadIdx.x; k < kSortWaves * RANGE / 2; k += 64 * kSortWaves)
+    counts[k / (RANGE / 2)][k % (RANGE / 2)] = 0;
   __syncthreads();
 
   // Counts (or, once the counts hold places, places) the first `len` listed.
-  auto settle = [&](int len, bool place) {
+  auto settle = [&](int len, bool placing) {
     for (int k = 0; k < len; k += 64) {
       const bool in = k + lane < len;
       const uint32_t entry = in ? list[k + lane] : 0;
@@ -125,11 +231,11 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
       const int b0 = __builtin_amdgcn_readfirstlane(b);
       uint64_t peers = live & __ballot(b == b0);
       const bool one = peers == live;       // all of them the same token
-      if (!place) {
+      if (!placing) {
         if (one) {
-          if (lane == 0) count[b0] = count[b0] + __popcll(live);
+          if (lane == 0) count[b0] = (uint16_t)(count[b0] + __popcll(live));
         } else if (in) {
-          __hip_atomic_fetch_add(&counts[w * range + b], 1, __ATOMIC_RELAXED,
+          __hip_atomic_fetch_add(&counts[w][b >> 1], 1u << (b & 1) * 16, __ATOMIC_RELAXED,
                                  __HIP_MEMORY_SCOPE_WORKGROUP);
         }
         continue;
@@ -137,92 +243,90 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
       if (!one) {
         uint32_t lo = (uint32_t)live, hi = (uint32_t)(live >> 32);
         for (int d = 0; d < bits; ++d) {
-          const int32_t set = (int32_t)((uint32_t)b << (31 - d)) >> 31;
-          const uint64_t v = __ballot(set != 0);
-          lo &= ~((uint32_t)v ^ set);
-          hi &= ~((uint32_t)(v >> 32) ^ set);
+          const int32_t bit = (int32_t)((uint32_t)b << (31 - d)) >> 31;
+          const uint64_t v = __ballot(bit != 0);
+          lo &= ~((uint32_t)v ^ bit);
+          hi &= ~((uint32_t)(v >> 32) ^ bit);
         }
         peers = ((uint64_t)hi << 32) | lo;
       }
       if (in) {
-        const int32_t c = count[b];
-        const int32_t p = c + __popcll(peers & before);
+        const int c = count[b];
+        const int32_t p = place[b] + c + __popcll(peers & before);
         order[p] = (int32_t)(i0 + (entry & ((1u << kRunBits) - 1)));
-        sorted[p] = (int32_t)(((uint32_t)b << shift) + block);
+        sorted[p] = (int32_t)(((uint32_t)b << shift) + set);
         __builtin_amdgcn_wave_barrier();
-        if ((peers & before) == 0) count[b] = c + __popcll(peers);
+        if ((peers & before) == 0) count[b] = (uint16_t)(c + __popcll(peers));
       }
       __builtin_amdgcn_wave_barrier();
     }
   };
-  // Lists the wave's run, settling full lists; returns what is still listed.
+  // Lists the wave's part, settling full lists; returns what is still listed.
   bool whole = true;      // the list holds all of the wave's positions
   int32_t under = 0;
-  auto scan = [&](bool place) {
+  auto scan = [&](bool placing) {
     int len = 0;
-    Token<TI> next[kBatch];       // the batch after the one at work
-    auto fetch = [&](int i) {
-      const TI* at = mine + i;
-      if (i + kList <= run) {
+    each_batch<TI, SHIFT, PAD>(
+        tokens + i0, run, vocab, padding, shift, set, under,
+        [&](int i, const uint32_t(&t)[kBatch], const uint64_t(&m)[kBatch], int more) {
+          if (len + more > kList) {
+            settle(len, placing);
+            whole = false;
+            len = 0;
+          }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) next[u].load(at + 64 * u + lane);
-      } else {
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int k = 64 * u + lane;
-          next[u].load(at + (i + k < run ? k : 0));
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (i + 64 * u + lane >= run) next[u].drop();
-      }
-    };
-    if (run > 0) fetch(0);
-    for (int i = 0; i < run; i += kList) {
-      uint64_t m[kBatch];
-      uint32_t t[kBatch];
-      int more = 0;
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        t[u] = next[u].lo;
-        uint64_t valid = __ballot(t[u] < vocab);
-        if (sizeof(TI) == 8) valid &= __ballot(next[u].whole());
-        if (PAD) valid &= ~__ballot(t[u] == padding);
-        const uint32_t b = SHIFT ? t[u] & ((1u << SHIFT) - 1) : t[u] & mask;
-        under += __popcll(valid & __ballot(b < block));
-        m[u] = valid & __ballot(b == block);
-        more += __popcll(m[u]);
-      }
-      if (i + kList < run) fetch(i + kList);
-      if (more == 0) continue;
-      if (len + more > kList) {
-        settle(len, place);
-        whole = false;
-        len = 0;
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (m[u] == 0) continue;
-        if (m[u] >> lane & 1)
-          list[len + __popcll(m[u] & before)] =
-              (t[u] >> shift) << kRunBits | (uint32_t)(i + 64 * u + lane);
-        len += __popcll(m[u]);
-      }
-    }
+          for (int u = 0; u < kBatch; ++u) {
+            if (m[u] == 0) continue;
+            if (m[u] >> lane & 1)
+              list[len + __popcll(m[u] & before)] =
+                  (t[u] >> shift) << kRunBits | (uint32_t)(i + 64 * u + lane);
+            len += __popcll(m[u]);
+          }
+        });
     return len;
   };
 
   int len = scan(false);
   settle(len, false);
+  if (SPLIT) {
+    // tokens of the sets before this one, in all runs
+    under = 0;
+    for (int k = threadIdx.x; k < (int)(gridDim.x * gridDim.y); k += 64 * kSortWaves)
+      under += k % gridDim.x < set ? sums[k] : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) under += __shfl_xor(under, o);
+  }
   if (lane == 0) below[w] = under;
   __syncthreads();
-  // thread k holds bin k (range <= the threads of the block)
-  const int k = threadIdx.x;
-  int32_t base = 0;
-  for (int j = 0; j < kSortWaves; ++j) base += below[j];
-  int32_t sum = 0;
-  if (k < range)
-    for (int j = 0; j < kSortWaves; ++j) sum += counts[j * range + k];
+  // thread k holds the bins from k BINS on
+  int32_t all[BINS], sum = 0;
+#pragma unroll
+  for (int q = 0; q < BINS; ++q) {
+    const int k = threadIdx.x * BINS + q;
+    int32_t earlier = 0;              // in the runs before this one
+    all[q] = 0;
+    if (k < range) {
+      if (SPLIT) {
+        for (int r = 0; r < (int)gridDim.y; ++r) {
+          const int32_t c = table[((int64_t)r * gridDim.x + set) * range + k];
+          all[q] += c;
+          earlier += r < (int)blockIdx.y ? c : 0;
+        }
+      }
+      int32_t here = 0;
+#pragma unroll
+      for (int j = 0; j < kSortWaves; ++j) {
+        lds_u16* slot = (lds_u16*)counts[j] + k;
+        const int c = *slot;
+        *slot = (uint16_t)here;
+        here += c;
+      }
+      if (!SPLIT) all[q] = here;
+      place[k] = earlier;
+      empty[k] = all[q] == 0 && ((uint32_t)k << shift) + set < vocab;
+    }
+    sum += all[q];
+  }
   int32_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -231,16 +335,14 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
   }
   if (lane == 63) wave_total[w] = incl;
   __syncthreads();
-  for (int j = 0; j < w; ++j) base += wave_total[j];
-  if (k < range) {
-    int32_t at = base + incl - sum;
-    empty[k] = sum == 0 && ((uint32_t)k << shift) + block < vocab;
-    for (int j = 0; j < kSortWaves; ++j) {
-      const int32_t c = counts[j * range + k];
-      counts[j * range + k] = at;
-      at += c;
-    }
-    if (k == range - 1 && block == gridDim.x - 1) *total = at;
+  int32_t at = incl - sum;
+  for (int j = 0; j < kSortWaves; ++j) at += below[j] + (j < w ? wave_total[j] : 0);
+#pragma unroll
+  for (int q = 0; q < BINS; ++q) {
+    const int k = threadIdx.x * BINS + q;
+    if (k < range) place[k] += at;
+    at += all[q];
+    if (k == range - 1 && set == gridDim.x - 1 && blockIdx.y == 0) *total = at;
   }
   __syncthreads();
   if (dW) {
@@ -250,9 +352,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
     int lanes = 64;                       // threads a row
     while (lanes > 1 && lanes >= 2 * pieces) lanes >>= 1;
     const int rows = 64 / lanes;
-    for (int r = w * rows + lane / lanes; r < range; r += kSortWaves * rows)
+    for (int r = (blockIdx.y * kSortWaves + w) * rows + lane / lanes; r < range;
+         r += gridDim.y * kSortWaves * rows)
       if (empty[r]) {
-        TO* row = dW + (((int64_t)r << shift) + block) * dim;
+        TO* row = dW + (((int64_t)r << shift) + set) * dim;
         for (int c = lane % lanes * V; c < dim; c += lanes * V) {
           if (c + V <= dim) store_vec<V>(row + c, zero);
           else
@@ -424,7 +527,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_embed_small(
   __shared__ uint32_t bins[kSmall + W];
   __shared__ int16_t at_list[kSmall], order[kSmall];
   __shared__ int32_t sorted[kSmall];
-  __shared__ uint8_t touched[kMaxRange];
+  __shared__ uint8_t touched[kOneRange];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t block = blockIdx.x;
@@ -491,14 +594,15 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_embed_small(
 
 // Adds the parts of a token that begins in block b of the sums (blockIdx.x)
 // and goes on in the next, for 64 V columns: a wave each over a quarter of the
-// consecutive parts.
+// consecutive parts.  In double: there can be thousands of parts, and their
+// sum is where a float would lose most.
 template <typename TO, int V>
 __global__ __launch_bounds__(256) void k_embed_join(const float* __restrict__ part,
                                                     const int32_t* __restrict__ sorted,
                                                     const int32_t* __restrict__ total, int dim,
                                                     int positions, float scale,
                                                     TO* __restrict__ dW, int accumulate) {
-  __shared__ float sh[4][64 * V];
+  __shared__ double sh[4][64 * V];
   const int64_t b = blockIdx.x, p0 = b * positions, p1 = p0 + positions;
   const int64_t n = *total;
   if (p1 >= n) return;
@@ -517,9 +621,9 @@ __global__ __launch_bounds__(256) void k_embed_join(const float* __restrict__ pa
   const Place<V> at(((int)blockIdx.y * 64 + lane) * V, dim);
   const int64_t run = (more + 4) / 4;
   const int64_t j1 = (w + 1) * run < more + 1 ? (w + 1) * run : more + 1;
-  float acc[V];
+  double acc[V];
 #pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+  for (int k = 0; k < V; ++k) acc[k] = 0.;
 #pragma unroll 8
   for (int64_t j = w * run; j < j1; ++j) {
     Piece<float, V> v;
@@ -527,13 +631,16 @@ __global__ __launch_bounds__(256) void k_embed_join(const float* __restrict__ pa
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] += v[k];
   }
-  store_vec<V>(&sh[w][lane * V], acc);
+#pragma unroll
+  for (int k = 0; k < V; ++k) sh[w][k * 64 + lane] = acc[k];
   __syncthreads();
   if (w > 0) return;
-  for (int q = 1; q < 4; ++q)
+  float sum[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] += sh[q][lane * V + k];
-  write_row<V>(dW + (int64_t)t * dim + at.c, acc, at.skip, scale, accumulate);
+  for (int k = 0; k < V; ++k)
+    sum[k] = (float)(((acc[k] + sh[1][k * 64 + lane]) + sh[2][k * 64 + lane]) +
+                     sh[3][k * 64 + lane]);
+  write_row<V>(dW + (int64_t)t * dim + at.c, sum, at.skip, scale, accumulate);
 }
 
 namespace {
@@ -551,23 +658,41 @@ int span_of(int64_t n) { return n <= 32768 ? 8 : n <= 131072 ? 16 : 32; }
 // launches (300 tokens, 300 x 4000: 20.2 against 15.4 us).
 constexpr int64_t kSmallBlocks = 1024;
 
+// Runs of the sort.  One launch reads the batch in every block: 65536 tokens
+// over 1024 x 768 take 32 us with it and 35 in two, 131072 over 3000 x 512 85
+// and 49 us (one token repeated: 65536 over 300 x 1024 101 and 74 us).
+int64_t runs_of(int64_t n) {
+  if (n <= 65536) return 1;
+  const int64_t r = std::min<int64_t>((n + 16383) / 16384, 16);
+  return std::max<int64_t>(r, (n + (1 << 19) - 1) >> 19);   // a wave's part below 2^kRunBits
+}
+
 struct GradPlan {
   int shift, range, bits, span;
-  int64_t blocks;       // of the sums
-  bool small;           // one launch, no workspace
-  size_t order, sorted, count, part, total;
+  int64_t runs, chunk, sets;   // of the sort
+  int64_t blocks;              // of the sums
+  bool small;                  // one launch for all, no workspace
+  size_t order, sorted, count, table, sums, part, total;
   GradPlan(int64_t n, int64_t vocab, int64_t dim) {
-    for (shift = kMinShift; (vocab - 1) >> shift >= kMaxRange;) ++shift;
+    runs = runs_of(n);
+    chunk = runs == 1 ? n : ((n + runs - 1) / runs + 1023) / 1024 * 1024;
+    // sets: about a block a CU, and no more tokens a set than it can count
+    const int most = runs == 1 ? kOneRange : kSplitRange;
+    shift = kOneShift;
+    while (runs > 1 && shift > 4 && (runs << (shift - 1)) >= 256) --shift;
+    while ((vocab - 1) >> shift >= most) ++shift;
     range = (int)((vocab - 1) >> shift) + 1;
     for (bits = 0; (1 << bits) < range;) ++bits;
+    sets = std::min<int64_t>((int64_t)1 << shift, vocab);
     span = span_of(n);
     blocks = (n + span * kSumWaves - 1) / (span * kSumWaves);
-    const int64_t tokens = std::min<int64_t>((int64_t)1 << shift, vocab);
-    small = n <= kSmall && tokens * ((dim + 255) / 256) <= kSmallBlocks;
+    small = n <= kSmall && sets * ((dim + 255) / 256) <= kSmallBlocks;
     order = 0;
     sorted = order + align256((size_t)n * 4);
     count = sorted + align256((size_t)n * 4);
-    part = count + 256;
+    table = count + 256;
+    sums = table + (runs > 1 ? align256((size_t)runs * sets * range * 4) : 0);
+    part = sums + (runs > 1 ? align256((size_t)runs * sets * 4) : 0);
     // one block has no neighbours
     total = small ? 0 : part + (blocks > 1 ? align256((size_t)blocks * 2 * dim * 4) : 0);
   }
@@ -597,25 +722,27 @@ hipError_t embed(const EmbedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename TI, typename TO, int SHIFT, bool PAD>
-void token_sort_go(const EmbedGradArgs& a, const GradPlan& pl, int32_t* order, int32_t* sorted,
-                   int32_t* total, hipStream_t s) {
-  const int64_t grid = std::min<int64_t>((int64_t)1 << pl.shift, a.vocab);
-  hipLaunchKernelGGL((k_token_sort<TI, TO, SHIFT, PAD>), dim3((unsigned)grid),
-                     dim3(64 * kSortWaves), 0, s, (const TI*)a.tokens, a.n, (uint32_t)a.vocab,
-                     (uint32_t)a.padding, pl.shift, pl.range, pl.bits, order, sorted, total,
-                     a.accumulate ? nullptr : (TO*)a.dW, (int)a.dim);
-}
-
 template <typename TI, typename TO>
 hipError_t token_sort(const EmbedGradArgs& a, const GradPlan& pl, int32_t* order, int32_t* sorted,
                       int32_t* total, hipStream_t s) {
-  // up to 2^17 tokens, without padding: the reading loop has 5 vector
-  // instructions for 64 tokens instead of 7
-  if (pl.shift == kMinShift && a.padding < 0)
-    token_sort_go<TI, TO, kMinShift, false>(a, pl, order, sorted, total, s);
-  else
-    token_sort_go<TI, TO, 0, true>(a, pl, order, sorted, total, s);
+  const dim3 grid((unsigned)pl.sets, (unsigned)pl.runs), block(64 * kSortWaves);
+  int32_t* table = (int32_t*)((char*)a.ws + pl.table);
+  int32_t* sums = (int32_t*)((char*)a.ws + pl.sums);
+  const bool pad = a.padding >= 0;
+  if (pl.runs > 1) {
+    hipLaunchKernelGGL((pad ? k_token_count<TI, true> : k_token_count<TI, false>), grid, block, 0,
+                       s, (const TI*)a.tokens, a.n, (int)pl.chunk, (uint32_t)a.vocab,
+                       (uint32_t)a.padding, pl.shift, pl.range, table, sums);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const auto kernel = pl.runs > 1 ? (pad ? k_token_sort<TI, TO, 0, true, true>
+                                         : k_token_sort<TI, TO, 0, false, true>)
+                      : pl.shift == kOneShift && !pad ? k_token_sort<TI, TO, kOneShift, false, false>
+                                                      : k_token_sort<TI, TO, 0, true, false>;
+  hipLaunchKernelGGL(kernel, grid, block, 0, s, (const TI*)a.tokens, a.n, (int)pl.chunk,
+                     (uint32_t)a.vocab, (uint32_t)a.padding, pl.shift, pl.range, pl.bits, table,
+                     sums, order, sorted, total, a.accumulate ? nullptr : (TO*)a.dW, (int)a.dim);
   return hipGetLastError();
 }
 
@@ -640,7 +767,7 @@ hipError_t embed_sum(const EmbedGradArgs& a, const GradPlan& pl, const int32_t* 
 template <typename T, typename TI, typename TO>
 hipError_t embed_small(const EmbedGradArgs& a, const GradPlan& pl, hipStream_t s) {
   const auto go = [&](auto kernel, int v) {
-    const dim3 grid((unsigned)std::min<int64_t>((int64_t)1 << pl.shift, a.vocab),
+    const dim3 grid((unsigned)pl.sets,
                     (unsigned)((a.dim + 64 * v - 1) / (64 * v)));
     hipLaunchKernelGGL(kernel, grid, dim3(64 * kSmallWaves), 0, s, (const T*)a.dY, a.dy_stride,
                        (const TI*)a.tokens, (int)a.n, (uint32_t)a.vocab, (uint32_t)a.padding,

@@ -332,7 +332,10 @@ GRADS = [(1, 1, 1, "uniform"), (2, 3, 5, "same"), (63, 7, 4, "uniform"), (64, 64
          (50000, 4096, 3, "zipf"), (70000, 100, 1, "uniform"), (33000, 70000, 2, "zipf"),
          (150000, 30000, 2, "zipf"), (131073, 3, 5, "same"), (4000, 64, 2048, "zipf"),
          (20000, 70000, 8, "skew"), (800, 70000, 40, "skew"), (896, 300, 30, "zipf"),
-         (897, 300, 30, "zipf"), (896, 513, 5, "same"), (40000, 200000, 3, "skew")]
+         (897, 300, 30, "zipf"), (896, 513, 5, "same"), (40000, 200000, 3, "skew"),
+         (65536, 2000, 3, "zipf"), (65537, 2000, 3, "zipf"), (131072, 131072, 2, "zipf"),
+         (100001, 300000, 2, "skew"), (262145, 17, 2, "uniform"), (70001, 1, 3, "same"),
+         (600001, 1048576, 1, "uniform")]
 
 
 @pytest.mark.parametrize("dy_dtype,dw_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"),
