@@ -398,15 +398,15 @@ __device__ __forceinline__ void write_row(TO* out, const float (&acc)[V], int sk
 
 // The sums of a block of WAVES waves, each over `have` sorted positions.  Lane
 // i's tok: the token at the wave's position i - 1 (-1 outside the order), row:
-// the batch position at its position i.  ONCE: dY is read with the
-// non-temporal hint.  parts: where the two sums go that
-// cross the block's borders (null where none does).
-template <int WAVES, int V, bool ONCE, typename T, typename TO>
+// the batch position at its position i.  leave(0, sum): of a token begun before
+// the block, leave(1, sum): of one begun in it that goes on after it.  ONCE: dY
+// is read with the non-temporal hint.
+template <int WAVES, int V, bool ONCE, typename T, typename TO, typename Leave>
 __device__ __forceinline__ void sum_block(const T* __restrict__ dY, int64_t dys, int32_t tok,
                                           int32_t row, int have, const Place<V>& at, int w,
                                           float (&heads)[WAVES][64 * V], int (&through)[WAVES],
                                           TO* __restrict__ dW, int dim, float scale,
-                                          int accumulate, float* __restrict__ parts) {
+                                          int accumulate, const Leave& leave) {
   constexpr int U = 8;      // rows in flight
   const int lane = threadIdx.x & 63;
   // bit i: the token at position i is not the one before it
@@ -470,15 +470,14 @@ __device__ __forceinline__ void sum_block(const T* __restrict__ dY, int64_t dys,
     return true;
   };
   if (tail) {
-    const bool leaves = collect(w + 1);
-    if (parts && leaves) store_own<V>(parts + dim + at.c, at.skip, acc);
+    if (collect(w + 1)) leave(1, acc);
     else write_row<V>(dW + (int64_t)cur * dim + at.c, acc, at.skip, scale, accumulate);
   }
-  if (parts && w == 0 && begun) {
+  if (w == 0 && begun) {
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
     collect(0);
-    store_own<V>(parts + at.c, at.skip, acc);
+    leave(0, acc);
   }
 }
 
@@ -500,96 +499,140 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_embed_sum(
   const int64_t q = p0 + lane - 1;
   const int32_t tok = lane <= span + 1 && q >= 0 && q < n ? sorted[q] : -1;
   const int32_t row = lane < have ? order[p0 + lane] : 0;
-  sum_block<kSumWaves, V, ONCE>(dY, dys, tok, row, have, Place<V>((slice * 64 + lane) * V, dim), w,
-                          heads, through, dW, dim, scale, accumulate,
-                          part + 2 * (int64_t)block * dim);
+  const Place<V> at((slice * 64 + lane) * V, dim);
+  sum_block<kSumWaves, V, ONCE>(dY, dys, tok, row, have, at, w, heads, through, dW, dim, scale,
+                                accumulate, [&](int which, const float(&acc)[V]) {
+                                  store_own<V>(part + (2 * (int64_t)block + which) * dim + at.c,
+                                               at.skip, acc);
+                                });
 }
 
 // ---------------------------------------------------------------------------
-// Small batches, in one launch: a block reads the batch, one token a thread,
-// lists the positions of its own tokens (t % B as above) in order, gives each
-// its place by counting the listed ones that go before it, and sums the rows
-// from there.  No position is another block's, so nothing crosses a border.
-// Blocks of the same tokens divide the columns (64 V each).
+// Small batches, in one launch: a block reads the batch, H tokens a thread,
+// lists the positions of its set's tokens in order, gives each its place by
+// counting the listed ones that go before it, and sums the rows from there: 16
+// waves of up to kSmallSpan positions a round.  H = 1 has all in one round; with
+// H = 2 what crosses from one round to the next stays in the block.  Blocks of
+// the same set divide the columns (64 V each).
 // ---------------------------------------------------------------------------
 constexpr int kSmallWaves = 16;
 constexpr int kSmallSpan = 56;      // positions a wave, + 2 neighbours, in 64 lanes
-constexpr int kSmall = kSmallWaves * kSmallSpan;
+constexpr int small_batch(int h) { return kSmallWaves * (h == 1 ? kSmallSpan : 64 * h); }
 
-template <typename T, typename TI, typename TO, int V>
+template <typename T, typename TI, typename TO, int V, int H>
 __global__ __launch_bounds__(64 * kSmallWaves) void k_embed_small(
     const T* __restrict__ dY, int64_t dys, const TI* __restrict__ tokens, int n, uint32_t vocab,
     uint32_t padding, int shift, int range, float scale, TO* __restrict__ dW, int dim,
     int accumulate) {
-  constexpr int W = 8;                  // listed tokens a step
-  __shared__ float heads[kSmallWaves][64 * V];
-  __shared__ int through[kSmallWaves], found[kSmallWaves];
+  constexpr int W = 8, THREADS = 64 * kSmallWaves;     // W: listed tokens a step
+  constexpr int kSmall = small_batch(H);
+  __shared__ float heads[kSmallWaves][64 * V], crossing[2][64 * V];
+  __shared__ int through[kSmallWaves], found[H * kSmallWaves];
   __shared__ uint32_t bins[kSmall + W];
-  __shared__ int16_t at_list[kSmall], order[kSmall];
+  __shared__ uint16_t at_list[kSmall], order[kSmall];
   __shared__ int32_t sorted[kSmall];
   __shared__ uint8_t touched[kOneRange];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t block = blockIdx.x;
-  const int me = threadIdx.x;
-  uint32_t t = ~0u;
-  bool in = false;
-  if (me < n) {
-    Token<TI> token;
-    token.load(tokens + me);
-    t = token.lo;
-    in = token.whole() && t < vocab && t != padding && (t & ((1u << shift) - 1)) == block;
-  }
-  const uint64_t m = __ballot(in);
-  if (lane == 0) found[w] = __popcll(m);
-  for (int k = me; k < range; k += 64 * kSmallWaves) touched[k] = 0;
-  __syncthreads();
-  int count = 0, first = 0;
+  const uint32_t set = blockIdx.x;
+  uint32_t t[H];
+  bool in[H];
+  uint64_t m[H];
 #pragma unroll
-  for (int j = 0; j < kSmallWaves; ++j) {
-    if (j == w) first = count;
+  for (int h = 0; h < H; ++h) {
+    const int p = h * THREADS + threadIdx.x;
+    t[h] = ~0u;
+    in[h] = false;
+    if (p < n) {
+      Token<TI> token;
+      token.load(tokens + p);
+      t[h] = token.lo;
+      in[h] = token.whole() && t[h] < vocab && t[h] != padding &&
+              (t[h] & ((1u << shift) - 1)) == set;
+    }
+    m[h] = __ballot(in[h]);
+    if (lane == 0) found[h * kSmallWaves + w] = __popcll(m[h]);
+  }
+  for (int k = threadIdx.x; k < range; k += THREADS) touched[k] = 0;
+  __syncthreads();
+  int count = 0, first[H] = {};
+#pragma unroll
+  for (int j = 0; j < H * kSmallWaves; ++j) {
+    if (j % kSmallWaves == w) first[j / kSmallWaves] = count;
     count += found[j];
   }
-  if (in) {
-    const int k = first + __popcll(m & (((uint64_t)1 << lane) - 1));
-    bins[k] = t >> shift;
-    at_list[k] = (int16_t)me;
-    touched[t >> shift] = 1;
-  }
-  if (me < W) bins[count + me] = ~0u;   // goes before no other
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (in[h]) {
+      const int k = first[h] + __popcll(m[h] & (((uint64_t)1 << lane) - 1));
+      bins[k] = t[h] >> shift;
+      at_list[k] = (uint16_t)(h * THREADS + threadIdx.x);
+      touched[t[h] >> shift] = 1;
+    }
+  if (threadIdx.x < W) bins[count + threadIdx.x] = ~0u;   // goes before no other
   __syncthreads();
-  const uint32_t mine = me < count ? bins[me] : 0;
   // a table of up to B rows, or a frequent token: nothing to sort (800 equal
   // tokens would take 60 us)
-  const bool one = __syncthreads_and(me >= count || mine == bins[0]);
-  if (me < count) {
-    int place = one ? me : 0;
+  bool same = true;
+  for (int k = threadIdx.x; k < count; k += THREADS) same &= bins[k] == bins[0];
+  const bool one = __syncthreads_and(same);
+  for (int k = threadIdx.x; k < count; k += THREADS) {
+    const uint32_t mine = bins[k];
+    int place = one ? k : 0;
     if (!one)
       for (int j = 0; j < count; j += W)
 #pragma unroll
         for (int u = 0; u < W; ++u) {
           const uint32_t other = bins[j + u];
-          place += other < mine || (other == mine && j + u < me);
+          place += other < mine || (other == mine && j + u < k);
         }
-    order[place] = at_list[me];
-    sorted[place] = (int32_t)((mine << shift) + block);
+    order[place] = at_list[k];
+    sorted[place] = (int32_t)((mine << shift) + set);
   }
   const Place<V> at(((int)blockIdx.y * 64 + lane) * V, dim);
   if (!accumulate) {
     const float zero[V] = {};
     for (int r = w; r < range; r += kSmallWaves)
-      if (!touched[r] && ((uint32_t)r << shift) + block < vocab)
-        store_own<V>(dW + (((int64_t)r << shift) + block) * dim + at.c, at.skip, zero);
+      if (!touched[r] && ((uint32_t)r << shift) + set < vocab)
+        store_own<V>(dW + (((int64_t)r << shift) + set) * dim + at.c, at.skip, zero);
   }
   __syncthreads();
-  const int span = (count + 8 * kSmallWaves - 1) / (8 * kSmallWaves) * 8;
-  const int p0 = w * span;
-  const int have = count - p0 < span ? (count > p0 ? count - p0 : 0) : span;
-  const int q = p0 + lane - 1;
-  const int32_t tok = lane <= span + 1 && q >= 0 && q < count ? sorted[q] : -1;
-  const int32_t row = lane < have ? order[p0 + lane] : 0;
-  sum_block<kSmallWaves, V, false>(dY, dys, tok, row, have, at, w, heads, through, dW, dim, scale,
-                            accumulate, (float*)nullptr);
+  const auto token = [&](int p) { return p >= 0 && p < count ? sorted[p] : -1; };
+  float held[V];        // wave 0: of a token that goes on from the last round
+#pragma unroll
+  for (int k = 0; k < V; ++k) held[k] = 0.f;
+  for (int base = 0; base < count;) {
+    const int left = count - base;
+    const int want = (left + 8 * kSmallWaves - 1) / (8 * kSmallWaves) * 8;
+    const int span = want < kSmallSpan ? want : kSmallSpan;
+    const int end = left < span * kSmallWaves ? count : base + span * kSmallWaves;
+    const int p0 = base + w * span;
+    const int have = end - p0 < span ? (end > p0 ? end - p0 : 0) : span;
+    const int32_t tok = lane <= span + 1 ? token(p0 + lane - 1) : -1;
+    const int32_t row = lane < have ? order[p0 + lane] : 0;
+    sum_block<kSmallWaves, V, false>(dY, dys, tok, row, have, at, w, heads, through, dW, dim,
+                                     scale, accumulate, [&](int which, const float(&acc)[V]) {
+                                       store_vec<V>(&crossing[which][lane * V], acc);
+                                     });
+    if (H == 1) return;
+    __syncthreads();
+    const int32_t front = token(base), back = token(end - 1);
+    const bool begun = token(base - 1) == front, on = token(end) == back;
+    if (w == 0) {
+      const bool all = begun && on && front == back;    // the whole round
+      if (begun) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) held[k] += crossing[0][lane * V + k];
+        if (!all)
+          write_row<V>(dW + (int64_t)front * dim + at.c, held, at.skip, scale, accumulate);
+      }
+      if (on && !all)
+#pragma unroll
+        for (int k = 0; k < V; ++k) held[k] = crossing[1][lane * V + k];
+    }
+    __syncthreads();
+    base = end;
+  }
 }
 
 // Adds the parts of a token that begins in block b of the sums (blockIdx.x)
@@ -653,9 +696,10 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int span_of(int64_t n) { return n <= 32768 ? 8 : n <= 131072 ? 16 : 32; }
 
 // Blocks of the one-launch form, each of which lists the batch anew.  800
-// tokens take 8.6 us instead of 16.1 (table of 30000 x 64) and 22.3 instead of
-// 31.4 (50257 x 768); with more column slices the listing costs more than two
-// launches (300 tokens, 300 x 4000: 20.2 against 15.4 us).
+// tokens take 8.9 us instead of 16.1 (table of 30000 x 64) and 22.3 instead of
+// 31.4 (50257 x 768), 1618 tokens 11.6 instead of 16.5 (53813 x 10); with more
+// column slices the listing costs more than two launches (300 tokens, 300 x
+// 4000: 20.2 against 15.4 us).
 constexpr int64_t kSmallBlocks = 1024;
 
 // Runs of the sort.  One launch reads the batch in every block: 65536 tokens
@@ -686,7 +730,7 @@ struct GradPlan {
     sets = std::min<int64_t>((int64_t)1 << shift, vocab);
     span = span_of(n);
     blocks = (n + span * kSumWaves - 1) / (span * kSumWaves);
-    small = n <= kSmall && sets * ((dim + 255) / 256) <= kSmallBlocks;
+    small = n <= small_batch(2) && sets * ((dim + 255) / 256) <= kSmallBlocks;
     order = 0;
     sorted = order + align256((size_t)n * 4);
     count = sorted + align256((size_t)n * 4);
@@ -774,7 +818,11 @@ hipError_t embed_small(const EmbedGradArgs& a, const GradPlan& pl, hipStream_t s
                        pl.shift, pl.range, a.scale, (TO*)a.dW, (int)a.dim, a.accumulate);
     return hipGetLastError();
   };
-  return a.dim >= 4 ? go(k_embed_small<T, TI, TO, 4>, 4) : go(k_embed_small<T, TI, TO, 1>, 1);
+  if (a.n <= small_batch(1))
+    return a.dim >= 4 ? go(k_embed_small<T, TI, TO, 4, 1>, 4)
+                      : go(k_embed_small<T, TI, TO, 1, 1>, 1);
+  return a.dim >= 4 ? go(k_embed_small<T, TI, TO, 4, 2>, 4)
+                    : go(k_embed_small<T, TI, TO, 1, 2>, 1);
 }
 
 template <typename T, typename TO>

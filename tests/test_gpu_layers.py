@@ -335,7 +335,9 @@ GRADS = [(1, 1, 1, "uniform"), (2, 3, 5, "same"), (63, 7, 4, "uniform"), (64, 64
          (897, 300, 30, "zipf"), (896, 513, 5, "same"), (40000, 200000, 3, "skew"),
          (65536, 2000, 3, "zipf"), (65537, 2000, 3, "zipf"), (131072, 131072, 2, "zipf"),
          (100001, 300000, 2, "skew"), (262145, 17, 2, "uniform"), (70001, 1, 3, "same"),
-         (600001, 1048576, 1, "uniform")]
+         (600001, 1048576, 1, "uniform"), (2048, 300, 70, "same"), (2047, 5000, 260, "zipf"),
+         (2048, 1000, 5, "skew"), (1793, 2, 9, "uniform"), (2049, 1000, 7, "skew"),
+         (2048, 600, 3, "skew"), (1500, 131072, 4, "skew")]
 
 
 @pytest.mark.parametrize("dy_dtype,dw_dtype", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"),
