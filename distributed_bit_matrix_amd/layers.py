@@ -9,9 +9,9 @@ tensors; ``LayerNorm`` and ``Embedding`` are modules over them.
 
 Under an optimizer made with ``SignMuon(..., direct_grads=True)`` the backward
 passes write the parameter gradients in float32 straight into the flat array
-that the step reads (see ``optim``); ``p.grad`` stays None then.  Otherwise, and
-while a HIP graph is being captured, they return them in the parameter's
-dtype as any other operator does.  The gradients cannot be differentiated
+that the step reads (see ``optim``); ``p.grad`` stays None then.  Otherwise, in
+``torch.autograd.grad`` and while a HIP graph is being captured, they return
+them in the parameter's dtype as any other operator does.  The gradients cannot be differentiated
 again.
 """
 from __future__ import annotations
@@ -37,10 +37,22 @@ def _slot(p):
     return None if p is None else p.__dict__.get("_signmuon_slot")
 
 
-def _direct(slot):
-    """Whether a gradient goes to its slot: not once the optimizer is gone, nor
-    into a graph, whose replays would not tell the optimizer what they wrote."""
-    return slot is not None and slot.alive() and not torch.cuda.is_current_stream_capturing()
+def _accumulates(ctx, i) -> bool:
+    """Whether this backward pass adds to the grad of input i, a leaf: not where
+    backward(inputs=...) leaves it out, nor in torch.autograd.grad, which hands
+    the gradient to its caller (or drops it)."""
+    try:
+        return torch._C._will_engine_execute_node(ctx.next_functions[i][0])
+    except RuntimeError:      # the engine's answer where grad() asks for the leaf
+        return False
+
+
+def _direct(ctx, i, slot):
+    """Whether the gradient of input i goes to its slot: not once the optimizer
+    is gone, nor into a graph, whose replays would not tell the optimizer what
+    they wrote."""
+    return (slot is not None and slot.alive() and _accumulates(ctx, i)
+            and not torch.cuda.is_current_stream_capturing())
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -60,8 +72,10 @@ class _LayerNorm(torch.autograd.Function):
         want_x, want_w, want_b = ctx.needs_input_grad[:3]
         dw = db = dtype = None
         add = False
-        direct = [s if want and _direct(s) else None
-                  for s, want in zip(ctx.slots, (want_w, want_b))]
+        direct = [s if want and _direct(ctx, i, s) else None
+                  for i, s, want in zip((1, 2), ctx.slots, (want_w, want_b))]
+        if direct[0] is direct[1]:      # one parameter as weight and bias
+            direct = [None, None]
         if any(direct):
             dtype = torch.float32
             add = any(s is not None and s.filled for s in direct)
@@ -111,7 +125,7 @@ class _Embedding(torch.autograd.Function):
         tokens, = ctx.saved_tensors
         vocab, dtype, scale, padding, slot = ctx.table
         dy = _dense_rows(dy)
-        if _direct(slot):
+        if _direct(ctx, 1, slot):
             add = slot.filled
             B.embedding_backward(dy, tokens, vocab, scale, padding, dW=slot.open(add),
                                  accumulate=add)

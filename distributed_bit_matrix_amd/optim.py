@@ -56,6 +56,9 @@ class GradSlot:
         self.filled = False          # holds a gradient that no step has used
         self._state = weakref.ref(state)
 
+    def __reduce__(self):
+        return type(None), ()        # a saved or copied parameter has none
+
     def alive(self) -> bool:
         return self._state() is not None
 
@@ -105,7 +108,8 @@ class _GroupState:
                             tie_value=group["tie_value"], encoding=encoding)
         with torch.cuda.device(dev):
             self.plan = B.StepPlan(self.layout, self.hp, post_vote, device=dev)
-            self.event = torch.cuda.Event()
+            self.event = torch.cuda.Event() if direct else None
+        if direct:
             self.mark()
         self.slots = []
         for p, (_, _, off, _) in zip(params, self.layout):
@@ -159,8 +163,9 @@ class SignMuon(torch.optim.Optimizer):
     to a bfloat16 parameter's dtype nor copied.  The parameters have to be on
     their GPU already: they move into the flat buffer here.  Such a gradient
     is the sum since the last step or zero_grad of this optimizer; p.grad
-    stays None for it, and what other operators put there is added to it (a
-    table shared with the output product)."""
+    stays None for it (hooks on the parameter and what clips or scales p.grad do
+    not see it), and what other operators put there is added to it (a table
+    shared with the output product)."""
 
     def __init__(self, params, lr: float = 0.02, beta: float = 0.9,
                  weight_decay: float = 0.0, eps: float = 1e-7, K: int = 5,

@@ -17,8 +17,8 @@
  * do not overlap.  Pointers are aligned to their element type; no larger
  * alignment is needed.
  *
- * Dtypes are sm_dtype codes.  Every sum is held in float32; a bfloat16 result
- * is rounded once, to nearest even, when it is stored.
+ * Dtypes are sm_dtype codes.  Every sum is held in float32 or wider; a
+ * bfloat16 result is rounded once, to nearest even, when it is stored.
  */
 #ifndef SIGNMUON_LAYERS_H
 #define SIGNMUON_LAYERS_H

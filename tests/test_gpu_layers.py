@@ -704,3 +704,65 @@ def test_foreign_token_is_reported_by_the_step():
     assert opt.nonfinite()
     for p, b in zip(model.parameters(), before):
         assert torch.equal(p, b)
+
+
+def _filled(p):
+    return p._signmuon_slot.filled
+
+
+def test_direct_gradients_only_where_a_pass_adds_to_the_parameter():
+    """torch.autograd.grad returns its gradients and leaves the step's alone,
+    backward(inputs=...) writes those it names, and the next plain backward
+    pass writes all."""
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    rng = np.random.default_rng(12)
+    t = torch.arange(24, device="cuda") % 7
+    table = torch.nn.Parameter(dev(values(rng, (7, 40), "f32")))
+    w = torch.nn.Parameter(dev(values(rng, (40,), "f32")))
+    b = torch.nn.Parameter(dev(values(rng, (40,), "f32")))
+    c = dev(values(rng, (24, 40), "f32"))
+    params = [table, w, b]
+
+    def loss():
+        return (L.layer_norm(L.embedding(t, table), w, b, EPS) * c).sum()
+
+    want = torch.autograd.grad(loss(), params)
+    opt = SO.SignMuon(params, scale="fro", K=1, direct_grads=True)
+    got = torch.autograd.grad(loss(), params)
+    assert not any(_filled(p) for p in params)
+    for g, q in zip(got, want):
+        assert torch.equal(g, q)
+    got = torch.autograd.grad(loss(), [w])
+    assert torch.equal(got[0], want[1]) and not any(_filled(p) for p in params)
+    loss().backward(inputs=[w])
+    assert [_filled(p) for p in params] == [False, True, False]
+    opt.zero_grad()
+    loss().backward()
+    assert all(_filled(p) and p.grad is None for p in params)
+    for p, q in zip(params, want):
+        assert torch.equal(p._signmuon_slot.grad, q)
+
+
+def test_direct_gradients_of_one_parameter_in_both_places():
+    """weight and bias the same parameter: its gradient is the sum of both."""
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    rng = np.random.default_rng(13)
+    x = dev(values(rng, (50, 24), "f32"))
+    c = dev(values(rng, (50, 24), "f32"))
+    w = torch.nn.Parameter(dev(values(rng, (24,), "f32")))
+    want, = torch.autograd.grad((L.layer_norm(x, w, w, EPS) * c).sum(), [w])
+    opt = SO.SignMuon([w], scale="fro", K=1, direct_grads=True)
+    (L.layer_norm(x, w, w, EPS) * c).sum().backward()
+    opt.step()
+    assert torch.equal(opt._groups[0].G[:24], want)
+
+
+def test_norm_gradient_refuses_one_array_for_both_sums():
+    x = torch.randn(6, 8, device="cuda")
+    y, m, r = B.layer_norm(x, want_stats=True)
+    both = torch.zeros(8, device="cuda")
+    with pytest.raises(B.SignMuonError):
+        B.layer_norm_backward(x, x, None, m, r, dweight=both, dbias=both)
+    assert float(both.abs().max()) == 0.0

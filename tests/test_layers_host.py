@@ -223,3 +223,65 @@ def test_embed_grad_bounds_reject_mistakes():
     for i in range(500):
         s32[t[i]] += dy[i]
     assert (np.abs(np.float32(0.5) * s32 - dw) <= e).all()
+
+
+@built
+def test_norm_grad_refuses_one_array_for_both_sums():
+    both = ctypes.c_void_p(9 << 20)
+    assert _norm_grad(dg=both, db=both) == B.SM_EINVAL
+    assert _norm_grad(dX=None, dg=both, db=both) == B.SM_EINVAL
+
+
+class _Probe(torch.autograd.Function):
+    """x * w that records whether the pass adds to the grads of x and w."""
+    seen = []
+
+    @staticmethod
+    def forward(ctx, x, w):
+        ctx.save_for_backward(x, w)
+        return x * w
+
+    @staticmethod
+    def backward(ctx, g):
+        from distributed_bit_matrix_amd import layers as L
+        x, w = ctx.saved_tensors
+        _Probe.seen.append(tuple(L._accumulates(ctx, i) for i in (0, 1)))
+        return g * w, g * x
+
+
+def test_a_pass_knows_whether_it_adds_to_a_leaf():
+    x, w = torch.ones(3, requires_grad=True), torch.nn.Parameter(torch.ones(3))
+
+    def run(call):
+        _Probe.seen.clear()
+        call(_Probe.apply(x, w).sum())
+        return _Probe.seen[0]
+
+    assert run(lambda y: y.backward()) == (True, True)
+    assert run(lambda y: y.backward(inputs=[x])) == (True, False)
+    assert run(lambda y: y.backward(inputs=[w])) == (False, True)
+    assert run(lambda y: torch.autograd.grad(y, [w])) == (False, False)
+    assert run(lambda y: torch.autograd.grad(y, [x])) == (False, False)
+    assert run(lambda y: torch.autograd.grad(y, [x, w])) == (False, False)
+
+
+def test_parameters_with_a_slot_can_be_saved_and_copied():
+    import copy
+    import io
+    from distributed_bit_matrix_amd import optim as SO
+
+    class State:
+        pass
+
+    state, p = State(), torch.nn.Parameter(torch.arange(4.))
+    p._signmuon_slot = SO.GradSlot(state, torch.zeros(4))
+    f = io.BytesIO()
+    torch.save(p, f)
+    f.seek(0)
+    q = torch.load(f, weights_only=False)          # the file written above
+    for r in (q, copy.deepcopy(p)):
+        assert torch.equal(r.detach(), p.detach())
+        assert r.__dict__.get("_signmuon_slot") is None
+    assert p._signmuon_slot.alive()
+    del state
+    assert not p._signmuon_slot.alive()
