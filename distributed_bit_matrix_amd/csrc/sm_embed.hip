@@ -48,12 +48,12 @@ __global__ __launch_bounds__(256) void k_embed(const TW* __restrict__ W, int64_t
 // blocks, set b takes the tokens t with t % B = b, so that frequent tokens,
 // which vocabularies number next to each other, spread over the sets.
 //
-// Small batches (SPLIT = false): one block a set and one launch.  Every block
+// Small batches (kOneLaunch): one block a set and one launch.  Every block
 // reads the whole batch and needs nothing of the others: it counts the tokens
 // of the sets before it on the way, which gives its place in the order.
-// Larger ones: a set has a block for each of S runs of the batch; a first
-// launch (k_token_count) counts every block's tokens, the second one knows
-// from these counts where each token of each run goes.
+// Larger ones (kRuns, kLongRuns): a set has a block for each of S runs of the
+// batch; a first launch (k_token_count) counts every block's tokens, the
+// second one knows from these counts where each token of each run goes.
 //
 // Each of a block's 16 waves reads a part of its run and lists the positions
 // that are the set's; the list is counted by token, the counts are scanned
@@ -74,6 +74,7 @@ constexpr int kList = 64 * kBatch;   // listed positions a wave
 constexpr int kRunBits = 16;     // a listed position: bin << 16 | place in the part
 constexpr int kOneRange = 512, kOneShift = 8;   // one launch: tokens a block, fewest sets
 constexpr int kSplitRange = 2048;               // two launches
+constexpr int kWideRange = 1024;                // two launches over long runs
 
 typedef volatile __attribute__((address_space(3))) int32_t lds_i32;
 typedef volatile __attribute__((address_space(3))) uint32_t lds_u32;
@@ -193,15 +194,27 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_count(
   }
 }
 
-template <typename TI, typename TO, int SHIFT, bool PAD, bool SPLIT>
+// A run of at most kShortRun tokens has room for a token's places in 16 bits
+// (the last of them may wrap to 0: nothing comes after it); longer ones (more
+// than 16 kShortRun tokens in all) take 32 bits and half as many bins a block.
+constexpr int kShortRun = 1 << 16;
+enum Split { kOneLaunch, kRuns, kLongRuns };
+
+template <typename TI, typename TO, int SHIFT, bool PAD, Split SPLIT>
 __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
     const TI* __restrict__ tokens, int64_t n, int chunk, uint32_t vocab, uint32_t padding,
     int shift, int range, int bits, const int32_t* __restrict__ table,
     const int32_t* __restrict__ sums, int32_t* __restrict__ order, int32_t* __restrict__ sorted,
     int32_t* __restrict__ total, TO* __restrict__ dW, int dim) {
-  constexpr int RANGE = SPLIT ? kSplitRange : kOneRange;
+  constexpr int RANGE = SPLIT == kOneLaunch ? kOneRange
+                        : SPLIT == kRuns    ? kSplitRange
+                                            : kWideRange;
+  constexpr bool WIDE = SPLIT == kLongRuns;
+  using Count = std::conditional_t<WIDE, uint32_t, uint16_t>;
+  using lds_count = std::conditional_t<WIDE, lds_u32, lds_u16>;
+  constexpr int WORDS = RANGE * (int)sizeof(Count) / 4;
   constexpr int BINS = RANGE > 64 * kSortWaves ? RANGE / (64 * kSortWaves) : 1;   // a thread
-  __shared__ uint32_t counts[kSortWaves][RANGE / 2];   // two 16-bit counts a word
+  __shared__ uint32_t counts[kSortWaves][WORDS];
   __shared__ int32_t place[RANGE];
   __shared__ uint32_t lists[kSortWaves][kList];
   __shared__ int32_t below[kSortWaves], wave_total[kSortWaves];
@@ -215,10 +228,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
   const int share = ((size + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;   // < 2^kRunBits
   const int left = size - w * share, run = left < 0 ? 0 : left < share ? left : share;
   const int64_t i0 = c0 + w * share;
-  lds_u16* count = (lds_u16*)counts[w];
+  lds_count* count = (lds_count*)counts[w];
   lds_u32* list = (lds_u32*)lists[w];
-  for (int k = threadIdx.x; k < kSortWaves * RANGE / 2; k += 64 * kSortWaves)
-    counts[k / (RANGE / 2)][k % (RANGE / 2)] = 0;
+  for (int k = threadIdx.x; k < kSortWaves * WORDS; k += 64 * kSortWaves)
+    counts[k / WORDS][k % WORDS] = 0;
   __syncthreads();
 
   // Counts (or, once the counts hold places, places) the first `len` listed.
@@ -233,10 +246,10 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
       const bool one = peers == live;       // all of them the same token
       if (!placing) {
         if (one) {
-          if (lane == 0) count[b0] = (uint16_t)(count[b0] + __popcll(live));
+          if (lane == 0) count[b0] = (Count)(count[b0] + __popcll(live));
         } else if (in) {
-          __hip_atomic_fetch_add(&counts[w][b >> 1], 1u << (b & 1) * 16, __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_WORKGROUP);
+          __hip_atomic_fetch_add(&counts[w][WIDE ? b : b >> 1], WIDE ? 1u : 1u << (b & 1) * 16,
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
         continue;
       }
@@ -251,12 +264,12 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
         peers = ((uint64_t)hi << 32) | lo;
       }
       if (in) {
-        const int c = count[b];
+        const int c = (int)count[b];
         const int32_t p = place[b] + c + __popcll(peers & before);
         order[p] = (int32_t)(i0 + (entry & ((1u << kRunBits) - 1)));
         sorted[p] = (int32_t)(((uint32_t)b << shift) + set);
         __builtin_amdgcn_wave_barrier();
-        if ((peers & before) == 0) count[b] = (uint16_t)(c + __popcll(peers));
+        if ((peers & before) == 0) count[b] = (Count)(c + __popcll(peers));
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -288,7 +301,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
 
   int len = scan(false);
   settle(len, false);
-  if (SPLIT) {
+  if (SPLIT != kOneLaunch) {
     // tokens of the sets before this one, in all runs
     under = 0;
     for (int k = threadIdx.x; k < (int)(gridDim.x * gridDim.y); k += 64 * kSortWaves)
@@ -306,7 +319,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
     int32_t earlier = 0;              // in the runs before this one
     all[q] = 0;
     if (k < range) {
-      if (SPLIT) {
+      if (SPLIT != kOneLaunch) {
         for (int r = 0; r < (int)gridDim.y; ++r) {
           const int32_t c = table[((int64_t)r * gridDim.x + set) * range + k];
           all[q] += c;
@@ -316,12 +329,12 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_token_sort(
       int32_t here = 0;
 #pragma unroll
       for (int j = 0; j < kSortWaves; ++j) {
-        lds_u16* slot = (lds_u16*)counts[j] + k;
-        const int c = *slot;
-        *slot = (uint16_t)here;
+        lds_count* slot = (lds_count*)counts[j] + k;
+        const int c = (int)*slot;
+        *slot = (Count)here;
         here += c;
       }
-      if (!SPLIT) all[q] = here;
+      if (SPLIT == kOneLaunch) all[q] = here;
       place[k] = earlier;
       empty[k] = all[q] == 0 && ((uint32_t)k << shift) + set < vocab;
     }
@@ -714,6 +727,7 @@ int64_t runs_of(int64_t n) {
 struct GradPlan {
   int shift, range, bits, span;
   int64_t runs, chunk, sets;   // of the sort
+  bool wide;                   // runs too long for 16-bit counts
   int64_t blocks;              // of the sums
   bool small;                  // one launch for all, no workspace
   size_t order, sorted, count, table, sums, part, total;
@@ -721,7 +735,8 @@ struct GradPlan {
     runs = runs_of(n);
     chunk = runs == 1 ? n : ((n + runs - 1) / runs + 1023) / 1024 * 1024;
     // sets: about a block a CU, and no more tokens a set than it can count
-    const int most = runs == 1 ? kOneRange : kSplitRange;
+    wide = chunk > kShortRun;
+    const int most = runs == 1 ? kOneRange : wide ? kWideRange : kSplitRange;
     shift = kOneShift;
     while (runs > 1 && shift > 4 && (runs << (shift - 1)) >= 256) --shift;
     while ((vocab - 1) >> shift >= most) ++shift;
@@ -780,10 +795,13 @@ hipError_t token_sort(const EmbedGradArgs& a, const GradPlan& pl, int32_t* order
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const auto kernel = pl.runs > 1 ? (pad ? k_token_sort<TI, TO, 0, true, true>
-                                         : k_token_sort<TI, TO, 0, false, true>)
-                      : pl.shift == kOneShift && !pad ? k_token_sort<TI, TO, kOneShift, false, false>
-                                                      : k_token_sort<TI, TO, 0, true, false>;
+  const auto kernel = pl.wide ? (pad ? k_token_sort<TI, TO, 0, true, kLongRuns>
+                                     : k_token_sort<TI, TO, 0, false, kLongRuns>)
+                      : pl.runs > 1 ? (pad ? k_token_sort<TI, TO, 0, true, kRuns>
+                                           : k_token_sort<TI, TO, 0, false, kRuns>)
+                      : pl.shift == kOneShift && !pad
+                          ? k_token_sort<TI, TO, kOneShift, false, kOneLaunch>
+                          : k_token_sort<TI, TO, 0, true, kOneLaunch>;
   hipLaunchKernelGGL(kernel, grid, block, 0, s, (const TI*)a.tokens, a.n, (int)pl.chunk,
                      (uint32_t)a.vocab, (uint32_t)a.padding, pl.shift, pl.range, pl.bits, table,
                      sums, order, sorted, total, a.accumulate ? nullptr : (TO*)a.dW, (int)a.dim);

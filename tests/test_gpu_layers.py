@@ -766,3 +766,42 @@ def test_norm_gradient_refuses_one_array_for_both_sums():
     with pytest.raises(B.SignMuonError):
         B.layer_norm_backward(x, x, None, m, r, dweight=both, dbias=both)
     assert float(both.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("n,vocab,kind", [((1 << 20) + 1, 40, "same"), ((1 << 21) + 5, 3000, "same"),
+                                          ((1 << 20) - 7, 3, "same"), (1 << 20, 70000, "same"),
+                                          ((1 << 22) + 77, 50, "zipf"),
+                                          ((1 << 21) + 1, 5000, "half"),
+                                          (1300000, 200000, "half")])
+def test_embedding_backward_of_tokens_repeated_in_long_batches(n, vocab, kind):
+    """A token that fills most of a batch past 2^20 tokens.  Entries 0, 1 and 2:
+    every partial sum is an integer below 2^24 and so exact in float32."""
+    print(f"long batch n={n} vocab={vocab} {kind}", flush=True)
+    rng = np.random.default_rng(n + vocab)
+    if kind == "half":
+        t = np.where(rng.random(n) < 0.9, vocab - 2, rng.integers(0, vocab, n))
+    else:
+        t = _tokens(rng, kind, n, vocab)
+    dy = rng.integers(0, 3, (n, 2)).astype(np.float32)
+    want = np.stack([np.bincount(t, dy[:, k], minlength=vocab) for k in (0, 1)], 1)
+    assert want.max() < 1 << 24
+    T, DY = torch.from_numpy(t).cuda(), dev(dy)
+    assert np.array_equal(host(B.embedding_backward(DY, T, vocab)), want)
+    assert np.array_equal(host(B.embedding_backward(DY, T.int(), vocab)), want)
+    keep = t != t[0]
+    got = host(B.embedding_backward(DY, T, vocab, padding=int(t[0])))
+    want[t[0]] = 0
+    assert keep.any() == bool(want.any()) and np.array_equal(got, want)
+
+
+def test_embedding_backward_of_the_longest_batch():
+    """2^27 tokens, the most that a call takes, seven of eight of them the same:
+    sums of ones are exact up to 2^24, and parts are joined in double."""
+    n, vocab = 1 << 27, 2000
+    T = torch.full((n,), 1234, device="cuda", dtype=torch.int32)
+    T[::8] = torch.arange(n // 8, device="cuda", dtype=torch.int32) % vocab
+    dy = torch.ones(n, 1, device="cuda", dtype=torch.bfloat16)
+    got = host(B.embedding_backward(dy, T, vocab))[:, 0]
+    want = np.bincount(np.arange(n // 8) % vocab, minlength=vocab).astype(np.float64)
+    want[1234] += n - n // 8
+    assert np.array_equal(got, want.astype(np.float32))
