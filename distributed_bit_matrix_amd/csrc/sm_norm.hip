@@ -8,6 +8,7 @@
 // lose a large mean's variance), and the result is written from registers.
 // Both passes are bound by HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "sm_layers.h"
 #include "sm_rows.h"
@@ -42,7 +43,9 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int& turn) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward
+// Forward.  16384 x 4096 float32 takes 88 us (6.1 TB/s), 12288 x 768 bfloat16
+// 8.8 us (4.3 TB/s of what the cache holds: one load, two sums and one store
+// deep, with nothing left to overlap).
 // ---------------------------------------------------------------------------
 template <typename T, typename TW, int V, int LANES, int NV, bool ONCE>
 __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_norm(
@@ -103,41 +106,108 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_norm(
   }
 }
 
-// Sum over a block of 1024 threads in a fixed order; valid in every thread.
-__device__ __forceinline__ float block_total(float v) {
-  __shared__ float sh[16];
-  v = lanes_sum<64>(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float t = 0.f;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) t += sh[k];
-  return t;
-}
+// Count, mean and sum of squared deviations from it; joined with those of
+// other values by the update that needs no difference of large squares
+// (Chan, Golub and LeVeque 1979).
+struct Moments {
+  float n, mu, m2;
+  __device__ __forceinline__ void join(float nb, float mb, float qb) {
+    const float t = n + nb, share = t > 0.f ? nb * __builtin_amdgcn_rcpf(t) : 0.f, d = mb - mu;
+    mu += d * share;
+    m2 += qb + d * d * (n * share);
+    n = t;
+  }
+};
 
-// Rows too long for registers: one block per row, which is read once for the
-// mean, once for the squared deviations from it and once for the result.
-template <typename T, typename TW>
-__global__ __launch_bounds__(1024) void k_norm_long(const T* X, int64_t xs, const TW* gamma,
+// Rows too long for registers.  A block takes the moments of the whole row in
+// one read, 32 entries a thread and step, and then writes its share of the row
+// from a second read that comes from a cache.  gridDim.y blocks share a row
+// where there are few: each takes the moments for itself, which costs no more
+// time than one of them would (one CU's bandwidth), and no workspace.  Float32
+// 2048 x 40000: 161 us (4.1 TB/s; 170 with 1024 threads, 195 with 256), 16 x
+// 2^20: 73 us, one row of 2^20: 47 us (44 and 81).
+constexpr int kLongThreads = 512;
+template <typename T, typename TW, int V>
+__global__ __launch_bounds__(kLongThreads) void k_norm_long(const T* X, int64_t xs, const TW* gamma,
                                                     const TW* beta, int64_t rows, int cols,
                                                     float eps, T* Y, float* mean, float* rstd) {
+  constexpr int U = 32 / V, U2 = 16 / V, STEP = kLongThreads * V;
+  __shared__ Moments sh[2][kLongThreads / 64];       // by turns, as in group_sums
+  const int lane = threadIdx.x & 63;
+  const int64_t pieces = (cols + V - 1) / V;
+  const int p0 = (int)(pieces * blockIdx.y / gridDim.y);
+  const int p1 = (int)(pieces * (blockIdx.y + 1) / gridDim.y);
+  int turn = 0;
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* x = X + r * xs;
     T* y = Y + r * cols;
-    float s = 0.f;
-    for (int c = threadIdx.x; c < cols; c += 1024) s += to_f32(x[c]);
-    const float mu = block_total(s) / cols;
-    float q = 0.f;
-    for (int c = threadIdx.x; c < cols; c += 1024) {
-      const float d = to_f32(x[c]) - mu;
-      q += d * d;
+    Moments all = {0.f, 0.f, 0.f};
+    for (int c = threadIdx.x * V; c < cols; c += U * STEP) {
+      Piece<T, V> in[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) in[u].load(x + Place<V>(c + u * STEP, cols).c);
+      float s = 0.f, q = 0.f;
+      if (c + (U - 1) * STEP + V <= cols) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < V; ++k) s += in[u][k];
+        const float mb = s * (1.f / (U * V));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < V; ++k) q += (in[u][k] - mb) * (in[u][k] - mb);
+        all.join(U * V, mb, q);
+      } else {
+        int own = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int skip = Place<V>(c + u * STEP, cols).skip;
+          own += V - skip;
+#pragma unroll
+          for (int k = 0; k < V; ++k) s += k >= skip ? in[u][k] : 0.f;
+        }
+        const float mb = s / own;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int skip = Place<V>(c + u * STEP, cols).skip;
+#pragma unroll
+          for (int k = 0; k < V; ++k) q += k >= skip ? (in[u][k] - mb) * (in[u][k] - mb) : 0.f;
+        }
+        all.join(own, mb, q);
+      }
     }
-    const float rs = 1.0f / sqrtf(block_total(q) / cols + eps);
-    for (int c = threadIdx.x; c < cols; c += 1024)
-      put(y + c, (to_f32(x[c]) - mu) * rs * (gamma ? to_f32(gamma[c]) : 1.f) +
-                     (beta ? to_f32(beta[c]) : 0.f));
-    if (threadIdx.x == 0) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1)
+      all.join(__shfl_xor(all.n, o), __shfl_xor(all.mu, o), __shfl_xor(all.m2, o));
+    if (lane == 0) sh[turn][threadIdx.x >> 6] = all;
+    __syncthreads();
+    all = sh[turn][0];
+#pragma unroll
+    for (int j = 1; j < kLongThreads / 64; ++j) all.join(sh[turn][j].n, sh[turn][j].mu, sh[turn][j].m2);
+    turn ^= 1;
+    const float mu = all.mu, rs = 1.0f / sqrtf(all.m2 / cols + eps);
+    for (int p = p0 + threadIdx.x; p < p1; p += U2 * kLongThreads) {
+      Piece<T, V> in[U2];
+      Piece<TW, V> g[U2], b[U2];
+#pragma unroll
+      for (int u = 0; u < U2; ++u) {
+        const int c = Place<V>((p + u * kLongThreads) * V, cols).c;
+        in[u].load(x + c);
+        if (gamma) g[u].load(gamma + c);
+        if (beta) b[u].load(beta + c);
+      }
+#pragma unroll
+      for (int u = 0; u < U2; ++u) {
+        const Place<V> at((p + u * kLongThreads) * V, cols);
+        float v[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          v[k] = (in[u][k] - mu) * rs * (gamma ? g[u][k] : 1.f) + (beta ? b[u][k] : 0.f);
+        store_own<V>(y + at.c, p + u * kLongThreads < p1 ? at.skip : V, v);
+      }
+    }
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
     }
@@ -148,7 +218,9 @@ __global__ __launch_bounds__(1024) void k_norm_long(const T* X, int64_t xs, cons
 // Backward.  One pass over dY and X: a block takes every gridDim-th set of
 // rows, writes their dX, and adds dY * xhat and dY of its columns up in
 // registers; its groups' sums meet in LDS at the end, and k_norm_join adds the
-// blocks' (part[block][2][cols]).
+// blocks' (part[block][2][cols]).  16384 x 4096 bfloat16 takes 73 + 5 us (5.5
+// TB/s), 12288 x 768 15 + 4 us: three rows a wave, one after the other, since
+// registers for a next row are not there.
 // ---------------------------------------------------------------------------
 // One row of the backward pass: g = dY gamma, xhat, and the lane's shares of
 // the sums of g and g xhat; `each` sees every entry's dY and xhat.  Contraction
@@ -271,61 +343,126 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
   }
 }
 
-// dX of rows too long for registers.
-template <typename T, typename TW>
-__global__ __launch_bounds__(1024) void k_norm_grad_long(
+// Rows too long for registers.  A first launch reads dY and X once: a wave
+// takes kLongCols columns of a run of rows, keeps their column sums in
+// registers (part[run][2][cols]) and leaves each row's shares of the sums of g
+// and g xhat in share[row][wave].  A second one adds a row's shares, reads dY
+// and X again and writes dX.  Bound by HBM: 2048 x 40000 in 312 us (float32,
+// 5 passes over 328 MB at 5.3 TB/s) and 170 us (bfloat16).
+constexpr int kLongCols = 512;
+
+template <typename T, typename TW, int V>
+__global__ __launch_bounds__(256) void k_norm_long_sums(
     const T* dY, int64_t dys, const T* X, int64_t xs, const TW* gamma, const float* mean,
-    const float* rstd, int64_t rows, int cols, T* dX) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const T* x = X + r * xs;
-    const T* dy = dY + r * dys;
-    T* dx = dX + r * cols;
-    const float mu = mean[r], rs = rstd[r];
-    float s1 = 0.f, s2 = 0.f;
-    for (int c = threadIdx.x; c < cols; c += 1024) {
-      const float g = to_f32(dy[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
-      s1 += g;
-      s2 += g * ((to_f32(x[c]) - mu) * rs);
+    const float* rstd, int64_t rows, int cols, int64_t run, float* part, float2* share) {
+  constexpr int NV = kLongCols / (64 * V), R = 4;      // R rows in flight
+  const int lane = threadIdx.x & 63;
+  const int waves = (cols + kLongCols - 1) / kLongCols;
+  const int w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (w >= waves) return;
+  int c[NV], skip[NV];
+  Piece<TW, V> wg[NV];
+  float ag[NV][V], ab[NV][V];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const Place<V> at(w * kLongCols + (j * 64 + lane) * V, cols);
+    c[j] = at.c;
+    skip[j] = at.skip;
+    if (gamma) wg[j].load(gamma + at.c);
+#pragma unroll
+    for (int k = 0; k < V; ++k) ag[j][k] = ab[j][k] = 0.f;
+  }
+  const int64_t r0 = blockIdx.y * run, r1 = r0 + run < rows ? r0 + run : rows;
+  for (int64_t r = r0; r < r1; r += R) {
+    Piece<T, V> pd[R][NV], px[R][NV];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t at = r + i < r1 ? r + i : r;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        pd[i][j].load(dY + at * dys + c[j]);
+        px[i][j].load(X + at * xs + c[j]);
+      }
     }
-    const float c1 = block_total(s1) / cols, c2 = block_total(s2) / cols;
-    for (int c = threadIdx.x; c < cols; c += 1024) {
-      const float g = to_f32(dy[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
-      const float xh = (to_f32(x[c]) - mu) * rs;
-      put(dx + c, rs * (g - c1 - xh * c2));
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (r + i >= r1) break;
+      const float mu = mean[r + i], rs = rstd[r + i];
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const bool own = k >= skip[j];
+          const float dy = own ? pd[i][j][k] : 0.f;
+          const float xh = own ? (px[i][j][k] - mu) * rs : 0.f;
+          ag[j][k] += dy * xh;
+          ab[j][k] += dy;
+          const float g = gamma ? dy * wg[j][k] : dy;
+          s1 += g;
+          s2 += g * xh;
+        }
+      if (share) {
+        s1 = lanes_sum<64>(s1);
+        s2 = lanes_sum<64>(s2);
+        if (lane == 0) share[(r + i) * waves + w] = make_float2(s1, s2);
+      }
     }
+  }
+  if (!part) return;
+  float* out = part + (int64_t)blockIdx.y * 2 * cols;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    store_own<V>(out + c[j], skip[j], ag[j]);
+    store_own<V>(out + cols + c[j], skip[j], ab[j]);
   }
 }
 
-// Column sums of dY * xhat and of dY over one run of such rows: 64 columns by
-// 4 row lanes a block, to part[run][2][cols].
-template <typename T>
-__global__ __launch_bounds__(256) void k_norm_cols(const T* dY, int64_t dys, const T* X,
-                                                   int64_t xs, const float* mean,
-                                                   const float* rstd, int64_t rows, int cols,
-                                                   int64_t run, float* part) {
-  __shared__ float sh[2][4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  const int64_t r0 = (int64_t)blockIdx.y * run;
-  const int64_t r1 = r0 + run < rows ? r0 + run : rows;
-  float sg = 0.f, sb = 0.f;
-  if (c < cols)
-    for (int64_t r = r0 + w; r < r1; r += 4) {
-      const float dy = to_f32(dY[r * dys + c]);
-      sg += dy * ((to_f32(X[r * xs + c]) - mean[r]) * rstd[r]);
-      sb += dy;
+template <typename T, typename TW, int V>
+__global__ __launch_bounds__(256) void k_norm_grad_long(
+    const T* dY, int64_t dys, const T* X, int64_t xs, const TW* gamma, const float* mean,
+    const float* rstd, int64_t rows, int cols, const float2* share, T* dX) {
+  constexpr int U = 16 / V;
+  const int lane = threadIdx.x & 63;
+  const int waves = (cols + kLongCols - 1) / kLongCols;
+  const int c0 = (blockIdx.x * U * 256 + threadIdx.x) * V;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    Piece<T, V> pd[U], px[U];
+    Piece<TW, V> wg[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = Place<V>(c0 + u * 256 * V, cols).c;
+      pd[u].load(dY + r * dys + c);
+      px[u].load(X + r * xs + c);
+      if (gamma) wg[u].load(gamma + c);
     }
-  sh[0][w][lane] = sg;
-  sh[1][w][lane] = sb;
-  __syncthreads();
-  if (w < 2 && c < cols)
-    part[((int64_t)blockIdx.y * 2 + w) * cols + c] =
-        ((sh[w][0][lane] + sh[w][1][lane]) + sh[w][2][lane]) + sh[w][3][lane];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll 4
+    for (int k = lane; k < waves; k += 64) {
+      const float2 v = share[r * waves + k];
+      s1 += v.x;
+      s2 += v.y;
+    }
+    const float c1 = lanes_sum<64>(s1) / cols, c2 = lanes_sum<64>(s2) / cols;
+    const float mu = mean[r], rs = rstd[r];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Place<V> at(c0 + u * 256 * V, cols);
+      float v[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float g = gamma ? pd[u][k] * wg[u][k] : pd[u][k];
+        v[k] = rs * (g - c1 - (px[u][k] - mu) * rs * c2);
+      }
+      store_own<V>(dX + r * cols + at.c, at.skip, v);
+    }
+  }
 }
 
 // Few rows, in one launch: the first row_blocks blocks write dX as k_norm_grad
 // does, the others take 16 columns each, by 32 lanes over the rows, and write
 // dgamma and dbeta.  dY and X are read twice, the second time from the cache.
+// Bound by its launch: 333 x 1001 float32 takes 3.6 us.
 // (Where dX is dY the two kinds of blocks go in two launches.)
 template <typename T, typename TW, typename TO, int V, int LANES, int NV>
 __global__ __launch_bounds__(LANES > 512 ? LANES : 512) void k_norm_grad_few(
@@ -413,6 +550,20 @@ __global__ __launch_bounds__(1024) void k_norm_join(const float* part, int block
   }
 }
 
+// The same for few blocks (of few long rows): a thread a column.  One row of
+// 2^20: 23 us in all, 115 with 32 lanes a column.
+template <typename TO>
+__global__ __launch_bounds__(256) void k_norm_join_few(const float* part, int blocks, int cols,
+                                                       TO* dgamma, TO* dbeta, int accumulate) {
+  TO* out = blockIdx.y ? dbeta : dgamma;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (!out || c >= cols) return;
+  float s = 0.f;
+#pragma unroll 4
+  for (int b = 0; b < blocks; ++b) s += part[((int64_t)b * 2 + blockIdx.y) * cols + c];
+  put(out + c, accumulate ? to_f32(out[c]) + s : s);
+}
+
 namespace {
 
 constexpr int64_t kMaxBlocks = 1 << 16;   // larger grids loop
@@ -425,14 +576,17 @@ int vec_of(int32_t dtype) { return dtype == SM_BF16 ? 8 : 4; }
 //
 // Forward: up to 4 pieces a thread, in as few threads as hold the row, so that
 // few of them idle past its end: 12288 x 768 bfloat16 takes 9.1 us with 32 x 3
-// pieces, 10.6 us with 64 x 2 (a quarter idle) and 12.7 us with 128 x 1.
+// pieces, 10.6 us with 64 x 2 (a quarter idle) and 12.7 us with 128 x 1.  Four
+// pieces of bfloat16 in 1024 threads need more than their 128 registers: 2048 x
+// 24576 takes 46 us from registers and 52 in k_norm_long, 2048 x 25000 83 and
+// 54.
 int norm_lanes(int64_t cols, int32_t dtype) {
   const int vec = vec_of(dtype);
   for (int lanes : {8, 16, 32})
     if (cols <= lanes * vec) return lanes;
   if (vec == 8 && cols <= 32 * 8 * 4) return 32;
   for (int lanes : {64, 128, 256, 512, 1024})
-    if (cols <= (int64_t)lanes * vec * 4) return lanes;
+    if (cols <= (int64_t)lanes * vec * (lanes == 1024 && vec == 8 ? 3 : 4)) return lanes;
   return 0;
 }
 // Backward: a thread holds five values an entry.  16 entries a thread leave
@@ -453,9 +607,29 @@ int grad_lanes(int64_t cols, int32_t dtype) {
 // Blocks whose partial sums k_norm_join adds.
 int64_t grad_blocks(int64_t rows, int64_t cols, int32_t dtype) {
   const int lanes = grad_lanes(cols, dtype);
-  if (lanes == 0) return std::min<int64_t>((rows + 63) / 64, 64);
+  if (lanes == 0)     // runs of rows: 16 waves a CU, at least 8 rows a wave
+    return std::min((rows + 7) / 8, std::max<int64_t>(1, 4096 * kLongCols / cols));
   const int groups = lanes > 512 ? 1 : 512 / lanes;
   return std::min<int64_t>((rows + groups - 1) / groups, lanes > 512 ? 256 : kGradBlocks);
+}
+
+// Calls f with the number of pieces a thread as a constant, between LEAST and
+// MOST, which are all that norm_lanes and grad_lanes leave for a group's width.
+template <int LEAST, int MOST, typename F>
+void with_pieces(int64_t nv, const F& f) {
+  if constexpr (LEAST < MOST)
+    if (nv > LEAST) return with_pieces<LEAST + 1, MOST>(nv, f);
+  f(std::integral_constant<int, LEAST>());
+}
+template <int V, int LANES>
+struct GradPieces {
+  static constexpr int kLeast = LANES == 64 || V == 8 ? 1 : 2;
+  static constexpr int kMost = LANES == 64 ? 2 : LANES == 1024 ? (V == 8 ? 2 : 4) : kLeast;
+};
+
+// Workspace: the blocks' column sums, and for long rows the rows' shares.
+size_t column_bytes(int64_t blocks, int64_t cols) {
+  return ((size_t)blocks * 2 * cols * 4 + 255) / 256 * 256;
 }
 
 template <typename T, typename TW, int V, int LANES, int NV>
@@ -474,12 +648,11 @@ template <typename T, typename TW, int LANES>
 void norm_pieces(const NormArgs& a, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   const int64_t per = (int64_t)LANES * V;
-  switch ((a.cols + per - 1) / per) {
-    case 1: return norm_go<T, TW, V, LANES, 1>(a, s);
-    case 2: return norm_go<T, TW, V, LANES, 2>(a, s);
-    case 3: return norm_go<T, TW, V, LANES, 3>(a, s);
-    default: return norm_go<T, TW, V, LANES, 4>(a, s);
-  }
+  constexpr int LEAST = LANES == 32 ? 2 : LANES == 64 && V == 4 ? 1 : 3;
+  constexpr int MOST = LANES == 1024 && V == 8 ? 3 : 4;
+  with_pieces<LEAST, MOST>((a.cols + per - 1) / per, [&](auto nv) {
+    norm_go<T, TW, V, LANES, decltype(nv)::value>(a, s);
+  });
 }
 
 template <typename T, typename TW>
@@ -491,16 +664,24 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
       else norm_go<T, TW, V, 8, 1>(a, s);
       break;
     case 16: norm_go<T, TW, V, 16, 1>(a, s); break;
-    case 32: norm_pieces<T, TW, 32>(a, s); break;
+    case 32:
+      if (a.cols <= 32 * V) norm_go<T, TW, V, 32, 1>(a, s);
+      else if constexpr (V == 8) norm_pieces<T, TW, 32>(a, s);
+      break;
     case 64: norm_pieces<T, TW, 64>(a, s); break;
     case 128: norm_pieces<T, TW, 128>(a, s); break;
     case 256: norm_pieces<T, TW, 256>(a, s); break;
     case 512: norm_pieces<T, TW, 512>(a, s); break;
     case 1024: norm_pieces<T, TW, 1024>(a, s); break;
-    default:
-      hipLaunchKernelGGL((k_norm_long<T, TW>), dim3((unsigned)std::min(a.rows, kMaxBlocks)),
-                         dim3(1024), 0, s, (const T*)a.X, a.x_stride, (const TW*)a.gamma,
+    default: {
+      // blocks that share a row; in place they would read what others wrote
+      const int64_t share =
+          a.X == a.Y ? 1 : std::max<int64_t>(1, std::min(256 / a.rows, a.cols / 8192));
+      hipLaunchKernelGGL((k_norm_long<T, TW, V>),
+                         dim3((unsigned)std::min(a.rows, kMaxBlocks), (unsigned)share),
+                         dim3(kLongThreads), 0, s, (const T*)a.X, a.x_stride, (const TW*)a.gamma,
                          (const TW*)a.beta, a.rows, (int)a.cols, a.eps, (T*)a.Y, a.mean, a.rstd);
+    }
   }
   return hipGetLastError();
 }
@@ -519,13 +700,10 @@ template <typename T, typename TW, int LANES>
 void norm_grad_pieces(const NormGradArgs& a, int64_t grid, float* part, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   const int64_t per = (int64_t)LANES * V;
-  const int64_t nv = (a.cols + per - 1) / per;
-  if (nv == 1) return norm_grad_go<T, TW, V, LANES, 1>(a, grid, part, s);
-  if (nv == 2) return norm_grad_go<T, TW, V, LANES, 2>(a, grid, part, s);
-  if constexpr (V == 4 && LANES == 1024) {
-    if (nv == 3) return norm_grad_go<T, TW, V, LANES, 3>(a, grid, part, s);
-    return norm_grad_go<T, TW, V, LANES, 4>(a, grid, part, s);
-  }
+  with_pieces<GradPieces<V, LANES>::kLeast, GradPieces<V, LANES>::kMost>(
+      (a.cols + per - 1) / per, [&](auto nv) {
+        norm_grad_go<T, TW, V, LANES, decltype(nv)::value>(a, grid, part, s);
+      });
 }
 
 template <typename T, typename TW, typename TO, int V, int LANES, int NV>
@@ -553,13 +731,10 @@ template <typename T, typename TW, typename TO, int LANES>
 void norm_grad_few_pieces(const NormGradArgs& a, hipStream_t s) {
   constexpr int V = 16 / (int)sizeof(T);
   const int64_t per = (int64_t)LANES * V;
-  const int64_t nv = (a.cols + per - 1) / per;
-  if (nv == 1) return norm_grad_few_go<T, TW, TO, V, LANES, 1>(a, s);
-  if (nv == 2) return norm_grad_few_go<T, TW, TO, V, LANES, 2>(a, s);
-  if constexpr (V == 4 && LANES == 1024) {
-    if (nv == 3) return norm_grad_few_go<T, TW, TO, V, LANES, 3>(a, s);
-    return norm_grad_few_go<T, TW, TO, V, LANES, 4>(a, s);
-  }
+  with_pieces<GradPieces<V, LANES>::kLeast, GradPieces<V, LANES>::kMost>(
+      (a.cols + per - 1) / per, [&](auto nv) {
+        norm_grad_few_go<T, TW, TO, V, LANES, decltype(nv)::value>(a, s);
+      });
 }
 
 template <typename T, typename TW, typename TO>
@@ -573,7 +748,9 @@ hipError_t norm_grad_few(const NormGradArgs& a, hipStream_t s) {
     case 16: norm_grad_few_go<T, TW, TO, V, 16, 1>(a, s); break;
     case 32: norm_grad_few_go<T, TW, TO, V, 32, 1>(a, s); break;
     case 64: norm_grad_few_pieces<T, TW, TO, 64>(a, s); break;
-    case 128: norm_grad_few_pieces<T, TW, TO, 128>(a, s); break;
+    case 128:       // bfloat16 goes from 64 to 256
+      if constexpr (V == 4) norm_grad_few_pieces<T, TW, TO, 128>(a, s);
+      break;
     case 256: norm_grad_few_pieces<T, TW, TO, 256>(a, s); break;
     case 512: norm_grad_few_pieces<T, TW, TO, 512>(a, s); break;
     default: norm_grad_few_pieces<T, TW, TO, 1024>(a, s); break;
@@ -590,6 +767,12 @@ bool few(int64_t rows, int64_t cols) {
 
 template <typename TO>
 hipError_t norm_join(const NormGradArgs& a, const float* part, int64_t blocks, hipStream_t s) {
+  if (blocks <= 16) {
+    hipLaunchKernelGGL((k_norm_join_few<TO>), dim3((unsigned)((a.cols + 255) / 256), 2), dim3(256),
+                       0, s, part, (int)blocks, (int)a.cols, (TO*)a.dgamma, (TO*)a.dbeta,
+                       a.accumulate);
+    return hipGetLastError();
+  }
   const bool wide = a.cols > 2048;
   const int c = wide ? 32 : 16;
   hipLaunchKernelGGL((wide ? k_norm_join<TO, 32> : k_norm_join<TO, 16>),
@@ -617,26 +800,30 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
       case 16: norm_grad_go<T, TW, V, 16, 1>(a, blocks, part, s); break;
       case 32: norm_grad_go<T, TW, V, 32, 1>(a, blocks, part, s); break;
       case 64: norm_grad_pieces<T, TW, 64>(a, blocks, part, s); break;
-      case 128: norm_grad_pieces<T, TW, 128>(a, blocks, part, s); break;
+      case 128:     // bfloat16 goes from 64 to 256
+        if constexpr (V == 4) norm_grad_pieces<T, TW, 128>(a, blocks, part, s);
+        break;
       case 256: norm_grad_pieces<T, TW, 256>(a, blocks, part, s); break;
       case 512: norm_grad_pieces<T, TW, 512>(a, blocks, part, s); break;
       case 1024: norm_grad_pieces<T, TW, 1024>(a, blocks, part, s); break;
       default:
-        // the column sums first: dX may be dY
-        if (sums) {
-          const int64_t run = (a.rows + blocks - 1) / blocks;
-          hipLaunchKernelGGL((k_norm_cols<T>),
-                             dim3((unsigned)((a.cols + 63) / 64), (unsigned)blocks), dim3(256),
-                             0, s, (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride,
-                             a.mean, a.rstd, a.rows, (int)a.cols, run, part);
-          if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+        // all of dY is read before dX, which may be dY, is written
+        const int64_t run = (a.rows + blocks - 1) / blocks;
+        float2* share = a.dX ? (float2*)((char*)a.ws + column_bytes(blocks, a.cols)) : nullptr;
+        hipLaunchKernelGGL((k_norm_long_sums<T, TW, V>),
+                           dim3((unsigned)((a.cols + 4 * kLongCols - 1) / (4 * kLongCols)),
+                                (unsigned)blocks),
+                           dim3(256), 0, s, (const T*)a.dY, a.dy_stride, (const T*)a.X,
+                           a.x_stride, (const TW*)a.gamma, a.mean, a.rstd, a.rows, (int)a.cols,
+                           run, part, share);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
         if (a.dX)
-          hipLaunchKernelGGL((k_norm_grad_long<T, TW>),
-                             dim3((unsigned)std::min(a.rows, kMaxBlocks)), dim3(1024), 0, s,
-                             (const T*)a.dY, a.dy_stride, (const T*)a.X, a.x_stride,
-                             (const TW*)a.gamma, a.mean, a.rstd, a.rows, (int)a.cols,
-                             (T*)a.dX);
+          hipLaunchKernelGGL((k_norm_grad_long<T, TW, V>),
+                             dim3((unsigned)((a.cols + 4095) / 4096),
+                                  (unsigned)std::min<int64_t>(a.rows, 65535)),
+                             dim3(256), 0, s, (const T*)a.dY, a.dy_stride, (const T*)a.X,
+                             a.x_stride, (const TW*)a.gamma, a.mean, a.rstd, a.rows, (int)a.cols,
+                             share, (T*)a.dX);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
@@ -652,7 +839,8 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
 size_t norm_grad_workspace(int64_t rows, int64_t cols) {
   if (few(rows, cols)) return 0;
   const int64_t blocks = std::max(grad_blocks(rows, cols, SM_F32), grad_blocks(rows, cols, SM_BF16));
-  return ((size_t)blocks * 2 * cols * 4 + 255) / 256 * 256;
+  const int64_t waves = (cols + kLongCols - 1) / kLongCols;
+  return column_bytes(blocks, cols) + (grad_lanes(cols, SM_F32) ? 0 : (size_t)(rows * waves) * 8);
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {

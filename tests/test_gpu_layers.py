@@ -805,3 +805,53 @@ def test_embedding_backward_of_the_longest_batch():
     want = np.bincount(np.arange(n // 8) % vocab, minlength=vocab).astype(np.float64)
     want[1234] += n - n // 8
     assert np.array_equal(got, want.astype(np.float32))
+
+
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(1, 65536), (1, 65537), (3, 131071), (5, 40003), (100, 32769),
+                                       (260, 33000), (31, 24577), (9, 16391), (2, 1 << 20)])
+def test_norm_long_rows(rows, cols, x_dtype):
+    """Rows past the registers: few, which blocks share, and many; strided,
+    misaligned and in place; each gradient alone."""
+    print(f"norm long rows {rows}x{cols} {x_dtype}", flush=True)
+    rng = np.random.default_rng(rows + cols)
+    x, dy = values(rng, (rows, cols), x_dtype, 1.5, 20.0), values(rng, (rows, cols), x_dtype)
+    g, b = values(rng, cols, "f32", 0.3, 1.0), values(rng, cols, "f32", 0.3)
+    wide = torch.full((rows, cols + 9), float("nan"), device="cuda", dtype=DT[x_dtype])
+    wide[:, 1:cols + 1] = dev(x, x_dtype)
+    X, DY, G, BB = dev(x, x_dtype), dev(dy, x_dtype), dev(g), dev(b)
+    y, m, r = B.layer_norm(X, G, BB, EPS, want_stats=True)
+    for a, w, e, name in zip((y, m, r), R.norm(x, g, b, EPS), R.norm_bounds(x, g, b, EPS, x_dtype),
+                             ("y", "mean", "rstd")):
+        within(host(a), w, e, name)
+    assert torch.equal(bits(B.layer_norm(wide[:, 1:cols + 1], G, BB, EPS)), bits(y))
+    same = X.clone()
+    assert torch.equal(bits(B.layer_norm(same, G, BB, EPS, Y=same)), bits(y))
+    got = B.layer_norm_backward(DY, X, G, m, r)
+    for a, w, e, name in zip(got, R.norm_grad(dy, x, g, host(m), host(r)),
+                             R.norm_grad_bounds(dy, x, g, host(m), host(r), x_dtype, "f32"),
+                             ("dx", "dgamma", "dbeta")):
+        within(host(a), w, e, name)
+    for k in range(3):
+        one = B.layer_norm_backward(DY, wide[:, 1:cols + 1], G, m, r, want_x=k == 0,
+                                    want_weight=k == 1, want_bias=k == 2)
+        assert torch.equal(bits(one[k]), bits(got[k]))
+    inplace = B.layer_norm_backward(DY, X, G, m, r, dX=DY)
+    for a, c in zip(got, inplace):
+        assert torch.equal(bits(a), bits(c))
+
+
+def test_norm_long_rows_of_unlike_parts():
+    """Rows whose start says nothing of the rest: a step from 0 to 1000, a
+    ramp, and one large entry among small ones."""
+    cols = 50000
+    x = np.zeros((3, cols), np.float32)
+    x[0, 7:] = 1000.0
+    x[0] += np.sin(np.arange(cols, dtype=np.float32))
+    x[1] = np.arange(cols, dtype=np.float32)
+    x[2] = np.cos(np.arange(cols, dtype=np.float32))
+    x[2, 31] = 1e4
+    y, m, r = B.layer_norm(dev(x), None, None, EPS, want_stats=True)
+    for a, w, e, name in zip((y, m, r), R.norm(x, None, None, EPS),
+                             R.norm_bounds(x, None, None, EPS, "f32"), ("y", "mean", "rstd")):
+        within(host(a), w, e, name)
