@@ -758,11 +758,13 @@ hipError_t norm_grad_few(const NormGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Whether k_norm_grad_few serves these rows: 333 x 1001 float32 takes 14.0 us
-// with it and 17.2 us in two launches, 512 x 4096 alone 32 against 39 us, but
-// 512 x 16384 61 against 57 us and 2048 x 768 36 against 32 us.
+// Whether k_norm_grad_few serves these rows.  Kernels alone, against the two
+// launches: 1500 x 57 5.3 against 5.4 + 2.5 us, 2048 x 768 10.7 (float32 13.4)
+// against 5.9 + 3.3 (6.8 + 3.5), 2048 x 2000 14.7 (18.0) against 13.7 + 4.5
+// (13.0 + 4.4); the launch that it saves is 4 us of host time.  4000 x 57: 11
+// against 4.4 + 3.5, 512 x 16384 in a loop of calls 61 against 57.
 bool few(int64_t rows, int64_t cols) {
-  return rows > 0 && rows <= 1024 && rows * cols <= ((int64_t)1 << 22) && cols <= 16384;
+  return rows > 0 && rows <= 2048 && rows * cols <= ((int64_t)1 << 22) && cols <= 16384;
 }
 
 template <typename TO>

@@ -855,3 +855,11 @@ def test_norm_long_rows_of_unlike_parts():
     for a, w, e, name in zip((y, m, r), R.norm(x, None, None, EPS),
                              R.norm_bounds(x, None, None, EPS, "f32"), ("y", "mean", "rstd")):
         within(host(a), w, e, name)
+
+
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(r, c) for r in (2048, 2049) for c in
+                                       (1, 3, 4, 7, 8, 31, 33, 63, 65, 129, 257, 513, 767, 1001,
+                                        1025)] + [(2048, 2047), (2048, 2049), (1025, 4071)])
+def test_norm_backward_at_the_last_row_of_one_launch(rows, cols, x_dtype):
+    test_norm_backward_large(rows, cols, x_dtype)
