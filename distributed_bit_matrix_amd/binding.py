@@ -403,7 +403,7 @@ def _workspace(ws, nbytes, like, dev):
     if nbytes == 0:
         return None, None, 0
     if ws is None:
-        ws = like.new_empty(nbytes, dtype=torch.uint8)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     elif not ws.is_contiguous():
         raise TypeError("ws must be contiguous")
     elif ws.get_device() != dev:
@@ -439,7 +439,9 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, want_stats: bool = 
     if mean is not None:
         _check_arg(mean, X.shape[:-1], torch.float32, dev, "mean")
     elif want_stats:
-        mean = X.new_empty(X.shape[:-1], dtype=torch.float32)
+        mean = torch.empty(rows, dtype=torch.float32, device=X.device)
+        if X.dim() != 2:
+            mean = mean.view(X.shape[:-1])
     if rstd is not None:
         _check_arg(rstd, X.shape[:-1], torch.float32, dev, "rstd")
     elif want_stats:
@@ -501,13 +503,13 @@ def layer_norm_backward(dY, X, weight, mean, rstd, want_x: bool = True, want_wei
     dwd = SM_F32
     if want_weight:
         if dweight is None:
-            dweight = X.new_empty(cols, dtype=dtype)
+            dweight = torch.empty(cols, dtype=dtype, device=X.device)
         else:
             _check_arg(dweight, (cols,), dtype, dev, "dweight")
         dwd = _code(dweight.dtype, "dweight")
     if want_bias:
         if dbias is None:
-            dbias = X.new_empty(cols, dtype=dtype)
+            dbias = torch.empty(cols, dtype=dtype, device=X.device)
         else:
             _check_arg(dbias, (cols,), dtype, dev, "dbias")
         dwd = _code(dbias.dtype, "dbias")
@@ -535,6 +537,7 @@ def _token_bits(t) -> int:
 def embedding(tokens, weight, scale: float = 1.0, out=None, out_dtype=None, stream=None):
     """scale * weight[tokens], of shape tokens.shape + (dim,), in out_dtype
     (default: weight's).  A token outside the table makes its row NaN."""
+    import torch
     dev = _here(tokens, stream)
     if dev < 0:
         with _placed(tokens, stream):
@@ -548,7 +551,8 @@ def embedding(tokens, weight, scale: float = 1.0, out=None, out_dtype=None, stre
     vocab, dim = shape
     wd = _code(weight.dtype, "weight")
     if out is None:
-        out = weight.new_empty(tokens.shape + (dim,), dtype=out_dtype)
+        out = torch.empty(*tokens.shape, dim, dtype=out_dtype or weight.dtype,
+                          device=weight.device)
     else:
         _check_arg(out, tokens.shape + (dim,), out_dtype or out.dtype, dev, "out")
     _check("signmuon_embedding", lib().signmuon_embedding(
@@ -587,7 +591,7 @@ def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Opti
     if dW is None:
         if accumulate:
             raise ValueError("accumulate needs the dW to add to")
-        dW = dY.new_empty((vocab, dim), dtype=dtype or torch.float32)
+        dW = torch.empty(vocab, dim, dtype=dtype or torch.float32, device=dY.device)
     else:
         _check_arg(dW, (vocab, dim), dtype or dW.dtype, dev, "dW")
     ws, wsp, nbytes = _workspace(ws, embedding_backward_workspace(n, vocab, dim), dY, dev)
