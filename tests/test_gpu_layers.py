@@ -863,3 +863,90 @@ def test_norm_long_rows_of_unlike_parts():
                                         1025)] + [(2048, 2047), (2048, 2049), (1025, 4071)])
 def test_norm_backward_at_the_last_row_of_one_launch(rows, cols, x_dtype):
     test_norm_backward_large(rows, cols, x_dtype)
+
+
+# every path of several launches: the sort and its sums, runs of a long batch,
+# runs past 16-bit places, and rows past the registers
+RUNS = [(5000, 90, 160), (70000, 300, 24), ((1 << 20) + 500, 40, 3), (60, 50, 20011)]
+
+
+@pytest.mark.parametrize("n,vocab,dim", RUNS)
+def test_several_launches_on_two_streams_at_once(n, vocab, dim):
+    print(f"two streams {n} {vocab}x{dim}", flush=True)
+    sets = [_batch(s, n, vocab, dim) for s in (21, 22)]
+    want = [_all(*b) for b in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(4):
+        for k in (0, 1):
+            got[k].append(_all(*sets[k], stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for o in got[k]:
+            for name in o:
+                assert torch.equal(o[name], want[k][name]), (k, name)
+
+
+@pytest.mark.parametrize("n,vocab,dim", RUNS)
+def test_graphs_of_several_launches_match_eager(n, vocab, dim):
+    """Replayed with changed inputs, eager work in between; the workspaces are
+    the graph's own and allocated in it."""
+    print(f"graph {n} {vocab}x{dim}", flush=True)
+    b = _batch(31, n, vocab, dim)
+    o = _all(*b)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        _all(*b, out=o)
+    for rep in range(3):
+        fresh = _batch(40 + rep, n, vocab, dim)
+        for old, new in zip(b, fresh):
+            old.copy_(new)
+        for t in o.values():
+            t.fill_(float("nan"))
+        want = _all(*fresh)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for name in want:
+            assert torch.equal(o[name], want[name]), (rep, name)
+
+
+def test_captured_layers_return_their_gradients():
+    """Forward and backward captured while an optimizer takes gradients
+    directly: the replays' gradients are returned, the step's are left alone."""
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    rng = np.random.default_rng(5)
+    w = torch.nn.Parameter(dev(values(rng, (64,), "f32", 0.3, 1.0)))
+    table = torch.nn.Parameter(dev(values(rng, (30, 64), "f32")))
+    opt = SO.SignMuon([w, table], scale="fro", K=1, direct_grads=True)
+    t = torch.arange(50, device="cuda") % 30
+    c = dev(values(rng, (50, 64), "f32"))
+
+    def run():
+        return torch.autograd.grad((L.layer_norm(L.embedding(t, table), w) * c).sum(), [w, table])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = run()
+    for rep in range(3):
+        c.copy_(dev(values(np.random.default_rng(60 + rep), (50, 64), "f32")))
+        g.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), rep
+        assert not _filled(w) and not _filled(table)
+    (L.layer_norm(L.embedding(t, table), w) * c).sum().backward()
+    assert _filled(w) and torch.equal(w._signmuon_slot.grad, want[0])
+    assert torch.equal(table._signmuon_slot.grad, want[1])
