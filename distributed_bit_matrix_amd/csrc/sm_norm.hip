@@ -219,8 +219,8 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const T* X, int64_t 
 // rows, writes their dX, and adds dY * xhat and dY of its columns up in
 // registers; its groups' sums meet in LDS at the end, and k_norm_join adds the
 // blocks' (part[block][2][cols]).  16384 x 4096 bfloat16 takes 73 + 5 us (5.5
-// TB/s), 12288 x 768 15 + 4 us: three rows a wave, one after the other, since
-// registers for a next row are not there.
+// TB/s), 12288 x 768 15 + 4 us: three rows a wave between the weights' load and
+// the groups' join.  Fetching the next row ahead costs more (16.8 us).
 // ---------------------------------------------------------------------------
 // One row of the backward pass: g = dY gamma, xhat, and the lane's shares of
 // the sums of g and g xhat; `each` sees every entry's dY and xhat.  Contraction
