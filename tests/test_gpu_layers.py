@@ -950,3 +950,42 @@ def test_captured_layers_return_their_gradients():
     (L.layer_norm(L.embedding(t, table), w) * c).sum().backward()
     assert _filled(w) and torch.equal(w._signmuon_slot.grad, want[0])
     assert torch.equal(table._signmuon_slot.grad, want[1])
+
+
+def test_direct_gradients_of_groups_added_and_of_saved_models():
+    """Two parameter groups, one added later; a model saved and loaded again
+    has ordinary gradients until an optimizer takes it."""
+    import io
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    rng = np.random.default_rng(14)
+    a, b = L.LayerNorm(40, device="cuda"), L.LayerNorm(40, bias=False, device="cuda")
+    x = dev(values(rng, (9, 40), "f32"))
+    c = dev(values(rng, (9, 40), "f32"))
+    want = torch.autograd.grad((b(a(x)) * c).sum(), [a.weight, a.bias, b.weight])
+    opt = SO.SignMuon(a.parameters(), scale="fro", K=1, direct_grads=True)
+    opt.add_param_group({"params": list(b.parameters()), "lr": 0.5})
+    (b(a(x)) * c).sum().backward()
+    # the added group moves at its first step, and takes what is in p.grad then
+    assert a.weight.grad is None and b.weight.grad is not None
+    opt.step()
+    assert torch.equal(opt._groups[0].G[:40], want[0])
+    assert torch.equal(opt._groups[1].G[:40], want[2])
+    opt.zero_grad(set_to_none=False)
+    now = torch.autograd.grad((b(a(x)) * c).sum(), [a.weight, a.bias, b.weight])
+    (b(a(x)) * c).sum().backward()
+    opt.step()
+    assert torch.equal(opt._groups[0].G[:40], now[0])
+    assert torch.equal(opt._groups[1].G[:40], now[2])
+    assert not opt.nonfinite()
+    f = io.BytesIO()
+    torch.save(a, f)
+    f.seek(0)
+    a2 = torch.load(f, weights_only=False)       # the file written above
+    assert torch.equal(a2.weight, a.weight)
+    (a2(x) * c).sum().backward()
+    assert a2.weight.grad is not None and not _filled(a.weight)
+    opt2 = SO.SignMuon(a2.parameters(), scale="fro", K=1, direct_grads=True)
+    opt2.zero_grad()
+    (a2(x) * c).sum().backward()
+    assert a2.weight.grad is None and _filled(a2.weight)

@@ -285,3 +285,15 @@ def test_parameters_with_a_slot_can_be_saved_and_copied():
     assert p._signmuon_slot.alive()
     del state
     assert not p._signmuon_slot.alive()
+
+
+def test_direct_gradients_need_parameters_on_a_gpu():
+    from distributed_bit_matrix_amd import optim as SO
+    p = torch.nn.Parameter(torch.zeros(4))
+    with pytest.raises(ValueError):
+        SO.SignMuon([p], direct_grads=True)
+    assert "_signmuon_slot" not in p.__dict__
+    opt = SO.SignMuon([p])              # without them, they may move later
+    opt.zero_grad()
+    with pytest.raises(ValueError):
+        opt.step()
