@@ -184,7 +184,8 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_long(const T* X, int64_t 
     __syncthreads();
     all = sh[turn][0];
 #pragma unroll
-    for (int j = 1; j < kLongThreads / 64; ++j) all.join(sh[turn][j].n, sh[turn][j].mu, sh[turn][j].m2);
+    for (int j = 1; j < kLongThreads / 64; ++j)
+      all.join(sh[turn][j].n, sh[turn][j].mu, sh[turn][j].m2);
     turn ^= 1;
     const float mu = all.mu, rs = 1.0f / sqrtf(all.m2 / cols + eps);
     for (int p = p0 + threadIdx.x; p < p1; p += U2 * kLongThreads) {
@@ -295,11 +296,11 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512, 4) void k_norm_grad(
     float rs = 0.f;
     if (live) {
       rs = rstd[r];
-      grad_row<V, LANES, NV, ONCE>(dY + r * dys, X + r * xs, w, gamma != nullptr, last, mean[r], rs, g,
-                             xh, s, [&](int j, int k, float dy, float x) {
-                               ag[j][k] = __builtin_fmaf(dy, x, ag[j][k]);
-                               ab[j][k] += dy;
-                             });
+      grad_row<V, LANES, NV, ONCE>(dY + r * dys, X + r * xs, w, gamma != nullptr, last, mean[r], rs,
+                                   g, xh, s, [&](int j, int k, float dy, float x) {
+                                     ag[j][k] = __builtin_fmaf(dy, x, ag[j][k]);
+                                     ab[j][k] += dy;
+                                   });
     }
     if (!dX) continue;
     group_sums<LANES, 2>(s, turn);
@@ -484,8 +485,8 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512) void k_norm_grad_few(
     const float rs = rstd[at], inv = 1.0f / cols;
     float s[2] = {0.f, 0.f};
     float g[NV][V], xh[NV][V];
-    grad_row<V, LANES, NV, false>(dY + at * dys, X + at * xs, w, gamma != nullptr, last, mean[at], rs, g,
-                           xh, s, [](int, int, float, float) {});
+    grad_row<V, LANES, NV, false>(dY + at * dys, X + at * xs, w, gamma != nullptr, last, mean[at],
+                                  rs, g, xh, s, [](int, int, float, float) {});
     group_sums<LANES, 2>(s, turn);
     if (r < rows)
       grad_store<V, LANES, NV>(dX + (int64_t)r * cols, last, rs, s[0] * inv, s[1] * inv, g, xh);
@@ -508,7 +509,8 @@ __global__ __launch_bounds__(LANES > 512 ? LANES : 512) void k_norm_grad_few(
   sh[1][y][x] = sb;
   __syncthreads();
   // 16 lanes a column and sum: a wave has 4 of the 32
-  const int l = threadIdx.x & 15, q = threadIdx.x >> 4, d = (blockIdx.x - row_blocks) * 16 + (q & 15);
+  const int l = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int d = (blockIdx.x - row_blocks) * 16 + (q & 15);
   if (q >= 32) return;
   TO* out = q < 16 ? dgamma : dbeta;
   float t = 0.f;
@@ -840,7 +842,8 @@ hipError_t norm_grad(const NormGradArgs& a, hipStream_t s) {
 
 size_t norm_grad_workspace(int64_t rows, int64_t cols) {
   if (few(rows, cols)) return 0;
-  const int64_t blocks = std::max(grad_blocks(rows, cols, SM_F32), grad_blocks(rows, cols, SM_BF16));
+  const int64_t blocks =
+      std::max(grad_blocks(rows, cols, SM_F32), grad_blocks(rows, cols, SM_BF16));
   const int64_t waves = (cols + kLongCols - 1) / kLongCols;
   return column_bytes(blocks, cols) + (grad_lanes(cols, SM_F32) ? 0 : (size_t)(rows * waves) * 8);
 }
