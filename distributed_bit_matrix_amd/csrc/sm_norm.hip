@@ -108,13 +108,14 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_norm(
 
 // Count, mean and sum of squared deviations from it; joined with those of
 // other values by the update that needs no difference of large squares
-// (Chan, Golub and LeVeque 1979).
+// (Chan, Golub and LeVeque 1979).  What joins nothing is taken as it is: its
+// mean is no deviation, and the square of a large one is past float32.
 struct Moments {
   float n, mu, m2;
   __device__ __forceinline__ void join(float nb, float mb, float qb) {
     const float t = n + nb, share = t > 0.f ? nb * __builtin_amdgcn_rcpf(t) : 0.f, d = mb - mu;
-    mu += d * share;
-    m2 += qb + d * d * (n * share);
+    mu = n > 0.f ? mu + d * share : mb;
+    m2 = n > 0.f ? m2 + (qb + d * (d * (n * share))) : qb;
     n = t;
   }
 };

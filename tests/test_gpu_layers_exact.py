@@ -1,0 +1,41 @@
+"""Layer norm and embedding on inputs whose sums are exact in float32, so that
+a lost row, column or token of any size of sum shows."""
+import numpy as np
+import pytest
+
+from distributed_bit_matrix_amd import binding as B
+from tests import layer_reference as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+EPS = float(np.float32(1e-5))
+
+
+def dev(a, dtype="f32"):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda().to(DT[dtype])
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [700, 16384, 16385, 24576, 24577, 40003, 1 << 20])
+def test_norm_of_constant_rows_of_large_values(cols, x_dtype):
+    """Constant rows of powers of two: every partial sum is exact (counts below
+    2^24), so the mean is the constant, the deviations are zero and y is beta,
+    also where the constant's square is past float32."""
+    print(f"norm constant rows {cols} {x_dtype}", flush=True)
+    value = np.array([2.0 ** 67, -2.0 ** 90, 2.0 ** 63, 1.0])
+    x = np.broadcast_to(value[:, None], (4, cols)).astype(np.float32)
+    b = np.linspace(-1, 1, cols).astype(np.float32)
+    y, m, r = B.layer_norm(dev(x, x_dtype), None, dev(b), EPS, want_stats=True)
+    assert np.array_equal(host(m), value)
+    # one addition, a root and a reciprocal
+    want = 1 / np.sqrt(EPS)
+    assert (np.abs(host(r) - want) <= 4 * R.U32 * want).all()
+    assert np.array_equal(host(y), np.broadcast_to(host(dev(b, x_dtype)), (4, cols)))
