@@ -11,14 +11,15 @@ Under an optimizer made with ``SignMuon(..., direct_grads=True)`` the backward
 passes write the parameter gradients in float32 straight into the flat array
 that the step reads (see ``optim``); ``p.grad`` stays None then.  Otherwise, in
 ``torch.autograd.grad`` and while a HIP graph is being captured, they return
-them in the parameter's dtype as any other operator does.  The gradients cannot be differentiated
-again.
+them in the parameter's dtype as any other operator does.  The gradients cannot
+be differentiated again, and there are no forward-mode derivatives.
 """
 from __future__ import annotations
 
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import binding as B
@@ -31,6 +32,19 @@ def _dense_rows(t):
     except TypeError:
         return t.contiguous()
     return t
+
+
+def _followed(*inputs) -> bool:
+    """Whether a gradient, a tangent or a trace follows a call on these inputs.
+    The kernels are hidden from all three, so it goes through the autograd
+    function: that gives the gradient, refuses the tangent and is what a trace
+    records."""
+    if torch.jit.is_tracing():
+        return True
+    grad = torch.is_grad_enabled()
+    return any(t is not None and (grad and t.requires_grad
+                                  or forward_ad.unpack_dual(t).tangent is not None)
+               for t in inputs)
 
 
 def _slot(p):
@@ -106,8 +120,7 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """Layer norm over x's last dimension, times weight plus bias (vectors of
     one dtype, or None).  x: float32 or bfloat16, of any leading shape."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (x, weight, bias)):
+    if _followed(x, weight, bias):
         return _LayerNorm.apply(x, weight, bias, eps, (_slot(weight), _slot(bias)))
     return B.layer_norm(_dense_rows(x), weight, bias, eps)
 
@@ -142,7 +155,7 @@ def embedding(tokens, weight, scale: float = 1.0, padding_idx: Optional[int] = N
     if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
         raise ValueError("padding_idx must lie in the table")
     tokens = tokens.contiguous()
-    if torch.is_grad_enabled() and weight.requires_grad:
+    if _followed(weight):
         return _Embedding.apply(tokens, weight.contiguous(), float(scale), padding_idx,
                                 _slot(weight))
     return B.embedding(tokens, weight.contiguous(), scale)

@@ -39,3 +39,15 @@ def test_norm_of_constant_rows_of_large_values(cols, x_dtype):
     want = 1 / np.sqrt(EPS)
     assert (np.abs(host(r) - want) <= 4 * R.U32 * want).all()
     assert np.array_equal(host(y), np.broadcast_to(host(dev(b, x_dtype)), (4, cols)))
+
+
+def test_traced_layers_run_the_kernels():
+    from distributed_bit_matrix_amd import layers as L
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, x2 = (torch.randn(7, 40, device="cuda", generator=g) for _ in range(2))
+    w, table = (torch.randn(s, device="cuda", generator=g) for s in ((40,), (30, 40)))
+    t, t2 = (torch.randint(30, (7,), device="cuda", generator=g) for _ in range(2))
+    norm = torch.jit.trace(lambda x: L.layer_norm(x, w), x)
+    look = torch.jit.trace(lambda t: L.embedding(t, table), t)
+    assert torch.equal(norm(x2), B.layer_norm(x2, w))
+    assert torch.equal(look(t2), table[t2])

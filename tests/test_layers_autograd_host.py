@@ -1,0 +1,95 @@
+"""Autograd through the layers, on the CPU: the library's calls are replaced by
+elementary torch operations, so that what layers.py and optim.py do around them
+can be seen without a GPU."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from torch.autograd import forward_ad as fw  # noqa: E402
+
+from distributed_bit_matrix_amd import binding as B  # noqa: E402
+from distributed_bit_matrix_amd import layers as L  # noqa: E402
+
+
+def _norm(x, weight=None, bias=None, eps=1e-5, want_stats=False):
+    x = x.detach()
+    mean = x.mean(-1)
+    d = x - mean[..., None]
+    rstd = 1 / torch.sqrt((d * d).mean(-1) + eps)
+    y = d * rstd[..., None]
+    y = y if weight is None else y * weight.detach()
+    y = y if bias is None else y + bias.detach()
+    return (y, mean, rstd) if want_stats else y
+
+
+def _sums(out, value, dtype, accumulate):
+    if out is None:
+        return value.to(dtype or torch.float32)
+    return out.add_(value) if accumulate else out.copy_(value)
+
+
+def _norm_backward(dy, x, weight, mean, rstd, want_x=True, want_weight=True, want_bias=True,
+                   dweight=None, dbias=None, dtype=None, accumulate=False):
+    xh = (x - mean[..., None]) * rstd[..., None]
+    g = dy if weight is None else dy * weight
+    dx = rstd[..., None] * (g - g.mean(-1, keepdim=True) - xh * (g * xh).mean(-1, keepdim=True))
+    cols = x.shape[-1]
+    return (dx if want_x else None,
+            _sums(dweight, (dy * xh).reshape(-1, cols).sum(0), dtype, accumulate)
+            if want_weight else None,
+            _sums(dbias, dy.reshape(-1, cols).sum(0), dtype, accumulate) if want_bias else None)
+
+
+def _embedding(tokens, weight, scale=1.0):
+    return scale * weight.detach()[tokens]
+
+
+def _embedding_backward(dy, tokens, vocab, scale=1.0, padding=None, dW=None, dtype=None,
+                        accumulate=False):
+    keep = torch.ones_like(tokens, dtype=torch.bool) if padding is None else tokens != padding
+    dw = torch.zeros(vocab, dy.shape[-1]).index_add_(0, tokens[keep], scale * dy[keep])
+    return _sums(dW, dw, dtype, accumulate)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    monkeypatch.setattr(B, "layer_norm", _norm)
+    monkeypatch.setattr(B, "layer_norm_backward", _norm_backward)
+    monkeypatch.setattr(B, "embedding", _embedding)
+    monkeypatch.setattr(B, "embedding_backward", _embedding_backward)
+
+
+def _tensors(seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(s, generator=g) for s in ((5, 6), (6,), (6,), (9, 6))]
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_forward_mode_derivatives_are_refused(calls, grad):
+    """A tangent of any input, with or without requires_grad, is not dropped."""
+    x, w, b, table = _tensors()
+    t = torch.tensor([1, 4])
+    with fw.dual_level(), torch.set_grad_enabled(grad):
+        dual = [fw.make_dual(v, torch.ones_like(v)) for v in (x, w, b, table)]
+        for call in (lambda: L.layer_norm(dual[0]), lambda: L.layer_norm(x, dual[1]),
+                     lambda: L.layer_norm(x, w, dual[2]), lambda: L.layer_norm(x, None, dual[2]),
+                     lambda: L.embedding(t, dual[3])):
+            with pytest.raises(NotImplementedError):
+                call()
+        # without a tangent nothing changes
+        assert torch.equal(L.layer_norm(x, w, b), _norm(x, w, b))
+        assert torch.equal(L.embedding(t, table), table[t])
+
+
+def test_traced_layers_run_again(calls):
+    """A trace holds the layers themselves, not the memory that they return
+    (the kernels are hidden from it)."""
+    x, w, b, table = _tensors()
+    t = torch.tensor([1, 4, 0])
+    norm = torch.jit.trace(lambda x: L.layer_norm(x, w, b), x)
+    look = torch.jit.trace(lambda t: L.embedding(t, table, 2.0), t)
+    assert "_LayerNorm" in str(norm.graph) and "_Embedding" in str(look.graph)
+    x2, t2 = _tensors(1)[0], torch.tensor([8, 8, 2])
+    assert torch.equal(norm(x2), _norm(x2, w, b))
+    assert torch.equal(look(t2), 2.0 * table[t2])
