@@ -52,7 +52,8 @@ def _slot(p):
 
 
 def _accumulates(ctx, i) -> bool:
-    """Whether this backward pass adds to the grad of input i, a leaf: not where
+    """Whether this backward pass adds to the grad of tensor input i (inputs
+    that are None or no tensors are not counted), a leaf: not where
     backward(inputs=...) leaves it out, nor in torch.autograd.grad, which hands
     the gradient to its caller (or drops it)."""
     try:
@@ -62,7 +63,7 @@ def _accumulates(ctx, i) -> bool:
 
 
 def _direct(ctx, i, slot):
-    """Whether the gradient of input i goes to its slot: not once the optimizer
+    """Whether the gradient of tensor input i goes to its slot: not once the optimizer
     is gone, nor into a graph, whose replays would not tell the optimizer what
     they wrote."""
     return (slot is not None and slot.alive() and _accumulates(ctx, i)
@@ -87,7 +88,8 @@ class _LayerNorm(torch.autograd.Function):
         dw = db = dtype = None
         add = False
         direct = [s if want and _direct(ctx, i, s) else None
-                  for i, s, want in zip((1, 2), ctx.slots, (want_w, want_b))]
+                  for i, s, want in zip((1, 1 + (weight is not None)), ctx.slots,
+                                        (want_w, want_b))]
         if direct[0] is direct[1]:      # one parameter as weight and bias
             direct = [None, None]
         if any(direct):

@@ -93,3 +93,50 @@ def test_traced_layers_run_again(calls):
     x2, t2 = _tensors(1)[0], torch.tensor([8, 8, 2])
     assert torch.equal(norm(x2), _norm(x2, w, b))
     assert torch.equal(look(t2), 2.0 * table[t2])
+
+
+class _State:
+    """Stands for the optimizer's flat arrays of one group."""
+
+    def __init__(self):
+        self.log = []
+
+    def wait(self):
+        self.log.append("wait")
+
+    def mark(self):
+        self.log.append("mark")
+
+
+def _with_slot(p, state):
+    from distributed_bit_matrix_amd import optim as SO
+    p = torch.nn.Parameter(p)
+    p._signmuon_slot = SO.GradSlot(state, torch.full_like(p, float("nan")))
+    return p
+
+
+@pytest.fixture
+def not_capturing(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+@pytest.mark.parametrize("with_x", [True, False])
+@pytest.mark.parametrize("form", ["weight", "bias", "both"])
+def test_direct_gradients_of_every_form(calls, not_capturing, form, with_x):
+    """A weight alone, a bias alone and both, with and without the input's
+    gradient, over two passes that add up."""
+    state = _State()
+    x, w, b, _ = _tensors()
+    x.requires_grad_(with_x)
+    w = _with_slot(w, state) if form != "bias" else None
+    b = _with_slot(b, state) if form != "weight" else None
+    params = [p for p in (w, b) if p is not None]
+    c = torch.arange(30.).view(5, 6)
+    want = torch.autograd.grad((L.layer_norm(x, w, b) * c).sum(), params)
+    assert not any(p._signmuon_slot.filled for p in params)
+    for turn in (1, 2):
+        (L.layer_norm(x, w, b) * c).sum().backward()
+        for p, g in zip(params, want):
+            assert p.grad is None and p._signmuon_slot.filled
+            assert torch.equal(p._signmuon_slot.grad, turn * g)
+    assert (x.grad is not None) == with_x
