@@ -122,7 +122,12 @@ class _GroupState:
         torch.cuda.current_stream(self.G.device).wait_event(self.event)
 
     def mark(self):
-        self.event.record(torch.cuda.current_stream(self.G.device))
+        """Work on G was enqueued on the current stream: later work on any stream
+        can wait for it, and its memory is not given away before it is done,
+        even if G goes with its optimizer first."""
+        stream = torch.cuda.current_stream(self.G.device)
+        self.event.record(stream)
+        self.G.record_stream(stream)
 
     def gather(self, i):
         """Parameter i's gradient into its place in the flat array."""

@@ -51,3 +51,28 @@ def test_traced_layers_run_the_kernels():
     look = torch.jit.trace(lambda t: L.embedding(t, table), t)
     assert torch.equal(norm(x2), B.layer_norm(x2, w))
     assert torch.equal(look(t2), table[t2])
+
+
+def test_direct_gradients_outlive_their_optimizer():
+    """A backward pass on another stream, still under way when its optimizer
+    and the gradients' array go: new tensors do not get its memory."""
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    t = torch.arange(3000, device="cuda")
+    busy = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for rep in range(4):
+        w = torch.nn.Parameter(torch.zeros(3000, 512, device="cuda"))
+        opt = SO.SignMuon([w], scale="fro", K=1, direct_grads=True)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy @ busy
+            L.embedding(t, w).sum().backward()
+        assert w.grad is None
+        del opt
+        SO.SignMuon([w], scale="fro", K=1, direct_grads=True)      # drops the old array
+        new = [torch.full((3000, 512), 7.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        for n in new:
+            assert bool((n == 7.0).all()), rep

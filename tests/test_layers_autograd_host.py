@@ -140,3 +140,37 @@ def test_direct_gradients_of_every_form(calls, not_capturing, form, with_x):
             assert p.grad is None and p._signmuon_slot.filled
             assert torch.equal(p._signmuon_slot.grad, turn * g)
     assert (x.grad is not None) == with_x
+
+
+class _Stream:
+    pass
+
+
+class _Array:
+    """Stands for a tensor on a GPU: its streams are remembered."""
+    device = None
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_a_write_on_another_stream_keeps_the_array(monkeypatch):
+    """The flat gradient may go with its optimizer while a backward pass still
+    writes it on a stream that the allocator does not know of."""
+    from distributed_bit_matrix_amd import optim as SO
+    state = SO._GroupState.__new__(SO._GroupState)
+    log = []
+
+    class Event:
+        def record(self, stream):
+            log.append(stream)
+
+    state.G, state.event = _Array(), Event()
+    stream = _Stream()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    slot = SO.GradSlot(state, torch.zeros(4))
+    slot.close()
+    assert slot.filled and log == [stream] and state.G.streams == [stream]
