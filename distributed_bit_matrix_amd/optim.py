@@ -129,6 +129,13 @@ class _GroupState:
         self.event.record(stream)
         self.G.record_stream(stream)
 
+    def hold(self):
+        """A step was enqueued on the current stream: the arrays it uses are not
+        given away before it is done, even if the optimizer goes first."""
+        stream = torch.cuda.current_stream(self.G.device)
+        for t in (self.G, self.W, self.Mom, self.bits, self.plan.ws):
+            t.record_stream(stream)
+
     def gather(self, i):
         """Parameter i's gradient into its place in the flat array."""
         p, (rows, cols, off, _) = self.params[i], self.layout[i]
@@ -224,6 +231,7 @@ class SignMuon(torch.optim.Optimizer):
             if self.workers > 1:
                 self.fill_other_workers(st.bits, st.stride, self.workers)
             st.plan(st.G, st.W, st.Mom, st.bits, st.stride, self.workers, 0)
+            st.hold()
             for slot in st.slots:
                 slot.filled = False
             if st.slots:

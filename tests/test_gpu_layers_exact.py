@@ -76,3 +76,32 @@ def test_direct_gradients_outlive_their_optimizer():
         torch.cuda.synchronize()
         for n in new:
             assert bool((n == 7.0).all()), rep
+
+
+def test_step_outlives_its_optimizer():
+    """A step on another stream, still under way when the optimizer goes: the
+    weights move as they do without the deletion, and new tensors keep theirs."""
+    from distributed_bit_matrix_amd import optim as SO
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w0, grad = (torch.randn(512, 700, device="cuda", generator=g) for _ in range(2))
+
+    def run(drop):
+        w = torch.nn.Parameter(w0.clone())
+        w.grad = grad.clone()
+        opt = SO.SignMuon([w], scale="fro", K=2)
+        opt._state(0, opt.param_groups[0])
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                w0.t() @ w0
+            opt.step()
+        if drop:
+            del opt
+        new = [torch.full((512, 700), 7.0, device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        return w.detach().clone(), all(bool((n == 7.0).all()) for n in new)
+
+    want, _ = run(False)
+    got, kept = run(True)
+    assert kept and torch.equal(got, want) and not torch.equal(got, w0)

@@ -174,3 +174,29 @@ def test_a_write_on_another_stream_keeps_the_array(monkeypatch):
     slot = SO.GradSlot(state, torch.zeros(4))
     slot.close()
     assert slot.filled and log == [stream] and state.G.streams == [stream]
+
+
+def test_a_step_on_another_stream_keeps_its_arrays(monkeypatch):
+    from distributed_bit_matrix_amd import optim as SO
+    opt = SO.SignMuon([torch.nn.Parameter(torch.zeros(4))])
+    state = SO._GroupState.__new__(SO._GroupState)
+    arrays = [_Array() for _ in range(5)]
+    state.G, state.W, state.Mom, state.bits = arrays[:4]
+    state.slots, state.params, state.stride = [], [], 1
+    ran = []
+
+    class Plan:
+        ws = arrays[4]
+
+        def set_eta(self, eta):
+            pass
+
+        def __call__(self, *args):
+            ran.append(args[:4])
+
+    state.plan = Plan()
+    opt._groups[0] = state
+    stream = _Stream()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    opt.step()
+    assert len(ran) == 1 and all(a.streams == [stream] for a in arrays)
