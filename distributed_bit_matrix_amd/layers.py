@@ -63,11 +63,14 @@ def _accumulates(ctx, i) -> bool:
 
 
 def _direct(ctx, i, slot):
-    """Whether the gradient of tensor input i goes to its slot: not once the optimizer
-    is gone, nor into a graph, whose replays would not tell the optimizer what
-    they wrote."""
-    return (slot is not None and slot.alive() and _accumulates(ctx, i)
-            and not torch.cuda.is_current_stream_capturing())
+    """The owner of the slot that the gradient of tensor input i goes to, to be
+    held until it is written; None where it does not: once the optimizer is
+    gone, or in a graph, whose replays would not tell the optimizer what they
+    wrote."""
+    owner = None if slot is None else slot.owner()
+    if owner is None or not _accumulates(ctx, i) or torch.cuda.is_current_stream_capturing():
+        return None
+    return owner
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -87,9 +90,10 @@ class _LayerNorm(torch.autograd.Function):
         want_x, want_w, want_b = ctx.needs_input_grad[:3]
         dw = db = dtype = None
         add = False
-        direct = [s if want and _direct(ctx, i, s) else None
+        owners = [_direct(ctx, i, s) if want else None
                   for i, s, want in zip((1, 1 + (weight is not None)), ctx.slots,
                                         (want_w, want_b))]
+        direct = [None if o is None else s for o, s in zip(owners, ctx.slots)]
         if direct[0] is direct[1]:      # one parameter as weight and bias
             direct = [None, None]
         if any(direct):
@@ -140,7 +144,8 @@ class _Embedding(torch.autograd.Function):
         tokens, = ctx.saved_tensors
         vocab, dtype, scale, padding, slot = ctx.table
         dy = _dense_rows(dy)
-        if _direct(ctx, 1, slot):
+        owner = _direct(ctx, 1, slot)
+        if owner is not None:
             add = slot.filled
             B.embedding_backward(dy, tokens, vocab, scale, padding, dW=slot.open(add),
                                  accumulate=add)

@@ -47,20 +47,31 @@ class GradSlot:
     """Where a parameter's gradient goes under ``direct_grads``: its place in
     the group's flat float32 array.  ``open`` and ``close`` enclose a write on the
     current stream, in order with other writes and with the step, on whatever
-    streams those run."""
+    streams those run.  The place goes with the optimizer, however long the
+    parameter keeps its slot; who writes holds the owner meanwhile."""
 
-    __slots__ = ("grad", "filled", "_state")
+    __slots__ = ("grad", "filled", "_state", "__weakref__")
 
     def __init__(self, state, grad):
         self.grad = grad
         self.filled = False          # holds a gradient that no step has used
-        self._state = weakref.ref(state)
+        me = weakref.ref(self)       # a strong one would keep both until a collection
+
+        def drop(_):
+            if me() is not None:
+                me().grad = None
+
+        self._state = weakref.ref(state, drop)
 
     def __reduce__(self):
         return type(None), ()        # a saved or copied parameter has none
 
+    def owner(self):
+        """The optimizer's state, None once that is gone."""
+        return self._state()
+
     def alive(self) -> bool:
-        return self._state() is not None
+        return self.owner() is not None
 
     def open(self, add: bool):
         """The float32 array to write: to be overwritten, or with `add` to be

@@ -105,3 +105,22 @@ def test_step_outlives_its_optimizer():
     want, _ = run(False)
     got, kept = run(True)
     assert kept and torch.equal(got, want) and not torch.equal(got, w0)
+
+
+def test_a_kept_parameter_frees_the_optimizers_arrays():
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    w = torch.nn.Parameter(torch.zeros(4096, 512, device="cuda"))
+    t = torch.arange(64, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    opt = SO.SignMuon([w], scale="fro", K=1, direct_grads=True)
+    L.embedding(t, w).sum().backward()
+    opt.step()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() - before >= 2 * 4 * w.numel()
+    del opt
+    # the weights take the place of the parameter's own memory; nothing else stays
+    assert torch.cuda.memory_allocated() - before < w.numel()
+    L.embedding(t, w).sum().backward()
+    assert w.grad is not None

@@ -200,3 +200,40 @@ def test_a_step_on_another_stream_keeps_its_arrays(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
     opt.step()
     assert len(ran) == 1 and all(a.streams == [stream] for a in arrays)
+
+
+def test_a_slot_does_not_keep_the_array():
+    """A parameter that outlives its optimizer holds nothing of its arrays."""
+    import weakref
+    from distributed_bit_matrix_amd import optim as SO
+    state, flat = _State(), torch.zeros(100)
+    p = torch.nn.Parameter(torch.zeros(4))
+    p._signmuon_slot = SO.GradSlot(state, flat[8:12])
+    assert p._signmuon_slot.grad.data_ptr() == flat.data_ptr() + 32
+    gone = []
+    weakref.finalize(p._signmuon_slot.grad, gone.append, True)
+    del state
+    assert gone == [True] and not p._signmuon_slot.alive()
+
+
+def test_an_optimizer_may_go_during_a_pass(calls, not_capturing):
+    """The state that took a gradient lives until the gradient is written."""
+    x, w, _, _ = _tensors()
+    state = _State()
+    w = _with_slot(w, state)
+    log = state.log
+    y = L.layer_norm(x, w).sum()
+
+    real = B.layer_norm_backward
+
+    def drop(*args, **kw):
+        nonlocal state
+        state = None                # the last reference outside of the pass
+        return real(*args, **kw)
+
+    B.layer_norm_backward = drop
+    try:
+        y.backward()
+    finally:
+        B.layer_norm_backward = real
+    assert log == ["wait", "mark"] and w.grad is None and not w._signmuon_slot.alive()
