@@ -22,11 +22,16 @@ exchange; the step then votes over all M.
 from __future__ import annotations
 
 import weakref
-from typing import Callable, Optional
+from typing import Callable, Optional, cast
 
 import torch
 
 from . import binding as B
+
+
+# What a saved parameter has in the place of its slot is made by this identity,
+# which torch.load with weights_only has to be told of.
+torch.serialization.add_safe_globals([cast])
 
 
 def matrix_shape(shape) -> tuple:
@@ -64,7 +69,7 @@ class GradSlot:
         self._state = weakref.ref(state, drop)
 
     def __reduce__(self):
-        return type(None), ()        # a saved or copied parameter has none
+        return cast, (None, None)    # a saved or copied parameter has none
 
     def owner(self):
         """The optimizer's state, None once that is gone."""
@@ -188,7 +193,9 @@ class SignMuon(torch.optim.Optimizer):
     is the sum since the last step or zero_grad of this optimizer; p.grad
     stays None for it (hooks on the parameter and what clips or scales p.grad do
     not see it), and what other operators put there is added to it (a table
-    shared with the output product)."""
+    shared with the output product).  A state_dict holds plain tensors; a file of
+    the parameters themselves is loaded with weights_only where this module is
+    imported (or typing.cast is among torch's safe globals)."""
 
     def __init__(self, params, lr: float = 0.02, beta: float = 0.9,
                  weight_decay: float = 0.0, eps: float = 1e-7, K: int = 5,

@@ -237,3 +237,17 @@ def test_an_optimizer_may_go_during_a_pass(calls, not_capturing):
     finally:
         B.layer_norm_backward = real
     assert log == ["wait", "mark"] and w.grad is None and not w._signmuon_slot.alive()
+
+
+def test_parameters_with_a_slot_load_as_weights_only():
+    """torch.load's default: parameters saved by themselves (a state_dict holds
+    plain tensors), as they were before an optimizer took their gradients."""
+    import io
+    state = _State()
+    p = _with_slot(torch.arange(4.), state)
+    f = io.BytesIO()
+    torch.save({"p": p}, f)
+    f.seek(0)
+    q = torch.load(f, weights_only=True)["p"]
+    assert torch.equal(q.detach(), p.detach())
+    assert q.__dict__.get("_signmuon_slot") is None and p._signmuon_slot.alive()
