@@ -124,3 +124,56 @@ def test_a_kept_parameter_frees_the_optimizers_arrays():
     assert torch.cuda.memory_allocated() - before < w.numel()
     L.embedding(t, w).sum().backward()
     assert w.grad is not None
+
+
+def test_captured_backward_fills_the_parameters_grads():
+    """A plain backward pass captured while an optimizer takes gradients
+    directly: each replay's gradients are in p.grad, the step's array and the
+    slots stay as they are, and the next eager pass writes to them again."""
+    from distributed_bit_matrix_amd import layers as L
+    from distributed_bit_matrix_amd import optim as SO
+    g = torch.Generator(device="cuda").manual_seed(9)
+    w, b, table = params = [torch.nn.Parameter(torch.randn(s, device="cuda", generator=g))
+                            for s in ((64,), (64,), (30, 64))]
+    opt = SO.SignMuon(params, scale="fro", K=1, direct_grads=True)
+    t = torch.randint(30, (50,), device="cuda", generator=g)
+    c = torch.randn(50, 64, device="cuda", generator=g)
+
+    def run():      # no graph of the parameters lives on after it
+        L.layer_norm(L.embedding(t, table), w, b).backward(c)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    opt.zero_grad()
+    flat = opt._groups[0].G
+    flat.fill_(5.0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    got = [p.grad for p in params]
+    assert all(v is not None for v in got)
+    for rep in range(4):
+        c.copy_(torch.randn(50, 64, device="cuda", generator=g))
+        t.copy_(torch.randint(30, (50,), device="cuda", generator=g))
+        for v in got:
+            v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.autograd.grad(L.layer_norm(L.embedding(t, table), w, b), params, c)
+        torch.cuda.synchronize()
+        for p, v, e in zip(params, got, want):
+            assert p.grad is v and torch.equal(v, e), rep
+            assert not p._signmuon_slot.filled
+        assert bool((flat == 5.0).all()), rep
+    for p in params:
+        p.grad = None
+    run()
+    for p, e in zip(params, want):
+        assert p.grad is None and p._signmuon_slot.filled
+        assert torch.equal(p._signmuon_slot.grad, e)

@@ -251,3 +251,23 @@ def test_parameters_with_a_slot_load_as_weights_only():
     q = torch.load(f, weights_only=True)["p"]
     assert torch.equal(q.detach(), p.detach())
     assert q.__dict__.get("_signmuon_slot") is None and p._signmuon_slot.alive()
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_captured_pass_returns_its_gradients(calls, monkeypatch, capturing):
+    """backward() in a capture puts the gradients into p.grad and leaves the
+    slots alone; the same pass outside of one fills the slots."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    x, w, b, table = _tensors()
+    state = _State()
+    params = [w, b, table] = [_with_slot(p, state) for p in (w, b, table)]
+    t = torch.tensor([1, 4, 1, 0, 8])
+    c = torch.arange(30.).view(5, 6)
+    want = torch.autograd.grad((L.layer_norm(L.embedding(t, table), w, b) * c).sum(), params)
+    (L.layer_norm(L.embedding(t, table), w, b) * c).sum().backward()
+    for p, g in zip(params, want):
+        slot = p._signmuon_slot
+        assert slot.filled != capturing and (p.grad is None) != capturing
+        assert torch.equal(p.grad if capturing else slot.grad, g)
+        assert not capturing or bool(slot.grad.isnan().all())
+    assert (state.log == []) == capturing
