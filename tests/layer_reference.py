@@ -124,3 +124,63 @@ def embed_grad_bounds(dw, mag, counts, dtype, before=0.0):
     was there."""
     err = (chain(counts)[:, None] + 2 * U32) * mag + U32 * np.abs(before)
     return stored(dw + before, err, dtype)
+
+
+# --------------------------------------------------------------------------
+# Inputs whose sums are exact: small integers times powers of two, so that every
+# partial sum is an integer below 2^24 in units of its row or column, in
+# whatever order it is taken.  What is lost from a sum shows then, however
+# many terms the sum has, where a bound for inexact ones grows with their
+# number.
+# --------------------------------------------------------------------------
+def pattern(cols):
+    """1, -1, 1, -1, ..., and a last 0 if cols is odd: it and its products with
+    constants sum to 0, also over any run of pairs."""
+    p = np.where(np.arange(cols) % 2 == 0, 1.0, -1.0)
+    if cols % 2:
+        p[-1] = 0.0
+    return p
+
+
+def exact_norm(rows, cols, eps, dtype):
+    """x, (y, mean, rstd) and their bounds, without weights.  Row r is 2^k (2 +
+    pattern), k = r mod 8: the mean is 2^(k+1) exactly, the deviations and
+    their squares are exact, and the sum of squares is 4^k times the number of
+    nonzero entries.  The variance then takes up to 2 roundings (times the
+    rounded reciprocal of cols; or one, divided by cols), eps one, the root
+    halves these 3, and the root and the reciprocal add one each: 3.5.  y
+    adds one."""
+    p = pattern(cols)
+    k = 2.0 ** (np.arange(rows) % 8)[:, None]
+    x = (k * (2 + p)).astype(np.float32)
+    rstd = 1 / np.sqrt(k[:, 0] ** 2 * ((p != 0).sum() / cols) + eps)
+    y = k * p * rstd[:, None]
+    return x, (y, 2 * k[:, 0], rstd), (stored(y, 5 * U32 * np.abs(y), dtype),
+                                       0 * rstd, 4 * U32 * rstd)
+
+
+def exact_norm_grad(rows, cols, dtype):
+    """dy, x, (dx, dgamma, dbeta) and dx's bound, for mean 0, rstd 1 and no
+    gamma; dgamma and dbeta are exact.  xhat is the pattern p; dy is 2, 3 p and
+    1 + 2 p in turn, times 2^(r mod 4).  Both row sums are exact; their means
+    take 2 roundings at most (times the rounded reciprocal of cols), and dx is
+    put together with 3 more."""
+    assert rows * 8 * 3 < 2 ** 24 and cols * 8 * 3 <= 3 * 2 ** 23
+    p = pattern(cols)
+    r = np.arange(rows)
+    kinds = np.stack([0 * p + 2, 3 * p, 1 + 2 * p])
+    dy = kinds[r % 3] * 2.0 ** (r % 4)[:, None]
+    x = np.broadcast_to(p, (rows, cols))
+    c1, c2 = dy.mean(1, keepdims=True), (dy * x).mean(1, keepdims=True)
+    dx = dy - c1 - x * c2
+    e = 6 * U32 * (np.abs(dy) + np.abs(c1) + np.abs(x * c2))
+    return (dy.astype(np.float32), x.astype(np.float32), (dx, (dy * x).sum(0), dy.sum(0)),
+            stored(dx, e, dtype))
+
+
+def exact_embed_grad(dy, tokens, vocab):
+    """Sums of integer rows by token, one column at a time."""
+    dy = np.asarray(dy, np.float64)
+    dw = np.stack([np.bincount(tokens, dy[:, c], minlength=vocab) for c in range(dy.shape[1])], 1)
+    assert np.abs(dw).max() < 2 ** 24
+    return dw

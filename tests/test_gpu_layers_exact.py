@@ -23,6 +23,12 @@ def host(t):
     return t.detach().float().cpu().numpy().astype(np.float64)
 
 
+def within(got, want, bound, what):
+    off = np.abs(got - want)
+    bad = ~(off <= bound)
+    assert not bad.any(), (what, np.argwhere(bad)[:4].tolist(), off[bad][:4])
+
+
 @pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("cols", [700, 16384, 16385, 24576, 24577, 40003, 1 << 20])
 def test_norm_of_constant_rows_of_large_values(cols, x_dtype):
@@ -177,3 +183,116 @@ def test_captured_backward_fills_the_parameters_grads():
     for p, e in zip(params, want):
         assert p.grad is None and p._signmuon_slot.filled
         assert torch.equal(p._signmuon_slot.grad, e)
+
+
+# one of every width of the kernels' rows, in registers and past them, and of
+# every number of rows a block or a launch takes
+EXACT = [(5, 1), (9, 2), (7, 7), (40, 64), (33, 129), (11, 511), (19, 768), (17, 1001),
+         (2048, 257), (2049, 257), (3, 2049), (5, 4097), (3, 8192), (4, 8193), (3, 16384),
+         (2, 16385), (3, 24577), (9, 32769), (40, 40003), (2, 100003), (1, 1 << 20)]
+
+
+@pytest.mark.parametrize("rows,cols", EXACT)
+def test_norm_loses_no_column(rows, cols):
+    print(f"exact norm {rows}x{cols}", flush=True)
+    for x_dtype in DT:
+        x, want, bound = R.exact_norm(rows, cols, EPS, x_dtype)
+        got = B.layer_norm(dev(x, x_dtype), None, None, EPS, want_stats=True)
+        for a, w, e, name in zip(got, want, bound, ("y", "mean", "rstd")):
+            within(host(a), w, e, (x_dtype, name))
+
+
+def _exact_grad(rows, cols):
+    for x_dtype in DT:
+        dy, x, want, e = R.exact_norm_grad(rows, cols, x_dtype)
+        DY, X = dev(dy, x_dtype), dev(x, x_dtype)
+        m, r = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+        for dw_dtype in DT:
+            dx, dg, db = B.layer_norm_backward(DY, X, None, m, r, dtype=DT[dw_dtype])
+            within(host(dx), want[0], e, (x_dtype, "dx"))
+            for a, w, name in ((dg, want[1], "dgamma"), (db, want[2], "dbeta")):
+                w = R.bf16_values(w) if dw_dtype == "bf16" else w
+                assert np.array_equal(host(a), w), (x_dtype, dw_dtype, name)
+        old = np.arange(cols) % 7
+        acc = [dev(old.astype(np.float32)) for _ in range(2)]
+        B.layer_norm_backward(DY, X, None, m, r, want_x=False, dweight=acc[0], dbias=acc[1],
+                              accumulate=True)
+        for a, w in zip(acc, want[1:]):
+            assert np.array_equal(host(a), w + old), x_dtype
+
+
+@pytest.mark.parametrize("rows,cols", EXACT)
+def test_norm_backward_loses_no_row_or_column(rows, cols):
+    print(f"exact norm grad {rows}x{cols}", flush=True)
+    _exact_grad(rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols", [(2049, 1), (140000, 3), (40000, 8), (70000, 24),
+                                       (33000, 33), (4097, 65), (12289, 768), (4200, 1001),
+                                       (2100, 2049), (3001, 4096), (513, 8193), (300, 16384),
+                                       (1100, 16385), (600, 33000)])
+def test_norm_backward_of_several_launches_loses_no_row(rows, cols):
+    print(f"exact norm grad, several launches {rows}x{cols}", flush=True)
+    assert B.layer_norm_backward_workspace(rows, cols) > 0
+    _exact_grad(rows, cols)
+
+
+def test_sums_over_rows_past_32_bits():
+    """2^21 + 1 rows of 1024: dY and X are 1 or 2, in turns of their own, so that
+    every sum is an integer below 2^23 and a bit."""
+    n, dim = (1 << 21) + 1, 1024
+    print(f"exact sums past 32 bits: {n} x {dim}", flush=True)
+    i, c = torch.arange(n, device="cuda")[:, None], torch.arange(dim, device="cuda")[None]
+    DY = torch.empty(n, dim, device="cuda", dtype=torch.bfloat16)
+    X = torch.empty_like(DY)
+    for a in range(0, n, 1 << 18):
+        k = i[a:a + (1 << 18)]
+        DY[a:a + (1 << 18)] = (1 + (k + c) % 2).bfloat16()
+        X[a:a + (1 << 18)] = (1 + (k // 2 + c) % 2).bfloat16()
+    m, r = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    _, dg, db = B.layer_norm_backward(DY, X, None, m, r, want_x=False)
+    i, c = np.arange(4)[:, None], np.arange(dim)[None]      # the rows repeat after 4
+    times = np.bincount(np.arange(n) % 4)[:, None]
+    dy, x = 1 + (i + c) % 2, 1 + (i // 2 + c) % 2
+    assert np.array_equal(host(db), (times * dy).sum(0))
+    assert np.array_equal(host(dg), (times * dy * x).sum(0))
+    T = torch.arange(n, device="cuda") % 4
+    dW = B.embedding_backward(DY, T, 5, 0.5)
+    assert np.array_equal(host(dW), 0.5 * np.concatenate([times * dy, 0 * dy[:1]]))
+
+
+def _tokens(rng, kind, n, vocab):
+    if kind == "same":
+        return np.full(n, rng.integers(0, vocab))
+    if kind == "positions":
+        return np.arange(n) % vocab
+    if kind == "skew":                  # many tokens of one residue
+        return 5 + 256 * rng.integers(0, vocab // 256, n)
+    if kind == "zipf":
+        return np.minimum((vocab ** rng.random(n)).astype(np.int64) - 1, vocab - 1)
+    return rng.integers(0, vocab, n)
+
+
+@pytest.mark.parametrize("n,vocab,dim,kind", [
+    (896, 513, 5, "same"), (2048, 300, 70, "same"), (2047, 5000, 260, "zipf"),
+    (2048, 1000, 5, "skew"), (2049, 1000, 7, "skew"), (4000, 64, 1030, "zipf"),
+    (12288, 50257, 96, "zipf"), (33000, 70000, 2, "zipf"), (50000, 4096, 3, "zipf"),
+    (65536, 1024, 96, "positions"), (65536, 300, 20, "same"), (65537, 2000, 3, "zipf"),
+    (70001, 1, 3, "same"), (70000, 100, 1, "uniform"), (131073, 3, 5, "same"),
+    (150000, 30000, 2, "zipf"), (100001, 300000, 2, "skew"), (262145, 17, 2, "uniform"),
+    (600001, 1048576, 1, "uniform")])
+def test_embedding_backward_loses_no_token(n, vocab, dim, kind):
+    print(f"exact embed grad n={n} {vocab}x{dim} {kind}", flush=True)
+    rng = np.random.default_rng(n + vocab + dim)
+    t = _tokens(rng, kind, n, vocab)
+    dy = rng.integers(1, 4, (n, dim)).astype(np.float32)
+    want = 0.5 * R.exact_embed_grad(dy, t, vocab)
+    T, old = torch.from_numpy(t).cuda(), (np.arange(vocab) % 7)[:, None] + np.zeros(dim)
+    for dy_dtype in DT:
+        DY = dev(dy, dy_dtype)
+        assert np.array_equal(host(B.embedding_backward(DY, T, vocab, 0.5)), want)
+        got = B.embedding_backward(DY, T.int(), vocab, 0.5, dtype=torch.bfloat16)
+        assert np.array_equal(host(got), R.bf16_values(want))
+        acc = dev(old.astype(np.float32))
+        B.embedding_backward(DY, T, vocab, 0.5, dW=acc, accumulate=True)
+        assert np.array_equal(host(acc), want + old)
