@@ -11,15 +11,18 @@ namespace {
 constexpr int64_t kMaxDim = 1 << 20;                 // cols, dim, vocab
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
-constexpr int64_t kMaxSorted = (int64_t)1 << 27;      // a 16th of it has a 23-bit place
+constexpr int64_t kMaxSorted = (int64_t)1 << 27;     // 256 runs of 2^19, 2^15 tokens a wave
+constexpr int64_t kMaxStride = (int64_t)1 << 39;      // elements; past any memory
 
 bool dtype_ok(int32_t d) { return d == SM_F32 || d == SM_BF16; }
 bool aligned(const void* p, int32_t dtype) {
   return (uintptr_t)p % (dtype == SM_F32 ? 4 : 2) == 0;
 }
 bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
-// a row stride whose last row still has a 63-bit byte offset
-bool stride_ok(int64_t stride, int64_t cols) { return in(stride, cols, (int64_t)1 << 28); }
+// a row stride that memory can hold, and whose last row has a 63-bit byte offset
+bool stride_ok(int64_t stride, int64_t rows, int64_t cols) {
+  return in(stride, cols, kMaxStride) && stride <= ((int64_t)1 << 60) / rows;
+}
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && have >= need && (uintptr_t)ws % 256 == 0);
 }
@@ -36,7 +39,7 @@ sm_status signmuon_layer_norm(const void* X, int32_t x_dtype, int64_t x_stride,
   if (!in(rows, 0, kMaxRows) || !in(cols, 1, kMaxDim)) return SM_EINVAL;
   if (!std::isfinite(eps) || eps < 0.f) return SM_EINVAL;
   if (rows == 0) return SM_OK;
-  if (!X || !Y || !stride_ok(x_stride, cols)) return SM_EINVAL;
+  if (!X || !Y || !stride_ok(x_stride, rows, cols)) return SM_EINVAL;
   if (X == Y && x_stride != cols) return SM_EINVAL;
   if (!aligned(X, x_dtype) || !aligned(Y, x_dtype) || !aligned(gamma, w_dtype) ||
       !aligned(beta, w_dtype) || !aligned(mean, SM_F32) || !aligned(rstd, SM_F32))
@@ -62,7 +65,7 @@ sm_status signmuon_layer_norm_backward(const void* dY, int64_t dy_stride, const 
   if (!dX && !dgamma && !dbeta) return SM_OK;
   if (rows > 0) {
     if (!dY || !X || !mean || !rstd) return SM_EINVAL;
-    if (!stride_ok(dy_stride, cols) || !stride_ok(x_stride, cols)) return SM_EINVAL;
+    if (!stride_ok(dy_stride, rows, cols) || !stride_ok(x_stride, rows, cols)) return SM_EINVAL;
     if (dX && (dX == X || (dX == dY && dy_stride != cols))) return SM_EINVAL;
     if (!aligned(dY, x_dtype) || !aligned(X, x_dtype) || !aligned(gamma, w_dtype) ||
         !aligned(mean, SM_F32) || !aligned(rstd, SM_F32) || !aligned(dX, x_dtype))
@@ -109,7 +112,7 @@ sm_status signmuon_embedding_backward(const void* dY, int32_t dy_dtype, int64_t 
   if (n == 0 && accumulate) return SM_OK;
   if (!dW || !aligned(dW, dw_dtype)) return SM_EINVAL;
   if (n > 0) {
-    if (!dY || !tokens || !stride_ok(dy_stride, dim)) return SM_EINVAL;
+    if (!dY || !tokens || !stride_ok(dy_stride, n, dim)) return SM_EINVAL;
     if (!aligned(dY, dy_dtype) || (uintptr_t)tokens % (token_bits / 8)) return SM_EINVAL;
   }
   if (!workspace_ok(ws, ws_bytes, embed_grad_workspace(n, vocab, dim))) return SM_EWORKSPACE;

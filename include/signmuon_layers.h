@@ -19,6 +19,9 @@
  *
  * Dtypes are sm_dtype codes.  Every sum is held in float32 or wider; a
  * bfloat16 result is rounded once, to nearest even, when it is stored.
+ *
+ * A row stride counts elements; it is at most 2^39, and times the number of rows
+ * at most 2^60.
  */
 #ifndef SIGNMUON_LAYERS_H
 #define SIGNMUON_LAYERS_H
@@ -39,7 +42,9 @@ extern "C" {
  * beta: [cols] of w_dtype; gamma NULL stands for ones, beta NULL for zeros.
  * mean, rstd: float32[rows] outputs for the backward pass, or NULL.
  * 0 <= rows < 2^31, 1 <= cols <= 2^20, eps >= 0 and finite.  rows = 0 is a
- * no-op.  A non-finite entry makes its own row NaN and no other.
+ * no-op.  A non-finite entry makes its own row NaN and no other.  So may a row
+ * whose sum is past float32; where the sum of the squared deviations is, the
+ * variance counts as infinite and rstd is 0.
  */
 sm_status signmuon_layer_norm(const void *X, int32_t x_dtype, int64_t x_stride,
                               const void *gamma, const void *beta,

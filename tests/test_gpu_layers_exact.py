@@ -296,3 +296,27 @@ def test_embedding_backward_loses_no_token(n, vocab, dim, kind):
         acc = dev(old.astype(np.float32))
         B.embedding_backward(DY, T, vocab, 0.5, dW=acc, accumulate=True)
         assert np.array_equal(host(acc), want + old)
+
+
+def test_rows_far_apart():
+    """Rows 2^28 + 24 entries apart, as in a slice of a large matrix: the bits
+    of the dense rows, and the memory between them stays."""
+    gap, cols = (1 << 28) + 24, 768
+    print("rows far apart", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    big = torch.full((3, gap), 7.0, device="cuda", dtype=torch.bfloat16)
+    X, DY = big[:, 5:5 + cols], big[:, 5 + 2 * cols:5 + 3 * cols]
+    X.copy_(torch.randn(3, cols, device="cuda", generator=g))
+    DY.copy_(torch.randn(3, cols, device="cuda", generator=g))
+    x, dy = X.contiguous(), DY.contiguous()
+    got, want = (B.layer_norm(a, None, None, EPS, want_stats=True) for a in (X, x))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for a, b in zip(B.layer_norm_backward(DY, X, None, *got[1:]),
+                    B.layer_norm_backward(dy, x, None, *got[1:])):
+        assert torch.equal(a, b)
+    T = torch.tensor([4, 1, 4], device="cuda")
+    assert torch.equal(B.embedding_backward(DY, T, 6), B.embedding_backward(dy, T, 6))
+    X.fill_(7.0)
+    DY.fill_(7.0)
+    assert bool((big == 7.0).all())

@@ -297,3 +297,14 @@ def test_direct_gradients_need_parameters_on_a_gpu():
     opt.zero_grad()
     with pytest.raises(ValueError):
         opt.step()
+
+
+@built
+def test_row_strides_are_limited():
+    """More than memory holds is refused, whatever the number of rows."""
+    far = 1 << 39
+    for bad in (dict(xs=far + 1), dict(xs=far, rows=(1 << 21) + 1), dict(xs=-8)):
+        assert _norm(**bad) == B.SM_EINVAL, bad
+        assert _norm_grad(**bad) == B.SM_EINVAL, bad
+    for bad in (dict(dys=far + 1), dict(dys=far, n=(1 << 21) + 1, nbytes=1 << 62)):
+        assert _embed_grad(**bad) == B.SM_EINVAL, bad
