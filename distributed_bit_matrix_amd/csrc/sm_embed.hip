@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void k_embed(const TW* __restrict__ W, int64_t
 //   order[p], sorted[p]: batch position and token of the p-th in sorted order
 //   total: how many tokens count
 // Bound by the clearing where the table is large (131072 x 2048 float32: 912 MB
-// in 156 to 179 us; 50257 x 768: 140 MB in 25 us), else by the instructions
+// in 160 to 180 us; 50257 x 768: 140 MB in 25 us), else by the instructions
 // that look at every token in every block, 5 to 7 for 64 of them: 65536 tokens
 // take 15 us in 256 blocks, 15.5 in 128 and 18 in 64.
 // ---------------------------------------------------------------------------
@@ -78,7 +78,6 @@ constexpr int kOneRange = 512, kOneShift = 8;   // one launch: tokens a block, f
 constexpr int kSplitRange = 2048;               // two launches
 constexpr int kWideRange = 1024;                // two launches over long runs
 
-typedef volatile __attribute__((address_space(3))) int32_t lds_i32;
 typedef volatile __attribute__((address_space(3))) uint32_t lds_u32;
 typedef volatile __attribute__((address_space(3))) uint16_t lds_u16;
 

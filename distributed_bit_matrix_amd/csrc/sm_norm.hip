@@ -43,9 +43,9 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int& turn) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  16384 x 4096 float32 takes 88 us (6.1 TB/s), 12288 x 768 bfloat16
-// 8.8 us (4.3 TB/s of what the cache holds: one load, two sums and one store
-// deep, with nothing left to overlap).
+// Forward.  16384 x 4096 float32 takes 80 to 90 us (6.0 to 6.7 TB/s), 12288 x
+// 768 bfloat16 8.6 us (4.4 TB/s of what the cache holds: one load, two sums and
+// one store deep, with nothing left to overlap).
 // ---------------------------------------------------------------------------
 template <typename T, typename TW, int V, int LANES, int NV, bool ONCE>
 __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_norm(
@@ -125,8 +125,8 @@ struct Moments {
 // from a second read that comes from a cache.  gridDim.y blocks share a row
 // where there are few: each takes the moments for itself, which costs no more
 // time than one of them would (one CU's bandwidth), and no workspace.  Float32
-// 2048 x 40000: 161 us (4.1 TB/s; 170 with 1024 threads, 195 with 256), 16 x
-// 2^20: 73 us, one row of 2^20: 47 us (44 and 81).
+// 2048 x 40000: 151 us (4.3 TB/s; 157 with 1024 threads, 173 with 256), 16 x
+// 2^20: 66 us (65 and 98), one row of 2^20: 40 us (40 and 72).
 constexpr int kLongThreads = 512;
 template <typename T, typename TW, int V>
 __global__ __launch_bounds__(kLongThreads) void k_norm_long(const T* X, int64_t xs, const TW* gamma,
@@ -764,8 +764,10 @@ hipError_t norm_grad_few(const NormGradArgs& a, hipStream_t s) {
 // Whether k_norm_grad_few serves these rows.  Kernels alone, against the two
 // launches: 1500 x 57 5.3 against 5.4 + 2.5 us, 2048 x 768 10.7 (float32 13.4)
 // against 5.9 + 3.3 (6.8 + 3.5), 2048 x 2000 14.7 (18.0) against 13.7 + 4.5
-// (13.0 + 4.4); the launch that it saves is 4 us of host time.  4000 x 57: 11
-// against 4.4 + 3.5, 512 x 16384 in a loop of calls 61 against 57.
+// (13.0 + 4.4); the launch that it saves is 4 us of host time.  So it is the
+// faster one for eager calls, which the host bounds at these sizes; replayed from
+// a graph, 2048 x 768 takes 1.5 us more than the two would (float32 3.1).  4000 x
+// 57: 11 against 4.4 + 3.5, 512 x 16384 in a loop of calls 61 against 57.
 bool few(int64_t rows, int64_t cols) {
   return rows > 0 && rows <= 2048 && rows * cols <= ((int64_t)1 << 22) && cols <= 16384;
 }

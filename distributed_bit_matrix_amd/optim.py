@@ -190,7 +190,8 @@ class SignMuon(torch.optim.Optimizer):
     float32 straight into the flat array that the step reads, neither rounded
     to a bfloat16 parameter's dtype nor copied.  The parameters have to be on
     their GPU already: they move into the flat buffer here.  Such a gradient
-    is the sum since the last step or zero_grad of this optimizer; p.grad
+    is the sum since the last step or zero_grad of this optimizer (50257 x 768
+    and 12288 tokens: 54 us less GPU time a pass, 30 us more host time); p.grad
     stays None for it (hooks on the parameter and what clips or scales p.grad do
     not see it), and what other operators put there is added to it (a table
     shared with the output product).  A state_dict holds plain tensors; a file of

@@ -110,8 +110,8 @@ def test_norm_backward(rows, cols, x_dtype):
         assert torch.equal(bits(one[k]), bits(both[k]))
 
 
-# rows times columns past what one launch serves, at the boundaries of the
-# kernels' row widths
+# many rows at the boundaries of the kernels' row widths (up to 2048 rows and
+# 2^22 entries still go in one launch)
 LARGE = [(1030, c) for c in (1, 3, 4, 7, 8, 31, 33, 63, 65, 127, 129, 255, 257, 511, 513, 767,
                              1001, 1023, 1025, 2047, 2049, 4071)] + \
     [(1025, 4097), (513, 8191), (512, 8193), (350, 12287), (340, 12289), (257, 16383),
