@@ -1,7 +1,6 @@
 """Autograd through the layers, on the CPU: the library's calls are replaced by
 elementary torch operations, so that what layers.py and optim.py do around them
 can be seen without a GPU."""
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
