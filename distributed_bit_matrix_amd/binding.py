@@ -25,6 +25,7 @@ SM_F32, SM_BF16 = 0, 1
 NS_F32, NS_BF16, NS_BF16X3 = 0, 1, 2
 SCALE_FRO, SCALE_SPECTRAL = 0, 1
 SIGNS_PACKED, SIGNS_TERNARY = 0, 1
+REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 MAX_WORKERS = 32767
 _NO_SIZE = ctypes.c_size_t(-1).value    # a workspace query refused its arguments
 
@@ -42,6 +43,8 @@ LAYER_EXPORTS = (
     "signmuon_layer_norm", "signmuon_layer_norm_backward",
     "signmuon_layer_norm_backward_workspace", "signmuon_embedding",
     "signmuon_embedding_backward", "signmuon_embedding_backward_workspace",
+    "signmuon_linear_cross_entropy", "signmuon_linear_cross_entropy_backward",
+    "signmuon_linear_cross_entropy_workspace",
 )
 PHASES = {0: "start", 1: "momentum", 2: "prescale", 3: "gemm", 4: "pack", 5: "vote",
           6: "gram", 7: "square", 8: "update", 9: "gap"}
@@ -147,6 +150,14 @@ def lib():
             "signmuon_embedding_backward": (i32, [vp, i32, i64, vp, i32, i64, i64, f32, vp, i32,
                                                   i64, i64, i32, vp, sz, vp]),
         }
+        sig.update({
+            "signmuon_linear_cross_entropy_workspace": (sz, [i64, i64, i64, i32, i32]),
+            "signmuon_linear_cross_entropy": (i32, [vp, i64, vp, i32, vp, i32, i64, i64, i64, i64,
+                                                    i32, vp, vp, vp, sz, vp]),
+            "signmuon_linear_cross_entropy_backward": (i32, [vp, vp, i64, vp, i32, vp, i32, vp,
+                                                             i64, i64, i64, i64, i32, vp, vp, i32,
+                                                             i32, vp, sz, vp]),
+        })
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
             fn.restype = res
@@ -600,6 +611,112 @@ def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Opti
         -1 if padding is None else int(padding), scale, dW.data_ptr(), _code(dW.dtype, "dW"), vocab,
         dim, accumulate, wsp, nbytes, _raw_stream(dev)))
     return dW
+
+
+def _loss_args(X, weight, targets, reduction, dev):
+    """(rows, dim, row stride, vocab, dtype code, target bits, reduction code)."""
+    rows, dim, xs = _rows(X, "X")
+    code = _code(X.dtype, "X")
+    if weight.dim() != 2 or weight.shape[1] != dim:
+        raise TypeError("weight must be a 2-D tensor with X's last dimension")
+    _check_arg(weight, weight.shape, X.dtype, dev, "weight")
+    bits = _token_bits(targets)
+    if targets.shape != X.shape[:-1]:
+        raise ValueError("targets must have X's leading shape")
+    if targets.get_device() != dev:
+        raise ValueError("targets are not on the first tensor's device")
+    if reduction not in REDUCTIONS:
+        raise ValueError("reduction must be none, sum or mean")
+    return rows, dim, xs, weight.shape[0], code, bits, REDUCTIONS[reduction]
+
+
+def linear_cross_entropy_workspace(rows: int, dim: int, vocab: int, dtype, backward: bool) -> int:
+    nbytes = lib().signmuon_linear_cross_entropy_workspace(rows, dim, vocab,
+                                                           _code(dtype, "dtype"), bool(backward))
+    if nbytes == _NO_SIZE:
+        _check("signmuon_linear_cross_entropy_workspace", SM_EINVAL)
+    return nbytes
+
+
+def linear_cross_entropy(X, weight, targets, ignore_index: int = -100, reduction: str = "mean",
+                         want_lse: bool = False, loss=None, lse=None, ws=None, stream=None):
+    """Softmax cross entropy of the logits X weight^T, which are not kept: loss,
+    or with want_lse (loss, lse).  X: float32 or bfloat16, (..., dim); weight:
+    (vocab, dim) of the same dtype; targets: int32 or int64 of X's leading shape.
+    loss is a float32 scalar for reduction "mean" (over the rows whose target is
+    not ignore_index; 0 where none is left) and "sum", and of the targets' shape
+    for "none"; lse, float32 of the targets' shape, is what the backward pass
+    needs."""
+    import torch
+    dev = _here(X, stream)
+    if dev < 0:
+        with _placed(X, stream):
+            return linear_cross_entropy(X, weight, targets, ignore_index, reduction, want_lse,
+                                        loss, lse, ws)
+    rows, dim, xs, vocab, code, bits, red = _loss_args(X, weight, targets, reduction, dev)
+    shape = targets.shape if red == 0 else targets.shape[:0]
+    if loss is None:
+        loss = torch.empty(shape, dtype=torch.float32, device=X.device)
+    else:
+        _check_arg(loss, shape, torch.float32, dev, "loss")
+    if lse is None:
+        lse = torch.empty(targets.shape, dtype=torch.float32, device=X.device)
+    else:
+        _check_arg(lse, targets.shape, torch.float32, dev, "lse")
+    ws, wsp, nbytes = _workspace(ws, linear_cross_entropy_workspace(rows, dim, vocab, X.dtype,
+                                                                    False), X, dev)
+    _check("signmuon_linear_cross_entropy", lib().signmuon_linear_cross_entropy(
+        X.data_ptr(), xs, weight.data_ptr(), code, targets.data_ptr(), bits, rows, dim, vocab,
+        int(ignore_index), red, loss.data_ptr(), lse.data_ptr(), wsp, nbytes, _raw_stream(dev)))
+    return (loss, lse) if want_lse else loss
+
+
+def linear_cross_entropy_backward(dloss, X, weight, targets, lse, ignore_index: int = -100,
+                                  reduction: str = "mean", want_x: bool = True,
+                                  want_weight: bool = True, dX=None, dweight=None, dtype=None,
+                                  accumulate: bool = False, ws=None, stream=None):
+    """(dX, dweight) of linear_cross_entropy for the float32 gradient dloss of its
+    loss, None in the place of one that is not wanted.  lse is the forward
+    pass's.  dX may be X.  dtype: dweight's (default: what dweight has, else
+    float32).  accumulate adds to the float32 dweight passed in; dX is
+    overwritten."""
+    import torch
+    dev = _here(X, stream)
+    if dev < 0:
+        with _placed(X, stream):
+            return linear_cross_entropy_backward(dloss, X, weight, targets, lse, ignore_index,
+                                                 reduction, want_x, want_weight, dX, dweight,
+                                                 dtype, accumulate, ws)
+    rows, dim, xs, vocab, code, bits, red = _loss_args(X, weight, targets, reduction, dev)
+    _check_arg(dloss, targets.shape if red == 0 else targets.shape[:0], torch.float32, dev,
+               "dloss")
+    _check_arg(lse, targets.shape, torch.float32, dev, "lse")
+    if not want_x:
+        dX = None
+    elif dX is None:
+        dX = _dense_like(X)
+    else:
+        _check_arg(dX, X.shape, X.dtype, dev, "dX")
+    dwd = SM_F32
+    if not want_weight:
+        dweight = None
+    elif dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dweight to add to")
+        dweight = torch.empty(weight.shape, dtype=dtype or torch.float32, device=X.device)
+    else:
+        _check_arg(dweight, weight.shape, dtype or dweight.dtype, dev, "dweight")
+    if want_weight:
+        dwd = _code(dweight.dtype, "dweight")
+    ws, wsp, nbytes = _workspace(ws, linear_cross_entropy_workspace(rows, dim, vocab, X.dtype,
+                                                                    True), X, dev)
+    _check("signmuon_linear_cross_entropy_backward",
+           lib().signmuon_linear_cross_entropy_backward(
+               dloss.data_ptr(), X.data_ptr(), xs, weight.data_ptr(), code, targets.data_ptr(),
+               bits, lse.data_ptr(), rows, dim, vocab, int(ignore_index), red, _ptr(dX),
+               _ptr(dweight), dwd, bool(accumulate) and want_weight, wsp, nbytes,
+               _raw_stream(dev)))
+    return dX, dweight
 
 
 def step_workspace(mats, hp: HParams, post_vote: int) -> int:

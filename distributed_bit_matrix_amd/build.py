@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsignmuon.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["sm_api.cpp", "sm_gemm.hip", "sm_elementwise.hip", "sm_layers_api.cpp",
-           "sm_norm.hip", "sm_embed.hip"]
+           "sm_norm.hip", "sm_embed.hip", "sm_mm_ops.hip", "sm_loss.hip"]
 ARCH = "gfx950"
 
 
@@ -46,7 +46,7 @@ def _compile(src: str, objdir: str = OBJDIR, defines=()) -> str:
     return obj
 
 
-def build(jobs: int = 3, verbose: bool = False, out: str = LIB, defines=()) -> str:
+def build(jobs: int = 6, verbose: bool = False, out: str = LIB, defines=()) -> str:
     """Compile the library; `out`/`defines` build a variant elsewhere."""
     objdir = OBJDIR if out == LIB else os.path.join(os.path.dirname(out), "_obj")
     os.makedirs(objdir, exist_ok=True)
@@ -64,7 +64,7 @@ def build(jobs: int = 3, verbose: bool = False, out: str = LIB, defines=()) -> s
 
 
 if __name__ == "__main__":
-    j = 3
+    j = 6
     if "-j" in sys.argv:
         j = int(sys.argv[sys.argv.index("-j") + 1])
     build(j, verbose=True)

@@ -58,4 +58,36 @@ struct EmbedGradArgs {
 size_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t s);
 
+struct LossArgs {
+  const void* X;
+  int64_t x_stride;
+  const void* W;
+  int32_t dtype;
+  const void* targets;
+  int32_t target_bits;
+  int64_t rows, dim, vocab, ignore;
+  int32_t reduction;
+  float *loss, *lse;
+  void* ws;
+};
+size_t loss_workspace(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool backward);
+hipError_t launch_loss(const LossArgs& a, hipStream_t s);   // rows > 0 for SM_LOSS_ROWS
+
+struct LossGradArgs {
+  const float* dloss;
+  const void* X;
+  int64_t x_stride;
+  const void* W;
+  int32_t dtype;
+  const void* targets;
+  int32_t target_bits;
+  const float* lse;
+  int64_t rows, dim, vocab, ignore;
+  int32_t reduction;
+  void *dX, *dW;
+  int32_t dw_dtype, accumulate;
+  void* ws;
+};
+hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s);
+
 }  // namespace sm

@@ -12,6 +12,8 @@ constexpr int64_t kMaxDim = 1 << 20;                 // cols, dim, vocab
 constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxSorted = (int64_t)1 << 27;     // 256 runs of 2^19, 2^15 tokens a wave
+constexpr int64_t kMaxMmRows = (int64_t)1 << 22;     // rows, widths of the matrix products
+constexpr int64_t kMaxMmDim = 1 << 16;
 constexpr int64_t kMaxStride = (int64_t)1 << 39;      // elements; past any memory
 
 bool dtype_ok(int32_t d) { return d == SM_F32 || d == SM_BF16; }
@@ -119,6 +121,67 @@ sm_status signmuon_embedding_backward(const void* dY, int32_t dy_dtype, int64_t 
   const EmbedGradArgs a{dY, dy_dtype, dw_dtype, token_bits, accumulate, dy_stride, tokens, n,
                         padding, scale, dW, vocab, dim, ws};
   return launch_embed_grad(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
+}
+
+size_t signmuon_linear_cross_entropy_workspace(int64_t rows, int64_t dim, int64_t vocab,
+                                               int32_t dtype, int32_t backward) {
+  if (!dtype_ok(dtype) || !in(backward, 0, 1) || !in(rows, 0, kMaxMmRows) ||
+      !in(dim, 1, kMaxMmDim) || !in(vocab, 1, kMaxDim))
+    return SIZE_MAX;
+  return loss_workspace(rows, dim, vocab, dtype, backward);
+}
+
+sm_status signmuon_linear_cross_entropy(const void* X, int64_t x_stride, const void* W,
+                                        int32_t dtype, const void* targets, int32_t target_bits,
+                                        int64_t rows, int64_t dim, int64_t vocab, int64_t ignore,
+                                        int32_t reduction, float* loss, float* lse, void* ws,
+                                        size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype) || !in(reduction, SM_LOSS_ROWS, SM_LOSS_MEAN)) return SM_EINVAL;
+  if (target_bits != 32 && target_bits != 64) return SM_EINVAL;
+  if (!in(rows, 0, kMaxMmRows) || !in(dim, 1, kMaxMmDim) || !in(vocab, 1, kMaxDim))
+    return SM_EINVAL;
+  if (rows == 0 && reduction == SM_LOSS_ROWS) return SM_OK;
+  if (!loss || !aligned(loss, SM_F32)) return SM_EINVAL;
+  if (rows > 0) {
+    if (!X || !W || !targets || !lse || !stride_ok(x_stride, rows, dim)) return SM_EINVAL;
+    if (!aligned(X, dtype) || !aligned(W, dtype) || !aligned(lse, SM_F32) ||
+        (uintptr_t)targets % (target_bits / 8))
+      return SM_EINVAL;
+  }
+  if (!workspace_ok(ws, ws_bytes, loss_workspace(rows, dim, vocab, dtype, false)))
+    return SM_EWORKSPACE;
+  const LossArgs a{X, x_stride, W, dtype, targets, target_bits, rows, dim, vocab, ignore,
+                   reduction, loss, lse, ws};
+  return launch_loss(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
+}
+
+sm_status signmuon_linear_cross_entropy_backward(
+    const float* dloss, const void* X, int64_t x_stride, const void* W, int32_t dtype,
+    const void* targets, int32_t target_bits, const float* lse, int64_t rows, int64_t dim,
+    int64_t vocab, int64_t ignore, int32_t reduction, void* dX, void* dW, int32_t dw_dtype,
+    int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(dw_dtype) || !in(reduction, SM_LOSS_ROWS, SM_LOSS_MEAN))
+    return SM_EINVAL;
+  if (target_bits != 32 && target_bits != 64) return SM_EINVAL;
+  if (!in(rows, 0, kMaxMmRows) || !in(dim, 1, kMaxMmDim) || !in(vocab, 1, kMaxDim))
+    return SM_EINVAL;
+  if (!in(accumulate, 0, 1) || (accumulate && dw_dtype != SM_F32)) return SM_EINVAL;
+  if (!dX && !dW) return SM_OK;
+  if (rows > 0) {
+    if (!dloss || !X || !W || !targets || !lse || !stride_ok(x_stride, rows, dim))
+      return SM_EINVAL;
+    if (dX && (dX == W || (dX == X && x_stride != dim))) return SM_EINVAL;
+    if (dW && (dW == X || dW == W)) return SM_EINVAL;
+    if (!aligned(dloss, SM_F32) || !aligned(X, dtype) || !aligned(W, dtype) ||
+        !aligned(lse, SM_F32) || !aligned(dX, dtype) || (uintptr_t)targets % (target_bits / 8))
+      return SM_EINVAL;
+  }
+  if (!aligned(dW, dw_dtype) || (dX && dX == dW)) return SM_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, loss_workspace(rows, dim, vocab, dtype, true)))
+    return SM_EWORKSPACE;
+  const LossGradArgs a{dloss, X, x_stride, W, dtype, targets, target_bits, lse, rows, dim,
+                       vocab, ignore, reduction, dX, dW, dw_dtype, accumulate, ws};
+  return launch_loss_grad(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
 }
 
 }  // extern "C"

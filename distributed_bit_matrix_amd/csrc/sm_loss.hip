@@ -1,0 +1,452 @@
+// Softmax cross entropy of a linear output layer (signmuon_layers.h), forward
+// and backward, without the logits in memory.
+//
+// Rows to be ignored leave first: their targets and activations are gathered
+// out, so they cost no product, and whatever they hold reaches no gradient.
+// The number of rows left stays on the device; the products' tiles past it end
+// at once.
+//
+// Forward: the product's epilogue keeps of a tile of logits each row's maximum
+// and sum of exponentials over the wave's 128 features, and the target's logit;
+// one launch joins them.  Backward, in pieces of the vocabulary: the logits of a
+// piece again, with G = (softmax - onehot) * upstream written by the epilogue
+// (the softmax's statistics are known), then dX += G W and dW = G^T X of it.
+// G is rounded to the operands' precision: for bfloat16 half a step of 2^-8 an
+// entry, as much as the rounding of the gradients themselves.
+#include <cmath>
+
+#include "sm_layers.h"
+#include "sm_mm_ops.h"
+
+namespace sm {
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+// ---------------------------------------------------------------------------
+// The list of rows that count, in order: list[i] the row, target[i] its target,
+// pos[r] its place or -1.  One block, 1024 rows a step: 12288 rows take 12
+// steps of a ballot and a sum over waves.
+// ---------------------------------------------------------------------------
+template <typename I>
+__global__ __launch_bounds__(1024) void k_loss_list(const I* targets, int rows, int64_t ignore,
+                                                    int32_t* list, int32_t* target, int32_t* pos,
+                                                    int32_t* count, int vocab) {
+  __shared__ int sums[2][16];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int base = 0, turn = 0;
+  for (int r0 = 0; r0 < rows; r0 += 1024, turn ^= 1) {
+    const int r = r0 + threadIdx.x;
+    const int64_t t = r < rows ? (int64_t)targets[r] : ignore;
+    const bool keep = r < rows && t != ignore;
+    const uint64_t b = __ballot(keep);
+    if (lane == 0) sums[turn][w] = __popcll(b);
+    __syncthreads();
+    int before = base, all = base;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k < w) before += sums[turn][k];
+      all += sums[turn][k];
+    }
+    const int at = before + __popcll(b & (((uint64_t)1 << lane) - 1));
+    if (keep) {
+      list[at] = r;
+      target[at] = t >= 0 && t < vocab ? (int)t : -1;    // -1: no such entry
+    }
+    if (r < rows) pos[r] = keep ? at : -1;
+    base = all;
+  }
+  if (threadIdx.x == 0) *count = base;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues
+// ---------------------------------------------------------------------------
+// Per row and 128 (or 64) features: maximum and sum of exp(z - maximum); the
+// target's logit.  part: [strip][cap], strips of TI * 16 features.
+struct EpiLse {
+  struct Args {
+    float2* part;
+    int64_t cap;
+    const int32_t* target;
+    float* picked;
+  };
+  template <int TI, int TJ>
+  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
+                                             const f32x4_t (&acc)[TI][TJ]) {
+    const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
+    if (at.m0 >= at.m) return;
+    const int64_t strip = at.m0 / (TI * 16);
+    const bool whole = at.m0 + TI * 16 <= at.m;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int n = nc + 16 * j;
+      const int t = n < at.n ? e.target[n] : -1;
+      const bool mine = t >= at.m0 && t < at.m0 + TI * 16 && ((t >> 2) & 3) == at.lane >> 4;
+      float mx = -INFINITY, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float v = acc[i][j][k];
+          if (whole || mc + 16 * i + k < at.m) mx = fmaxf(mx, v);
+          z = mc + 16 * i + k == t ? v : z;
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - ref) * kLog2e);
+          s += whole || mc + 16 * i + k < at.m ? p : 0.f;
+        }
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (n < at.n) {
+        if (at.lane < 16) e.part[strip * e.cap + n] = make_float2(mx, s);
+        if (mine) e.picked[n] = z;
+      }
+    }
+  }
+};
+
+// G = (exp(z - lse) - onehot) * scale of a piece of the vocabulary that begins
+// at v0: to planes of [rows][ld].
+template <int P>
+struct EpiGrad {
+  struct Args {
+    bf16_t* g;
+    int64_t ld, plane;
+    int32_t v0;
+    const int32_t* target;
+    const float *lse, *scale;
+  };
+  template <int TI, int TJ>
+  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
+                                             const f32x4_t (&acc)[TI][TJ]) {
+    const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int n = nc + 16 * j;
+      if (n >= at.n) continue;
+      const int t = e.target[n] - e.v0;
+      const float lse = e.lse[n], scale = e.scale[n];
+      bf16_t* row = e.g + (int64_t)n * e.ld;
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        const int m = mc + 16 * i;
+        if (m >= ((at.m + 7) & ~7)) continue;      // zeros up to a whole piece of 16 bytes
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * kLog2e);
+          v[k] = m + k < at.m ? (p - (m + k == t ? 1.f : 0.f)) * scale : 0.f;
+        }
+        store_planes<P>(row + m, e.plane, v);
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Forward: the strips' sums joined, 16 rows by 64 lanes over the strips.
+// loss[r], lse[r] of the caller's rows; a row whose target does not exist has
+// a NaN for its loss.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(1024) void k_loss_join(const float2* part, int64_t cap, int strips,
+                                                    const int32_t* count, const int32_t* list,
+                                                    const int32_t* target, const float* picked,
+                                                    float* loss, float* lse) {
+  __shared__ float2 sh[64][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const int n = blockIdx.x * 16 + x, live = *count;
+  if (blockIdx.x * 16 >= live) return;
+  float m = -INFINITY, s = 0.f;
+  if (n < live) {
+#pragma unroll 4
+    for (int k = y; k < strips; k += 64) {
+      const float2 v = part[k * cap + n];
+      const float top = fmaxf(m, v.x);
+      if (top == -INFINITY) {
+        s += v.y;
+      } else {
+        s = s * __builtin_amdgcn_exp2f((m - top) * kLog2e) +
+            v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2e);
+        m = top;
+      }
+    }
+  }
+  sh[y][x] = make_float2(m, s);
+  __syncthreads();
+  // a wave joins one row
+  const int row = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const float2 v = sh[lane][row];
+  float top = v.x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  float t = v.y;
+  if (v.x != -INFINITY) t *= __builtin_amdgcn_exp2f((v.x - top) * kLog2e);
+  t = lanes_sum<64>(t);
+  const int at = blockIdx.x * 16 + row;
+  if (lane == 0 && at < live) {
+    const float ln = logf(t);
+    const int r = list[at];
+    lse[r] = top + ln;
+    loss[r] = target[at] < 0 ? NAN : top - picked[at] + ln;
+  }
+}
+
+// What the ignored rows hold, and the loss summed up (in double, in an order that
+// the number of rows decides).  total: the sum, or the mean over the rows that
+// count (0 where none does).
+__global__ __launch_bounds__(1024) void k_loss_sum(const int32_t* pos, int rows,
+                                                   const int32_t* count, float* loss, float* lse,
+                                                   float* total, int mean) {
+  __shared__ double sh[1024];
+  double s = 0.0;
+  for (int r = blockIdx.x * 1024 + threadIdx.x; r < rows; r += gridDim.x * 1024) {
+    if (pos[r] < 0) loss[r] = lse[r] = 0.f;
+    else s += loss[r];
+  }
+  if (!total) return;
+  sh[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 512; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const int live = *count;
+    *total = (float)(mean && live ? sh[0] / live : sh[0]);
+  }
+}
+
+// Backward: what the epilogue needs of each row that counts.
+__global__ __launch_bounds__(256) void k_loss_rows(const int32_t* count, const int32_t* list,
+                                                   const int32_t* target, const float* lse,
+                                                   const float* dloss, int reduction, float* lse_at,
+                                                   float* scale) {
+  const int live = *count, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= live) return;
+  const int r = list[i];
+  lse_at[i] = lse[r];
+  const float up = dloss[reduction == 0 ? r : 0];
+  scale[i] = target[i] < 0 ? NAN : reduction == 2 ? up / live : up;
+}
+
+namespace {
+
+// Places in a workspace, each 256-byte aligned.
+struct Places {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += ((size_t)n * sizeof(T) + 255) / 256 * 256;
+    return p;
+  }
+};
+
+struct LossPlan {
+  int planes;
+  int32_t dim_ld;                 // row length of operand copies
+  bool copy_w, wide;
+  int64_t strips;
+  // backward
+  int64_t piece;                  // columns of a piece of the vocabulary
+  int x_splits, w_splits;
+  bool x_wide, w_wide;
+  // arrays
+  int32_t *list, *target, *pos, *count;
+  bf16_t *x, *w, *g;
+  float *picked, *loss, *lse_at, *scale, *dx, *dw;
+  float2* part;
+  size_t bytes;
+};
+
+constexpr int64_t kPieceBytes = (int64_t)1 << 30;
+
+// w_fits: the table is an operand as it lies
+LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool w_fits,
+                   bool backward, void* ws) {
+  LossPlan p{};
+  p.planes = dtype == SM_BF16 ? 1 : 3;
+  p.dim_ld = (int32_t)round_up(dim, 8);
+  p.copy_w = !w_fits;
+  p.wide = wide_tiles(vocab, rows);
+  p.strips = (vocab + (p.wide ? 127 : 63)) / (p.wide ? 128 : 64);
+  Places at{static_cast<char*>(ws)};
+  p.list = at.take<int32_t>(rows);
+  p.target = at.take<int32_t>(rows);
+  p.pos = at.take<int32_t>(rows);
+  p.count = at.take<int32_t>(1);
+  p.x = at.take<bf16_t>(p.planes * rows * p.dim_ld);
+  if (p.copy_w) p.w = at.take<bf16_t>(p.planes * vocab * p.dim_ld);
+  if (!backward) {
+    p.picked = at.take<float>(rows);
+    p.loss = at.take<float>(rows);
+    p.part = at.take<float2>(p.strips * rows);
+  } else {
+    p.lse_at = at.take<float>(rows);
+    p.scale = at.take<float>(rows);
+    const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * p.planes * rows) / 256 * 256);
+    const int64_t pieces = (vocab + most - 1) / most;
+    p.piece = std::min(round_up((vocab + pieces - 1) / pieces, 256), round_up(vocab, 8));
+    p.g = at.take<bf16_t>(p.planes * rows * p.piece);
+    const int segs = p.planes == 1 ? 1 : 6;
+    p.x_wide = wide_tiles(dim, 4 * rows);
+    p.x_splits = k_splits(dim, rows, segs * ((p.piece + 63) / 64), p.x_wide);
+    p.w_wide = wide_tiles(dim, p.piece);
+    p.w_splits = k_splits(dim, p.piece, segs * ((rows + 63) / 64), p.w_wide);
+    p.dx = at.take<float>(p.x_splits * rows * round_up(dim, 4));
+    if (p.w_splits > 1) p.dw = at.take<float>(p.w_splits * p.piece * round_up(dim, 4));
+  }
+  p.bytes = at.used;
+  return p;
+}
+
+template <typename A>
+hipError_t gather(const LossPlan& p, const A& a, hipStream_t s) {
+  const auto list = [&](auto* t) {
+    hipLaunchKernelGGL(k_loss_list, dim3(1), dim3(1024), 0, s, t, (int)a.rows, a.ignore, p.list,
+                       p.target, p.pos, p.count, (int)a.vocab);
+  };
+  if (a.target_bits == 64) list(static_cast<const int64_t*>(a.targets));
+  else list(static_cast<const int32_t*>(a.targets));
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  if (hipError_t e = launch_planes({a.X, a.x_stride, a.dtype, p.planes, a.rows, (int)a.dim, p.dim_ld,
+                                    p.list, p.count, p.x}, s); e != hipSuccess)
+    return e;
+  if (!p.copy_w) return hipSuccess;
+  return launch_planes({a.W, a.dim, a.dtype, p.planes, a.vocab, (int)a.dim, p.dim_ld, nullptr,
+                        nullptr, p.w}, s);
+}
+
+// The logits of rows [v0, v0 + cols) of the table.
+MmArgs logits(const LossPlan& p, const void* W, int64_t rows, int64_t dim, int64_t vocab,
+              int64_t v0, int64_t cols) {
+  MmArgs m{};
+  m.jobs = 1;
+  m.n_rows = p.count;
+  MmJob& j = m.job[0];
+  j.lda = p.copy_w ? p.dim_ld : dim;
+  j.a = (p.copy_w ? (const char*)p.w : (const char*)W) + v0 * j.lda * 2;
+  j.b = (const char*)p.x;
+  j.ldb = p.dim_ld;
+  j.m = (int)cols;
+  j.n = (int)rows;
+  j.k = (int)dim;
+  j.splits = 1;
+  add_segs(j, p.planes, vocab * p.dim_ld * 2, rows * p.dim_ld * 2);
+  return m;
+}
+
+template <int P>
+hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0, hipStream_t s) {
+  const int64_t cols = std::min(p.piece, a.vocab - v0), plane = a.rows * p.piece;
+  MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, v0, cols);
+  const char* w = m.job[0].a;
+  const int64_t ldw = m.job[0].lda;
+  const typename EpiGrad<P>::Args eg{p.g, p.piece, plane, (int)v0, p.target, p.lse_at, p.scale};
+  if (hipError_t e = run_mm<false, false, false, EpiGrad<P>>(m, eg, wide_tiles(cols, a.rows), s);
+      e != hipSuccess)
+    return e;
+  if (a.dX) {
+    MmArgs x{};
+    x.jobs = 1;
+    x.n_rows = p.count;
+    MmJob& j = x.job[0];
+    j.a = w;
+    j.lda = ldw;
+    j.b = (const char*)p.g;
+    j.ldb = p.piece;
+    j.m = (int)a.dim;
+    j.n = (int)a.rows;
+    j.k = (int)cols;
+    j.splits = p.x_splits;
+    add_segs(j, P, a.vocab * p.dim_ld * 2, plane * 2);
+    const int64_t ld = round_up(a.dim, 4);
+    EpiStore::Args es{};
+    es.out[0] = {p.dx, ld, a.rows * ld, SM_F32, v0 > 0};
+    if (hipError_t e = run_mm<true, false, false, EpiStore>(x, es, p.x_wide, s); e != hipSuccess)
+      return e;
+  }
+  if (a.dW) {
+    MmArgs x{};
+    x.jobs = 1;
+    x.k_rows = p.count;
+    MmJob& j = x.job[0];
+    j.a = (const char*)p.x;
+    j.lda = p.dim_ld;
+    j.b = (const char*)p.g;
+    j.ldb = p.piece;
+    j.m = (int)a.dim;
+    j.n = (int)cols;
+    j.k = (int)a.rows;
+    j.splits = p.w_splits;
+    add_segs(j, P, a.rows * p.dim_ld * 2, plane * 2);
+    const int64_t size = a.dw_dtype == SM_F32 ? 4 : 2, ld = round_up(a.dim, 4);
+    char* out = static_cast<char*>(a.dW) + v0 * a.dim * size;
+    EpiStore::Args es{};
+    if (p.w_splits > 1) es.out[0] = {p.dw, ld, cols * ld, SM_F32, 0};
+    else es.out[0] = {out, a.dim, 0, a.dw_dtype, a.accumulate};
+    if (hipError_t e = run_mm<true, true, false, EpiStore>(x, es, p.w_wide, s); e != hipSuccess)
+      return e;
+    if (p.w_splits > 1)
+      return launch_join({p.dw, cols * ld, ld, p.w_splits, nullptr, cols, (int)a.dim, a.dw_dtype,
+                          a.accumulate, out, a.dim}, s);
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t loss_workspace(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool backward) {
+  if (rows == 0) return 0;
+  // room for a table that has to be copied
+  return loss_plan(rows, dim, vocab, dtype, false, backward, nullptr).bytes;
+}
+
+hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
+  if (a.rows == 0) return launch_zero(a.loss, SM_F32, 1, s);
+  const LossPlan p = loss_plan(a.rows, a.dim, a.vocab, a.dtype,
+                               operand_fits(a.W, a.dtype, a.dim, a.dim), false, a.ws);
+  if (hipError_t e = gather(p, a, s); e != hipSuccess) return e;
+  MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, 0, a.vocab);
+  if (hipError_t e = run_mm<false, false, false, EpiLse>(
+          m, {p.part, a.rows, p.target, p.picked}, p.wide, s);
+      e != hipSuccess)
+    return e;
+  float* loss = a.reduction == 0 ? a.loss : p.loss;
+  hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, p.part,
+                     a.rows, (int)p.strips, p.count, p.list, p.target, p.picked, loss, a.lse);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_loss_sum, dim3(1), dim3(1024), 0, s, p.pos, (int)a.rows, p.count, loss,
+                     a.lse, a.reduction == 0 ? nullptr : a.loss, (int)(a.reduction == 2));
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s) {
+  if (a.rows == 0)        // a sum of nothing
+    return a.dW && !a.accumulate ? launch_zero(a.dW, a.dw_dtype, a.vocab * a.dim, s) : hipSuccess;
+  const LossPlan p = loss_plan(a.rows, a.dim, a.vocab, a.dtype,
+                               operand_fits(a.W, a.dtype, a.dim, a.dim), true, a.ws);
+  if (hipError_t e = gather(p, a, s); e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_loss_rows, dim3((unsigned)((a.rows + 255) / 256)), dim3(256), 0, s, p.count,
+                     p.list, p.target, a.lse, a.dloss, (int)a.reduction, p.lse_at, p.scale);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+    const hipError_t e = p.planes == 1 ? loss_grad_piece<1>(p, a, v0, s)
+                                       : loss_grad_piece<3>(p, a, v0, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dX) return hipSuccess;
+  const int64_t ld = round_up(a.dim, 4);
+  return launch_join({p.dx, a.rows * ld, ld, p.x_splits, p.pos, a.rows, (int)a.dim, a.dtype, 0,
+                      a.dX, a.dim}, s);
+}
+
+}  // namespace sm

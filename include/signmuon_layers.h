@@ -110,6 +110,53 @@ sm_status signmuon_embedding_backward(
     int32_t dw_dtype, int64_t vocab, int64_t dim, int32_t accumulate, void *ws,
     size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Softmax cross entropy of a linear output layer, whose logits Z = X W^T
+ * (rows x vocab) are not kept: with t = targets[r],
+ *   lse[r] = log(sum_v exp(Z[r,v])),  loss_r = lse[r] - Z[r,t].
+ * Row r of X starts at element r * x_stride (x_stride >= dim); W: contiguous
+ * vocab x dim; both of `dtype`.  targets: rows integers of target_bits (32 or
+ * 64) bits.  A row whose target is `ignore` (any integer) counts nowhere,
+ * whatever it holds, and has loss_r = lse[r] = 0; a target that is neither
+ * `ignore` nor in [0, vocab) makes its row's loss and gradients NaN.
+ * loss: float32, loss_r of every row (SM_LOSS_ROWS), or one value: their sum
+ * (SM_LOSS_SUM) or their mean over the rows that are not ignored
+ * (SM_LOSS_MEAN; 0 where none is left).  lse: float32[rows], for the backward
+ * pass.  0 <= rows <= 2^22, 1 <= dim <= 2^16, 1 <= vocab <= 2^20.
+ * ws: signmuon_linear_cross_entropy_workspace() bytes (backward = 1 for the
+ * backward call), 256-byte aligned; NULL where that is 0.  Its contents on
+ * entry do not matter.  The query returns SIZE_MAX for arguments outside the
+ * limits.
+ */
+enum { SM_LOSS_ROWS = 0, SM_LOSS_SUM = 1, SM_LOSS_MEAN = 2 };
+size_t signmuon_linear_cross_entropy_workspace(int64_t rows, int64_t dim,
+                                               int64_t vocab, int32_t dtype,
+                                               int32_t backward);
+sm_status signmuon_linear_cross_entropy(
+    const void *X, int64_t x_stride, const void *W, int32_t dtype,
+    const void *targets, int32_t target_bits, int64_t rows, int64_t dim,
+    int64_t vocab, int64_t ignore, int32_t reduction, float *loss, float *lse,
+    void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Its backward pass for the gradient dloss of loss (float32 on the device:
+ * [rows] for SM_LOSS_ROWS, else one value): with
+ *   G[r,v] = (exp(Z[r,v] - lse[r]) - [v = t]) * dloss (/ rows that count),
+ *   dX = G W,  dW = G^T X.
+ * The logits are computed again, a piece of the vocabulary after the other; a
+ * piece of G is held in the workspace, rounded to `dtype`.  lse is what the
+ * forward pass wrote.  dX: contiguous rows x dim of `dtype`, zeros in ignored
+ * rows; it may be X itself if X is contiguous.  dW: contiguous vocab x dim of
+ * dw_dtype; accumulate = 1 adds to what is there (float32 only).  Either may
+ * be NULL: it is not computed then.
+ */
+sm_status signmuon_linear_cross_entropy_backward(
+    const float *dloss, const void *X, int64_t x_stride, const void *W,
+    int32_t dtype, const void *targets, int32_t target_bits, const float *lse,
+    int64_t rows, int64_t dim, int64_t vocab, int64_t ignore,
+    int32_t reduction, void *dX, void *dW, int32_t dw_dtype,
+    int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
