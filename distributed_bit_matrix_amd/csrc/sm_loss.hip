@@ -340,7 +340,7 @@ MmArgs logits(const LossPlan& p, const void* W, int64_t rows, int64_t dim, int64
   j.n = (int)rows;
   j.k = (int)dim;
   j.splits = 1;
-  add_segs(j, p.planes, vocab * p.dim_ld * 2, rows * p.dim_ld * 2);
+  set_planes(j, p.planes, vocab * p.dim_ld * 2, rows * p.dim_ld * 2);
   return m;
 }
 
@@ -367,7 +367,7 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.n = (int)a.rows;
     j.k = (int)cols;
     j.splits = p.x_splits;
-    add_segs(j, P, a.vocab * p.dim_ld * 2, plane * 2);
+    set_planes(j, P, a.vocab * p.dim_ld * 2, plane * 2);
     const int64_t ld = round_up(a.dim, 4);
     EpiStore::Args es{};
     es.out[0] = {p.dx, ld, a.rows * ld, SM_F32, v0 > 0};
@@ -387,7 +387,7 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.n = (int)cols;
     j.k = (int)a.rows;
     j.splits = p.w_splits;
-    add_segs(j, P, a.rows * p.dim_ld * 2, plane * 2);
+    set_planes(j, P, a.rows * p.dim_ld * 2, plane * 2);
     const int64_t size = a.dw_dtype == SM_F32 ? 4 : 2, ld = round_up(a.dim, 4);
     char* out = static_cast<char*>(a.dW) + v0 * a.dim * size;
     EpiStore::Args es{};

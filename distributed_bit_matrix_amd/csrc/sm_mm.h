@@ -26,18 +26,24 @@
 namespace sm {
 
 constexpr int kSlab = 64;          // k of one slab
-constexpr int kMaxSegs = 12;       // 6 pairs of planes, two products
 constexpr int kMaxJobs = 3;
+
+// The pairs of planes of a float32 product: those whose products reach 2^-24 of
+// the largest, the small ones first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0), as
+// codes a + 4 b in four bits each.
+constexpr int kPairCode = 2 | (1 + 4) << 4 | (2 * 4) << 8 | 1 << 12 | 4 << 16;
 
 // One product of a launch.  Row lengths count elements.
 struct MmJob {
   const char *a, *a2, *b;          // a2: the second weight of a paired product
   int64_t lda, ldb;
   int32_t m, n, k;
-  int32_t segs, splits;            // splits: blocks that share a tile's k
+  int32_t pairs, parts;            // of planes: 1 or 6; products that are summed: 1 or 2
+  int32_t splits;                  // blocks that share a tile's k
   int32_t m_tiles, n_tiles;
   int32_t block0;                  // its first block
-  int64_t a_seg[kMaxSegs], b_seg[kMaxSegs];   // bytes from a and b to a segment
+  int64_t a_plane, b_plane;        // bytes from one plane to the next
+  int64_t a_part, b_part;          // bytes to the second product's operands
 };
 // n_rows, k_rows: where not null, *n_rows replaces n of every job, *k_rows k.
 struct MmArgs {
@@ -51,124 +57,196 @@ struct MmPlace {
   int job, split, m0, n0, m, n, lane;
 };
 
-template <int TM_, int TN_, int WM_, int WN_>
+template <int TM_, int TN_, int WM_, int WN_, int WPE_ = 2>
 struct MmShape {
+  static constexpr int WPE = WPE_;
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
   static constexpr int WAVES = WM * WN, TI = TM / WM / 16, TJ = TN / WN / 16;
   static constexpr int A_BYTES = TM * kSlab * 2, B_BYTES = TN * kSlab * 2;
   static constexpr int LDS = 2 * (A_BYTES + B_BYTES);
+  static constexpr int PER_CU = 131072 / LDS;     // blocks a CU
 };
 
-// One operand's slabs on their way to LDS.  Load q of a wave fills 1 KiB.
-template <bool KM, int T, int Q>
+// Where a lane's 16 bytes of load q of a slab lie: load q of a wave fills the
+// 1 KiB of LDS after the one before it, the layouts' swizzles are applied by the
+// choice of global bytes.  k along rows: 8 rows of a load, whose swizzles repeat
+// every two loads; k-major: 4 rows (of 128 columns each), every four.  So two
+// offsets serve all loads, the rest is uniform.
+template <bool KM, bool PAIR>
 struct MmSource {
-  uint32_t off[Q];
-  int chunk[Q];
-  // row0: the tile's first row (k along rows) or column (k-major) is at base
-  __device__ __forceinline__ void place(int wave, int lane, int64_t ld, int row_step) {
+  uint32_t off[2];
+  int chunk;                // k along rows: first k of the lane's bytes (load 0; load 1: ^ 32)
+  int64_t row_bytes;
+  __device__ __forceinline__ void place(int lane, int64_t ld) {
+    row_bytes = ld * 2;
+    if constexpr (KM) {
+      const int p = lane & 15, kr = lane >> 4;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int i = wave * Q + q;
-      if constexpr (KM) {
-        const int half = i >> 4, kr = 4 * (i & 15) + (lane >> 4), p = lane & 15;
-        off[q] = (uint32_t)(kr * (ld * 2) + half * 256 + (((p >> 1) ^ km_swz(kr)) << 5) +
-                            ((p & 1) << 4));
-      } else {
-        const int r = 8 * i + (lane >> 3), g = (lane & 7) ^ swz<128>(r);
-        // paired: rows of 16 alternate between two matrices
-        const int at = row_step == 2 ? (r >> 5) * 16 + (r & 15) : r;
-        off[q] = (uint32_t)(at * (ld * 2) + g * 16);
-        chunk[q] = g * 8;
-      }
+      for (int v = 0; v < 2; ++v)
+        off[v] = (uint32_t)(kr * row_bytes + ((((p >> 1) ^ km_swz(kr + 8 * v)) << 5) | (p & 1) << 4));
+    } else {
+      const int r = lane >> 3, g = (lane & 7) ^ swz<128>(r);
+      chunk = g * 8;
+      off[0] = (uint32_t)(r * row_bytes + g * 16);
+      off[1] = (uint32_t)((r + 8) * row_bytes + (g ^ 4) * 16);
     }
+  }
+  // The offsets of a slab with `left` k to the end: what is past it is out of
+  // any descriptor's range.
+  __device__ __forceinline__ void slab(int left, uint32_t (&o)[2]) const {
+    o[0] = KM || chunk < left ? off[0] : 0x80000000u;
+    o[1] = KM || (chunk ^ 32) < left ? off[1] : 0x80000000u;
+    // (opaque, or the loads' sums would be held in registers of their own)
+    if constexpr (KM) asm volatile("" : "+v"(o[0]), "+v"(o[1]));
+  }
+  // load i of the operand's tile
+  __device__ __forceinline__ uint32_t at(const uint32_t (&o)[2], int i) const {
+    if constexpr (KM) return o[(i >> 1) & 1] + (uint32_t)(4 * (i & 15) * row_bytes + (i >> 4) * 256);
+    // 16 rows of a group; paired, groups alternate between two matrices
+    return o[i & 1] + (uint32_t)((PAIR ? i >> 2 : i >> 1) * 16 * row_bytes);
   }
 };
 
+// A descriptor of `bytes` from p on; everything in it is uniform, which the
+// compiler has to be told of what was divided.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_rsrc(const char* p, int64_t bytes) {
   const int64_t cap = 0x7FFFFFFF;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0,
-                                           (int)(bytes < 0 ? 0 : bytes < cap ? bytes : cap),
-                                           0x00020000);
+  const int size = (int)(bytes < 0 ? 0 : bytes < cap ? bytes : cap);
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<char*>(uniform(reinterpret_cast<int64_t>(p))), 0,
+      __builtin_amdgcn_readfirstlane(size), 0x00020000);
+}
+
+// The transposing read behind a pointer of its own: without that scope the
+// compiler takes the read for one of what the loads to LDS still bring, and waits
+// for all of them (8192^3, both operands k-major: 1070 TFLOP/s without the wait).
+// The kernel waits for them itself.
+__device__ __forceinline__ u32x2_t mm_read_tr16(const char* __restrict__ p) {
+  return lds_read_tr16(p);
 }
 
 // AKM, BKM: the operand is k-major.  PAIR: A's rows alternate in groups of 16
 // between a and a2 (a tile has TM / 2 features of each).
 template <bool AKM, bool BKM, bool PAIR, class Sh, class Epi>
-__global__ __launch_bounds__(64 * Sh::WAVES, 2) void k_mm(MmArgs args, typename Epi::Args ea) {
+__global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args, typename Epi::Args ea) {
+#ifdef __HIP_DEVICE_COMPILE__      // (its buffer instructions are unknown to the host's pass)
   constexpr int TM = Sh::TM, TN = Sh::TN, TI = Sh::TI, TJ = Sh::TJ;
   constexpr int QA = Sh::A_BYTES / 1024 / Sh::WAVES, QB = Sh::B_BYTES / 1024 / Sh::WAVES;
-  static_assert(!PAIR || (!AKM && QA == 4), "paired rows");
+  static_assert(!PAIR || (!AKM && QA % 4 == 0), "paired rows");
   __shared__ __align__(1024) char smem[Sh::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
 
-  int ji = 0;
+  constexpr int STAGE_A = Sh::A_BYTES, STAGE_B = Sh::B_BYTES;
+  char* const lds_a = smem + wave * QA * 1024;
+  char* const lds_b = smem + 2 * STAGE_A + wave * QB * 1024;
+  MmSource<AKM, PAIR> sa;
+  MmSource<BKM, false> sb;
+
+  // The tile whose slabs are loaded (every value is uniform): where its operands
+  // begin, how far they may be read, and the next slab's segment and first k.
+  int ji, split, m0, n0, m_all, n_all, k_all;
+  int slabs, to_load, seg, k0, pairs, a_rows, b_rows, m_end, n_end;
+  int64_t lda, ldb, a_plane, b_plane, a_part, b_part;
+  const char *pa, *pa2, *pb;
+  // Takes tile `at` of the launch; false where there is none.
+  auto take = [&](int at) SM_INLINE -> bool {
+    ji = 0;
 #pragma unroll
-  for (int i = 1; i < kMaxJobs; ++i)
-    if (i < args.jobs && (int)blockIdx.x >= args.job[i].block0) ji = i;
-  const MmJob& job = args.job[ji];
-  const int n_all = args.n_rows ? *args.n_rows : job.n;
-  const int k_all = args.k_rows ? *args.k_rows : job.k;
-  const int m_tiles = job.m_tiles, n_tiles = args.n_rows ? (n_all + TN - 1) / TN : job.n_tiles;
-  // Blocks go round the 8 XCDs: each gets a run of neighbouring tiles, in
-  // groups of 4 tiles along n, so that its L2 holds what they share.
-  const int total = m_tiles * n_tiles * job.splits;
-  int at = blockIdx.x - job.block0;
-  if (at >= total) return;
-  {
+    for (int i = 1; i < kMaxJobs; ++i)
+      if (i < args.jobs && at >= args.job[i].block0) ji = i;
+    const MmJob& job = args.job[ji];
+    m_all = job.m;
+    n_all = __builtin_amdgcn_readfirstlane(args.n_rows ? *args.n_rows : job.n);
+    k_all = __builtin_amdgcn_readfirstlane(args.k_rows ? *args.k_rows : job.k);
+    const int m_tiles = job.m_tiles;
+    const int n_tiles = args.n_rows ? (n_all + TN - 1) / TN : job.n_tiles;
+    // Blocks go round the 8 XCDs: each gets a run of neighbouring tiles, in
+    // groups of 4 tiles along n, so that its L2 holds what they share.
+    const int total = m_tiles * n_tiles * job.splits;
+    at -= job.block0;
+    if (at >= total) return false;
     const int x = at & 7, q = total >> 3, r = total & 7;
     at = x * q + (x < r ? x : r) + (at >> 3);
-  }
-  const int split = at / (m_tiles * n_tiles);
-  at -= split * m_tiles * n_tiles;
-  const int group = at / (4 * m_tiles), g0 = group * 4;
-  const int gn = n_tiles - g0 < 4 ? n_tiles - g0 : 4;
-  at -= g0 * m_tiles;
-  const int mt = at / gn, nt = g0 + at % gn;
-  const int m0 = mt * (PAIR ? TM / 2 : TM), n0 = nt * TN;
-  const int m_here = job.m - m0, n_here = n_all - n0 < TN ? n_all - n0 : TN;
+    split = __builtin_amdgcn_readfirstlane(at / (m_tiles * n_tiles));
+    at -= split * m_tiles * n_tiles;
+    const int g0 = __builtin_amdgcn_readfirstlane(at / (4 * m_tiles)) * 4;
+    const int gn = n_tiles - g0 < 4 ? n_tiles - g0 : 4;
+    at -= g0 * m_tiles;
+    const int mt = __builtin_amdgcn_readfirstlane(at / gn);
+    m0 = mt * (PAIR ? TM / 2 : TM);
+    n0 = (g0 + at - mt * gn) * TN;
+    lda = job.lda * 2;
+    ldb = job.ldb * 2;
+    const int a_tile = PAIR ? TM / 2 : TM;
+    a_rows = m_all - m0 < a_tile ? m_all - m0 : a_tile;
+    b_rows = n_all - n0 < TN ? n_all - n0 : TN;
+    m_end = (m_all - m0 + 7) & ~7;
+    n_end = (n_all - n0 + 7) & ~7;
+    sa.place(lane, job.lda);
+    sb.place(lane, job.ldb);
+    const int64_t a0 = AKM ? (int64_t)m0 * 2 : m0 * lda;
+    const int64_t b0 = BKM ? (int64_t)n0 * 2 : n0 * ldb;
+    pa = job.a + a0;
+    if constexpr (PAIR) pa2 = job.a2 + a0;
+    pb = job.b + b0;
+    a_plane = job.a_plane;
+    b_plane = job.b_plane;
+    a_part = job.a_part;
+    b_part = job.b_part;
+    pairs = job.pairs;
+    const int per_seg = (k_all + kSlab - 1) / kSlab, all = per_seg * pairs * job.parts;
+    const int per = __builtin_amdgcn_readfirstlane((all + job.splits - 1) / job.splits);
+    const int s0 = split * per;
+    const int s1 = __builtin_amdgcn_readfirstlane(s0 + per < all ? s0 + per : all);
+    to_load = slabs = s1 - s0;
+    seg = __builtin_amdgcn_readfirstlane(s0 < s1 ? s0 / per_seg : 0);
+    k0 = (s0 - seg * per_seg) * kSlab;
+    return true;
+  };
 
-  MmSource<AKM, TM, QA> sa;
-  MmSource<BKM, TN, QB> sb;
-  sa.place(wave, lane, job.lda, PAIR ? 2 : 1);
-  sb.place(wave, lane, job.ldb, 1);
-  const int64_t a0 = AKM ? (int64_t)m0 * 2 : (int64_t)m0 * job.lda * 2;
-  const int64_t b0 = BKM ? (int64_t)n0 * 2 : (int64_t)n0 * job.ldb * 2;
-  const int m_rows = PAIR ? (m_here < TM / 2 ? m_here : TM / 2) : (m_here < TM ? m_here : TM);
-  const int per_seg = (k_all + kSlab - 1) / kSlab;
-  const int slabs = per_seg * job.segs;
-  const int per = (slabs + job.splits - 1) / job.splits;
-  const int s0 = split * per, s1 = s0 + per < slabs ? s0 + per : slabs;
-
-  auto issue = [&](int s, int stage) SM_INLINE {
-    const int seg = s / per_seg, k0 = (s - seg * per_seg) * kSlab, left = k_all - k0;
-    const int rows = left < kSlab ? left : kSlab;
-    char* la = smem + stage * (Sh::A_BYTES + Sh::B_BYTES) + wave * QA * 1024;
-    char* lb = smem + stage * (Sh::A_BYTES + Sh::B_BYTES) + Sh::A_BYTES + wave * QB * 1024;
+  __amdgpu_buffer_rsrc_t ra, ra2, rb;
+  uint32_t oa[2], ob[2];
+  // What the next slab's loads need, and the loads.  Past the last slab the
+  // descriptors are empty, and zeros come.
+  auto aim = [&]() SM_INLINE {
+    const int left = k_all - k0, rows = left < kSlab ? left : kSlab;
+    const int part = seg >= pairs ? 1 : 0, pair = seg - part * pairs;
+    // the planes of a pair, in kPairs' order; one plane has one pair (0, 0)
+    const int pl = pairs == 1 ? 0 : kPairCode >> (4 * pair);
+    const int64_t a_at = (pl & 3) * a_plane + part * a_part + (AKM ? k0 * lda : (int64_t)k0 * 2);
+    const int64_t b_at =
+        (pl >> 2 & 3) * b_plane + part * b_part + (BKM ? k0 * ldb : (int64_t)k0 * 2);
     // bytes from the slab's base to the end of what may be read
-    const int64_t a_at = a0 + job.a_seg[seg] + (AKM ? k0 * job.lda * 2 : (int64_t)k0 * 2);
-    const int64_t b_at = b0 + job.b_seg[seg] + (BKM ? k0 * job.ldb * 2 : (int64_t)k0 * 2);
-    const int64_t a_end = AKM ? ((rows - 1) * job.lda + ((m_here + 7) & ~7)) * 2
-                              : ((m_rows - 1) * job.lda + ((left + 7) & ~7)) * 2;
-    const int64_t b_end = BKM ? ((rows - 1) * job.ldb + ((n_all - n0 + 7) & ~7)) * 2
-                              : ((n_here - 1) * job.ldb + ((left + 7) & ~7)) * 2;
-    const auto ra = mm_rsrc(job.a + a_at, a_end);
-    const auto ra2 = PAIR ? mm_rsrc(job.a2 + a_at, a_end) : ra;
-    const auto rb = mm_rsrc(job.b + b_at, b_end);
+    const int64_t a_end = AKM ? (rows - 1) * lda + m_end * 2
+                              : (a_rows - 1) * lda + ((left + 7) & ~7) * 2;
+    const int64_t b_end = BKM ? (rows - 1) * ldb + n_end * 2
+                              : (b_rows - 1) * ldb + ((left + 7) & ~7) * 2;
+    ra = mm_rsrc(pa + a_at, to_load > 0 ? a_end : 0);
+    if constexpr (PAIR) ra2 = mm_rsrc(pa2 + a_at, to_load > 0 ? a_end : 0);
+    rb = mm_rsrc(pb + b_at, to_load > 0 ? b_end : 0);
+    sa.slab(left, oa);
+    sb.slab(left, ob);
+    --to_load;
+    k0 += kSlab;
+    if (k0 >= k_all) k0 = 0, ++seg;
+  };
+  auto fire = [&](int stage) SM_INLINE {
 #pragma unroll
-    for (int q = 0; q < QA; ++q) {
-      uint32_t o = sa.off[q];
-      if constexpr (!AKM) o = sa.chunk[q] < left ? o : 0x80000000u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(PAIR && q >= 2 ? ra2 : ra,
-                                               (lds_void*)(la + q * 1024), 16, o, 0, 0, 0);
-    }
+    for (int q = 0; q < QA; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(PAIR && (q >> 1 & 1) ? ra2 : ra,
+                                               (lds_void*)(lds_a + stage * STAGE_A + q * 1024), 16,
+                                               sa.at(oa, wave * QA + q), 0, 0, 0);
 #pragma unroll
-    for (int q = 0; q < QB; ++q) {
-      uint32_t o = sb.off[q];
-      if constexpr (!BKM) o = sb.chunk[q] < left ? o : 0x80000000u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(lb + q * 1024), 16, o, 0, 0, 0);
-    }
+    for (int q = 0; q < QB; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb,
+                                               (lds_void*)(lds_b + stage * STAGE_B + q * 1024), 16,
+                                               sb.at(ob, wave * QB + q), 0, 0, 0);
   };
 
   // A fragment of MFMA tile t (16 rows from the wave's first) and k-step kk.
@@ -179,51 +257,120 @@ __global__ __launch_bounds__(64 * Sh::WAVES, 2) void k_mm(MmArgs args, typename 
                            km_off<bf16_t>(8 * (lane >> 4) + ((lane & 15) >> 2),
                                           2 * (wm * RA & 127) + 8 * (lane & 3))
                      : lds_off<128>(wm * RA + (lane & 15), lane >> 4);
-  const int fb = Sh::A_BYTES +
+  const int fb = 2 * STAGE_A +
                  (BKM ? (wn * RB >> 7) * 16384 +
                             km_off<bf16_t>(8 * (lane >> 4) + ((lane & 15) >> 2),
                                            2 * (wn * RB & 127) + 8 * (lane & 3))
                       : lds_off<128>(wn * RB + (lane & 15), lane >> 4));
-  auto frag = [&](auto km, const char* st, int base, int t, int kk) SM_INLINE -> bf16x8_t {
+  auto frag = [&](auto km, int base, int stage_at, int t, int kk) SM_INLINE -> bf16x8_t {
     if constexpr (decltype(km)::value) {
-      const char* p = st + (base ^ (t << 5)) + kk * 8192;
-      const u32x2_t lo = lds_read_tr16(p), hi = lds_read_tr16(p + 1024);
+      const char* p = smem + (base ^ (t << 5)) + stage_at + kk * 8192;
+      const u32x2_t lo = mm_read_tr16(p), hi = mm_read_tr16(p + 1024);
       return __builtin_bit_cast(bf16x8_t, u32x4_t{lo[0], lo[1], hi[0], hi[1]});
     } else {
-      return *reinterpret_cast<const bf16x8_t*>(st + (base ^ (kk << 6)) + t * 2048);
+      return *reinterpret_cast<const bf16x8_t*>(smem + (base ^ (kk << 6)) + stage_at + t * 2048);
     }
   };
 
   f32x4_t acc[TI][TJ];
+  // A slab goes in four steps: its two k-steps of 32, by halves of A's rows.
+  // While one is multiplied the fragments of the next are read.  The next slab
+  // is waited for before the last step: past that barrier every wave has read
+  // all of this slab, whose place the loads of the slab after next then take.
+  constexpr int HI = TI / 2;
+  bf16x8_t a[2][HI], b[2][TJ];
+  auto read_a = [&](auto set, int stage, int kk, int half) SM_INLINE {
+    constexpr int S = decltype(set)::value;
+#pragma unroll
+    for (int i = 0; i < HI; ++i)
+      a[S][i] = frag(std::bool_constant<AKM>{}, fa, stage * STAGE_A, half * HI + i, kk);
+  };
+  auto read_b = [&](auto set, int stage, int kk) SM_INLINE {
+    constexpr int S = decltype(set)::value;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      b[S][j] = frag(std::bool_constant<BKM>{}, fb, stage * STAGE_B, j, kk);
+  };
+  auto multiply = [&](auto kk, auto half) SM_INLINE {
+    constexpr int K = decltype(kk)::value, H = decltype(half)::value;
+#pragma unroll
+    for (int i = 0; i < HI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[H * HI + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[H][i], b[K][j],
+                                                                    acc[H * HI + i][j], 0, 0, 0);
+  };
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
+  // the order of a step's instructions: its reads first, then the products, with
+  // `loads` loads among them
+  auto order = [&](auto reads, auto loads) SM_INLINE {
+    constexpr int R = decltype(reads)::value, L = decltype(loads)::value;
+    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    if constexpr (L == 0) {
+      __builtin_amdgcn_sched_group_barrier(0x008, HI * TJ, 0);
+    } else {
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        __builtin_amdgcn_sched_group_barrier(0x008, HI * TJ / L, 0);
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int RDA = HI * (AKM ? 2 : 1), RDB = TJ * (BKM ? 2 : 1);
+  constexpr std::integral_constant<int, RDA> reads_a{};
+  constexpr std::integral_constant<int, RDA + RDB> reads_ab{};
+  constexpr std::integral_constant<int, QA + QB> loads{};
+  auto slab = [&](int stage) SM_INLINE {
+    read_a(c1, stage, 0, 1);
+    multiply(c0, c0);
+    order(reads_a, c0);
+    read_b(c1, stage, 1);
+    read_a(c0, stage, 1, 0);
+    aim();
+    multiply(c0, c1);
+    order(reads_ab, c0);
+    read_a(c1, stage, 1, 1);
+    multiply(c1, c0);
+    order(reads_a, c0);
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read_b(c0, stage ^ 1, 0);
+    read_a(c0, stage ^ 1, 0, 0);
+    fire(stage);
+    multiply(c1, c1);
+    order(reads_ab, loads);
+  };
+  if (!take(blockIdx.x)) return;
+  aim();
+  fire(0);
+  aim();
+  fire(1);
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  if (s0 < s1) issue(s0, 0);
-  for (int s = s0; s < s1; ++s) {
-    const int stage = (s - s0) & 1;
-    wait_vmcnt<0>();
-    wait_lgkmcnt0();
-    __builtin_amdgcn_s_barrier();
-    if (s + 1 < s1) issue(s + 1, stage ^ 1);
-    const char* st = smem + stage * (Sh::A_BYTES + Sh::B_BYTES);
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8_t a[TI], b[TJ];
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) b[j] = frag(std::bool_constant<BKM>{}, st, fb, j, kk);
-#pragma unroll
-      for (int i = 0; i < TI; ++i) a[i] = frag(std::bool_constant<AKM>{}, st, fa, i, kk);
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-    }
+  wait_vmcnt<QA + QB>();
+  __builtin_amdgcn_s_barrier();
+  read_b(c0, 0, 0);
+  read_a(c0, 0, 0, 0);
+  // (an odd slab too many is zeros)
+  for (int s = 0; s < slabs; s += 2) {
+    slab(0);
+    slab(1);
   }
-  const MmPlace at_wave{ji, split, m0 + wm * (PAIR ? RA / 2 : RA), n0 + wn * RB, job.m, n_all, lane};
-  Epi::template run<TI, TJ>(ea, at_wave, acc);
+  wait_vmcnt<0>();      // nothing may arrive in LDS after the block's end
+  // (opaque, so that the epilogue's addresses are not held through the loop)
+  int lane_after = lane;
+  asm volatile("" : "+v"(lane_after));
+  Epi::template run<TI, TJ>(ea,
+                            MmPlace{ji, split, m0 + wm * (PAIR ? RA / 2 : RA), n0 + wn * RB, m_all,
+                                    n_all, lane_after},
+                            acc);
+#endif
 }
 
 }  // namespace sm

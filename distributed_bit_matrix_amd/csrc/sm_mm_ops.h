@@ -45,42 +45,47 @@ struct EpiStore {
   struct Args {
     MmOut out[kMaxJobs];
   };
-  template <int TI, int TJ>
-  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
-                                             const f32x4_t (&acc)[TI][TJ]) {
-    const MmOut o = e.out[at.job];
+  template <typename T, bool WHOLE, bool ADD, int TI, int TJ>
+  static __device__ __forceinline__ void store(T* p, int64_t ld, const MmPlace& at,
+                                               const f32x4_t (&acc)[TI][TJ]) {
     const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int n = nc + 16 * j;
-      if (n >= at.n) continue;
-      const int64_t row = (int64_t)n * o.ld + at.split * o.split_step;
+      if (!WHOLE && nc + 16 * j >= at.n) continue;
+      T* row = p + (int64_t)(nc + 16 * j) * ld + mc;
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
-        const int m = mc + 16 * i;
-        if (m >= at.m) continue;
-        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        const int here = at.m - m;
-        if (o.dtype == SM_F32) {
-          float* p = static_cast<float*>(o.p) + row + m;
-          if (here >= 4) {
-            if (o.add) {
-              const u32x4_a4 t = *reinterpret_cast<const u32x4_a4*>(p);
+        const int here = WHOLE ? 4 : at.m - mc - 16 * i;
+        float v[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] += __uint_as_float(t[k]);
-            }
-            store_vec<4>(p, v);
-          } else {
-            for (int k = 0; k < here; ++k) p[k] = (o.add ? p[k] : 0.f) + v[k];
-          }
+        for (int k = 0; k < 4; ++k)
+          v[k] = (ADD && k < here ? to_f32(row[16 * i + k]) : 0.f) + acc[i][j][k];
+        if (here >= 4) {
+          store_vec<4>(row + 16 * i, v);
         } else {
-          bf16_t* p = static_cast<bf16_t*>(o.p) + row + m;
-          if (here >= 4) store_vec<4>(p, v);
-          else
-            for (int k = 0; k < here; ++k) p[k] = f32_to_bf16(v[k]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (k < here) put(row + 16 * i + k, v[k]);
         }
       }
     }
+  }
+  template <typename T, bool ADD, int TI, int TJ>
+  static __device__ __forceinline__ void store_as(const MmOut& o, const MmPlace& at,
+                                                  const f32x4_t (&acc)[TI][TJ]) {
+    T* p = static_cast<T*>(o.p) + at.split * o.split_step;
+    if (at.m0 + 16 * TI <= at.m && at.n0 + 16 * TJ <= at.n)
+      store<T, true, ADD>(p, o.ld, at, acc);
+    else
+      store<T, false, ADD>(p, o.ld, at, acc);
+  }
+  template <int TI, int TJ>
+  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
+                                             const f32x4_t (&acc)[TI][TJ]) {
+    const MmOut& o = e.out[at.job];
+    if (o.dtype == SM_BF16) store_as<bf16_t, false>(o, at, acc);
+    else if (o.add) store_as<float, true>(o, at, acc);
+    else store_as<float, false>(o, at, acc);
   }
 };
 
@@ -121,17 +126,12 @@ inline bool operand_fits(const void* p, int32_t dtype, int64_t cols, int64_t str
          stride <= ((int64_t)1 << 21);
 }
 
-// The pairs of planes of a float32 product: those whose products reach 2^-24 of
-// the largest.  The small ones come first.
-constexpr int kPairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
-// Adds the segments of one product to a job; planes: 1 or 3, a_plane and b_plane
-// in bytes, a_at and b_at where the product's operands begin.
-inline void add_segs(MmJob& j, int planes, int64_t a_plane, int64_t b_plane, int64_t a_at = 0,
-                     int64_t b_at = 0) {
-  for (int s = 0; s < (planes == 1 ? 1 : 6); ++s) {
-    j.a_seg[j.segs] = a_at + (planes == 1 ? 0 : kPairs[s][0] * a_plane);
-    j.b_seg[j.segs++] = b_at + (planes == 1 ? 0 : kPairs[s][1] * b_plane);
-  }
+// The planes of a job's operands; a_plane and b_plane in bytes.
+inline void set_planes(MmJob& j, int planes, int64_t a_plane, int64_t b_plane) {
+  j.pairs = planes == 1 ? 1 : 6;
+  j.parts = 1;
+  j.a_plane = a_plane;
+  j.b_plane = b_plane;
 }
 
 constexpr int kCus = 256;
@@ -148,7 +148,7 @@ inline int k_splits(int64_t m, int64_t n, int64_t slabs, bool wide) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, slabs / 8, 16}));
 }
 
-// Launches the jobs of `a` (operands, extents, segments and splits are set).
+// Launches the jobs of `a` (operands, extents, planes and splits are set).
 template <bool AKM, bool BKM, bool PAIR, class Sh, class Epi>
 hipError_t run_mm_as(MmArgs& a, const typename Epi::Args& e, hipStream_t s) {
   int64_t blocks = 0;
