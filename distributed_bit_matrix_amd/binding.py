@@ -25,6 +25,7 @@ SM_F32, SM_BF16 = 0, 1
 NS_F32, NS_BF16, NS_BF16X3 = 0, 1, 2
 SCALE_FRO, SCALE_SPECTRAL = 0, 1
 SIGNS_PACKED, SIGNS_TERNARY = 0, 1
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 MAX_WORKERS = 32767
 _NO_SIZE = ctypes.c_size_t(-1).value    # a workspace query refused its arguments
@@ -44,7 +45,9 @@ LAYER_EXPORTS = (
     "signmuon_layer_norm_backward_workspace", "signmuon_embedding",
     "signmuon_embedding_backward", "signmuon_embedding_backward_workspace",
     "signmuon_linear_cross_entropy", "signmuon_linear_cross_entropy_backward",
-    "signmuon_linear_cross_entropy_workspace",
+    "signmuon_linear_cross_entropy_workspace", "signmuon_rms_norm", "signmuon_rms_norm_e4m3",
+    "signmuon_rms_norm_backward", "signmuon_rms_norm_backward_workspace", "signmuon_gated_mlp",
+    "signmuon_gated_mlp_backward", "signmuon_gated_mlp_workspace",
 )
 PHASES = {0: "start", 1: "momentum", 2: "prescale", 3: "gemm", 4: "pack", 5: "vote",
           6: "gram", 7: "square", 8: "update", 9: "gap"}
@@ -157,6 +160,19 @@ def lib():
             "signmuon_linear_cross_entropy_backward": (i32, [vp, vp, i64, vp, i32, vp, i32, vp,
                                                              i64, i64, i64, i64, i32, vp, vp, i32,
                                                              i32, vp, sz, vp]),
+            "signmuon_rms_norm": (i32, [vp, i64, vp, i64, i32, vp, i32, i64, i64, f32, vp, vp, vp,
+                                        vp]),
+            "signmuon_rms_norm_e4m3": (i32, [vp, i64, vp, i64, i32, vp, i32, i64, i64, f32, i64,
+                                             vp, vp, vp, vp, vp]),
+            "signmuon_rms_norm_backward_workspace": (sz, [i64, i64]),
+            "signmuon_rms_norm_backward": (i32, [vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, i64,
+                                                 i64, vp, vp, i32, i32, vp, sz, vp]),
+            "signmuon_gated_mlp_workspace": (sz, [i64, i64, i64, i32, i32]),
+            "signmuon_gated_mlp": (i32, [vp, i64, vp, vp, vp, i32, i32, i64, i64, i64, vp, vp, vp,
+                                         sz, vp]),
+            "signmuon_gated_mlp_backward": (i32, [vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i64,
+                                                  i64, i64, vp, vp, vp, vp, i32, i32, vp, sz,
+                                                  vp]),
         })
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -611,6 +627,250 @@ def embedding_backward(dY, tokens, vocab: int, scale: float = 1.0, padding: Opti
         -1 if padding is None else int(padding), scale, dW.data_ptr(), _code(dW.dtype, "dW"), vocab,
         dim, accumulate, wsp, nbytes, _raw_stream(dev)))
     return dW
+
+
+def _rms_args(X, weight, residual, H, rstd, want_stats, dev):
+    """(rows, cols, x stride, residual stride, x code, weight code, H, rstd)."""
+    import torch
+    rows, cols, xs = _rows(X, "X")
+    xd = wd = _code(X.dtype, "X")
+    rs = xs
+    if weight is not None:
+        wd = _code(weight.dtype, "weight")
+        _check_arg(weight, (cols,), weight.dtype, dev, "weight")
+    if residual is not None:
+        if residual.dtype != X.dtype or residual.shape != X.shape:
+            raise TypeError("residual must have X's dtype and shape")
+        if residual.get_device() != dev:
+            raise ValueError("residual is not on the first tensor's device")
+        rs = _rows(residual, "residual")[2]
+        if H is None:
+            H = _dense_like(X)
+        else:
+            _check_arg(H, X.shape, X.dtype, dev, "H")
+    elif H is not None:
+        raise ValueError("H is the sum with a residual")
+    if rstd is not None:
+        _check_arg(rstd, X.shape[:-1], torch.float32, dev, "rstd")
+    elif want_stats:
+        rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+    return rows, cols, xs, rs, xd, wd, H, rstd
+
+
+def rms_norm(X, weight=None, residual=None, eps: float = 1e-6, want_stats: bool = False, Y=None,
+             H=None, rstd=None, stream=None):
+    """Root-mean-square norm over the last dimension of X, or of X + residual: Y
+    without a residual, else (Y, H) with H the sum, rounded to X's dtype, that the
+    norm is taken of.  With want_stats always (Y, H, rstd), H being X without a
+    residual; rstd is float32 of X's leading shape.  X and residual: float32 or
+    bfloat16; weight: float32 or bfloat16, None for ones.  H may be X or residual, Y
+    may be X."""
+    dev = _here(X, stream)
+    if dev < 0:
+        with _placed(X, stream):
+            return rms_norm(X, weight, residual, eps, want_stats, Y, H, rstd)
+    rows, cols, xs, rs, xd, wd, H, rstd = _rms_args(X, weight, residual, H, rstd, want_stats, dev)
+    if Y is None:
+        Y = _dense_like(X)
+    else:
+        _check_arg(Y, X.shape, X.dtype, dev, "Y")
+    _check("signmuon_rms_norm", lib().signmuon_rms_norm(
+        X.data_ptr(), xs, _ptr(residual), rs, xd, _ptr(weight), wd, rows, cols, eps, _ptr(H),
+        Y.data_ptr(), _ptr(rstd), _raw_stream(dev)))
+    if want_stats:
+        return Y, X if H is None else H, rstd
+    return Y if H is None else (Y, H)
+
+
+def rms_norm_e4m3(X, weight=None, residual=None, eps: float = 1e-6, block: Optional[int] = 128,
+                  want_stats: bool = False, Q=None, scales=None, H=None, rstd=None, stream=None):
+    """rms_norm with its output in 8 bits: (Q, scales), (Q, scales, H) with a
+    residual, and with want_stats (Q, scales, H, rstd).  Q: float8_e4m3fn of X's
+    shape; scales: float32, one for each `block` = 128 columns of a row (None: one a
+    row); Q * scale stands for Y, the largest value of a block for 448 * scale.  Rows
+    of up to 16384 columns."""
+    import torch
+    dev = _here(X, stream)
+    if dev < 0:
+        with _placed(X, stream):
+            return rms_norm_e4m3(X, weight, residual, eps, block, want_stats, Q, scales, H, rstd)
+    rows, cols, xs, rs, xd, wd, H, rstd = _rms_args(X, weight, residual, H, rstd, want_stats, dev)
+    if Q is None:
+        Q = torch.empty(X.shape, dtype=torch.float8_e4m3fn, device=X.device)
+    else:
+        _check_arg(Q, X.shape, torch.float8_e4m3fn, dev, "Q")
+    if block is not None and block != 128:
+        raise ValueError("block must be 128, or None for a whole row")
+    shape = X.shape[:-1] + (1 if block is None else -(-cols // 128),)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=X.device)
+    else:
+        _check_arg(scales, shape, torch.float32, dev, "scales")
+    _check("signmuon_rms_norm_e4m3", lib().signmuon_rms_norm_e4m3(
+        X.data_ptr(), xs, _ptr(residual), rs, xd, _ptr(weight), wd, rows, cols, eps, block or 0,
+        _ptr(H), Q.data_ptr(), scales.data_ptr(), _ptr(rstd), _raw_stream(dev)))
+    if want_stats:
+        return Q, scales, X if H is None else H, rstd
+    return (Q, scales) if H is None else (Q, scales, H)
+
+
+def rms_norm_backward_workspace(rows: int, cols: int) -> int:
+    n = lib().signmuon_rms_norm_backward_workspace(rows, cols)
+    if n == _NO_SIZE:
+        _check("signmuon_rms_norm_backward_workspace", SM_EINVAL)
+    return n
+
+
+def rms_norm_backward(dY, H, weight, rstd, dH=None, want_x: bool = True, want_weight: bool = True,
+                      dX=None, dweight=None, dtype=None, accumulate: bool = False, ws=None,
+                      stream=None):
+    """(dX, dweight) of rms_norm for the gradients dY of Y and dH of H (None: H has
+    no other use), None in the place of one that is not wanted.  dX is the gradient
+    of X and of the residual.  H and rstd are the forward pass's; dX may be dY or dH.
+    dtype: dweight's (default: what dweight has, else float32).  accumulate adds to
+    the float32 dweight passed in; dX is overwritten."""
+    import torch
+    dev = _here(dY, stream)
+    if dev < 0:
+        with _placed(dY, stream):
+            return rms_norm_backward(dY, H, weight, rstd, dH, want_x, want_weight, dX, dweight,
+                                     dtype, accumulate, ws)
+    rows, cols, dys = _rows(dY, "dY")
+    xd = wd = _code(H.dtype, "H")
+    strides = []
+    for t, name in ((H, "H"), (dH, "dH")):
+        if t is None:
+            strides.append(cols)
+            continue
+        if t.dtype != dY.dtype or t.shape != dY.shape:
+            raise TypeError(f"{name} must have dY's dtype and shape")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is not on the first tensor's device")
+        strides.append(_rows(t, name)[2])
+    if weight is not None:
+        wd = _code(weight.dtype, "weight")
+        _check_arg(weight, (cols,), weight.dtype, dev, "weight")
+    _check_arg(rstd, H.shape[:-1], torch.float32, dev, "rstd")
+    if not want_x:
+        dX = None
+    elif dX is None:
+        dX = _dense_like(H)
+    else:
+        _check_arg(dX, H.shape, H.dtype, dev, "dX")
+    dwd = SM_F32
+    if not want_weight:
+        dweight = None
+    elif dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dweight to add to")
+        dweight = torch.empty(cols, dtype=dtype or torch.float32, device=H.device)
+    else:
+        _check_arg(dweight, (cols,), dtype or dweight.dtype, dev, "dweight")
+    if want_weight:
+        dwd = _code(dweight.dtype, "dweight")
+    ws, wsp, nbytes = _workspace(ws, rms_norm_backward_workspace(rows, cols), H, dev)
+    _check("signmuon_rms_norm_backward", lib().signmuon_rms_norm_backward(
+        dY.data_ptr(), dys, H.data_ptr(), strides[0], _ptr(dH), strides[1], xd, _ptr(weight), wd,
+        rstd.data_ptr(), rows, cols, _ptr(dX), _ptr(dweight), dwd, bool(accumulate and want_weight),
+        wsp, nbytes, _raw_stream(dev)))
+    return dX, dweight
+
+
+def _mlp_args(X, w_gate, w_up, w_down, activation, dev):
+    """(rows, dim, row stride, hidden, dtype code, activation code)."""
+    rows, dim, xs = _rows(X, "X")
+    code = _code(X.dtype, "X")
+    if w_gate.dim() != 2:
+        raise TypeError("w_gate must be a 2-D tensor")
+    hidden = w_gate.shape[0]
+    for t, shape, name in ((w_gate, (hidden, dim), "w_gate"), (w_up, (hidden, dim), "w_up"),
+                           (w_down, (dim, hidden), "w_down")):
+        _check_arg(t, shape, X.dtype, dev, name)
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be silu or gelu")
+    return rows, dim, xs, hidden, code, ACTIVATIONS[activation]
+
+
+def gated_mlp_workspace(rows: int, dim: int, hidden: int, dtype, backward: bool) -> int:
+    nbytes = lib().signmuon_gated_mlp_workspace(rows, dim, hidden, _code(dtype, "dtype"),
+                                                bool(backward))
+    if nbytes == _NO_SIZE:
+        _check("signmuon_gated_mlp_workspace", SM_EINVAL)
+    return nbytes
+
+
+def gated_mlp(X, w_gate, w_up, w_down, activation: str = "silu", want_pre: bool = False, Y=None,
+              pre=None, ws=None, stream=None):
+    """Gated feed-forward block (act(X w_gate^T) * (X w_up^T)) w_down^T over the last
+    dimension of X: Y, or with want_pre (Y, pre), the float32 pre-activations (...,
+    2 hidden), gate and then up, that the backward pass needs.  X: float32 or
+    bfloat16, (..., dim); w_gate, w_up: (hidden, dim) and w_down: (dim, hidden) of
+    the same dtype.  activation: "silu" or "gelu"."""
+    import torch
+    dev = _here(X, stream)
+    if dev < 0:
+        with _placed(X, stream):
+            return gated_mlp(X, w_gate, w_up, w_down, activation, want_pre, Y, pre, ws)
+    rows, dim, xs, hidden, code, act = _mlp_args(X, w_gate, w_up, w_down, activation, dev)
+    if Y is None:
+        Y = _dense_like(X)
+    else:
+        _check_arg(Y, X.shape, X.dtype, dev, "Y")
+    if pre is not None:
+        _check_arg(pre, X.shape[:-1] + (2 * hidden,), torch.float32, dev, "pre")
+    elif want_pre:
+        pre = torch.empty(X.shape[:-1] + (2 * hidden,), dtype=torch.float32, device=X.device)
+    ws, wsp, nbytes = _workspace(ws, gated_mlp_workspace(rows, dim, hidden, X.dtype, False), X,
+                                 dev)
+    _check("signmuon_gated_mlp", lib().signmuon_gated_mlp(
+        X.data_ptr(), xs, w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), code, act, rows,
+        dim, hidden, Y.data_ptr(), _ptr(pre), wsp, nbytes, _raw_stream(dev)))
+    return (Y, pre) if want_pre else Y
+
+
+def gated_mlp_backward(dY, X, w_gate, w_up, w_down, pre, activation: str = "silu",
+                       want=(True, True, True, True), dX=None, dw_gate=None, dw_up=None,
+                       dw_down=None, dtype=None, accumulate: bool = False, ws=None, stream=None):
+    """(dX, dw_gate, dw_up, dw_down) of gated_mlp, None in the place of one whose entry
+    of want is False.  pre is the forward pass's.  dtype: that of the weights'
+    gradients (default: what those passed in have, else float32).  accumulate adds to
+    the float32 ones, which have to be passed in then; dX is overwritten."""
+    import torch
+    dev = _here(X, stream)
+    if dev < 0:
+        with _placed(X, stream):
+            return gated_mlp_backward(dY, X, w_gate, w_up, w_down, pre, activation, want, dX,
+                                      dw_gate, dw_up, dw_down, dtype, accumulate, ws)
+    rows, dim, xs, hidden, code, act = _mlp_args(X, w_gate, w_up, w_down, activation, dev)
+    if dY.dtype != X.dtype or dY.shape != X.shape:
+        raise TypeError("dY must have X's dtype and shape")
+    if dY.get_device() != dev:
+        raise ValueError("dY is not on the first tensor's device")
+    dys = _rows(dY, "dY")[2]
+    _check_arg(pre, X.shape[:-1] + (2 * hidden,), torch.float32, dev, "pre")
+    if not want[0]:
+        dX = None
+    elif dX is None:
+        dX = _dense_like(X)
+    else:
+        _check_arg(dX, X.shape, X.dtype, dev, "dX")
+    grads = [g if w else None for g, w in zip((dw_gate, dw_up, dw_down), want[1:])]
+    if dtype is None:
+        dtype = next((g.dtype for g in grads if g is not None), torch.float32)
+    for i, (w, like) in enumerate(zip(want[1:], (w_gate, w_up, w_down))):
+        if w and grads[i] is None:
+            if accumulate:
+                raise ValueError("accumulate needs the weights' gradients to add to")
+            grads[i] = torch.empty(like.shape, dtype=dtype, device=X.device)
+        elif w:
+            _check_arg(grads[i], like.shape, dtype, dev, ("dw_gate", "dw_up", "dw_down")[i])
+    ws, wsp, nbytes = _workspace(ws, gated_mlp_workspace(rows, dim, hidden, X.dtype, True), X, dev)
+    _check("signmuon_gated_mlp_backward", lib().signmuon_gated_mlp_backward(
+        dY.data_ptr(), dys, X.data_ptr(), xs, w_gate.data_ptr(), w_up.data_ptr(),
+        w_down.data_ptr(), pre.data_ptr(), code, act, rows, dim, hidden, _ptr(dX),
+        _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _code(dtype, "dtype"),
+        bool(accumulate and any(want[1:])), wsp, nbytes, _raw_stream(dev)))
+    return (dX, *grads)
 
 
 def _loss_args(X, weight, targets, reduction, dev):

@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsignmuon.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["sm_api.cpp", "sm_gemm.hip", "sm_elementwise.hip", "sm_layers_api.cpp",
-           "sm_norm.hip", "sm_embed.hip", "sm_mm_ops.hip", "sm_loss.hip"]
+           "sm_norm.hip", "sm_embed.hip", "sm_mm_ops.hip", "sm_loss.hip", "sm_ffn.hip",
+           "sm_rms.hip"]
 ARCH = "gfx950"
 
 

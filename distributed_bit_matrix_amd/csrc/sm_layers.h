@@ -58,6 +58,32 @@ struct EmbedGradArgs {
 size_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t s);
 
+struct RmsArgs {
+  const void *X, *R;       // R: the residual stream, or null
+  int64_t x_stride, r_stride;
+  int32_t x_dtype, w_dtype;
+  const void* gamma;
+  int64_t rows, cols;
+  float eps;
+  int32_t block;           // columns of a scale: 128, or 0 for a whole row
+  void *H, *Y;             // Y: of X's type, or codes where scales is not null
+  float *scales, *rstd;
+};
+hipError_t launch_rms(const RmsArgs& a, hipStream_t s);   // rows > 0
+
+struct RmsGradArgs {
+  const void *dY, *H, *dH;
+  int64_t dy_stride, h_stride, dh_stride;
+  int32_t x_dtype, w_dtype, dw_dtype, accumulate;
+  const void* gamma;
+  const float* rstd;
+  int64_t rows, cols;
+  void *dX, *dgamma;
+  void* ws;
+};
+size_t rms_grad_workspace(int64_t rows, int64_t cols);
+hipError_t launch_rms_grad(const RmsGradArgs& a, hipStream_t s);
+
 struct LossArgs {
   const void* X;
   int64_t x_stride;
@@ -89,5 +115,33 @@ struct LossGradArgs {
   void* ws;
 };
 hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s);
+
+struct FfnArgs {
+  const void* X;
+  int64_t x_stride;
+  const void *Wg, *Wu, *Wd;
+  int32_t dtype, act;
+  int64_t rows, dim, hidden;
+  void* Y;
+  float* pre;
+  void* ws;
+};
+size_t ffn_workspace(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool backward);
+hipError_t launch_ffn(const FfnArgs& a, hipStream_t s);   // rows > 0
+
+struct FfnGradArgs {
+  const void* dY;
+  int64_t dy_stride;
+  const void* X;
+  int64_t x_stride;
+  const void *Wg, *Wu, *Wd;
+  const float* pre;
+  int32_t dtype, act;
+  int64_t rows, dim, hidden;
+  void *dX, *dWg, *dWu, *dWd;
+  int32_t dw_dtype, accumulate;
+  void* ws;
+};
+hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s);
 
 }  // namespace sm

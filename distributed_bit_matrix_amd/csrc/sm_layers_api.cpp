@@ -14,6 +14,7 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxSorted = (int64_t)1 << 27;     // 256 runs of 2^19, 2^15 tokens a wave
 constexpr int64_t kMaxMmRows = (int64_t)1 << 22;     // rows, widths of the matrix products
 constexpr int64_t kMaxMmDim = 1 << 16;
+constexpr int64_t kMaxCodesCols = 16384;              // rows that the norm holds in registers
 constexpr int64_t kMaxStride = (int64_t)1 << 39;      // elements; past any memory
 
 bool dtype_ok(int32_t d) { return d == SM_F32 || d == SM_BF16; }
@@ -121,6 +122,141 @@ sm_status signmuon_embedding_backward(const void* dY, int32_t dy_dtype, int64_t 
   const EmbedGradArgs a{dY, dy_dtype, dw_dtype, token_bits, accumulate, dy_stride, tokens, n,
                         padding, scale, dW, vocab, dim, ws};
   return launch_embed_grad(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
+}
+
+static sm_status rms_call(const void* X, int64_t x_stride, const void* R, int64_t r_stride,
+                          int32_t x_dtype, const void* gamma, int32_t w_dtype, int64_t rows,
+                          int64_t cols, float eps, int64_t block, void* H, void* Y, bool codes,
+                          float* scales, float* rstd, hipStream_t stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return SM_EINVAL;
+  if (!in(rows, 0, kMaxRows) || !in(cols, 1, codes ? kMaxCodesCols : kMaxDim)) return SM_EINVAL;
+  if (!std::isfinite(eps) || eps < 0.f) return SM_EINVAL;
+  if (codes && block != 0 && block != 128) return SM_EINVAL;
+  if (rows == 0) return SM_OK;
+  if (!X || !Y || !stride_ok(x_stride, rows, cols)) return SM_EINVAL;
+  if (R && (!H || !stride_ok(r_stride, rows, cols))) return SM_EINVAL;
+  if (codes && (!scales || Y == X)) return SM_EINVAL;
+  if (Y == X && x_stride != cols) return SM_EINVAL;
+  if (R && (Y == R || Y == H || (H == X && x_stride != cols) || (H == R && r_stride != cols)))
+    return SM_EINVAL;
+  if (!aligned(X, x_dtype) || !aligned(R, x_dtype) || !aligned(gamma, w_dtype) ||
+      !aligned(rstd, SM_F32) || !aligned(scales, SM_F32) || (R && !aligned(H, x_dtype)) ||
+      (!codes && !aligned(Y, x_dtype)))
+    return SM_EINVAL;
+  const RmsArgs a{X, R, x_stride, r_stride, x_dtype, w_dtype, gamma, rows, cols, eps,
+                  (int32_t)block, H, Y, scales, rstd};
+  return launch_rms(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
+}
+
+sm_status signmuon_rms_norm(const void* X, int64_t x_stride, const void* R, int64_t r_stride,
+                            int32_t x_dtype, const void* gamma, int32_t w_dtype, int64_t rows,
+                            int64_t cols, float eps, void* H, void* Y, float* rstd,
+                            hipStream_t stream) {
+  return rms_call(X, x_stride, R, r_stride, x_dtype, gamma, w_dtype, rows, cols, eps, 0, H, Y,
+                  false, nullptr, rstd, stream);
+}
+
+sm_status signmuon_rms_norm_e4m3(const void* X, int64_t x_stride, const void* R, int64_t r_stride,
+                                 int32_t x_dtype, const void* gamma, int32_t w_dtype, int64_t rows,
+                                 int64_t cols, float eps, int64_t block, void* H, void* Q,
+                                 float* scales, float* rstd, hipStream_t stream) {
+  return rms_call(X, x_stride, R, r_stride, x_dtype, gamma, w_dtype, rows, cols, eps, block, H, Q,
+                  true, scales, rstd, stream);
+}
+
+size_t signmuon_rms_norm_backward_workspace(int64_t rows, int64_t cols) {
+  if (!in(rows, 0, kMaxRows) || !in(cols, 1, kMaxDim)) return SIZE_MAX;
+  return rms_grad_workspace(rows, cols);
+}
+
+sm_status signmuon_rms_norm_backward(const void* dY, int64_t dy_stride, const void* H,
+                                     int64_t h_stride, const void* dH, int64_t dh_stride,
+                                     int32_t x_dtype, const void* gamma, int32_t w_dtype,
+                                     const float* rstd, int64_t rows, int64_t cols, void* dX,
+                                     void* dgamma, int32_t dw_dtype, int32_t accumulate, void* ws,
+                                     size_t ws_bytes, hipStream_t stream) {
+  if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype) || !dtype_ok(dw_dtype)) return SM_EINVAL;
+  if (!in(rows, 0, kMaxRows) || !in(cols, 1, kMaxDim)) return SM_EINVAL;
+  if (!in(accumulate, 0, 1) || (accumulate && dw_dtype != SM_F32)) return SM_EINVAL;
+  if (!dX && !dgamma) return SM_OK;
+  if (rows > 0) {
+    if (!dY || !H || !rstd) return SM_EINVAL;
+    if (!stride_ok(dy_stride, rows, cols) || !stride_ok(h_stride, rows, cols)) return SM_EINVAL;
+    if (dH && !stride_ok(dh_stride, rows, cols)) return SM_EINVAL;
+    if (dX && (dX == H || (dX == dY && dy_stride != cols) || (dX == dH && dh_stride != cols)))
+      return SM_EINVAL;
+    if (!aligned(dY, x_dtype) || !aligned(H, x_dtype) || !aligned(dH, x_dtype) ||
+        !aligned(gamma, w_dtype) || !aligned(rstd, SM_F32) || !aligned(dX, x_dtype))
+      return SM_EINVAL;
+  }
+  if (!aligned(dgamma, dw_dtype)) return SM_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, rms_grad_workspace(rows, cols))) return SM_EWORKSPACE;
+  const RmsGradArgs a{dY, H, dH, dy_stride, h_stride, dh_stride, x_dtype, w_dtype, dw_dtype,
+                      accumulate, gamma, rstd, rows, cols, dX, dgamma, ws};
+  return launch_rms_grad(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
+}
+
+size_t signmuon_gated_mlp_workspace(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype,
+                                    int32_t backward) {
+  if (!dtype_ok(dtype) || !in(backward, 0, 1) || !in(rows, 0, kMaxMmRows) ||
+      !in(dim, 1, kMaxMmDim) || !in(hidden, 1, kMaxMmDim))
+    return SIZE_MAX;
+  return ffn_workspace(rows, dim, hidden, dtype, backward);
+}
+
+sm_status signmuon_gated_mlp(const void* X, int64_t x_stride, const void* Wg, const void* Wu,
+                             const void* Wd, int32_t dtype, int32_t act, int64_t rows, int64_t dim,
+                             int64_t hidden, void* Y, float* pre, void* ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  if (!dtype_ok(dtype) || !in(act, SM_ACT_SILU, SM_ACT_GELU)) return SM_EINVAL;
+  if (!in(rows, 0, kMaxMmRows) || !in(dim, 1, kMaxMmDim) || !in(hidden, 1, kMaxMmDim))
+    return SM_EINVAL;
+  if (rows == 0) return SM_OK;
+  if (!X || !Wg || !Wu || !Wd || !Y || !stride_ok(x_stride, rows, dim)) return SM_EINVAL;
+  if (Y == X || Y == Wg || Y == Wu || Y == Wd) return SM_EINVAL;
+  if (!aligned(X, dtype) || !aligned(Wg, dtype) || !aligned(Wu, dtype) || !aligned(Wd, dtype) ||
+      !aligned(Y, dtype) || !aligned(pre, SM_F32))
+    return SM_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, ffn_workspace(rows, dim, hidden, dtype, false)))
+    return SM_EWORKSPACE;
+  const FfnArgs a{X, x_stride, Wg, Wu, Wd, dtype, act, rows, dim, hidden, Y, pre, ws};
+  return launch_ffn(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
+}
+
+sm_status signmuon_gated_mlp_backward(const void* dY, int64_t dy_stride, const void* X,
+                                      int64_t x_stride, const void* Wg, const void* Wu,
+                                      const void* Wd, const float* pre, int32_t dtype, int32_t act,
+                                      int64_t rows, int64_t dim, int64_t hidden, void* dX,
+                                      void* dWg, void* dWu, void* dWd, int32_t dw_dtype,
+                                      int32_t accumulate, void* ws, size_t ws_bytes,
+                                      hipStream_t stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(dw_dtype) || !in(act, SM_ACT_SILU, SM_ACT_GELU))
+    return SM_EINVAL;
+  if (!in(rows, 0, kMaxMmRows) || !in(dim, 1, kMaxMmDim) || !in(hidden, 1, kMaxMmDim))
+    return SM_EINVAL;
+  if (!in(accumulate, 0, 1) || (accumulate && dw_dtype != SM_F32)) return SM_EINVAL;
+  if (!dX && !dWg && !dWu && !dWd) return SM_OK;
+  if (rows > 0) {
+    if (!dY || !X || !Wg || !Wu || !Wd || !pre) return SM_EINVAL;
+    if (!stride_ok(dy_stride, rows, dim) || !stride_ok(x_stride, rows, dim)) return SM_EINVAL;
+    for (const void* in : {dY, X, Wg, Wu, Wd, (const void*)pre})
+      for (const void* out : {dX, dWg, dWu, dWd})
+        if (out && out == in) return SM_EINVAL;
+    if (!aligned(dY, dtype) || !aligned(X, dtype) || !aligned(Wg, dtype) || !aligned(Wu, dtype) ||
+        !aligned(Wd, dtype) || !aligned(pre, SM_F32) || !aligned(dX, dtype))
+      return SM_EINVAL;
+  }
+  if (!aligned(dWg, dw_dtype) || !aligned(dWu, dw_dtype) || !aligned(dWd, dw_dtype))
+    return SM_EINVAL;
+  const void* out[] = {dX, dWg, dWu, dWd};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (out[i] && out[i] == out[j]) return SM_EINVAL;
+  if (!workspace_ok(ws, ws_bytes, ffn_workspace(rows, dim, hidden, dtype, true)))
+    return SM_EWORKSPACE;
+  const FfnGradArgs a{dY, dy_stride, X, x_stride, Wg, Wu, Wd, pre, dtype, act, rows, dim, hidden,
+                      dX, dWg, dWu, dWd, dw_dtype, accumulate, ws};
+  return launch_ffn_grad(a, stream) == hipSuccess ? SM_OK : SM_EHIP;
 }
 
 size_t signmuon_linear_cross_entropy_workspace(int64_t rows, int64_t dim, int64_t vocab,

@@ -238,18 +238,6 @@ __global__ __launch_bounds__(256) void k_loss_rows(const int32_t* count, const i
 
 namespace {
 
-// Places in a workspace, each 256-byte aligned.
-struct Places {
-  char* base;
-  size_t used = 0;
-  template <typename T>
-  T* take(int64_t n) {
-    T* p = reinterpret_cast<T*>(base + used);
-    used += ((size_t)n * sizeof(T) + 255) / 256 * 256;
-    return p;
-  }
-};
-
 struct LossPlan {
   int planes;
   int32_t dim_ld;                 // row length of operand copies

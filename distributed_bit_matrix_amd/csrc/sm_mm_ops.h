@@ -134,6 +134,18 @@ inline void set_planes(MmJob& j, int planes, int64_t a_plane, int64_t b_plane) {
   j.b_plane = b_plane;
 }
 
+// Places in a workspace, each 256-byte aligned.
+struct Places {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += ((size_t)n * sizeof(T) + 255) / 256 * 256;
+    return p;
+  }
+};
+
 constexpr int kCus = 256;
 // Tiles of 256 x 256 where they fill the chip, or nearly; else 128 x 128.
 inline bool wide_tiles(int64_t m, int64_t n) {
@@ -172,5 +184,10 @@ hipError_t run_mm(MmArgs& a, const typename Epi::Args& e, bool wide, hipStream_t
   return wide ? run_mm_as<AKM, BKM, PAIR, MmShape<256, 256, 2, 4>, Epi>(a, e, s)
               : run_mm_as<AKM, BKM, PAIR, MmShape<128, 128, 2, 2>, Epi>(a, e, s);
 }
+
+#define SM_TRY(call)                                         \
+  do {                                                       \
+    if (hipError_t e_ = (call); e_ != hipSuccess) return e_; \
+  } while (0)
 
 }  // namespace sm

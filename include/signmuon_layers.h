@@ -1,11 +1,11 @@
 /*
- * signmuon_layers.h - C ABI of libsignmuon.so: the layers of a transformer
- * whose parameter gradients are not matrix products, forward and backward:
- * layer norm and embedding lookup, as HIP kernels for AMD Instinct MI355X
- * (gfx950).  Their weight gradients are sums over rows that end in the
- * float32 gradient G of signmuon_step; like every result of this library
- * they are bit-reproducible run to run, so that replicas which vote on one
- * bit per entry start from the same gradient.
+ * signmuon_layers.h - C ABI of libsignmuon.so: layers of a transformer, forward
+ * and backward, as HIP kernels for AMD Instinct MI355X (gfx950): layer norm and
+ * embedding lookup, the root-mean-square norm of a residual stream, the gated
+ * feed-forward block, and the softmax cross entropy of a linear output layer.
+ * Their weight gradients end in the float32 gradient G of signmuon_step; like
+ * every result of this library they are bit-reproducible run to run, so that
+ * replicas which vote on one bit per entry start from the same gradient.
  *
  * The conventions of signmuon.h hold: device pointers, caller-owned memory
  * and workspaces, asynchronous work on the caller's stream (a stream of the
@@ -109,6 +109,96 @@ sm_status signmuon_embedding_backward(
     int32_t token_bits, int64_t n, int64_t padding, float scale, void *dW,
     int32_t dw_dtype, int64_t vocab, int64_t dim, int32_t accumulate, void *ws,
     size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of a residual stream's rows, rows x cols:
+ *   H = X + R (rounded to x_dtype; H = X where R is NULL),
+ *   rstd_r = 1 / sqrt(sum_c H[r,c]^2 / cols + eps),
+ *   Y[r,c] = H[r,c] * rstd_r * gamma[c].
+ * X, R and H have x_dtype; X and R row strides of their own (>= cols), H and Y
+ * are contiguous.  H is written where R is given (and may be X or R itself if
+ * that is contiguous), and is ignored otherwise; Y may be X itself if that is
+ * contiguous (then H is not X).  gamma: [cols] of w_dtype, NULL for ones.
+ * rstd: float32[rows] for the backward pass, or NULL.  0 <= rows < 2^31,
+ * 1 <= cols <= 2^20, eps >= 0 and finite.  rows = 0 is a no-op.  A row with a NaN
+ * is NaN; where the sum of the squares is past float32, rstd is 0.
+ *
+ * signmuon_rms_norm_e4m3 writes Y in 8 bits: row r is cut into blocks of `block`
+ * = 128 columns (the last may be shorter), or is one block where block is 0;
+ *   scales[r,b] = max(max |Y| of the block / 448, 2^-126),
+ *   Q[r,c] = Y[r,c] / scales[r,b] to the nearest e4m3 value (OCP, no infinities).
+ * Q: rows x cols bytes; scales: float32, rows x number of blocks.  cols <= 16384.
+ */
+sm_status signmuon_rms_norm(const void *X, int64_t x_stride, const void *R,
+                            int64_t r_stride, int32_t x_dtype,
+                            const void *gamma, int32_t w_dtype, int64_t rows,
+                            int64_t cols, float eps, void *H, void *Y,
+                            float *rstd, hipStream_t stream);
+sm_status signmuon_rms_norm_e4m3(const void *X, int64_t x_stride,
+                                 const void *R, int64_t r_stride,
+                                 int32_t x_dtype, const void *gamma,
+                                 int32_t w_dtype, int64_t rows, int64_t cols,
+                                 float eps, int64_t block, void *H, void *Q,
+                                 float *scales, float *rstd,
+                                 hipStream_t stream);
+
+/*
+ * Backward pass of signmuon_rms_norm for the gradients dY of Y and dH of H (NULL
+ * for zeros): with xhat = H * rstd and g = dY * gamma,
+ *   dX[r,c] = dH[r,c] + rstd_r * (g - xhat * sum_c(g xhat) / cols),
+ *   dgamma[c] = sum_r dY[r,c] xhat[r,c];
+ * dX is the gradient of X and of R.  dY, H and dH have x_dtype and row strides of
+ * their own (>= cols); dX: contiguous, of x_dtype, and may be dY or dH itself if
+ * that is contiguous.  dgamma: [cols] of dw_dtype.  Either may be NULL: it is not
+ * computed then.  accumulate = 1 adds dgamma to what is there (float32 only).
+ * rows = 0 gives sums of nothing.  Workspace as for signmuon_layer_norm_backward.
+ */
+size_t signmuon_rms_norm_backward_workspace(int64_t rows, int64_t cols);
+sm_status signmuon_rms_norm_backward(
+    const void *dY, int64_t dy_stride, const void *H, int64_t h_stride,
+    const void *dH, int64_t dh_stride, int32_t x_dtype, const void *gamma,
+    int32_t w_dtype, const float *rstd, int64_t rows, int64_t cols, void *dX,
+    void *dgamma, int32_t dw_dtype, int32_t accumulate, void *ws,
+    size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gated feed-forward block of the rows of X, rows x dim:
+ *   gate = X Wg^T, up = X Wu^T,  Y = (act(gate) * up) Wd^T,
+ * act: SM_ACT_SILU, x / (1 + exp(-x)), or SM_ACT_GELU, x Phi(x).  Wg, Wu:
+ * contiguous hidden x dim; Wd: contiguous dim x hidden; Y: contiguous rows x dim;
+ * all of `dtype`.  Row r of X starts at element r * x_stride (x_stride >= dim).
+ * pre: float32[rows x 2 hidden], gate and then up of a row, for the backward pass,
+ * or NULL.  0 <= rows <= 2^22, 1 <= dim, hidden <= 2^16.  rows = 0 is a no-op.
+ * What lies between the products is rounded to `dtype` once.
+ * ws: signmuon_gated_mlp_workspace() bytes (backward = 1 for the backward call),
+ * 256-byte aligned; NULL where that is 0.  Its contents on entry do not matter.
+ * The query returns SIZE_MAX for arguments outside the limits.
+ */
+enum { SM_ACT_SILU = 0, SM_ACT_GELU = 1 };
+size_t signmuon_gated_mlp_workspace(int64_t rows, int64_t dim, int64_t hidden,
+                                    int32_t dtype, int32_t backward);
+sm_status signmuon_gated_mlp(const void *X, int64_t x_stride, const void *Wg,
+                             const void *Wu, const void *Wd, int32_t dtype,
+                             int32_t act, int64_t rows, int64_t dim,
+                             int64_t hidden, void *Y, float *pre, void *ws,
+                             size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Its backward pass for the gradient dY of Y, from what the forward pass wrote to
+ * pre: with h = act(gate) * up and dh = dY Wd,
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate),
+ *   dX = dgate Wg + dup Wu,  dWg = dgate^T X,  dWu = dup^T X,  dWd = dY^T h.
+ * dY has a row stride of its own (>= dim).  dX: contiguous, of `dtype`; dWg, dWu,
+ * dWd: contiguous, of dw_dtype; accumulate = 1 adds to what is there (float32
+ * only).  Each may be NULL: it is not computed then.  rows = 0 gives sums of
+ * nothing.
+ */
+sm_status signmuon_gated_mlp_backward(
+    const void *dY, int64_t dy_stride, const void *X, int64_t x_stride,
+    const void *Wg, const void *Wu, const void *Wd, const float *pre,
+    int32_t dtype, int32_t act, int64_t rows, int64_t dim, int64_t hidden,
+    void *dX, void *dWg, void *dWu, void *dWd, int32_t dw_dtype,
+    int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Softmax cross entropy of a linear output layer, whose logits Z = X W^T

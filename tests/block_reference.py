@@ -133,3 +133,154 @@ def loss_grad_bounds(dloss, x, w, targets, lse, ignore, reduction, dw_dtype):
     e_w = e_g.T.contiguous() @ ax + product_error(rows + 64, dtype) * (ag.T.contiguous() @ ax)
     return (stored(g @ w.double(), e_x, dtype),
             stored(g.T.contiguous() @ x.double(), e_w, dw_dtype))
+
+
+# --- residual root-mean-square norm ---------------------------------------
+
+def rms_sum(x, r):
+    """The sum as it is stored: one float32 addition, rounded to the stream's type."""
+    return x if r is None else (x.float() + r.float()).to(x.dtype)
+
+
+def rms(h, w, eps):
+    """(y, rstd) in float64 of the stored sum."""
+    h = h.double()
+    rstd = 1 / torch.sqrt((h * h).mean(-1) + eps)
+    y = h * rstd[..., None]
+    return (y if w is None else y * w.double()), rstd
+
+
+def rms_bounds(h, w, eps):
+    """Bounds of (y before it is stored, rstd): the squares' mean is off by the sum
+    and two roundings a term, rstd by half of that and 4 roundings (sum with eps,
+    root, reciprocal, division by the width), y by 3 more."""
+    y, rstd = rms(h, w, eps)
+    rel = 0.5 * (chain(h.shape[-1]) + 2 * U32) + 5 * U32
+    return y.abs() * (rel + 3 * U32) + TINY, rstd * rel
+
+
+def e4m3_half_step(v):
+    """Half the distance of the e4m3 values around v (|v| <= 448): 3 fraction bits
+    down to 2^-6, steps of 2^-9 below."""
+    return torch.exp2(torch.frexp(v).exponent.clamp(min=-5).double() - 5)
+
+
+def e4m3_scales(y, block):
+    """max |y| / 448 of a row's blocks, at least 2^-126."""
+    parts = [y] if block is None else y.split(block, -1)
+    s = torch.stack([p.abs().amax(-1) for p in parts], -1) / 448.0
+    return s.clamp(min=2.0 ** -126)
+
+
+def rms_grad(dy, h, w, rstd, dh):
+    """(dx, dw) in float64 from the saved statistics."""
+    dy, h, rs = dy.double(), h.double(), rstd.double()[..., None]
+    xh = h * rs
+    g = dy if w is None else dy * w.double()
+    dx = rs * (g - xh * (g * xh).mean(-1, keepdim=True))
+    if dh is not None:
+        dx = dx + dh.double()
+    return dx, (dy * xh).sum(0)
+
+
+def rms_grad_bounds(dy, h, w, rstd, dh, dw_dtype):
+    """Bounds of (dx, dw).  xhat is off by one rounding, g by one, a term of the
+    mean by three, the mean by its sum and two; dx by four more.  dw: a term's two
+    roundings and a sum over rows, in parts."""
+    dtype, rows, cols = dy.dtype, dy.shape[0], dy.shape[1]
+    dx, dw = rms_grad(dy, h, w, rstd, dh)
+    dy, h, rs = dy.double(), h.double(), rstd.double()[..., None]
+    xh = h * rs
+    g = dy if w is None else dy * w.double()
+    c2 = (g * xh).mean(-1, keepdim=True)
+    e_c2 = (chain(cols) + 4 * U32) * (g * xh).abs().mean(-1, keepdim=True) + 2 * U32 * c2.abs()
+    e_dx = rs * (6 * U32 * (g.abs() + (xh * c2).abs()) + xh.abs() * e_c2) + 2 * U32 * dx.abs()
+    if dh is not None:
+        e_dx = e_dx + 2 * U32 * dh.double().abs()
+    e_dw = (chain(rows + 64) + 3 * U32) * (dy * xh).abs().sum(0)
+    return stored(dx, e_dx, dtype), stored(dw, e_dw, dw_dtype)
+
+
+# --- gated feed-forward block ----------------------------------------------
+
+def _act(kind, g):
+    """(activation, slope) in float64."""
+    if kind == "silu":
+        s = torch.sigmoid(g)
+        return g * s, s * (1 + g * (1 - s))
+    p = 0.5 * torch.erfc(-g * 0.5 ** 0.5)
+    return g * p, p + g * torch.exp(-0.5 * g * g) * (2 * torch.pi) ** -0.5
+
+
+def mlp(x, wg, wu, wd, kind):
+    """(y, pre) in float64."""
+    x = x.double()
+    g, u = x @ wg.double().T, x @ wu.double().T
+    return (_act(kind, g)[0] * u) @ wd.double().T, torch.cat([g, u], 1)
+
+
+def _act_error(kind, g):
+    """Of the activation, for an exact argument: the exponential's argument is off
+    by three roundings of it (times its own slope: at most the activation and half
+    its argument), the error function by two steps of one; some products."""
+    a = _act(kind, g)[0].abs()
+    return 8 * U32 * (g.abs() + a) + 4 * U32 * g.abs() * a
+
+
+def mlp_bounds(x, wg, wu, wd, kind):
+    """Bounds of (y, pre).  Both slopes are below 1.13; h is rounded to the operands'
+    type before its product."""
+    dtype = x.dtype
+    ax, dim, hidden = x.double().abs(), x.shape[1], wg.shape[0]
+    g, u = x.double() @ wg.double().T, x.double() @ wu.double().T
+    e = product_error(dim, dtype)
+    e_g, e_u = e * (ax @ wg.double().abs().T), e * (ax @ wu.double().abs().T)
+    a = _act(kind, g)[0]
+    e_a = 1.13 * e_g + _act_error(kind, g)
+    h = a * u
+    e_h = kept(e_a * (u.abs() + e_u) + a.abs() * e_u + 2 * U32 * h.abs(), h, dtype)
+    awd = wd.double().abs().T.contiguous()
+    e_y = e_h @ awd + product_error(hidden + 64, dtype) * ((h.abs() + e_h) @ awd)
+    e_pre = torch.cat([e_g, e_u], 1)
+    return (stored(h @ wd.double().T, e_y, dtype),
+            stored(torch.cat([g, u], 1), e_pre, torch.float32))
+
+
+def mlp_grad(dy, x, wg, wu, wd, pre, kind):
+    """(dx, dwg, dwu, dwd) in float64 from the saved pre-activations."""
+    dy, x = dy.double(), x.double()
+    g, u = pre.double().chunk(2, 1)
+    a, slope = _act(kind, g)
+    dh = dy @ wd.double()
+    dg, du = dh * u * slope, dh * a
+    return (dg @ wg.double() + du @ wu.double(), dg.T.contiguous() @ x, du.T.contiguous() @ x,
+            dy.T.contiguous() @ (a * u))
+
+
+def mlp_grad_bounds(dy, x, wg, wu, wd, pre, kind, dw_dtype):
+    """Bounds of (dx, dwg, dwu, dwd): dg, du and h are rounded to the operands'
+    type before their products."""
+    dtype = x.dtype
+    want = mlp_grad(dy, x, wg, wu, wd, pre, kind)
+    rows, dim, hidden = x.shape[0], x.shape[1], wg.shape[0]
+    g, u = pre.double().chunk(2, 1)
+    a, slope = _act(kind, g)
+    ady, ax = dy.double().abs(), x.double().abs()
+    dh = dy.double() @ wd.double()
+    e_dh = product_error(dim, dtype) * (ady @ wd.double().abs())
+    e_a, e_s = _act_error(kind, g), 16 * U32 * (1 + g.abs())
+    s = slope.abs()
+    dg, du, h = dh * u * slope, dh * a, a * u
+    e_dg = kept(u.abs() * (e_dh * (s + e_s) + dh.abs() * e_s) + 3 * U32 * dg.abs(), dg, dtype)
+    e_du = kept(e_dh * (a.abs() + e_a) + dh.abs() * e_a + 2 * U32 * du.abs(), du, dtype)
+    e_h = kept(e_a * u.abs() + 2 * U32 * h.abs(), h, dtype)
+    adg, adu, ah = dg.abs() + e_dg, du.abs() + e_du, h.abs() + e_h
+    awg, awu = wg.double().abs(), wu.double().abs()
+    e_x = (e_dg @ awg + e_du @ awu
+           + product_error(2 * hidden + 64, dtype) * (adg @ awg + adu @ awu))
+    p = product_error(rows + 64, dtype)
+    t = lambda m: m.T.contiguous()  # noqa: E731
+    errors = (e_x, t(e_dg) @ ax + p * (t(adg) @ ax), t(e_du) @ ax + p * (t(adu) @ ax),
+              t(ady) @ e_h + p * (t(ady) @ ah))
+    return tuple(stored(v, e, dt) for v, e, dt in zip(want, errors,
+                                                      (dtype, dw_dtype, dw_dtype, dw_dtype)))
