@@ -55,33 +55,29 @@ struct EpiGate {
   template <int TI, int TJ>
   static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
                                              const f32x4_t (&acc)[TI][TJ]) {
-    const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
-    const int m_end = (at.m + 7) & ~7;     // zeros up to a whole piece of 16 bytes
+    constexpr int F = 8 * TI;                        // features of a wave
+    const int cols = at.m - at.m0;
+    const int cols8 = ((at.m + 7) & ~7) - at.m0;     // zeros up to a whole piece of 16 bytes
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int n = nc + 16 * j;
-      if (n >= at.n) continue;
+      // (features past the last one are products of zeros)
+      f32x4_t g[TI / 2], u[TI / 2], h[TI / 2];
 #pragma unroll
-      for (int i = 0; i < TI; i += 2) {
-        const int f = mc + 8 * i;
-        if (f >= m_end) continue;
-        float v[4], g[4], u[4];
+      for (int i = 0; i < TI / 2; ++i) {
+        g[i] = acc[2 * i][j];
+        u[i] = acc[2 * i + 1][j];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          g[k] = acc[i][j][k];
-          u[k] = acc[i + 1][j][k];
-          v[k] = f + k < at.m ? act<ACT>(g[k]) * u[k] : 0.f;
-        }
-        store_planes<P>(e.h + (int64_t)n * e.ld + f, e.plane, v);
-        if (e.pre) {
-          float* p = e.pre + (int64_t)n * 2 * at.m + f;
-          if (f + 4 <= at.m) {
-            store_vec<4>(p, g);
-            store_vec<4>(p + at.m, u);
-          } else {
-            for (int k = 0; k < at.m - f; ++k) p[k] = g[k], p[at.m + k] = u[k];
-          }
-        }
+        for (int k = 0; k < 4; ++k) h[i][k] = act<ACT>(g[i][k]) * u[i][k];
+      }
+      const int n = at.n0 + 16 * j;
+      put_planes<P, F>(at, h, e.h + (int64_t)n * e.ld + at.m0, e.plane, e.ld, at.n - n, cols8);
+      if (e.pre) {
+        const MmRows<float, F> rows{at.lds, at.lane};
+        float* p = e.pre + (int64_t)n * 2 * at.m + at.m0;
+#pragma unroll
+        for (int i = 0; i < TI / 2; ++i) rows.put(0, i, g[i]), rows.put(1, i, u[i]);
+        rows.flush(0, p, 2 * at.m, at.n - n, cols);
+        rows.flush(1, p + at.m, 2 * at.m, at.n - n, cols);
       }
     }
   }
@@ -99,29 +95,29 @@ struct EpiGateGrad {
   template <int TI, int TJ>
   static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
                                              const f32x4_t (&acc)[TI][TJ]) {
+    constexpr int F = 16 * TI;
     const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
-    const int m_end = (at.m + 7) & ~7;
+    const int cols8 = ((at.m + 7) & ~7) - at.m0;     // zeros up to a whole piece of 16 bytes
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int n = nc + 16 * j;
-      if (n >= at.n) continue;
-#pragma unroll
-      for (int i = 0; i < TI; ++i) {
+      const float* p = e.pre + (int64_t)(n < at.n ? n : at.n - 1) * 2 * at.m;
+      const int n0 = at.n0 + 16 * j;
+      const int64_t o = (int64_t)n0 * e.ld + at.m0;
+      const auto values = [&](int i, f32x4_t& dg, f32x4_t& du, f32x4_t& h) SM_INLINE {
         const int f = mc + 16 * i;
-        if (f >= m_end) continue;
-        const float* p = e.pre + (int64_t)n * 2 * at.m + f;
-        float dg[4], du[4], h[4], g[4], u[4];
+        float g[4], u[4];
         if (f + 4 <= at.m) {
           Piece<float, 4> pg, pu;
-          pg.load(p);
-          pu.load(p + at.m);
+          pg.load(p + f);
+          pu.load(p + at.m + f);
 #pragma unroll
           for (int k = 0; k < 4; ++k) g[k] = pg[k], u[k] = pu[k];
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            g[k] = f + k < at.m ? p[k] : 0.f;
-            u[k] = f + k < at.m ? p[at.m + k] : 0.f;
+            g[k] = f + k < at.m ? p[f + k] : 0.f;
+            u[k] = f + k < at.m ? p[at.m + f + k] : 0.f;
           }
         }
 #pragma unroll
@@ -133,10 +129,36 @@ struct EpiGateGrad {
           du[k] = dh * a;
           h[k] = a * u[k];
         }
-        const int64_t o = (int64_t)n * e.ld + f;
-        store_planes<P>(e.dg + o, e.plane, dg);
-        store_planes<P>(e.du + o, e.plane, du);
-        store_planes<P>(e.h + o, e.plane, h);
+      };
+      if constexpr (P == 1) {
+        const MmRows<bf16_t, F> rows{at.lds, at.lane};
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+          f32x4_t dg, du, h;
+          values(i, dg, du, h);
+          rows.put(0, i, dg);
+          rows.put(1, i, du);
+          rows.put(2, i, h);
+        }
+        rows.flush(0, e.dg + o, e.ld, at.n - n0, cols8);
+        rows.flush(1, e.du + o, e.ld, at.n - n0, cols8);
+        rows.flush(2, e.h + o, e.ld, at.n - n0, cols8);
+      } else {
+        // one after the other: nine planes do not fit the wave's LDS, nor the
+        // values of all three its registers
+        const auto one = [&](auto which, bf16_t* dst) SM_INLINE {
+          f32x4_t v[TI];
+#pragma unroll
+          for (int i = 0; i < TI; ++i) {
+            f32x4_t t[3];
+            values(i, t[0], t[1], t[2]);
+            v[i] = t[decltype(which)::value];
+          }
+          put_planes<P, F>(at, v, dst + o, e.plane, e.ld, at.n - n0, cols8);
+        };
+        one(std::integral_constant<int, 0>(), e.dg);
+        one(std::integral_constant<int, 1>(), e.du);
+        one(std::integral_constant<int, 2>(), e.h);
       }
     }
   }
@@ -199,18 +221,11 @@ struct FfnPlan {
   int64_t ld_d, ld_f;
   bf16_t *x, *dy, *wg, *wu, *wd, *h, *dg, *du;
   void* few_h;
-  float* part[4];          // sums of splits: dx, dwg, dwu, dwd (forward: y first)
-  int splits[4];
-  bool wide[4];
+  MmPlan first, out;       // tiles of the first product; of the others (forward: y;
+                           // backward: dx, dwg, dwu, dwd)
+  float* sums[4];          // of their splits
   size_t bytes;
 };
-
-// Splits and tiles of a product, and room for its sums.
-void plan_product(FfnPlan& p, Places& at, int i, int64_t m, int64_t n, int64_t k) {
-  p.wide[i] = wide_tiles(m, n);
-  p.splits[i] = k_splits(m, n, (k + 63) / 64, p.wide[i]);
-  if (p.splits[i] > 1) p.part[i] = at.take<float>(p.splits[i] * n * round_up(m, 4));
-}
 
 FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool backward,
                  void* ws) {
@@ -231,16 +246,28 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
   p.wu = at.take<bf16_t>(p.planes * hidden * p.ld_d);
   p.wd = at.take<bf16_t>(p.planes * dim * p.ld_f);
   p.h = at.take<bf16_t>(p.planes * rows * p.ld_f);
+  const auto slabs = [&](int64_t k) { return segs * ((k + 63) / 64); };
+  const auto room = [&](const MmSize* z, int jobs) {
+    p.out = plan_products(z, jobs);
+    for (int i = 0; i < jobs; ++i)
+      if (p.out.splits[i] > 1)
+        p.sums[i] = at.take<float>(p.out.splits[i] * z[i].n * round_up(z[i].m, 4));
+  };
   if (!backward) {
-    plan_product(p, at, 0, dim, rows, segs * hidden);
+    const MmSize z{2 * hidden, rows, slabs(dim), false}, y{dim, rows, slabs(hidden), true};
+    p.first = plan_products(&z, 1);
+    room(&y, 1);
   } else {
     p.dy = at.take<bf16_t>(p.planes * rows * p.ld_d);
     p.dg = at.take<bf16_t>(p.planes * rows * p.ld_f);
     p.du = at.take<bf16_t>(p.planes * rows * p.ld_f);
-    plan_product(p, at, 0, dim, rows, 2 * segs * hidden);
-    plan_product(p, at, 1, dim, hidden, segs * rows);
-    plan_product(p, at, 2, dim, hidden, segs * rows);
-    plan_product(p, at, 3, hidden, dim, segs * rows);
+    const MmSize z{hidden, rows, slabs(dim), false};
+    const MmSize o[4] = {{dim, rows, 2 * slabs(hidden), true},
+                         {dim, hidden, slabs(rows), true},
+                         {dim, hidden, slabs(rows), true},
+                         {hidden, dim, slabs(rows), true}};
+    p.first = plan_products(&z, 1);
+    room(o, 4);
   }
   p.bytes = at.used;
   return p;
@@ -258,8 +285,7 @@ hipError_t operand(Operand& o, const void* src, int32_t dtype, int64_t rows, int
                         copy}, s);
 }
 
-MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t k, int planes,
-              int splits) {
+MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t k, int planes) {
   MmJob j{};
   j.a = a.p;
   j.b = b.p;
@@ -268,23 +294,9 @@ MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t 
   j.m = (int)m;
   j.n = (int)n;
   j.k = (int)k;
-  j.splits = splits;
+  j.splits = 1;
   set_planes(j, planes, a.plane, b.plane);
   return j;
-}
-
-// Where product i's results go: its sums of splits, or the caller's array.
-MmOut out_of(const FfnPlan& p, int i, void* dst, int64_t m, int64_t n, int32_t dtype, int32_t add) {
-  const int64_t ld = round_up(m, 4);
-  if (p.splits[i] > 1) return {p.part[i], ld, n * ld, SM_F32, 0};
-  return {dst, m, 0, dtype, add};
-}
-hipError_t join(const FfnPlan& p, int i, void* dst, int64_t m, int64_t n, int32_t dtype,
-                int32_t add, hipStream_t s) {
-  if (p.splits[i] <= 1) return hipSuccess;
-  const int64_t ld = round_up(m, 4);
-  return launch_join({p.part[i], n * ld, ld, p.splits[i], nullptr, n, (int)m, dtype, add, dst, m},
-                     s);
 }
 
 template <typename T, int ACT>
@@ -329,19 +341,17 @@ hipError_t ffn(const FfnArgs& a, hipStream_t s) {
   SM_TRY(operand(wd, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, P, p.wd, s));
   MmArgs m{};
   m.jobs = 1;
-  m.job[0] = product(wg, x, a.hidden, a.rows, a.dim, P, 1);
+  m.job[0] = product(wg, x, a.hidden, a.rows, a.dim, P);
   m.job[0].a2 = wu.p;
   const int64_t plane = a.rows * p.ld_f;
-  SM_TRY((run_mm<false, false, true, EpiGate<P, ACT>>(m, {p.h, p.ld_f, plane, a.pre},
-                                                      wide_tiles(2 * a.hidden, a.rows), s)));
+  SM_TRY((run_mm<false, false, true, EpiGate<P, ACT>>(m, {p.h, p.ld_f, plane, a.pre}, p.first.wide,
+                                                      s)));
   const Operand h{(const char*)p.h, p.ld_f, plane * 2, nullptr};
-  m = MmArgs{};
-  m.jobs = 1;
-  m.job[0] = product(wd, h, a.dim, a.rows, a.hidden, P, p.splits[0]);
-  EpiStore::Args e{};
-  e.out[0] = out_of(p, 0, a.Y, a.dim, a.rows, a.dtype, 0);
-  SM_TRY((run_mm<false, false, false, EpiStore>(m, e, p.wide[0], s)));
-  return join(p, 0, a.Y, a.dim, a.rows, a.dtype, 0, s);
+  MmStores out;
+  out.add(product(wd, h, a.dim, a.rows, a.hidden, P), false, a.Y, a.dtype, 0, p.sums[0],
+          p.out.splits[0]);
+  SM_TRY((run_mm<false, false, false, EpiStore>(out.a, out.e, p.out.wide, s)));
+  return out.joins(s);
 }
 
 template <int P, int ACT>
@@ -353,12 +363,13 @@ hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   const int64_t plane = a.rows * p.ld_f;
   MmArgs m{};
   m.jobs = 1;
-  m.job[0] = product(wd, dy, a.hidden, a.rows, a.dim, P, 1);
+  m.job[0] = product(wd, dy, a.hidden, a.rows, a.dim, P);
   SM_TRY((run_mm<true, false, false, EpiGateGrad<P, ACT>>(
-      m, {p.dg, p.du, p.h, p.ld_f, plane, a.pre}, wide_tiles(a.hidden, a.rows), s)));
+      m, {p.dg, p.du, p.h, p.ld_f, plane, a.pre}, p.first.wide, s)));
   const Operand dg{(const char*)p.dg, p.ld_f, plane * 2, nullptr};
   const Operand du{(const char*)p.du, p.ld_f, plane * 2, nullptr};
   const Operand h{(const char*)p.h, p.ld_f, plane * 2, nullptr};
+  MmStores out;
   if (a.dX) {
     SM_TRY(operand(wg, a.Wg, a.dtype, a.hidden, a.dim, a.dim, P, p.wg, s));
     SM_TRY(operand(wu, a.Wu, a.dtype, a.hidden, a.dim, a.dim, P, p.wu, s));
@@ -367,35 +378,23 @@ hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
       SM_TRY(launch_planes({a.Wg, a.dim, a.dtype, P, a.hidden, (int)a.dim, (int32_t)p.ld_d,
                             nullptr, nullptr, p.wg}, s));
     }
-    m = MmArgs{};
-    m.jobs = 1;
-    m.job[0] = product(wg, dg, a.dim, a.rows, a.hidden, P, p.splits[0]);
-    m.job[0].parts = 2;
-    m.job[0].a_part = wu.p - wg.p;
-    m.job[0].b_part = du.p - dg.p;
-    EpiStore::Args e{};
-    e.out[0] = out_of(p, 0, a.dX, a.dim, a.rows, a.dtype, 0);
-    SM_TRY((run_mm<true, false, false, EpiStore>(m, e, p.wide[0], s)));
-    SM_TRY(join(p, 0, a.dX, a.dim, a.rows, a.dtype, 0, s));
+    MmJob j = product(wg, dg, a.dim, a.rows, a.hidden, P);
+    j.parts = 2;
+    j.a_part = wu.p - wg.p;
+    j.b_part = du.p - dg.p;
+    out.add(j, false, a.dX, a.dtype, 0, p.sums[0], p.out.splits[0]);
   }
-  if (!a.dWg && !a.dWu && !a.dWd) return hipSuccess;
   if (a.dWg || a.dWu) SM_TRY(operand(x, a.X, a.dtype, a.rows, a.dim, a.x_stride, P, p.x, s));
-  m = MmArgs{};
-  EpiStore::Args e{};
   const auto add = [&](int i, const Operand& A, const Operand& B, void* dst, int64_t mm,
                        int64_t nn) {
-    if (!dst) return;
-    e.out[m.jobs] = out_of(p, i, dst, mm, nn, a.dw_dtype, a.accumulate);
-    m.job[m.jobs++] = product(A, B, mm, nn, a.rows, P, p.splits[i]);
+    if (dst)
+      out.add(product(A, B, mm, nn, a.rows, P), true, dst, a.dw_dtype, a.accumulate, p.sums[i],
+              p.out.splits[i]);
   };
   add(1, x, dg, a.dWg, a.dim, a.hidden);
   add(2, x, du, a.dWu, a.dim, a.hidden);
   add(3, h, dy, a.dWd, a.hidden, a.dim);
-  SM_TRY((run_mm<true, true, false, EpiStore>(m, e, p.wide[1], s)));
-  if (a.dWg) SM_TRY(join(p, 1, a.dWg, a.dim, a.hidden, a.dw_dtype, a.accumulate, s));
-  if (a.dWu) SM_TRY(join(p, 2, a.dWu, a.dim, a.hidden, a.dw_dtype, a.accumulate, s));
-  if (a.dWd) SM_TRY(join(p, 3, a.dWd, a.hidden, a.dim, a.dw_dtype, a.accumulate, s));
-  return hipSuccess;
+  return out.run(p.out.wide, s);
 }
 
 }  // namespace

@@ -127,25 +127,24 @@ struct EpiGrad {
   static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
                                              const f32x4_t (&acc)[TI][TJ]) {
     const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
+    const int cols = ((at.m + 7) & ~7) - at.m0;      // zeros up to a whole piece of 16 bytes
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      const int n = nc + 16 * j;
-      if (n >= at.n) continue;
-      const int t = e.target[n] - e.v0;
-      const float lse = e.lse[n], scale = e.scale[n];
-      bf16_t* row = e.g + (int64_t)n * e.ld;
+      const int n = nc + 16 * j, r = n < at.n ? n : at.n - 1;
+      const int t = e.target[r] - e.v0;
+      const float lse = e.lse[r], scale = e.scale[r];
+      f32x4_t v[TI];
 #pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int m = mc + 16 * i;
-        if (m >= ((at.m + 7) & ~7)) continue;      // zeros up to a whole piece of 16 bytes
-        float v[4];
+      for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          const int m = mc + 16 * i + k;
           const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * kLog2e);
-          v[k] = m + k < at.m ? (p - (m + k == t ? 1.f : 0.f)) * scale : 0.f;
+          v[i][k] = m < at.m ? (p - (m == t ? 1.f : 0.f)) * scale : 0.f;
         }
-        store_planes<P>(row + m, e.plane, v);
-      }
+      const int n0 = at.n0 + 16 * j;
+      put_planes<P, 16 * TI>(at, v, e.g + (int64_t)n0 * e.ld + at.m0, e.plane, e.ld, at.n - n0,
+                             cols);
     }
   }
 };
@@ -245,8 +244,7 @@ struct LossPlan {
   int64_t strips;
   // backward
   int64_t piece;                  // columns of a piece of the vocabulary
-  int x_splits, w_splits;
-  bool x_wide, w_wide;
+  MmPlan both;                    // the products dX (job 0) and dW (job 1) of a piece
   // arrays
   int32_t *list, *target, *pos, *count;
   bf16_t *x, *w, *g;
@@ -264,7 +262,8 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
   p.planes = dtype == SM_BF16 ? 1 : 3;
   p.dim_ld = (int32_t)round_up(dim, 8);
   p.copy_w = !w_fits;
-  p.wide = wide_tiles(vocab, rows);
+  const MmSize z{vocab, rows, (p.planes == 1 ? 1 : 6) * ((dim + 63) / 64), false};
+  p.wide = plan_products(&z, 1).wide;
   p.strips = (vocab + (p.wide ? 127 : 63)) / (p.wide ? 128 : 64);
   Places at{static_cast<char*>(ws)};
   p.list = at.take<int32_t>(rows);
@@ -285,12 +284,12 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
     p.piece = std::min(round_up((vocab + pieces - 1) / pieces, 256), round_up(vocab, 8));
     p.g = at.take<bf16_t>(p.planes * rows * p.piece);
     const int segs = p.planes == 1 ? 1 : 6;
-    p.x_wide = wide_tiles(dim, 4 * rows);
-    p.x_splits = k_splits(dim, rows, segs * ((p.piece + 63) / 64), p.x_wide);
-    p.w_wide = wide_tiles(dim, p.piece);
-    p.w_splits = k_splits(dim, p.piece, segs * ((rows + 63) / 64), p.w_wide);
-    p.dx = at.take<float>(p.x_splits * rows * round_up(dim, 4));
-    if (p.w_splits > 1) p.dw = at.take<float>(p.w_splits * p.piece * round_up(dim, 4));
+    const MmSize sizes[2] = {{dim, rows, segs * ((p.piece + 63) / 64), true},
+                             {dim, p.piece, segs * ((rows + 63) / 64), true}};
+    p.both = plan_products(sizes, 2);
+    // (dX is summed up over pieces and has its rows to be placed: always in parts)
+    p.dx = at.take<float>(p.both.splits[0] * rows * round_up(dim, 4));
+    if (p.both.splits[1] > 1) p.dw = at.take<float>(p.both.splits[1] * p.piece * round_up(dim, 4));
   }
   p.bytes = at.used;
   return p;
@@ -318,8 +317,8 @@ MmArgs logits(const LossPlan& p, const void* W, int64_t rows, int64_t dim, int64
               int64_t v0, int64_t cols) {
   MmArgs m{};
   m.jobs = 1;
-  m.n_rows = p.count;
   MmJob& j = m.job[0];
+  j.n_rows = p.count;
   j.lda = p.copy_w ? p.dim_ld : dim;
   j.a = (p.copy_w ? (const char*)p.w : (const char*)W) + v0 * j.lda * 2;
   j.b = (const char*)p.x;
@@ -339,14 +338,13 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
   const char* w = m.job[0].a;
   const int64_t ldw = m.job[0].lda;
   const typename EpiGrad<P>::Args eg{p.g, p.piece, plane, (int)v0, p.target, p.lse_at, p.scale};
-  if (hipError_t e = run_mm<false, false, false, EpiGrad<P>>(m, eg, wide_tiles(cols, a.rows), s);
+  if (hipError_t e = run_mm<false, false, false, EpiGrad<P>>(m, eg, p.wide, s);
       e != hipSuccess)
     return e;
+  MmStores out;
   if (a.dX) {
-    MmArgs x{};
-    x.jobs = 1;
-    x.n_rows = p.count;
-    MmJob& j = x.job[0];
+    MmJob j{};
+    j.n_rows = p.count;
     j.a = w;
     j.lda = ldw;
     j.b = (const char*)p.g;
@@ -354,19 +352,15 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.m = (int)a.dim;
     j.n = (int)a.rows;
     j.k = (int)cols;
-    j.splits = p.x_splits;
     set_planes(j, P, a.vocab * p.dim_ld * 2, plane * 2);
     const int64_t ld = round_up(a.dim, 4);
-    EpiStore::Args es{};
-    es.out[0] = {p.dx, ld, a.rows * ld, SM_F32, v0 > 0};
-    if (hipError_t e = run_mm<true, false, false, EpiStore>(x, es, p.x_wide, s); e != hipSuccess)
-      return e;
+    out.add(j, false, nullptr, SM_F32, 0, p.dx, 1);
+    out.a.job[0].splits = p.both.splits[0];
+    out.e.out[0] = {p.dx, ld, a.rows * ld, SM_F32, v0 > 0};
   }
   if (a.dW) {
-    MmArgs x{};
-    x.jobs = 1;
-    x.k_rows = p.count;
-    MmJob& j = x.job[0];
+    MmJob j{};
+    j.k_rows = p.count;
     j.a = (const char*)p.x;
     j.lda = p.dim_ld;
     j.b = (const char*)p.g;
@@ -374,20 +368,12 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.m = (int)a.dim;
     j.n = (int)cols;
     j.k = (int)a.rows;
-    j.splits = p.w_splits;
     set_planes(j, P, a.rows * p.dim_ld * 2, plane * 2);
-    const int64_t size = a.dw_dtype == SM_F32 ? 4 : 2, ld = round_up(a.dim, 4);
-    char* out = static_cast<char*>(a.dW) + v0 * a.dim * size;
-    EpiStore::Args es{};
-    if (p.w_splits > 1) es.out[0] = {p.dw, ld, cols * ld, SM_F32, 0};
-    else es.out[0] = {out, a.dim, 0, a.dw_dtype, a.accumulate};
-    if (hipError_t e = run_mm<true, true, false, EpiStore>(x, es, p.w_wide, s); e != hipSuccess)
-      return e;
-    if (p.w_splits > 1)
-      return launch_join({p.dw, cols * ld, ld, p.w_splits, nullptr, cols, (int)a.dim, a.dw_dtype,
-                          a.accumulate, out, a.dim}, s);
+    const int64_t size = a.dw_dtype == SM_F32 ? 4 : 2;
+    out.add(j, true, static_cast<char*>(a.dW) + v0 * a.dim * size, a.dw_dtype, a.accumulate, p.dw,
+            p.both.splits[1]);
   }
-  return hipSuccess;
+  return out.run(p.both.wide, s);
 }
 
 }  // namespace
@@ -433,7 +419,7 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s) {
   }
   if (!a.dX) return hipSuccess;
   const int64_t ld = round_up(a.dim, 4);
-  return launch_join({p.dx, a.rows * ld, ld, p.x_splits, p.pos, a.rows, (int)a.dim, a.dtype, 0,
+  return launch_join({p.dx, a.rows * ld, ld, p.both.splits[0], p.pos, a.rows, (int)a.dim, a.dtype, 0,
                       a.dX, a.dim}, s);
 }
 

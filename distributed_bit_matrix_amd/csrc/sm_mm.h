@@ -26,7 +26,7 @@
 namespace sm {
 
 constexpr int kSlab = 64;          // k of one slab
-constexpr int kMaxJobs = 3;
+constexpr int kMaxJobs = 4;
 
 // The pairs of planes of a float32 product: those whose products reach 2^-24 of
 // the largest, the small ones first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0), as
@@ -36,25 +36,26 @@ constexpr int kPairCode = 2 | (1 + 4) << 4 | (2 * 4) << 8 | 1 << 12 | 4 << 16;
 // One product of a launch.  Row lengths count elements.
 struct MmJob {
   const char *a, *a2, *b;          // a2: the second weight of a paired product
+  const int32_t *n_rows, *k_rows;  // where not null, *n_rows replaces n, *k_rows k
   int64_t lda, ldb;
   int32_t m, n, k;
   int32_t pairs, parts;            // of planes: 1 or 6; products that are summed: 1 or 2
   int32_t splits;                  // blocks that share a tile's k
   int32_t m_tiles, n_tiles;
   int32_t block0;                  // its first block
+  int32_t b_km;                    // whether b is k-major, in launches of both kinds
   int64_t a_plane, b_plane;        // bytes from one plane to the next
   int64_t a_part, b_part;          // bytes to the second product's operands
 };
-// n_rows, k_rows: where not null, *n_rows replaces n of every job, *k_rows k.
 struct MmArgs {
   MmJob job[kMaxJobs];
-  int32_t jobs, blocks;
-  const int32_t *n_rows, *k_rows;
+  int32_t jobs;
 };
 
-// What an epilogue knows of its wave's part of a tile.
+// What an epilogue knows of its wave's part of a tile; lds: 16 KiB of its own.
 struct MmPlace {
   int job, split, m0, n0, m, n, lane;
+  char* lds;
 };
 
 template <int TM_, int TN_, int WM_, int WN_, int WPE_ = 2>
@@ -64,7 +65,7 @@ struct MmShape {
   static constexpr int WAVES = WM * WN, TI = TM / WM / 16, TJ = TN / WN / 16;
   static constexpr int A_BYTES = TM * kSlab * 2, B_BYTES = TN * kSlab * 2;
   static constexpr int LDS = 2 * (A_BYTES + B_BYTES);
-  static constexpr int PER_CU = 131072 / LDS;     // blocks a CU
+  static_assert(LDS / WAVES >= 16384, "an epilogue's LDS");
 };
 
 // Where a lane's 16 bytes of load q of a slab lie: load q of a wave fills the
@@ -129,15 +130,15 @@ __device__ __forceinline__ u32x2_t mm_read_tr16(const char* __restrict__ p) {
   return lds_read_tr16(p);
 }
 
-// AKM, BKM: the operand is k-major.  PAIR: A's rows alternate in groups of 16
-// between a and a2 (a tile has TM / 2 features of each).
+// Tile `at` of job ji: its slabs and its epilogue.  AKM, BKM: the operand is
+// k-major.  PAIR: A's rows alternate in groups of 16 between a and a2 (a tile has
+// TM / 2 features of each).
 template <bool AKM, bool BKM, bool PAIR, class Sh, class Epi>
-__global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args, typename Epi::Args ea) {
-#ifdef __HIP_DEVICE_COMPILE__      // (its buffer instructions are unknown to the host's pass)
+__device__ __forceinline__ void mm_tile(const MmArgs& args, const typename Epi::Args& ea, char* smem,
+                                        int ji, int at) {
   constexpr int TM = Sh::TM, TN = Sh::TN, TI = Sh::TI, TJ = Sh::TJ;
   constexpr int QA = Sh::A_BYTES / 1024 / Sh::WAVES, QB = Sh::B_BYTES / 1024 / Sh::WAVES;
   static_assert(!PAIR || (!AKM && QA % 4 == 0), "paired rows");
-  __shared__ __align__(1024) char smem[Sh::LDS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
@@ -145,70 +146,50 @@ __global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args, typ
   constexpr int STAGE_A = Sh::A_BYTES, STAGE_B = Sh::B_BYTES;
   char* const lds_a = smem + wave * QA * 1024;
   char* const lds_b = smem + 2 * STAGE_A + wave * QB * 1024;
-  MmSource<AKM, PAIR> sa;
-  MmSource<BKM, false> sb;
-
-  // The tile whose slabs are loaded (every value is uniform): where its operands
-  // begin, how far they may be read, and the next slab's segment and first k.
-  int ji, split, m0, n0, m_all, n_all, k_all;
-  int slabs, to_load, seg, k0, pairs, a_rows, b_rows, m_end, n_end;
-  int64_t lda, ldb, a_plane, b_plane, a_part, b_part;
-  const char *pa, *pa2, *pb;
-  // Takes tile `at` of the launch; false where there is none.
-  auto take = [&](int at) SM_INLINE -> bool {
-    ji = 0;
-#pragma unroll
-    for (int i = 1; i < kMaxJobs; ++i)
-      if (i < args.jobs && at >= args.job[i].block0) ji = i;
-    const MmJob& job = args.job[ji];
-    m_all = job.m;
-    n_all = __builtin_amdgcn_readfirstlane(args.n_rows ? *args.n_rows : job.n);
-    k_all = __builtin_amdgcn_readfirstlane(args.k_rows ? *args.k_rows : job.k);
-    const int m_tiles = job.m_tiles;
-    const int n_tiles = args.n_rows ? (n_all + TN - 1) / TN : job.n_tiles;
-    // Blocks go round the 8 XCDs: each gets a run of neighbouring tiles, in
-    // groups of 4 tiles along n, so that its L2 holds what they share.
-    const int total = m_tiles * n_tiles * job.splits;
-    at -= job.block0;
-    if (at >= total) return false;
+  // (what follows is uniform; the compiler has to be told of what was loaded or
+  // divided)
+  const MmJob& job = args.job[ji];
+  const int n_all = __builtin_amdgcn_readfirstlane(job.n_rows ? *job.n_rows : job.n);
+  const int k_all = __builtin_amdgcn_readfirstlane(job.k_rows ? *job.k_rows : job.k);
+  const int m_all = job.m, m_tiles = job.m_tiles;
+  const int n_tiles = job.n_rows ? (n_all + TN - 1) / TN : job.n_tiles;
+  // Blocks go round the 8 XCDs: each gets a run of neighbouring tiles, in
+  // groups of 4 tiles along n, so that its L2 holds what they share.
+  const int total = m_tiles * n_tiles * job.splits;
+  at -= job.block0;
+  if (at >= total) return;
+  {
     const int x = at & 7, q = total >> 3, r = total & 7;
     at = x * q + (x < r ? x : r) + (at >> 3);
-    split = __builtin_amdgcn_readfirstlane(at / (m_tiles * n_tiles));
-    at -= split * m_tiles * n_tiles;
-    const int g0 = __builtin_amdgcn_readfirstlane(at / (4 * m_tiles)) * 4;
-    const int gn = n_tiles - g0 < 4 ? n_tiles - g0 : 4;
-    at -= g0 * m_tiles;
-    const int mt = __builtin_amdgcn_readfirstlane(at / gn);
-    m0 = mt * (PAIR ? TM / 2 : TM);
-    n0 = (g0 + at - mt * gn) * TN;
-    lda = job.lda * 2;
-    ldb = job.ldb * 2;
-    const int a_tile = PAIR ? TM / 2 : TM;
-    a_rows = m_all - m0 < a_tile ? m_all - m0 : a_tile;
-    b_rows = n_all - n0 < TN ? n_all - n0 : TN;
-    m_end = (m_all - m0 + 7) & ~7;
-    n_end = (n_all - n0 + 7) & ~7;
-    sa.place(lane, job.lda);
-    sb.place(lane, job.ldb);
-    const int64_t a0 = AKM ? (int64_t)m0 * 2 : m0 * lda;
-    const int64_t b0 = BKM ? (int64_t)n0 * 2 : n0 * ldb;
-    pa = job.a + a0;
-    if constexpr (PAIR) pa2 = job.a2 + a0;
-    pb = job.b + b0;
-    a_plane = job.a_plane;
-    b_plane = job.b_plane;
-    a_part = job.a_part;
-    b_part = job.b_part;
-    pairs = job.pairs;
-    const int per_seg = (k_all + kSlab - 1) / kSlab, all = per_seg * pairs * job.parts;
-    const int per = __builtin_amdgcn_readfirstlane((all + job.splits - 1) / job.splits);
-    const int s0 = split * per;
-    const int s1 = __builtin_amdgcn_readfirstlane(s0 + per < all ? s0 + per : all);
-    to_load = slabs = s1 - s0;
-    seg = __builtin_amdgcn_readfirstlane(s0 < s1 ? s0 / per_seg : 0);
-    k0 = (s0 - seg * per_seg) * kSlab;
-    return true;
-  };
+  }
+  const int split = __builtin_amdgcn_readfirstlane(at / (m_tiles * n_tiles));
+  at -= split * m_tiles * n_tiles;
+  const int g0 = __builtin_amdgcn_readfirstlane(at / (4 * m_tiles)) * 4;
+  const int gn = n_tiles - g0 < 4 ? n_tiles - g0 : 4;
+  at -= g0 * m_tiles;
+  const int mt = __builtin_amdgcn_readfirstlane(at / gn);
+  constexpr int A_TILE = PAIR ? TM / 2 : TM;
+  const int m0 = mt * A_TILE, n0 = (g0 + at - mt * gn) * TN;
+  const int64_t lda = job.lda * 2, ldb = job.ldb * 2;
+  const int a_rows = m_all - m0 < A_TILE ? m_all - m0 : A_TILE;
+  const int b_rows = n_all - n0 < TN ? n_all - n0 : TN;
+  const int m_end = (m_all - m0 + 7) & ~7, n_end = (n_all - n0 + 7) & ~7;
+  const int64_t a0 = AKM ? (int64_t)m0 * 2 : m0 * lda, b0 = BKM ? (int64_t)n0 * 2 : n0 * ldb;
+  const char *pa = job.a + a0, *pa2 = job.a2 + a0, *pb = job.b + b0;
+  const int64_t a_plane = job.a_plane, b_plane = job.b_plane;
+  const int64_t a_part = job.a_part, b_part = job.b_part;
+  MmSource<AKM, PAIR> sa;
+  MmSource<BKM, false> sb;
+  sa.place(lane, job.lda);
+  sb.place(lane, job.ldb);
+  const int pairs = job.pairs, per_seg = (k_all + kSlab - 1) / kSlab;
+  const int all = per_seg * pairs * job.parts;
+  const int per = __builtin_amdgcn_readfirstlane((all + job.splits - 1) / job.splits);
+  const int s0 = split * per;
+  const int slabs = __builtin_amdgcn_readfirstlane((s0 + per < all ? s0 + per : all) - s0);
+  // the next slab to load: its segment and first k
+  int to_load = slabs, seg = __builtin_amdgcn_readfirstlane(slabs > 0 ? s0 / per_seg : 0);
+  int k0 = (s0 - seg * per_seg) * kSlab;
 
   __amdgpu_buffer_rsrc_t ra, ra2, rb;
   uint32_t oa[2], ob[2];
@@ -273,39 +254,40 @@ __global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args, typ
   };
 
   f32x4_t acc[TI][TJ];
-  // A slab goes in four steps: its two k-steps of 32, by halves of A's rows.
-  // While one is multiplied the fragments of the next are read.  The next slab
-  // is waited for before the last step: past that barrier every wave has read
-  // all of this slab, whose place the loads of the slab after next then take.
-  constexpr int HI = TI / 2;
+  // A slab goes in steps: its two k-steps of 32, by parts of A's rows.  While one
+  // is multiplied the fragments of the next are read.  The next slab is waited for
+  // before the last step: past that barrier every wave has read all of this slab,
+  // whose place the loads of the slab after next then take.  (Quarters of a
+  // k-major A of 128 rows: its addresses take the registers that halves would
+  // need, and a register spilled to memory waits for all loads to LDS.)
+  constexpr int NQ = AKM && TI == 8 ? 4 : 2, HI = TI / NQ;
   bf16x8_t a[2][HI], b[2][TJ];
-  auto read_a = [&](auto set, int stage, int kk, int half) SM_INLINE {
-    constexpr int S = decltype(set)::value;
+  auto read_a = [&](int stage, auto kk, auto part) SM_INLINE {
+    constexpr int K = decltype(kk)::value, H = decltype(part)::value;
 #pragma unroll
     for (int i = 0; i < HI; ++i)
-      a[S][i] = frag(std::bool_constant<AKM>{}, fa, stage * STAGE_A, half * HI + i, kk);
+      a[H & 1][i] = frag(std::bool_constant<AKM>{}, fa, stage * STAGE_A, H * HI + i, K);
   };
-  auto read_b = [&](auto set, int stage, int kk) SM_INLINE {
-    constexpr int S = decltype(set)::value;
+  auto read_b = [&](int stage, auto kk) SM_INLINE {
+    constexpr int K = decltype(kk)::value;
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
-      b[S][j] = frag(std::bool_constant<BKM>{}, fb, stage * STAGE_B, j, kk);
+      b[K][j] = frag(std::bool_constant<BKM>{}, fb, stage * STAGE_B, j, K);
   };
-  auto multiply = [&](auto kk, auto half) SM_INLINE {
-    constexpr int K = decltype(kk)::value, H = decltype(half)::value;
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
+  constexpr int RDA = HI * (AKM ? 2 : 1), RDB = TJ * (BKM ? 2 : 1);
+  // the products of a step, in this order: `reads` reads first, `loads` loads among
+  // the products
+  auto multiply = [&](auto kk, auto part, auto reads, auto loads) SM_INLINE {
+    constexpr int K = decltype(kk)::value, H = decltype(part)::value;
+    constexpr int R = decltype(reads)::value, L = decltype(loads)::value;
 #pragma unroll
     for (int i = 0; i < HI; ++i)
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
-        acc[H * HI + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[H][i], b[K][j],
-                                                                    acc[H * HI + i][j], 0, 0, 0);
-  };
-  constexpr std::integral_constant<int, 0> c0{};
-  constexpr std::integral_constant<int, 1> c1{};
-  // the order of a step's instructions: its reads first, then the products, with
-  // `loads` loads among them
-  auto order = [&](auto reads, auto loads) SM_INLINE {
-    constexpr int R = decltype(reads)::value, L = decltype(loads)::value;
+        acc[H * HI + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            a[H & 1][i], b[K][j], acc[H * HI + i][j], 0, 0, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
     if constexpr (L == 0) {
       __builtin_amdgcn_sched_group_barrier(0x008, HI * TJ, 0);
@@ -318,33 +300,33 @@ __global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args, typ
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  constexpr int RDA = HI * (AKM ? 2 : 1), RDB = TJ * (BKM ? 2 : 1);
-  constexpr std::integral_constant<int, RDA> reads_a{};
-  constexpr std::integral_constant<int, RDA + RDB> reads_ab{};
-  constexpr std::integral_constant<int, QA + QB> loads{};
+  auto parts_of = [&](int stage, auto kk, auto self, auto part) SM_INLINE {
+    constexpr int H = decltype(part)::value;
+    if constexpr (H + 1 < NQ) {
+      constexpr std::integral_constant<int, H + 1> next{};
+      read_a(stage, kk, next);
+      multiply(kk, part, std::integral_constant<int, RDA>{}, c0);
+      self(stage, kk, self, next);
+    }
+  };
   auto slab = [&](int stage) SM_INLINE {
-    read_a(c1, stage, 0, 1);
-    multiply(c0, c0);
-    order(reads_a, c0);
-    read_b(c1, stage, 1);
-    read_a(c0, stage, 1, 0);
+    constexpr std::integral_constant<int, NQ - 1> end{};
+    parts_of(stage, c0, parts_of, c0);
+    read_b(stage, c1);
+    read_a(stage, c1, c0);
     aim();
-    multiply(c0, c1);
-    order(reads_ab, c0);
-    read_a(c1, stage, 1, 1);
-    multiply(c1, c0);
-    order(reads_a, c0);
+    multiply(c0, end, std::integral_constant<int, RDA + RDB>{}, c0);
+    parts_of(stage, c1, parts_of, c0);
     wait_vmcnt<0>();
     wait_lgkmcnt0();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read_b(c0, stage ^ 1, 0);
-    read_a(c0, stage ^ 1, 0, 0);
+    read_b(stage ^ 1, c0);
+    read_a(stage ^ 1, c0, c0);
     fire(stage);
-    multiply(c1, c1);
-    order(reads_ab, loads);
+    multiply(c1, end, std::integral_constant<int, RDA + RDB>{},
+             std::integral_constant<int, QA + QB>{});
   };
-  if (!take(blockIdx.x)) return;
   aim();
   fire(0);
   aim();
@@ -355,21 +337,51 @@ __global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args, typ
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   wait_vmcnt<QA + QB>();
   __builtin_amdgcn_s_barrier();
-  read_b(c0, 0, 0);
-  read_a(c0, 0, 0, 0);
+  read_b(0, c0);
+  read_a(0, c0, c0);
   // (an odd slab too many is zeros)
   for (int s = 0; s < slabs; s += 2) {
     slab(0);
     slab(1);
   }
-  wait_vmcnt<0>();      // nothing may arrive in LDS after the block's end
+  // the last, empty loads: the epilogue's LDS, and the block's end, wait for them
+  wait_vmcnt<0>();
+  __builtin_amdgcn_s_barrier();
   // (opaque, so that the epilogue's addresses are not held through the loop)
   int lane_after = lane;
   asm volatile("" : "+v"(lane_after));
   Epi::template run<TI, TJ>(ea,
                             MmPlace{ji, split, m0 + wm * (PAIR ? RA / 2 : RA), n0 + wn * RB, m_all,
-                                    n_all, lane_after},
+                                    n_all, lane_after, smem + wave * (Sh::LDS / Sh::WAVES)},
                             acc);
+}
+
+__device__ __forceinline__ int mm_job(const MmArgs& args, int at) {
+  int ji = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxJobs; ++i)
+    if (i < args.jobs && at >= args.job[i].block0) ji = i;
+  return ji;
+}
+
+// (The kernels' buffer instructions are unknown to the host's pass.)
+template <bool AKM, bool BKM, bool PAIR, class Sh, class Epi>
+__global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm(MmArgs args,
+                                                                typename Epi::Args ea) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __align__(1024) char smem[Sh::LDS];
+  mm_tile<AKM, BKM, PAIR, Sh, Epi>(args, ea, smem, mm_job(args, blockIdx.x), blockIdx.x);
+#endif
+}
+// A k-major, B of either kind: products whose tiles share the chip.
+template <class Sh, class Epi>
+__global__ __launch_bounds__(64 * Sh::WAVES, Sh::WPE) void k_mm_both(MmArgs args,
+                                                                     typename Epi::Args ea) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __align__(1024) char smem[Sh::LDS];
+  const int ji = __builtin_amdgcn_readfirstlane(mm_job(args, blockIdx.x));
+  if (args.job[ji].b_km) mm_tile<true, true, false, Sh, Epi>(args, ea, smem, ji, blockIdx.x);
+  else mm_tile<true, false, false, Sh, Epi>(args, ea, smem, ji, blockIdx.x);
 #endif
 }
 

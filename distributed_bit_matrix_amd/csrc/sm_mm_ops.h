@@ -16,20 +16,95 @@ __device__ __forceinline__ void split3(float f, bf16_t (&p)[3]) {
   p[1] = f32_to_bf16(r);
   p[2] = f32_to_bf16(r - bf16_to_f32(p[1]));
 }
-// Four neighbouring entries to P planes, `plane` entries apart; 8-byte aligned.
-template <int P>
-__device__ __forceinline__ void store_planes(bf16_t* p, int64_t plane, const float (&v)[4]) {
+// 16 rows of an epilogue's F features on their way to memory.  In the accumulators
+// a lane has 4 features of one row: stores from there write 32 bytes of each of 16
+// rows (8 us for a tile of 256 x 256 bfloat16, as long as 5 slabs).  Through LDS
+// they become 16 bytes a lane of whole lines.  Rows are swizzled by 16-byte pieces:
+// lanes of 16 rows write, and lanes of one row read, distinct banks.  A wave uses
+// its own LDS, two buffers (three of bfloat16) in turn.
+template <typename T, int F>
+struct MmRows {
+  static constexpr int ES = (int)sizeof(T), RB = F * ES, CR = RB / 16, V = 16 / ES;
+  static_assert(CR >= 4 && CR <= 32 && (ES == 4 ? 2 : 3) * 16 * RB <= 16384, "rows of an epilogue");
+  char* lds;
+  int lane;
+  __device__ __forceinline__ char* piece(int buf, int row, int chunk) const {
+    return lds + buf * 16 * RB + row * RB + ((chunk ^ (row & (CR - 1))) << 4);
+  }
+  // features 16 i + 4 (lane / 16) .. +3 of row lane % 16
+  __device__ __forceinline__ void put(int buf, int i, const f32x4_t& v) const {
+    const int row = lane & 15, g = 4 * i + (lane >> 4);      // group of 4 features
+    if constexpr (ES == 4)
+      *reinterpret_cast<f32x4_t*>(piece(buf, row, g)) = v;
+    else
+      *reinterpret_cast<u32x2_t*>(piece(buf, row, g >> 1) + (g & 1) * 8) =
+          u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  }
+  // the first `rows` of the 16 and `cols` of the F to p; ADD: to what is there
+  template <bool ADD = false>
+  __device__ __forceinline__ void flush(int buf, T* p, int64_t ld, int rows, int cols) const {
+#pragma unroll
+    for (int it = 0; it < CR / 4; ++it) {
+      const int row = it * (64 / CR) + lane / CR, chunk = lane % CR, c = chunk * V;
+      const u32x4_t t = *reinterpret_cast<const u32x4_t*>(piece(buf, row, chunk));
+      if (row >= rows || c >= cols) continue;
+      T* q = p + row * ld + c;
+      if constexpr (ES == 4) {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(t[k]);
+        if (c + V <= cols) {
+          if constexpr (ADD) {
+            const u32x4_a4 old = *reinterpret_cast<const u32x4_a4*>(q);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] += __uint_as_float(old[k]);
+          }
+          store_vec<4>(q, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (c + k < cols) q[k] = (ADD ? q[k] : 0.f) + v[k];
+        }
+      } else {
+        if (c + V <= cols) {
+          *reinterpret_cast<u32x4_a2*>(q) = u32x4_a2{t[0], t[1], t[2], t[3]};
+        } else {
+#pragma unroll
+          for (int k = 0; k < 7; ++k)
+            if (c + k < cols) q[k] = (bf16_t)(t[k / 2] >> (16 * (k & 1)));
+        }
+      }
+    }
+  }
+};
+
+// 16 rows of F features to P planes, `plane` entries apart, from accumulators
+// v[i] as `put` takes them.
+template <int P, int F>
+__device__ __forceinline__ void put_planes(const MmPlace& at, const f32x4_t (&v)[F / 16], bf16_t* p,
+                                           int64_t plane, int64_t ld, int rows, int cols) {
+  const MmRows<bf16_t, F> out{at.lds, at.lane};
   if constexpr (P == 1) {
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+#pragma unroll
+    for (int i = 0; i < F / 16; ++i) out.put(0, i, v[i]);
+    out.flush(0, p, ld, rows, cols);
   } else {
-    bf16_t t[4][3];
+    f32x4_t left[F / 16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) split3(v[k], t[k]);
+    for (int i = 0; i < F / 16; ++i) left[i] = v[i];
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      *reinterpret_cast<u32x2_t*>(p + q * plane) =
-          u32x2_t{(uint32_t)t[0][q] | ((uint32_t)t[1][q] << 16),
-                  (uint32_t)t[2][q] | ((uint32_t)t[3][q] << 16)};
+    for (int q = 0; q < 3; ++q) {
+#pragma unroll
+      for (int i = 0; i < F / 16; ++i) {
+        out.put(q & 1, i, left[i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float hi = bf16_to_f32(f32_to_bf16(left[i][k]));
+          left[i][k] = __builtin_isfinite(hi) ? left[i][k] - hi : 0.f;
+        }
+      }
+      out.flush(q & 1, p + q * plane, ld, rows, cols);
+    }
   }
 }
 
@@ -45,47 +120,26 @@ struct EpiStore {
   struct Args {
     MmOut out[kMaxJobs];
   };
-  template <typename T, bool WHOLE, bool ADD, int TI, int TJ>
-  static __device__ __forceinline__ void store(T* p, int64_t ld, const MmPlace& at,
+  template <typename T, bool ADD, int TI, int TJ>
+  static __device__ __forceinline__ void store(const MmOut& o, const MmPlace& at,
                                                const f32x4_t (&acc)[TI][TJ]) {
-    const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
+    const MmRows<T, 16 * TI> rows{at.lds, at.lane};
+    T* p = static_cast<T*>(o.p) + at.split * o.split_step + at.m0;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      if (!WHOLE && nc + 16 * j >= at.n) continue;
-      T* row = p + (int64_t)(nc + 16 * j) * ld + mc;
 #pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        const int here = WHOLE ? 4 : at.m - mc - 16 * i;
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = (ADD && k < here ? to_f32(row[16 * i + k]) : 0.f) + acc[i][j][k];
-        if (here >= 4) {
-          store_vec<4>(row + 16 * i, v);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            if (k < here) put(row + 16 * i + k, v[k]);
-        }
-      }
+      for (int i = 0; i < TI; ++i) rows.put(j & 1, i, acc[i][j]);
+      const int n = at.n0 + 16 * j;
+      rows.template flush<ADD>(j & 1, p + (int64_t)n * o.ld, o.ld, at.n - n, at.m - at.m0);
     }
-  }
-  template <typename T, bool ADD, int TI, int TJ>
-  static __device__ __forceinline__ void store_as(const MmOut& o, const MmPlace& at,
-                                                  const f32x4_t (&acc)[TI][TJ]) {
-    T* p = static_cast<T*>(o.p) + at.split * o.split_step;
-    if (at.m0 + 16 * TI <= at.m && at.n0 + 16 * TJ <= at.n)
-      store<T, true, ADD>(p, o.ld, at, acc);
-    else
-      store<T, false, ADD>(p, o.ld, at, acc);
   }
   template <int TI, int TJ>
   static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
                                              const f32x4_t (&acc)[TI][TJ]) {
     const MmOut& o = e.out[at.job];
-    if (o.dtype == SM_BF16) store_as<bf16_t, false>(o, at, acc);
-    else if (o.add) store_as<float, true>(o, at, acc);
-    else store_as<float, false>(o, at, acc);
+    if (o.dtype == SM_BF16) store<bf16_t, false>(o, at, acc);
+    else if (o.add) store<float, true>(o, at, acc);
+    else store<float, false>(o, at, acc);
   }
 };
 
@@ -147,22 +201,26 @@ struct Places {
 };
 
 constexpr int kCus = 256;
-// Tiles of 256 x 256 where they fill the chip, or nearly; else 128 x 128.
-inline bool wide_tiles(int64_t m, int64_t n) {
-  return ((m + 255) / 256) * ((n + 255) / 256) >= 160;
-}
-// How many blocks share a tile's k: as many as fill the chip, each with 8 slabs
-// at least.
-inline int k_splits(int64_t m, int64_t n, int64_t slabs, bool wide) {
-  const int t = wide ? 256 : 128;
-  const int64_t tiles = ((m + t - 1) / t) * ((n + t - 1) / t);
-  const int64_t want = (wide ? kCus : 2 * kCus) / std::max<int64_t>(1, tiles);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, slabs / 8, 16}));
-}
 
-// Launches the jobs of `a` (operands, extents, planes and splits are set).
+// A product that is to be launched: its extents, in slabs of k; whether its k may
+// be split.
+struct MmSize {
+  int64_t m, n, slabs;
+  bool may_split;
+};
+// Tiles of 256 x 256 or 128 x 128, and how many blocks share a tile's k.
+struct MmPlan {
+  bool wide;
+  int splits[kMaxJobs];
+};
+// The plan whose blocks, dealt out longest first to the CUs as they fall free, are
+// done first.  A slab takes 1.65 us in a wide tile and 1.0 in one of two narrow
+// ones on a CU; a block 5 us more for its first loads and its epilogue; a split's
+// sums go to memory and back.
+MmPlan plan_products(const MmSize* sizes, int jobs);
+
 template <bool AKM, bool BKM, bool PAIR, class Sh, class Epi>
-hipError_t run_mm_as(MmArgs& a, const typename Epi::Args& e, hipStream_t s) {
+hipError_t run_mm_as(MmArgs& a, const typename Epi::Args& e, bool both, hipStream_t s) {
   int64_t blocks = 0;
   for (int i = 0; i < a.jobs; ++i) {
     MmJob& j = a.job[i];
@@ -171,19 +229,38 @@ hipError_t run_mm_as(MmArgs& a, const typename Epi::Args& e, hipStream_t s) {
     j.n_tiles = (j.n + Sh::TN - 1) / Sh::TN;
     j.block0 = (int)blocks;
     blocks += (int64_t)j.m_tiles * j.n_tiles * j.splits;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   }
   if (blocks == 0) return hipSuccess;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  a.blocks = (int)blocks;
-  hipLaunchKernelGGL((k_mm<AKM, BKM, PAIR, Sh, Epi>), dim3((unsigned)blocks),
-                     dim3(64 * Sh::WAVES), 0, s, a, e);
+  const dim3 grid((unsigned)blocks), block(64 * Sh::WAVES);
+  if constexpr (AKM && !PAIR && std::is_same_v<Epi, EpiStore>) {
+    if (both) {
+      hipLaunchKernelGGL((k_mm_both<Sh, Epi>), grid, block, 0, s, a, e);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_mm<AKM, BKM, PAIR, Sh, Epi>), grid, block, 0, s, a, e);
   return hipGetLastError();
 }
+// Launches the jobs of `a` (operands, extents, planes and splits are set).
 template <bool AKM, bool BKM, bool PAIR, class Epi>
 hipError_t run_mm(MmArgs& a, const typename Epi::Args& e, bool wide, hipStream_t s) {
-  return wide ? run_mm_as<AKM, BKM, PAIR, MmShape<256, 256, 2, 4>, Epi>(a, e, s)
-              : run_mm_as<AKM, BKM, PAIR, MmShape<128, 128, 2, 2>, Epi>(a, e, s);
+  return wide ? run_mm_as<AKM, BKM, PAIR, MmShape<256, 256, 2, 4>, Epi>(a, e, false, s)
+              : run_mm_as<AKM, BKM, PAIR, MmShape<128, 128, 2, 2>, Epi>(a, e, false, s);
 }
+
+// Products with a k-major A that end in arrays (or in sums of splits, joined here),
+// all in one launch.
+struct MmStores {
+  MmArgs a{};
+  EpiStore::Args e{};
+  JoinArgs join[kMaxJobs];
+  // job j, whose rows go to dst; sums: where those of its splits go, if it has any
+  void add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t accumulate, float* sums,
+           int splits);
+  hipError_t run(bool wide, hipStream_t s);
+  hipError_t joins(hipStream_t s);
+};
 
 #define SM_TRY(call)                                         \
   do {                                                       \

@@ -3,6 +3,23 @@
 
 namespace sm {
 
+// Four neighbouring entries to P planes, `plane` entries apart; 8-byte aligned.
+template <int P>
+__device__ __forceinline__ void store_planes(bf16_t* p, int64_t plane, const float (&v)[4]) {
+  if constexpr (P == 1) {
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  } else {
+    bf16_t t[4][3];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split3(v[k], t[k]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<u32x2_t*>(p + q * plane) =
+          u32x2_t{(uint32_t)t[0][q] | ((uint32_t)t[1][q] << 16),
+                  (uint32_t)t[2][q] | ((uint32_t)t[3][q] << 16)};
+  }
+}
+
 // A thread copies 8 entries of a row.  Bound by HBM.
 template <typename T, int P>
 __global__ __launch_bounds__(256) void k_planes(const T* src, int64_t stride, int64_t rows,
@@ -74,6 +91,138 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
       for (int q = 0; q < here; ++q) put(o + q, v[q]);
     }
   }
+}
+
+namespace {
+
+// When the blocks of the jobs are done, in microseconds: `len` a block of each job,
+// dealt out in order to `slots` places as they fall free.  Places are kept as
+// levels, equal ones together.
+double makespan(const int64_t* blocks, const double* len, int jobs, int slots) {
+  struct Level {
+    double t;
+    int64_t c;
+  } lv[64];
+  int n = 1;
+  lv[0] = {0.0, slots};
+  double last = 0.0;
+  for (int j = 0; j < jobs; ++j) {
+    int64_t left = blocks[j];
+    // whole rounds over all places change nothing but the time
+    if (left > 8 * slots) {
+      const int64_t rounds = left / slots - 7;
+      for (int i = 0; i < n; ++i) lv[i].t += rounds * len[j];
+      left -= rounds * slots;
+    }
+    while (left > 0) {
+      int lo = 0;
+      for (int i = 1; i < n; ++i)
+        if (lv[i].t < lv[lo].t) lo = i;
+      const int64_t k = std::min(left, lv[lo].c);
+      const double t = lv[lo].t + len[j];
+      left -= k;
+      lv[lo].c -= k;
+      if (lv[lo].c == 0) lv[lo] = lv[--n];
+      int at = 0;
+      while (at < n && lv[at].t != t) ++at;
+      if (at < n) lv[at].c += k;
+      else if (n < 64) lv[n++] = {t, k};
+      else lv[0].c += k;      // (no more than an estimate)
+    }
+  }
+  for (int i = 0; i < n; ++i) last = std::max(last, lv[i].t);
+  return last;
+}
+
+}  // namespace
+
+MmPlan plan_products(const MmSize* sizes, int jobs) {
+  MmPlan best{};
+  double least = 1e30;
+  for (const bool wide : {true, false}) {
+    const int t = wide ? 256 : 128, slots = wide ? kCus : 2 * kCus;
+    const double slab = wide ? 1.65 : 1.0;
+    int64_t longest = 1;
+    for (int j = 0; j < jobs; ++j) longest = std::max(longest, sizes[j].slabs);
+    for (int part = 1; part <= 16; ++part) {
+      const double target = (double)longest / part;
+      if (part > 1 && target < 4) break;
+      MmPlan p{};
+      p.wide = wide;
+      int64_t blocks[kMaxJobs];
+      double len[kMaxJobs], cost = 0;
+      bool split = false;
+      for (int j = 0; j < jobs; ++j) {
+        const MmSize& z = sizes[j];
+        const int64_t tiles = ((z.m + t - 1) / t) * ((z.n + t - 1) / t);
+        const int64_t most = z.may_split ? std::min<int64_t>(16, std::max<int64_t>(1, z.slabs / 4))
+                                         : 1;
+        p.splits[j] =
+            (int)std::max<int64_t>(1, std::min<int64_t>(most, (int64_t)(z.slabs / target + 0.5)));
+        split = split || p.splits[j] > 1;
+        blocks[j] = tiles * p.splits[j];
+        len[j] = slab * ((z.slabs + p.splits[j] - 1) / p.splits[j]) + 5.0;
+        // the sums are written and read (4 bytes, at about 5 MB a microsecond), by a
+        // launch of their own
+        if (p.splits[j] > 1) cost += p.splits[j] * z.m * z.n * 8 / 5e6 + 4.0;
+      }
+      if (part > 1 && !split) continue;
+      // longest first, as they are launched
+      for (int i = 0; i < jobs; ++i)
+        for (int j = i + 1; j < jobs; ++j)
+          if (len[j] > len[i]) std::swap(len[i], len[j]), std::swap(blocks[i], blocks[j]);
+      cost += makespan(blocks, len, jobs, slots);
+      if (cost < least) least = cost, best = p;
+    }
+  }
+  return best;
+}
+
+void MmStores::add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t accumulate,
+                   float* sums, int splits) {
+  const int i = a.jobs++;
+  a.job[i] = j;
+  a.job[i].b_km = b_km;
+  a.job[i].splits = splits;
+  const int64_t ld = round_up(j.m, 4);
+  join[i] = JoinArgs{};
+  if (splits > 1) {
+    e.out[i] = {sums, ld, j.n * ld, SM_F32, 0};
+    join[i] = {sums, j.n * ld, ld, splits, nullptr, j.n, j.m, dtype, accumulate, dst, j.m};
+  } else {
+    e.out[i] = {dst, j.m, 0, dtype, accumulate};
+  }
+}
+
+hipError_t MmStores::run(bool wide, hipStream_t s) {
+  if (a.jobs == 0) return hipSuccess;
+  // the longest blocks first
+  const auto length = [&](const MmJob& j) {
+    return (int64_t)j.k * j.pairs * j.parts / j.splits;
+  };
+  bool km = false, rows = false;
+  for (int i = 0; i < a.jobs; ++i) {
+    for (int k = i + 1; k < a.jobs; ++k)
+      if (length(a.job[k]) > length(a.job[i])) {
+        std::swap(a.job[i], a.job[k]);
+        std::swap(e.out[i], e.out[k]);
+        std::swap(join[i], join[k]);
+      }
+    (a.job[i].b_km ? km : rows) = true;
+  }
+  const auto go = [&](auto shape) {
+    typedef decltype(shape) Sh;
+    return km ? run_mm_as<true, true, false, Sh, EpiStore>(a, e, rows, s)
+              : run_mm_as<true, false, false, Sh, EpiStore>(a, e, false, s);
+  };
+  SM_TRY(wide ? go(MmShape<256, 256, 2, 4>{}) : go(MmShape<128, 128, 2, 2>{}));
+  return joins(s);
+}
+
+hipError_t MmStores::joins(hipStream_t s) {
+  for (int i = 0; i < a.jobs; ++i)
+    if (join[i].splits > 0) SM_TRY(launch_join(join[i], s));
+  return hipSuccess;
 }
 
 hipError_t launch_join(const JoinArgs& a, hipStream_t s) {
