@@ -207,13 +207,91 @@ struct FewStore {
   __device__ __forceinline__ void finish(int) {}
 };
 
+// What follows the first product where its k is split: the sums of the splits
+// joined, and what the epilogues above do.  A thread has 4 features of a row.
+struct MidArgs {
+  const float* sums[2];    // [split][rows][hidden rounded up to 4]: gate and up, or dh
+  int32_t splits;
+  int64_t rows;
+  int32_t hidden, ld;
+  int64_t plane;
+  const float* pre;        // backward
+  float* pre_out;          // forward, or null
+  bf16_t* out[3];          // h; or dg, du, h
+};
+template <int P>
+__device__ __forceinline__ void store_mid(bf16_t* p, int64_t plane, f32x4_t v) {
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+    *reinterpret_cast<u32x2_t*>(p + q * plane) = u32x2_t{lo, hi};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float t = bf16_to_f32((bf16_t)((k < 2 ? lo : hi) >> (16 * (k & 1))));
+      v[k] = __builtin_isfinite(t) ? v[k] - t : 0.f;
+    }
+  }
+}
+template <int P, int ACT, bool GRAD>
+__global__ __launch_bounds__(256) void k_mid(MidArgs a) {
+  const int hidden = a.hidden, hid4 = (hidden + 3) & ~3, per = ((hidden + 7) & ~7) / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.rows * per;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per;
+    const int f = (int)(i - r * per) * 4;
+    f32x4_t s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (f < hidden) {
+#pragma unroll
+      for (int w = 0; w < (GRAD ? 1 : 2); ++w) {
+        const float* p = a.sums[w] + r * hid4 + f;
+        for (int k = 0; k < a.splits; ++k, p += a.rows * hid4)
+          s[w] += *reinterpret_cast<const f32x4_t*>(p);
+      }
+    }
+    f32x4_t v[3];
+    const int64_t pre = r * 2 * hidden + f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool in = f + k < hidden;
+      if constexpr (GRAD) {
+        const float g = in ? a.pre[pre + k] : 0.f, u = in ? a.pre[pre + hidden + k] : 0.f;
+        const float dh = in ? s[0][k] : 0.f;
+        float act_g, slope;
+        act_slope<ACT>(g, act_g, slope);
+        v[0][k] = dh * u * slope;
+        v[1][k] = dh * act_g;
+        v[2][k] = act_g * u;
+      } else {
+        const float g = in ? s[0][k] : 0.f, u = in ? s[1][k] : 0.f;
+        v[0][k] = act<ACT>(g) * u;
+        if (a.pre_out && in) a.pre_out[pre + k] = g, a.pre_out[pre + hidden + k] = u;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < (GRAD ? 3 : 1); ++w)
+      store_mid<P>(a.out[w] + r * a.ld + f, a.plane, v[w]);
+  }
+}
+
 namespace {
 
-// An operand: the caller's matrix where it fits, else a copy.
+template <int P, int ACT, bool GRAD>
+hipError_t launch_mid(const MidArgs& a, hipStream_t s) {
+  const int64_t work = a.rows * (round_up(a.hidden, 8) / 4);
+  hipLaunchKernelGGL((k_mid<P, ACT, GRAD>),
+                     dim3((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16)), dim3(256), 0, s,
+                     a);
+  return hipGetLastError();
+}
+// A product's sums of splits, for a launch of its own that joins them.
+MmOut sums_out(float* sums, int64_t m, int64_t n) {
+  const int64_t ld = round_up(m, 4);
+  return {sums, ld, n * ld, SM_F32, 0};
+}
+
 struct Operand {
   const char* p;
   int64_t ld, plane;       // elements; bytes from one plane to the next
-  bf16_t* copy;
 };
 
 struct FfnPlan {
@@ -224,6 +302,8 @@ struct FfnPlan {
   MmPlan first, out;       // tiles of the first product; of the others (forward: y;
                            // backward: dx, dwg, dwu, dwd)
   float* sums[4];          // of their splits
+  bool split_first;        // the first product's k is split, and what follows it
+  float* mid;              // takes a launch of its own: its sums
   size_t bytes;
 };
 
@@ -231,8 +311,8 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
                  void* ws) {
   FfnPlan p{};
   p.planes = dtype == SM_BF16 ? 1 : 3;
-  p.ld_d = round_up(dim, 8);
-  p.ld_f = round_up(hidden, 8);
+  p.ld_d = operand_ld(dim);
+  p.ld_f = operand_ld(hidden);
   Places at{static_cast<char*>(ws)};
   if (!backward && rows <= kFewRows) {
     p.few_h = dtype == SM_BF16 ? (void*)at.take<bf16_t>(rows * hidden)
@@ -246,6 +326,13 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
   p.wu = at.take<bf16_t>(p.planes * hidden * p.ld_d);
   p.wd = at.take<bf16_t>(p.planes * dim * p.ld_f);
   p.h = at.take<bf16_t>(p.planes * rows * p.ld_f);
+  const auto first = [&](MmSize z, int jobs) {
+    const MmSize both[2] = {z, z};
+    p.first = plan_products(both, jobs);
+    p.split_first = p.first.splits[0] > 1;
+    if (p.split_first)
+      p.mid = at.take<float>(jobs * p.first.splits[0] * rows * round_up(hidden, 4));
+  };
   const auto slabs = [&](int64_t k) { return segs * ((k + 63) / 64); };
   const auto room = [&](const MmSize* z, int jobs) {
     p.out = plan_products(z, jobs);
@@ -254,35 +341,32 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
         p.sums[i] = at.take<float>(p.out.splits[i] * z[i].n * round_up(z[i].m, 4));
   };
   if (!backward) {
-    const MmSize z{2 * hidden, rows, slabs(dim), false}, y{dim, rows, slabs(hidden), true};
-    p.first = plan_products(&z, 1);
+    const MmSize y{dim, rows, slabs(hidden), true};
+    first({hidden, rows, slabs(dim), true}, 2);
     room(&y, 1);
   } else {
     p.dy = at.take<bf16_t>(p.planes * rows * p.ld_d);
     p.dg = at.take<bf16_t>(p.planes * rows * p.ld_f);
     p.du = at.take<bf16_t>(p.planes * rows * p.ld_f);
-    const MmSize z{hidden, rows, slabs(dim), false};
     const MmSize o[4] = {{dim, rows, 2 * slabs(hidden), true},
                          {dim, hidden, slabs(rows), true},
                          {dim, hidden, slabs(rows), true},
                          {hidden, dim, slabs(rows), true}};
-    p.first = plan_products(&z, 1);
+    first({hidden, rows, slabs(dim), true}, 1);
     room(o, 4);
   }
   p.bytes = at.used;
   return p;
 }
 
-hipError_t operand(Operand& o, const void* src, int32_t dtype, int64_t rows, int64_t cols,
-                   int64_t stride, int planes, bf16_t* copy, hipStream_t s) {
-  if (operand_fits(src, dtype, cols, stride)) {
-    o = {static_cast<const char*>(src), stride, 0, nullptr};
-    return hipSuccess;
-  }
-  const int64_t ld = round_up(cols, 8);
-  o = {reinterpret_cast<const char*>(copy), ld, rows * ld * 2, copy};
-  return launch_planes({src, stride, dtype, planes, rows, (int)cols, (int32_t)ld, nullptr, nullptr,
-                        copy}, s);
+// An operand: where the caller's matrix lies, or a copy that `c` is to make.
+Operand operand(PlanesJobs& c, const void* src, int32_t dtype, int64_t rows, int64_t cols,
+                int64_t stride, bf16_t* copy, bool copied = false) {
+  if (!copied && operand_fits(src, dtype, cols, stride))
+    return {static_cast<const char*>(src), stride, 0};
+  const int64_t ld = operand_ld(cols);
+  c.job[c.jobs++] = {src, stride, rows, (int)cols, (int32_t)ld, nullptr, nullptr, copy};
+  return {reinterpret_cast<const char*>(copy), ld, rows * ld * 2};
 }
 
 MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t k, int planes) {
@@ -322,31 +406,37 @@ hipError_t ffn(const FfnArgs& a, hipStream_t s) {
   const FfnPlan p = ffn_plan(a.rows, a.dim, a.hidden, a.dtype, false, a.ws);
   if (a.rows <= kFewRows)
     return ffn_few<std::conditional_t<P == 1, bf16_t, float>, ACT>(a, p, s);
-  Operand x, wg, wu, wd;
-  SM_TRY(operand(x, a.X, a.dtype, a.rows, a.dim, a.x_stride, P, p.x, s));
-  // both weights lie where they are, or both are copied: they share a row length
-  const bool fits = operand_fits(a.Wg, a.dtype, a.dim, a.dim) &&
-                    operand_fits(a.Wu, a.dtype, a.dim, a.dim);
-  if (fits) {
-    wg = {(const char*)a.Wg, a.dim, 0, nullptr};
-    wu = {(const char*)a.Wu, a.dim, 0, nullptr};
-  } else {
-    const int64_t plane = a.hidden * p.ld_d * 2;
-    wg = {(const char*)p.wg, p.ld_d, plane, p.wg};
-    wu = {(const char*)p.wu, p.ld_d, plane, p.wu};
-    for (auto [src, dst] : {std::pair{a.Wg, p.wg}, std::pair{a.Wu, p.wu}})
-      SM_TRY(launch_planes({src, a.dim, a.dtype, P, a.hidden, (int)a.dim, (int32_t)p.ld_d, nullptr,
-                            nullptr, dst}, s));
-  }
-  SM_TRY(operand(wd, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, P, p.wd, s));
-  MmArgs m{};
-  m.jobs = 1;
-  m.job[0] = product(wg, x, a.hidden, a.rows, a.dim, P);
-  m.job[0].a2 = wu.p;
+  // (Wg and Wu lie where they are, or both are copied: they share a row length)
+  const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
+                      !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
+  PlanesJobs c{};
+  const Operand x = operand(c, a.X, a.dtype, a.rows, a.dim, a.x_stride, p.x);
+  const Operand wg = operand(c, a.Wg, a.dtype, a.hidden, a.dim, a.dim, p.wg, copied);
+  const Operand wu = operand(c, a.Wu, a.dtype, a.hidden, a.dim, a.dim, p.wu, copied);
+  const Operand wd = operand(c, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, p.wd);
+  SM_TRY(launch_planes(c, a.dtype, s));
   const int64_t plane = a.rows * p.ld_f;
-  SM_TRY((run_mm<false, false, true, EpiGate<P, ACT>>(m, {p.h, p.ld_f, plane, a.pre}, p.first.wide,
-                                                      s)));
-  const Operand h{(const char*)p.h, p.ld_f, plane * 2, nullptr};
+  const Operand h{(const char*)p.h, p.ld_f, plane * 2};
+  if (p.split_first) {
+    MmStores z;
+    float* sums[2] = {p.mid, p.mid + p.first.splits[0] * a.rows * round_up(a.hidden, 4)};
+    for (int i = 0; i < 2; ++i) {
+      z.add(product(i ? wu : wg, x, a.hidden, a.rows, a.dim, P), false, nullptr, SM_F32, 0, sums[i],
+            p.first.splits[0]);
+      z.e.out[i] = sums_out(sums[i], a.hidden, a.rows);
+    }
+    SM_TRY((run_mm<false, false, false, EpiStore>(z.a, z.e, p.first.wide, s)));
+    const MidArgs g{{sums[0], sums[1]}, p.first.splits[0], a.rows, (int)a.hidden, (int)p.ld_f, plane,
+                    nullptr, a.pre, {p.h, nullptr, nullptr}};
+    SM_TRY((launch_mid<P, ACT, false>(g, s)));
+  } else {
+    MmArgs m{};
+    m.jobs = 1;
+    m.job[0] = product(wg, x, a.hidden, a.rows, a.dim, P);
+    m.job[0].a2 = wu.p;
+    SM_TRY((run_mm<false, false, true, EpiGate<P, ACT>>(m, {p.h, p.ld_f, plane, a.pre},
+                                                        p.first.wide, s)));
+  }
   MmStores out;
   out.add(product(wd, h, a.dim, a.rows, a.hidden, P), false, a.Y, a.dtype, 0, p.sums[0],
           p.out.splits[0]);
@@ -357,34 +447,46 @@ hipError_t ffn(const FfnArgs& a, hipStream_t s) {
 template <int P, int ACT>
 hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   const FfnPlan p = ffn_plan(a.rows, a.dim, a.hidden, a.dtype, true, a.ws);
-  Operand x, dy, wg, wu, wd;
-  SM_TRY(operand(dy, a.dY, a.dtype, a.rows, a.dim, a.dy_stride, P, p.dy, s));
-  SM_TRY(operand(wd, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, P, p.wd, s));
+  const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
+                      !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
+  PlanesJobs c{};
+  const Operand dy = operand(c, a.dY, a.dtype, a.rows, a.dim, a.dy_stride, p.dy);
+  const Operand wd = operand(c, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, p.wd);
+  Operand x{}, wg{}, wu{};
+  if (a.dX) {
+    wg = operand(c, a.Wg, a.dtype, a.hidden, a.dim, a.dim, p.wg, copied);
+    wu = operand(c, a.Wu, a.dtype, a.hidden, a.dim, a.dim, p.wu, copied);
+  }
+  if (a.dWg || a.dWu) x = operand(c, a.X, a.dtype, a.rows, a.dim, a.x_stride, p.x);
+  SM_TRY(launch_planes(c, a.dtype, s));
   const int64_t plane = a.rows * p.ld_f;
-  MmArgs m{};
-  m.jobs = 1;
-  m.job[0] = product(wd, dy, a.hidden, a.rows, a.dim, P);
-  SM_TRY((run_mm<true, false, false, EpiGateGrad<P, ACT>>(
-      m, {p.dg, p.du, p.h, p.ld_f, plane, a.pre}, p.first.wide, s)));
-  const Operand dg{(const char*)p.dg, p.ld_f, plane * 2, nullptr};
-  const Operand du{(const char*)p.du, p.ld_f, plane * 2, nullptr};
-  const Operand h{(const char*)p.h, p.ld_f, plane * 2, nullptr};
+  const MmJob first = product(wd, dy, a.hidden, a.rows, a.dim, P);
+  if (p.split_first) {
+    MmStores z;
+    z.add(first, false, nullptr, SM_F32, 0, p.mid, p.first.splits[0]);
+    z.e.out[0] = sums_out(p.mid, a.hidden, a.rows);
+    SM_TRY((run_mm<true, false, false, EpiStore>(z.a, z.e, p.first.wide, s)));
+    const MidArgs g{{p.mid, nullptr}, p.first.splits[0], a.rows, (int)a.hidden, (int)p.ld_f, plane,
+                    a.pre, nullptr, {p.dg, p.du, p.h}};
+    SM_TRY((launch_mid<P, ACT, true>(g, s)));
+  } else {
+    MmArgs m{};
+    m.jobs = 1;
+    m.job[0] = first;
+    SM_TRY((run_mm<true, false, false, EpiGateGrad<P, ACT>>(
+        m, {p.dg, p.du, p.h, p.ld_f, plane, a.pre}, p.first.wide, s)));
+  }
+  const Operand dg{(const char*)p.dg, p.ld_f, plane * 2};
+  const Operand du{(const char*)p.du, p.ld_f, plane * 2};
+  const Operand h{(const char*)p.h, p.ld_f, plane * 2};
   MmStores out;
   if (a.dX) {
-    SM_TRY(operand(wg, a.Wg, a.dtype, a.hidden, a.dim, a.dim, P, p.wg, s));
-    SM_TRY(operand(wu, a.Wu, a.dtype, a.hidden, a.dim, a.dim, P, p.wu, s));
-    if (wg.copy == nullptr && wu.copy != nullptr) {      // one row length for both
-      wg = {(const char*)p.wg, p.ld_d, wu.plane, p.wg};
-      SM_TRY(launch_planes({a.Wg, a.dim, a.dtype, P, a.hidden, (int)a.dim, (int32_t)p.ld_d,
-                            nullptr, nullptr, p.wg}, s));
-    }
     MmJob j = product(wg, dg, a.dim, a.rows, a.hidden, P);
     j.parts = 2;
     j.a_part = wu.p - wg.p;
     j.b_part = du.p - dg.p;
     out.add(j, false, a.dX, a.dtype, 0, p.sums[0], p.out.splits[0]);
   }
-  if (a.dWg || a.dWu) SM_TRY(operand(x, a.X, a.dtype, a.rows, a.dim, a.x_stride, P, p.x, s));
   const auto add = [&](int i, const Operand& A, const Operand& B, void* dst, int64_t mm,
                        int64_t nn) {
     if (dst)

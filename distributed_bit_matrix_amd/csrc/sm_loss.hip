@@ -243,7 +243,7 @@ struct LossPlan {
   bool copy_w, wide;
   int64_t strips;
   // backward
-  int64_t piece;                  // columns of a piece of the vocabulary
+  int64_t piece, g_ld;            // columns of a piece of the vocabulary, G's row length
   MmPlan both;                    // the products dX (job 0) and dW (job 1) of a piece
   // arrays
   int32_t *list, *target, *pos, *count;
@@ -260,7 +260,7 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
                    bool backward, void* ws) {
   LossPlan p{};
   p.planes = dtype == SM_BF16 ? 1 : 3;
-  p.dim_ld = (int32_t)round_up(dim, 8);
+  p.dim_ld = (int32_t)operand_ld(dim);
   p.copy_w = !w_fits;
   const MmSize z{vocab, rows, (p.planes == 1 ? 1 : 6) * ((dim + 63) / 64), false};
   p.wide = plan_products(&z, 1).wide;
@@ -282,7 +282,8 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
     const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * p.planes * rows) / 256 * 256);
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = std::min(round_up((vocab + pieces - 1) / pieces, 256), round_up(vocab, 8));
-    p.g = at.take<bf16_t>(p.planes * rows * p.piece);
+    p.g_ld = operand_ld(p.piece);
+    p.g = at.take<bf16_t>(p.planes * rows * p.g_ld);
     const int segs = p.planes == 1 ? 1 : 6;
     const MmSize sizes[2] = {{dim, rows, segs * ((p.piece + 63) / 64), true},
                              {dim, p.piece, segs * ((rows + 63) / 64), true}};
@@ -304,12 +305,11 @@ hipError_t gather(const LossPlan& p, const A& a, hipStream_t s) {
   if (a.target_bits == 64) list(static_cast<const int64_t*>(a.targets));
   else list(static_cast<const int32_t*>(a.targets));
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  if (hipError_t e = launch_planes({a.X, a.x_stride, a.dtype, p.planes, a.rows, (int)a.dim, p.dim_ld,
-                                    p.list, p.count, p.x}, s); e != hipSuccess)
-    return e;
-  if (!p.copy_w) return hipSuccess;
-  return launch_planes({a.W, a.dim, a.dtype, p.planes, a.vocab, (int)a.dim, p.dim_ld, nullptr,
-                        nullptr, p.w}, s);
+  PlanesJobs c{};
+  c.job[c.jobs++] = {a.X, a.x_stride, a.rows, (int)a.dim, p.dim_ld, p.list, p.count, p.x};
+  if (p.copy_w)
+    c.job[c.jobs++] = {a.W, a.dim, a.vocab, (int)a.dim, p.dim_ld, nullptr, nullptr, p.w};
+  return launch_planes(c, a.dtype, s);
 }
 
 // The logits of rows [v0, v0 + cols) of the table.
@@ -333,11 +333,11 @@ MmArgs logits(const LossPlan& p, const void* W, int64_t rows, int64_t dim, int64
 
 template <int P>
 hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0, hipStream_t s) {
-  const int64_t cols = std::min(p.piece, a.vocab - v0), plane = a.rows * p.piece;
+  const int64_t cols = std::min(p.piece, a.vocab - v0), plane = a.rows * p.g_ld;
   MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, v0, cols);
   const char* w = m.job[0].a;
   const int64_t ldw = m.job[0].lda;
-  const typename EpiGrad<P>::Args eg{p.g, p.piece, plane, (int)v0, p.target, p.lse_at, p.scale};
+  const typename EpiGrad<P>::Args eg{p.g, p.g_ld, plane, (int)v0, p.target, p.lse_at, p.scale};
   if (hipError_t e = run_mm<false, false, false, EpiGrad<P>>(m, eg, p.wide, s);
       e != hipSuccess)
     return e;
@@ -348,7 +348,7 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.a = w;
     j.lda = ldw;
     j.b = (const char*)p.g;
-    j.ldb = p.piece;
+    j.ldb = p.g_ld;
     j.m = (int)a.dim;
     j.n = (int)a.rows;
     j.k = (int)cols;
@@ -364,7 +364,7 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.a = (const char*)p.x;
     j.lda = p.dim_ld;
     j.b = (const char*)p.g;
-    j.ldb = p.piece;
+    j.ldb = p.g_ld;
     j.m = (int)a.dim;
     j.n = (int)cols;
     j.k = (int)a.rows;
@@ -419,8 +419,10 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s) {
   }
   if (!a.dX) return hipSuccess;
   const int64_t ld = round_up(a.dim, 4);
-  return launch_join({p.dx, a.rows * ld, ld, p.both.splits[0], p.pos, a.rows, (int)a.dim, a.dtype, 0,
-                      a.dX, a.dim}, s);
+  JoinJobs j{};
+  j.job[j.jobs++] = {p.dx, a.rows * ld, ld, p.both.splits[0], p.pos, a.rows, (int)a.dim, a.dtype, 0,
+                     a.dX, a.dim};
+  return launch_join(j, s);
 }
 
 }  // namespace sm

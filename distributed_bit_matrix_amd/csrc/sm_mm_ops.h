@@ -148,13 +148,19 @@ struct EpiStore {
 struct PlanesArgs {
   const void* src;
   int64_t stride;
-  int32_t dtype, planes;
   int64_t rows;
   int32_t cols, ld;
   const int32_t *list, *count;
   bf16_t* dst;
 };
-hipError_t launch_planes(const PlanesArgs& a, hipStream_t s);
+// Copies of one dtype and number of planes, in one launch.
+constexpr int kMaxPlanes = 5;
+struct PlanesJobs {
+  PlanesArgs job[kMaxPlanes];
+  int32_t jobs;
+  int32_t block0[kMaxPlanes];
+};
+hipError_t launch_planes(PlanesJobs& a, int32_t dtype, hipStream_t s);
 
 // Sums of splits joined: out[r][c] = sum over s of part[s][at(r)][c] (plus what
 // is there), at(r) = pos[r], or r where pos is null; a row whose pos is negative
@@ -169,7 +175,18 @@ struct JoinArgs {
   void* out;
   int64_t ld;
 };
-hipError_t launch_join(const JoinArgs& a, hipStream_t s);
+struct JoinJobs {
+  JoinArgs job[kMaxJobs];
+  int32_t jobs;
+  int32_t block0[kMaxJobs];
+};
+hipError_t launch_join(JoinJobs& a, hipStream_t s);      // in one launch
+
+// The row length of an operand copy: whole pieces of 128 bytes, an odd number of
+// them.  Rows a power of two apart meet in the same memory channels: 8192^3 with
+// both operands k along rows of 16 KiB 1122 TFLOP/s, with rows 128 bytes longer
+// 1322.
+inline int64_t operand_ld(int64_t cols) { return ((cols + 63) / 64 | 1) * 64; }
 
 hipError_t launch_zero(void* p, int32_t dtype, int64_t n, hipStream_t s);
 
@@ -254,7 +271,7 @@ hipError_t run_mm(MmArgs& a, const typename Epi::Args& e, bool wide, hipStream_t
 struct MmStores {
   MmArgs a{};
   EpiStore::Args e{};
-  JoinArgs join[kMaxJobs];
+  JoinJobs join{};
   // job j, whose rows go to dst; sums: where those of its splits go, if it has any
   void add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t accumulate, float* sums,
            int splits);

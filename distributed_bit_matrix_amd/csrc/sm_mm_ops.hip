@@ -20,18 +20,37 @@ __device__ __forceinline__ void store_planes(bf16_t* p, int64_t plane, const flo
   }
 }
 
+// The job of a block, and the block's place in it.
+template <int MAX>
+__device__ __forceinline__ int job_of(const int32_t (&block0)[MAX], int jobs, int& block) {
+  int ji = 0;
+#pragma unroll
+  for (int i = 1; i < MAX; ++i)
+    if (i < jobs && (int)blockIdx.x >= block0[i]) ji = i;
+  block = blockIdx.x - block0[ji];
+  return ji;
+}
+// Blocks of 256 threads for `work` pieces, about 8 pieces a thread where there are
+// many.
+int64_t copy_blocks(int64_t work) {
+  const int64_t b = (work + 255) / 256;
+  return b <= 2048 ? b : std::max<int64_t>(2048, b / 8);
+}
+
 // A thread copies 8 entries of a row.  Bound by HBM.
 template <typename T, int P>
-__global__ __launch_bounds__(256) void k_planes(const T* src, int64_t stride, int64_t rows,
-                                                int cols, int ld, const int32_t* list,
-                                                const int32_t* count, bf16_t* dst) {
-  const int64_t live = count ? *count : rows, plane = rows * ld;
-  const int per = ld / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < live * per;
-       i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void k_planes(PlanesJobs all) {
+  int block;
+  const int ji = job_of(all.block0, all.jobs, block);
+  const PlanesArgs& a = all.job[ji];
+  const int blocks = (ji + 1 < all.jobs ? all.block0[ji + 1] : (int)gridDim.x) - all.block0[ji];
+  const T* src = static_cast<const T*>(a.src);
+  const int64_t live = a.count ? *a.count : a.rows, plane = a.rows * a.ld;
+  const int per = a.ld / 8, cols = a.cols;
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < live * per; i += (int64_t)blocks * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 8;
-    const T* p = src + (list ? (int64_t)list[r] : r) * stride + c;
+    const T* p = src + (a.list ? (int64_t)a.list[r] : r) * a.stride + c;
     float v[8];
     if (c + 8 <= cols) {
       Piece<T, 8> in;
@@ -43,30 +62,32 @@ __global__ __launch_bounds__(256) void k_planes(const T* src, int64_t stride, in
       for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? to_f32(p[k]) : 0.f;
     }
     float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-    store_planes<P>(dst + r * ld + c, plane, lo);
-    store_planes<P>(dst + r * ld + c + 4, plane, hi);
+    store_planes<P>(a.dst + r * a.ld + c, plane, lo);
+    store_planes<P>(a.dst + r * a.ld + c + 4, plane, hi);
   }
 }
 
-hipError_t launch_planes(const PlanesArgs& a, hipStream_t s) {
-  if (a.rows == 0) return hipSuccess;
-  const int64_t work = a.rows * (a.ld / 8);
-  const dim3 grid((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16));
-  if (a.dtype == SM_BF16)
-    hipLaunchKernelGGL((k_planes<bf16_t, 1>), grid, dim3(256), 0, s, (const bf16_t*)a.src,
-                       a.stride, a.rows, a.cols, a.ld, a.list, a.count, a.dst);
+hipError_t launch_planes(PlanesJobs& a, int32_t dtype, hipStream_t s) {
+  int64_t blocks = 0;
+  for (int i = 0; i < a.jobs; ++i) {
+    a.block0[i] = (int)blocks;
+    blocks += copy_blocks(a.job[i].rows * (a.job[i].ld / 8));
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  }
+  if (blocks == 0) return hipSuccess;
+  if (dtype == SM_BF16)
+    hipLaunchKernelGGL((k_planes<bf16_t, 1>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((k_planes<float, 3>), grid, dim3(256), 0, s, (const float*)a.src, a.stride,
-                       a.rows, a.cols, a.ld, a.list, a.count, a.dst);
+    hipLaunchKernelGGL((k_planes<float, 3>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 // A thread joins 4 entries of a row, in the order of the splits.
 template <typename T>
-__global__ __launch_bounds__(256) void k_join(JoinArgs a) {
+__device__ __forceinline__ void join_rows(const JoinArgs& a, int block, int blocks) {
   const int per = (a.cols + 3) / 4;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.rows * per;
-       i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < a.rows * per;
+       i += (int64_t)blocks * 256) {
     const int64_t r = i / per;
     const int c = (int)(i - r * per) * 4, here = a.cols - c;
     const int64_t at = a.pos ? a.pos[r] : r;
@@ -91,6 +112,14 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
       for (int q = 0; q < here; ++q) put(o + q, v[q]);
     }
   }
+}
+__global__ __launch_bounds__(256) void k_join(JoinJobs all) {
+  int block;
+  const int ji = job_of(all.block0, all.jobs, block);
+  const JoinArgs& a = all.job[ji];
+  const int blocks = (ji + 1 < all.jobs ? all.block0[ji + 1] : (int)gridDim.x) - all.block0[ji];
+  if (a.dtype == SM_BF16) join_rows<bf16_t>(a, block, blocks);
+  else join_rows<float>(a, block, blocks);
 }
 
 namespace {
@@ -164,14 +193,14 @@ MmPlan plan_products(const MmSize* sizes, int jobs) {
         len[j] = slab * ((z.slabs + p.splits[j] - 1) / p.splits[j]) + 5.0;
         // the sums are written and read (4 bytes, at about 5 MB a microsecond), by a
         // launch of their own
-        if (p.splits[j] > 1) cost += p.splits[j] * z.m * z.n * 8 / 5e6 + 4.0;
+        if (p.splits[j] > 1) cost += p.splits[j] * z.m * z.n * 8 / 5e6;
       }
       if (part > 1 && !split) continue;
       // longest first, as they are launched
       for (int i = 0; i < jobs; ++i)
         for (int j = i + 1; j < jobs; ++j)
           if (len[j] > len[i]) std::swap(len[i], len[j]), std::swap(blocks[i], blocks[j]);
-      cost += makespan(blocks, len, jobs, slots);
+      cost += makespan(blocks, len, jobs, slots) + (split ? 5.0 : 0.0);
       if (cost < least) least = cost, best = p;
     }
   }
@@ -185,10 +214,10 @@ void MmStores::add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t 
   a.job[i].b_km = b_km;
   a.job[i].splits = splits;
   const int64_t ld = round_up(j.m, 4);
-  join[i] = JoinArgs{};
+  join.job[i] = JoinArgs{};
   if (splits > 1) {
     e.out[i] = {sums, ld, j.n * ld, SM_F32, 0};
-    join[i] = {sums, j.n * ld, ld, splits, nullptr, j.n, j.m, dtype, accumulate, dst, j.m};
+    join.job[i] = {sums, j.n * ld, ld, splits, nullptr, j.n, j.m, dtype, accumulate, dst, j.m};
   } else {
     e.out[i] = {dst, j.m, 0, dtype, accumulate};
   }
@@ -206,7 +235,7 @@ hipError_t MmStores::run(bool wide, hipStream_t s) {
       if (length(a.job[k]) > length(a.job[i])) {
         std::swap(a.job[i], a.job[k]);
         std::swap(e.out[i], e.out[k]);
-        std::swap(join[i], join[k]);
+        std::swap(join.job[i], join.job[k]);
       }
     (a.job[i].b_km ? km : rows) = true;
   }
@@ -220,17 +249,21 @@ hipError_t MmStores::run(bool wide, hipStream_t s) {
 }
 
 hipError_t MmStores::joins(hipStream_t s) {
+  JoinJobs j{};
   for (int i = 0; i < a.jobs; ++i)
-    if (join[i].splits > 0) SM_TRY(launch_join(join[i], s));
-  return hipSuccess;
+    if (join.job[i].splits > 0) j.job[j.jobs++] = join.job[i];
+  return launch_join(j, s);
 }
 
-hipError_t launch_join(const JoinArgs& a, hipStream_t s) {
-  if (a.rows == 0) return hipSuccess;
-  const int64_t work = a.rows * ((a.cols + 3) / 4);
-  const dim3 grid((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16));
-  if (a.dtype == SM_BF16) hipLaunchKernelGGL(k_join<bf16_t>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_join<float>, grid, dim3(256), 0, s, a);
+hipError_t launch_join(JoinJobs& a, hipStream_t s) {
+  int64_t blocks = 0;
+  for (int i = 0; i < a.jobs; ++i) {
+    a.block0[i] = (int)blocks;
+    blocks += copy_blocks(a.job[i].rows * ((a.job[i].cols + 3) / 4));
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  }
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_join, dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
