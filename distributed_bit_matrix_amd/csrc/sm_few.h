@@ -9,6 +9,9 @@
 // WK waves share a group's k and meet in LDS, in a fixed order.
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "sm_lds.h"
 #include "sm_rows.h"
 
@@ -50,19 +53,28 @@ __device__ __forceinline__ f32x4_t few_multiply(u32x4_t w, u32x4_t x, f32x4_t ac
   }
 }
 
+// Waves of a block, and how many of them share a group's k: as many as make 12
+// waves a CU, each with 8 steps at least.
+constexpr int few_waves(int wk) { return wk > 8 ? wk : 8; }
+inline int few_share(int64_t m, int64_t k, int step) {
+  const int64_t groups = (m + 15) / 16, steps = (k + step - 1) / step;
+  int wk = 1;
+  while (wk < 16 && groups * wk < 12 * 256 && steps >= 16 * wk) wk *= 2;
+  return wk;
+}
+
 // NA matrices of the same shape go side by side (w0, w1).  Epi gets, for rows m0 ..
 // m0 + 15 of W, acc[matrix][i] of row m0 + 4 (lane / 16) + i and row lane % 16 of x.
 template <typename T, int NA, int WK, class Epi>
-__global__ __launch_bounds__(512) void k_few(const T* w0, const T* w1, int64_t ldw, int m,
-                                             const T* x, int64_t xs, int n, const int32_t* count,
-                                             int k, typename Epi::Args ea) {
-  constexpr int V = 16 / (int)sizeof(T), STEP = 4 * V, U = 8, PER = 8 / WK;
-  __shared__ f32x4_t sh[WK > 1 ? 2 : 1][WK > 1 ? NA : 1][WK > 1 ? WK : 1][64];
+__global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T* w1, int64_t ldw,
+                                                            int m, const T* x, int64_t xs, int n,
+                                                            int k, bool once,
+                                                            typename Epi::Args ea) {
+  constexpr int V = 16 / (int)sizeof(T), STEP = 4 * V, U = 8, PER = few_waves(WK) / WK;
+  __shared__ f32x4_t sh[WK > 1 ? 2 : 1][WK > 1 ? NA : 1][WK > 1 ? PER * WK : 1][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = wave % WK;
-  if (count) n = *count;
-  if (n == 0) return;
+  const int part = wave % WK, mine = wave / WK;
   const int xr = (lane & 15) < n ? lane & 15 : n - 1;
   const T* xrow = x + (int64_t)xr * xs;
   const int steps = (k + STEP - 1) / STEP, per = (steps + WK - 1) / WK;
@@ -70,7 +82,9 @@ __global__ __launch_bounds__(512) void k_few(const T* w0, const T* w1, int64_t l
   const int groups = (m + 15) / 16;
   Epi epi(ea, lane, n);
   int turn = 0;
-  for (int g = blockIdx.x * PER + wave / WK; g < groups; g += gridDim.x * PER) {
+  // (a block's waves go through the same turns: they meet in barriers)
+  for (int g0 = blockIdx.x * PER; g0 < groups; g0 += gridDim.x * PER) {
+    const int g = g0 + mine < groups ? g0 + mine : groups - 1;
     const int row = g * 16 + (lane & 15);
     const int64_t at = (int64_t)(row < m ? row : m - 1) * ldw;
     f32x4_t acc[NA];
@@ -85,7 +99,8 @@ __global__ __launch_bounds__(512) void k_few(const T* w0, const T* w1, int64_t l
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
           Piece<T, V> p;
-          p.template load<true>((a ? w1 : w0) + at + c);
+          if (once) p.template load<true>((a ? w1 : w0) + at + c);
+          else p.load((a ? w1 : w0) + at + c);
           w[a][u] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
         }
       }
@@ -100,31 +115,94 @@ __global__ __launch_bounds__(512) void k_few(const T* w0, const T* w1, int64_t l
 #pragma unroll
         for (int a = 0; a < NA; ++a) acc[a] = few_multiply<T>(w[a][u], xv[u], acc[a]);
     }
-    for (; s < s1; ++s) {
-      const int c = s * STEP + (lane >> 4) * V;
-      const u32x4_t xv = few_piece(xrow, c, k);
+    if (s < s1) {
+      // what is left, in one go: pieces past the end (of the share, or of the row)
+      // are loaded from the row's beginning and count as zeros
+      u32x4_t w[NA][U], xv[U];
+      const u32x4_t zero = {0, 0, 0, 0};
+      if (V <= k) {
 #pragma unroll
-      for (int a = 0; a < NA; ++a)
-        acc[a] = few_multiply<T>(few_piece((a ? w1 : w0) + at, c, k), xv, acc[a]);
+        for (int u = 0; u < U; ++u) {
+          const int c = (s + u) * STEP + (lane >> 4) * V;
+          const int from = s + u < s1 && c + V <= k ? c : 0;
+          Piece<T, V> p;
+#pragma unroll
+          for (int a = 0; a < NA; ++a) {
+            p.load((a ? w1 : w0) + at + from);
+            w[a][u] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
+          }
+          p.load(xrow + from);
+          xv[u] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = (s + u) * STEP + (lane >> 4) * V;
+          const bool in = s + u < s1 && c + V <= k;
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            acc[a] = few_multiply<T>(in ? w[a][u] : zero, in ? xv[u] : zero, acc[a]);
+        }
+      }
+      // a row's last, shorter piece
+      for (; s < s1; ++s) {
+        if (s + 1 < steps || k % V == 0) continue;
+        const int c = s * STEP + (lane >> 4) * V;
+        const bool in = c < k && c + V > k;
+        const u32x4_t xe = in ? few_piece(xrow, c, k) : zero;
+#pragma unroll
+        for (int a = 0; a < NA; ++a)
+          acc[a] = few_multiply<T>(in ? few_piece((a ? w1 : w0) + at, c, k) : zero, xe, acc[a]);
+      }
     }
-    if constexpr (WK > 1) {      // (PER = 1: the block's waves go through the same groups)
-      static_assert(WK == 1 || WK == 8, "waves of a group");
+    if constexpr (WK > 1) {
 #pragma unroll
-      for (int a = 0; a < NA; ++a) sh[turn][a][part][lane] = acc[a];
+      for (int a = 0; a < NA; ++a) sh[turn][a][wave][lane] = acc[a];
       __syncthreads();
-      if (part == 0) {
+      if (part == 0 && g0 + mine < groups) {
 #pragma unroll
         for (int a = 0; a < NA; ++a)
 #pragma unroll
-          for (int q = 1; q < WK; ++q) acc[a] += sh[turn][a][q][lane];
+          for (int q = 1; q < WK; ++q) acc[a] += sh[turn][a][wave + q][lane];
         epi.group(g * 16, m, acc);
       }
       turn ^= 1;
-    } else {
+    } else if (g0 + mine < groups) {
       epi.group(g * 16, m, acc);
     }
   }
-  epi.finish(blockIdx.x * 8 + wave);
+  if (part == 0) epi.finish(blockIdx.x * PER + mine);
+}
+
+// Blocks of a launch: as many as there are groups for, up to 4096 waves.
+inline int64_t few_blocks(int64_t m, int wk) {
+  const int waves = few_waves(wk), per = waves / wk;
+  return std::min<int64_t>(((m + 15) / 16 + per - 1) / per, 4096 / waves);
+}
+// Numbers that `finish` gets are below this.
+template <typename T>
+int few_strips(int64_t m, int64_t k) {
+  const int wk = few_share(m, k, 64 / (int)sizeof(T));
+  return (int)few_blocks(m, wk) * (few_waves(wk) / wk);
+}
+
+template <typename T, int NA, class Epi>
+hipError_t launch_few(const T* w0, const T* w1, int64_t ldw, int64_t m, const T* x, int64_t xs,
+                      int64_t n, int64_t k, const typename Epi::Args& ea, hipStream_t s) {
+  const bool once = NA * m * k * (int64_t)sizeof(T) > kCacheBytes;
+  const auto go = [&](auto wk) {
+    constexpr int WK = decltype(wk)::value;
+    hipLaunchKernelGGL((k_few<T, NA, WK, Epi>), dim3((unsigned)few_blocks(m, WK)),
+                       dim3(64 * few_waves(WK)), 0, s, w0, w1, ldw, (int)m, x, xs, (int)n, (int)k,
+                       once, ea);
+    return hipGetLastError();
+  };
+  switch (few_share(m, k, 64 / (int)sizeof(T))) {
+    case 1: return go(std::integral_constant<int, 1>());
+    case 2: return go(std::integral_constant<int, 2>());
+    case 4: return go(std::integral_constant<int, 4>());
+    case 8: return go(std::integral_constant<int, 8>());
+    default: return go(std::integral_constant<int, 16>());
+  }
 }
 
 }  // namespace sm

@@ -385,20 +385,11 @@ MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t 
 
 template <typename T, int ACT>
 hipError_t ffn_few(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
-  const auto grid = [](int64_t m) {
-    return dim3((unsigned)std::min<int64_t>((m + 15) / 16, 2 * kCus));
-  };
-  typedef FewGate<T, ACT> Gate;
-  hipLaunchKernelGGL((k_few<T, 2, 8, Gate>), grid(a.hidden), dim3(512), 0, s, (const T*)a.Wg,
-                     (const T*)a.Wu, a.dim, (int)a.hidden, (const T*)a.X, a.x_stride, (int)a.rows,
-                     (const int32_t*)nullptr, (int)a.dim,
-                     (typename Gate::Args{(T*)p.few_h, a.pre}));
-  SM_TRY(hipGetLastError());
-  hipLaunchKernelGGL((k_few<T, 1, 8, FewStore<T>>), grid(a.dim), dim3(512), 0, s, (const T*)a.Wd,
-                     (const T*)nullptr, a.hidden, (int)a.dim, (const T*)p.few_h, a.hidden,
-                     (int)a.rows, (const int32_t*)nullptr, (int)a.hidden,
-                     (typename FewStore<T>::Args{(T*)a.Y}));
-  return hipGetLastError();
+  SM_TRY((launch_few<T, 2, FewGate<T, ACT>>((const T*)a.Wg, (const T*)a.Wu, a.dim, a.hidden,
+                                            (const T*)a.X, a.x_stride, a.rows, a.dim,
+                                            {(T*)p.few_h, a.pre}, s)));
+  return launch_few<T, 1, FewStore<T>>((const T*)a.Wd, nullptr, a.hidden, a.dim, (const T*)p.few_h,
+                                       a.hidden, a.rows, a.hidden, {(T*)a.Y}, s);
 }
 
 template <int P, int ACT>

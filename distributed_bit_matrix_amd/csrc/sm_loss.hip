@@ -15,6 +15,7 @@
 // entry, as much as the rounding of the gradients themselves.
 #include <cmath>
 
+#include "sm_few.h"
 #include "sm_layers.h"
 #include "sm_mm_ops.h"
 
@@ -112,6 +113,55 @@ struct EpiLse {
   }
 };
 
+// The same for few rows, which are all there (an ignored one is left out by the
+// join): a wave's strip is all groups of 16 features that it had.  part:
+// [row][strips].
+template <typename T>
+struct FewLse {
+  struct Args {
+    float2* part;
+    int32_t strips;
+    const void* targets;
+    int32_t target_bits;
+    float* picked;
+  };
+  Args e;
+  int lane, n;
+  int64_t t;
+  float m = -INFINITY, s = 0.f;
+  __device__ __forceinline__ FewLse(const Args& a, int l, int rows) : e(a), lane(l), n(rows) {
+    const int r = (l & 15) < rows ? l & 15 : rows - 1;
+    t = a.target_bits == 64 ? static_cast<const int64_t*>(a.targets)[r]
+                            : static_cast<const int32_t*>(a.targets)[r];
+  }
+  __device__ __forceinline__ void group(int m0, int all, const f32x4_t (&acc)[1]) {
+    const int f = m0 + 4 * (lane >> 4);
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (f + k < all) top = fmaxf(top, acc[0][k]);
+      if (f + k == t && (lane & 15) < n) e.picked[lane & 15] = acc[0][k];
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    s *= __builtin_amdgcn_exp2f((m - ref) * kLog2e);      // (0 where m is -inf)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (f + k < all) s += __builtin_amdgcn_exp2f((acc[0][k] - ref) * kLog2e);
+    m = top;
+  }
+  __device__ __forceinline__ void finish(int wave) {
+#pragma unroll
+    for (int o = 16; o < 64; o *= 2) {
+      const float mo = __shfl_xor(m, o), so = __shfl_xor(s, o), top = fmaxf(m, mo);
+      const float ref = top == -INFINITY ? 0.f : top;
+      s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) +
+          so * __builtin_amdgcn_exp2f((mo - ref) * kLog2e);
+      m = top;
+    }
+    if (lane < n) e.part[lane * e.strips + wave] = make_float2(m, s);
+  }
+};
+
 // G = (exp(z - lse) - onehot) * scale of a piece of the vocabulary that begins
 // at v0: to planes of [rows][ld].
 template <int P>
@@ -197,6 +247,53 @@ __global__ __launch_bounds__(1024) void k_loss_join(const float2* part, int64_t 
   }
 }
 
+// All of that for few rows, in one block: a wave a row.
+template <typename I>
+__global__ __launch_bounds__(1024) void k_loss_few(const float2* part, int strips, const I* targets,
+                                                   int rows, int64_t ignore, int vocab,
+                                                   const float* picked, float* loss, float* lse,
+                                                   float* total, int mean) {
+  __shared__ float each[kFewRows];
+  __shared__ int counts[kFewRows];
+  const int lane = threadIdx.x & 63, r = threadIdx.x >> 6;
+  float value = 0.f;
+  int count = 0;
+  if (r < rows) {
+    const int64_t t = (int64_t)targets[r];
+    float m = -INFINITY, s = 0.f;
+#pragma unroll 8
+    for (int k = lane; k < strips; k += 64) {
+      const float2 v = part[r * strips + k];
+      const float top = fmaxf(m, v.x), ref = top == -INFINITY ? 0.f : top;
+      s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) +
+          v.y * __builtin_amdgcn_exp2f((v.x - ref) * kLog2e);
+      m = top;
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    s = lanes_sum<64>(s * __builtin_amdgcn_exp2f((m - ref) * kLog2e));
+    const float ln = logf(s);
+    const bool keep = t != ignore, there = t >= 0 && t < vocab;
+    value = !keep ? 0.f : there ? ref - picked[r] + ln : NAN;
+    count = keep;
+    if (lane == 0) {
+      lse[r] = keep ? ref + ln : 0.f;
+      if (loss) loss[r] = value;
+    }
+  }
+  if (!total) return;
+  if (lane == 0) each[r] = value, counts[r] = count;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double sum = 0.0;
+    int live = 0;
+    for (int k = 0; k < rows; ++k) sum += each[k], live += counts[k];
+    *total = (float)(mean && live ? sum / live : sum);
+  }
+}
+
 // What the ignored rows hold, and the loss summed up (in double, in an order that
 // the number of rows decides).  total: the sum, or the mean over the rows that
 // count (0 where none does).
@@ -272,6 +369,13 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
   p.count = at.take<int32_t>(1);
   p.x = at.take<bf16_t>(p.planes * rows * p.dim_ld);
   if (p.copy_w) p.w = at.take<bf16_t>(p.planes * vocab * p.dim_ld);
+  if (!backward && rows <= kFewRows) {
+    Places few{static_cast<char*>(ws)};
+    p.picked = few.take<float>(kFewRows);
+    p.part = few.take<float2>(4096 * kFewRows);
+    p.bytes = few.used;
+    return p;
+  }
   if (!backward) {
     p.picked = at.take<float>(rows);
     p.loss = at.take<float>(rows);
@@ -384,10 +488,31 @@ size_t loss_workspace(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, b
   return loss_plan(rows, dim, vocab, dtype, false, backward, nullptr).bytes;
 }
 
+template <typename T>
+static hipError_t loss_few(const LossArgs& a, const LossPlan& p, hipStream_t s) {
+  const int strips = few_strips<T>(a.vocab, a.dim);
+  SM_TRY((launch_few<T, 1, FewLse<T>>((const T*)a.W, nullptr, a.dim, a.vocab, (const T*)a.X,
+                                      a.x_stride, a.rows, a.dim,
+                                      {p.part, strips, a.targets, a.target_bits, p.picked}, s)));
+  float* loss = a.reduction == SM_LOSS_ROWS ? a.loss : nullptr;
+  float* total = a.reduction == SM_LOSS_ROWS ? nullptr : a.loss;
+  const auto join = [&](auto* t) {
+    hipLaunchKernelGGL((k_loss_few<std::remove_const_t<std::remove_pointer_t<decltype(t)>>>),
+                       dim3(1), dim3(1024), 0, s, p.part, strips, t, (int)a.rows, a.ignore,
+                       (int)a.vocab, p.picked, loss, a.lse, total,
+                       (int)(a.reduction == SM_LOSS_MEAN));
+  };
+  if (a.target_bits == 64) join(static_cast<const int64_t*>(a.targets));
+  else join(static_cast<const int32_t*>(a.targets));
+  return hipGetLastError();
+}
+
 hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
   if (a.rows == 0) return launch_zero(a.loss, SM_F32, 1, s);
   const LossPlan p = loss_plan(a.rows, a.dim, a.vocab, a.dtype,
                                operand_fits(a.W, a.dtype, a.dim, a.dim), false, a.ws);
+  if (a.rows <= kFewRows)
+    return a.dtype == SM_BF16 ? loss_few<bf16_t>(a, p, s) : loss_few<float>(a, p, s);
   if (hipError_t e = gather(p, a, s); e != hipSuccess) return e;
   MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, 0, a.vocab);
   if (hipError_t e = run_mm<false, false, false, EpiLse>(
