@@ -162,7 +162,8 @@ def rms_bounds(h, w, eps):
 def e4m3_half_step(v):
     """Half the distance of the e4m3 values around v (|v| <= 448): 3 fraction bits
     down to 2^-6, steps of 2^-9 below."""
-    return torch.exp2(torch.frexp(v).exponent.clamp(min=-5).double() - 5)
+    e = torch.where(v == 0, -5, torch.frexp(v).exponent.clamp(min=-5))
+    return torch.exp2(e.double() - 5)
 
 
 def e4m3_scales(y, block):

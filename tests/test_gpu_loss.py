@@ -72,3 +72,253 @@ def test_shapes(rows, dim, vocab, dtype):
     x, w, t = inputs(rows, dim, vocab, dtype, rows * 7 + vocab, 0.25 if rows > 4 else 0.0,
                      bits_=32 if dim % 2 else 64)
     check(x, w, t, reduction, torch.float32 if vocab % 2 else None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_around_the_form_for_few(dtype):
+    """15, 16 and 17 rows, with padding among them, every reduction."""
+    for rows in (1, 15, 16, 17):
+        for reduction in ("none", "sum", "mean"):
+            x, w, t = inputs(rows, 200, 1111, dtype, rows, 0.3)
+            check(x, w, t, reduction)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [5, 100])
+def test_ignored_rows_reach_nothing(rows, dtype):
+    """Whatever they hold: NaN and infinities in the activations of padding change no
+    bit of the others' results."""
+    x, w, t = inputs(rows, 72, 333, dtype, 3, 0.4)
+    t[1] = IGNORE
+    loss, lse, dloss, dx, dw = check(x, w, t, "mean")
+    x2 = x.clone()
+    drop = t == IGNORE
+    x2[drop] = torch.where(torch.arange(72, device="cuda") % 2 == 0, float("nan"), float("inf")).to(
+        x.dtype)
+    loss2, lse2 = B.linear_cross_entropy(x2, w, t, IGNORE, "mean", want_lse=True)
+    dx2, dw2 = B.linear_cross_entropy_backward(dloss, x2, w, t, lse, IGNORE, "mean",
+                                               dtype=x.dtype)
+    for a, b in ((loss, loss2), (lse, lse2), (dx, dx2), (dw, dw2)):
+        assert torch.equal(bits(a), bits(b))
+    assert (dx2[drop] == 0).all() and (lse2[drop] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [7, 40])
+def test_all_rows_ignored(rows):
+    """A mean of nothing is 0 and has zero gradients."""
+    x, w, _ = inputs(rows, 40, 50, "bf16", 1)
+    t = torch.full((rows,), -1, device="cuda")
+    for reduction in ("none", "sum", "mean"):
+        loss, lse = B.linear_cross_entropy(x, w, t, -1, reduction, want_lse=True)
+        assert (loss == 0).all() and (lse == 0).all()
+        dx, dw = B.linear_cross_entropy_backward(torch.ones_like(loss), x, w, t, lse, -1, reduction)
+        assert (dx == 0).all() and (dw == 0).all()
+    # no rows at all
+    loss, lse = B.linear_cross_entropy(x[:0], w, t[:0], want_lse=True)
+    assert loss.item() == 0 and lse.shape == (0,)
+    acc = torch.full((50, 40), 3.0, device="cuda")
+    dx, dw = B.linear_cross_entropy_backward(loss, x[:0], w, t[:0], lse, dweight=acc,
+                                             accumulate=True)
+    assert dx.shape == (0, 40) and (dw == 3).all()
+    assert (B.linear_cross_entropy_backward(loss, x[:0], w, t[:0], lse)[1] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [6, 50])
+def test_targets_outside_the_table(rows):
+    """Their rows' loss and gradients are NaN, no others' loss is."""
+    x, w, t = inputs(rows, 40, 64, "f32", 2)
+    t[2], t[4] = 64, -3
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[2] = bad[4] = True
+    assert torch.equal(loss.isnan(), bad) and not lse.isnan().any()
+    assert B.linear_cross_entropy(x, w, t, IGNORE, "mean").isnan()
+    dx, dw = B.linear_cross_entropy_backward(torch.ones_like(loss), x, w, t, lse, IGNORE, "none")
+    assert torch.equal(dx.isnan().all(1), bad) and torch.equal(dx.isnan().any(1), bad)
+    assert dw.isnan().all()
+    # an ignored index inside the table is ignored all the same
+    t = torch.arange(rows, device="cuda") % 64
+    loss = B.linear_cross_entropy(x, w, t, 3, "none")
+    assert loss[3] == 0 and (loss != 0).sum() == rows - 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [9, 130])
+def test_nonfinite_values(rows, dtype):
+    """A NaN in a row that counts is its own row's; one in the table is everyone's."""
+    x, w, t = inputs(rows, 64, 100, dtype, 4)
+    x[3, 7] = float("nan")
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    assert loss.isnan().sum() == 1 and loss[3].isnan() and lse.isnan().sum() == 1
+    dx, dw = B.linear_cross_entropy_backward(torch.ones_like(loss), x, w, t, lse, IGNORE, "none")
+    assert dx.isnan().any(1).sum() == 1 and dx[3].isnan().all()
+    assert dw.isnan().all()
+    x, w, t = inputs(rows, 64, 100, dtype, 4)
+    w[50, 3] = float("nan")
+    assert B.linear_cross_entropy(x, w, t, IGNORE, "none").isnan().all()
+    w[50, 3] = 0
+    w[50] = 0
+    x[:, 0], w[50, 0] = 1, float("-inf")      # a logit of -inf: probability zero
+    t[t == 50] = 51
+    loss, lse = B.linear_cross_entropy(x[:, :8], w[:, :8].contiguous(), t, IGNORE, "none",
+                                       want_lse=True)
+    if dtype == "bf16":                        # (planes of a float32 infinity are not finite)
+        keep = torch.arange(100, device="cuda") != 50
+        want = torch.logsumexp(x[:, :8].double() @ w[keep][:, :8].double().T, 1)
+        assert (lse.double() - want).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_logits(dtype):
+    """Far apart and far from zero: the largest decides, nothing overflows."""
+    x, w, t = inputs(200, 64, 300, dtype, 5, spread=100.0)
+    loss, lse, *_ = check(x, w, t, "mean")
+    assert lse.isfinite().all() and lse.abs().max() > 200
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 65])
+def test_strides_alignment_and_dimensions(dim, dtype):
+    """Rows with gaps, starts off any 16 bytes, leading dimensions: the bits of
+    contiguous calls."""
+    x, w, t = inputs(60, dim, 200, dtype, 6, 0.2)
+    want = check(x, w, t, "sum")
+    pad = torch.zeros(60, dim + 7, device="cuda", dtype=x.dtype)
+    flat = torch.zeros(200 * dim + 1, device="cuda", dtype=x.dtype)
+    x2 = pad[:, 3:3 + dim]
+    x2.copy_(x)
+    w2 = flat[1:].view(200, dim)
+    w2.copy_(w)
+    for xs, ws in ((x2, w), (x, w2), (x2, w2)):
+        loss, lse = B.linear_cross_entropy(xs, ws, t, IGNORE, "sum", want_lse=True)
+        dx, dw = B.linear_cross_entropy_backward(want[2], xs, ws, t, lse, IGNORE, "sum",
+                                                 dtype=x.dtype)
+        for a, b in zip((loss, lse, dx, dw), (want[0], want[1], want[3], want[4])):
+            assert torch.equal(bits(a), bits(b))
+    x3, t3 = x.view(3, 4, 5, dim), t.view(3, 4, 5)
+    loss, lse = B.linear_cross_entropy(x3, w, t3, IGNORE, "none", want_lse=True)
+    assert loss.shape == lse.shape == (3, 4, 5)
+    dx, _ = B.linear_cross_entropy_backward(loss, x3, w, t3, lse, IGNORE, "none")
+    assert dx.shape == x3.shape
+
+
+def test_outputs_one_by_one_in_place_and_added():
+    x, w, t = inputs(90, 64, 300, "f32", 8, 0.1)
+    loss, lse = B.linear_cross_entropy(x, w, t, want_lse=True)
+    one = torch.ones((), device="cuda")
+    dx, dw = B.linear_cross_entropy_backward(one, x, w, t, lse)
+    a, b = B.linear_cross_entropy_backward(one, x, w, t, lse, want_x=False)
+    assert a is None and torch.equal(b, dw)
+    a, b = B.linear_cross_entropy_backward(one, x, w, t, lse, want_weight=False)
+    assert b is None and torch.equal(a, dx)
+    acc = torch.full_like(dw, 1.0)
+    B.linear_cross_entropy_backward(one, x, w, t, lse, dweight=acc, accumulate=True)
+    assert torch.equal(acc, 1.0 + dw)
+    x2 = x.clone()
+    B.linear_cross_entropy_backward(one, x2, w, t, lse, dX=x2, dweight=torch.empty_like(dw))
+    assert torch.equal(x2, dx)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pieces_of_the_vocabulary(dtype):
+    """Sums that are exact in any order: logits all zero, so every probability is
+    2^-16, and small integers elsewhere.  The gradient goes in several pieces of the
+    vocabulary (2^30 bytes of it at a time); one row, token or piece lost or twice
+    would show."""
+    rows, dim, vocab = (20000, 16, 65536)
+    x = torch.zeros(rows, dim, device="cuda", dtype=DT[dtype])
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randint(-3, 4, (vocab, dim), device="cuda", generator=gen).to(DT[dtype])
+    t = torch.randint(vocab, (rows,), device="cuda", generator=gen)
+    t[::3] = IGNORE
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    keep = t != IGNORE
+    ln = 16 * 0.6931471805599453
+    assert (lse[keep] - ln).abs().max() < 1e-5 and (loss[keep] - ln).abs().max() < 1e-5
+    dloss = torch.full((rows,), 65536.0, device="cuda")
+    dx, _ = B.linear_cross_entropy_backward(dloss, x, w, t, torch.full_like(lse, ln), IGNORE,
+                                            "none", want_weight=False, dX=torch.empty_like(x))
+    # G is exp(-lse) 65536 = 1 to 2^-20, but for the target's 1 - 65536
+    cols = w.double().sum(0)
+    want = torch.where(keep[:, None], cols - 65536.0 * w.double()[t.clamp(min=0)], 0.0)
+    tol = 2.0 ** -7 * 65536 * 4 if dtype == "bf16" else 2.0 ** -17 * 65536 * 20
+    assert (dx.double() - want).abs().max() <= tol
+    x.fill_(1.0)
+    w.zero_()
+    _, dw = B.linear_cross_entropy_backward(dloss, x, w, t, torch.full_like(lse, ln), IGNORE,
+                                            "none", want_x=False)
+    counts = torch.bincount(t[keep], minlength=vocab).double()
+    want = (int(keep.sum()) - 65536.0 * counts)[:, None].expand(vocab, dim)
+    tol = 65536 * counts.max() * 2.0 ** -8 + int(keep.sum()) * 2.0 ** -18
+    assert (dw.double() - want).abs().max() <= tol
+    empty = counts == 0
+    assert (dw.double() - want)[empty].abs().max() <= int(keep.sum()) * 2.0 ** -18
+
+
+def test_streams_and_graphs():
+    """Two calls at once on streams of their own, and a graph replayed between eager
+    calls with other inputs: the same bits each time."""
+    cases = [inputs(300, 64, 1000, "bf16", 11, 0.2), inputs(40, 128, 777, "f32", 12, 0.2),
+             inputs(8, 128, 777, "bf16", 13)]
+
+    def both(x, w, t):
+        loss, lse = B.linear_cross_entropy(x, w, t, want_lse=True)
+        dx, dw = B.linear_cross_entropy_backward(torch.ones_like(loss), x, w, t, lse)
+        return loss, lse, dx, dw
+
+    want = [both(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(3):
+        got = []
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(both(*c))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(bits(p), bits(q)) for p, q in zip(a, b))
+    for c, b in zip(cases, want):
+        static = [v.clone() for v in c]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            both(*static)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both(*static)
+        for turn in range(3):
+            static[0].copy_(c[0] if turn != 1 else c[0] * 0.5)
+            g.replay()
+            ref = b if turn != 1 else both(c[0] * 0.5, *c[1:])
+            torch.cuda.synchronize()
+            assert all(torch.equal(bits(p), bits(q)) for p, q in zip(out, ref))
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """Rows 2^33 bytes apart in X, a table and a gradient of 2^32 bytes and more."""
+    dim = 2048
+    store = torch.zeros((1 << 32) + 8192, dtype=torch.bfloat16, device="cuda")
+    x = store.as_strided((3, dim), (1 << 31, 1))
+    x.normal_()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    vocab = (1 << 20) + 0
+    w = torch.empty(vocab, dim, dtype=torch.bfloat16, device="cuda")
+    w.normal_(std=0.05, generator=gen)
+    t = torch.tensor([0, vocab - 1, vocab // 2 + 77], device="cuda")
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    z = x.float().contiguous() @ w.float().T
+    want = torch.logsumexp(z.double(), 1)
+    assert (lse.double() - want).abs().max() < 1e-4
+    assert (loss.double() - (want - z.double()[torch.arange(3), t])).abs().max() < 1e-4
+    dx, dw = B.linear_cross_entropy_backward(torch.ones_like(loss), x, w, t, lse, IGNORE, "none",
+                                             dtype=torch.bfloat16)
+    g = torch.exp(z - lse[:, None])
+    g[torch.arange(3), t] -= 1
+    ref = g @ w.float()
+    assert ((dx.float() - ref).norm() / ref.norm()) < 2.0 ** -7
+    for v in (0, 1, vocab // 2 + 77, vocab - 1):
+        row = g[:, v] @ x.float().contiguous()
+        assert (dw[v].float() - row).norm() <= 2.0 ** -7 * row.norm() + 1e-6

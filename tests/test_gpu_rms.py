@@ -122,3 +122,152 @@ def test_backward(rows, cols, x_dtype):
     acc = torch.full_like(dw, 2.0)
     B.rms_norm_backward(dy, h, w, rstd, dh, dweight=acc, accumulate=True)
     assert torch.equal(acc, 2.0 + dw)
+
+
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [768, 257, 20000])
+def test_strides_and_alignment(cols, x_dtype):
+    """Rows with gaps, starts off any 16 bytes, leading dimensions: the bits of
+    contiguous calls, and nothing written between the rows."""
+    rows = 12
+    x, r, dh, dy = (normal(cols + i, rows, cols, dtype=x_dtype) for i in range(4))
+    w = 1 + 0.2 * normal(9, cols)
+
+    def gaps(t):
+        pad = torch.full((rows, cols + 5), 7.0, device="cuda", dtype=t.dtype)
+        pad[:, 3:3 + cols] = t
+        return pad[:, 3:3 + cols]
+
+    y, h, rstd = B.rms_norm(x, w, r, EPS, want_stats=True)
+    y2, h2, rstd2 = B.rms_norm(gaps(x), w, gaps(r), EPS, want_stats=True)
+    for a, b in ((y, y2), (h, h2), (rstd, rstd2)):
+        assert torch.equal(bits(a), bits(b))
+    dx, dw = B.rms_norm_backward(dy, h, w, rstd, dh)
+    dx2, dw2 = B.rms_norm_backward(gaps(dy), gaps(h), w, rstd, gaps(dh))
+    assert torch.equal(bits(dx), bits(dx2)) and torch.equal(dw, dw2)
+    if cols <= 16384:
+        q, s = B.rms_norm_e4m3(x, w, None, EPS)
+        q2, s2 = B.rms_norm_e4m3(gaps(x), w, None, EPS)
+        assert torch.equal(bits(q), bits(q2)) and torch.equal(s, s2)
+        flat = torch.zeros(rows * cols + 3, dtype=torch.uint8, device="cuda")
+        q3 = flat[1:1 + rows * cols].view(rows, cols).view(torch.float8_e4m3fn)
+        B.rms_norm_e4m3(x, w, None, EPS, Q=q3)
+        assert torch.equal(bits(q3), bits(q)) and flat[0] == 0 and (flat[-2:] == 0).all()
+    lead = (3, 4, cols)
+    y3, h3, rstd3 = B.rms_norm(x.view(lead), w, r.view(lead), EPS, want_stats=True)
+    assert y3.shape == h3.shape == lead and rstd3.shape == (3, 4)
+    assert torch.equal(bits(y3.view(rows, cols)), bits(y))
+    dx3, _ = B.rms_norm_backward(dy.view(lead), h3, w, rstd3, dh.view(lead))
+    assert torch.equal(bits(dx3.view(rows, cols)), bits(dx))
+    if cols <= 16384:
+        assert B.rms_norm_e4m3(x.view(lead), w, block=None)[1].shape == (3, 4, 1)
+
+
+def test_no_rows():
+    x = torch.zeros(0, 64, device="cuda")
+    w = torch.ones(64, device="cuda")
+    y, h, rstd = B.rms_norm(x, w, x, want_stats=True)
+    assert y.shape == h.shape == (0, 64) and rstd.shape == (0,)
+    assert B.rms_norm_e4m3(x, w)[0].shape == (0, 64)
+    dx, dw = B.rms_norm_backward(x, x, w, rstd)
+    assert dx.shape == (0, 64) and (dw == 0).all()
+    acc = torch.full((64,), 2.0, device="cuda")
+    B.rms_norm_backward(x, x, w, rstd, dweight=acc, accumulate=True)
+    assert (acc == 2).all()
+
+
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [5, 100, 768, 4096, 20000])
+def test_values_out_of_range(cols, x_dtype):
+    """A NaN is its own row's; zeros stay zeros, with the least scale; a sum of
+    squares past float32 gives rstd 0."""
+    x = normal(1, 6, cols, dtype=x_dtype)
+    x[1, cols // 2] = float("nan")
+    x[2] = 0
+    x[3] = 3e19
+    y, h, rstd = B.rms_norm(x, None, None, EPS, want_stats=True)
+    assert y[1].isnan().all() and y.isnan().any(1).sum() == 1
+    assert (y[2] == 0).all() and rstd[2] == 2.0 ** 10
+    assert rstd[3] == 0 and (y[3] == 0).all()
+    if cols > 16384:
+        return
+    for block in (128, None):
+        q, s = B.rms_norm_e4m3(x, None, None, EPS, block)
+        assert (q[2].float() == 0).all() and (s[2] == 2.0 ** -126).all()
+        assert q[1].float().isnan().any() and not q[[0, 4, 5]].float().isnan().any()
+        assert (q[[0, 4, 5]].float().abs().amax(1) == 448).all()
+
+
+def test_streams_and_graphs():
+    """Calls at once on streams of their own, and a graph replayed between eager calls
+    with other inputs."""
+    cases = [(3000, 768), (40, 1001), (3, 20000)]
+    data = [[normal(i, r, c, dtype="bf16") for i in range(4)] for r, c in cases]
+
+    def all_of(x, r, dy, dh):
+        y, h, rstd = B.rms_norm(x, None, r, EPS, want_stats=True)
+        return (y, h, rstd, *B.rms_norm_backward(dy, h, None, rstd, dh))
+
+    want = [all_of(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(3):
+        got = []
+        for s, d in zip(streams, data):
+            with torch.cuda.stream(s):
+                got.append(all_of(*d))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(bits(p), bits(q)) for p, q in zip(a, b))
+    # on a stream that is passed
+    y, h = B.rms_norm(data[0][0], None, data[0][1], EPS, stream=streams[0])
+    streams[0].synchronize()
+    assert torch.equal(bits(y), bits(want[0][0]))
+    for d, b in zip(data, want):
+        static = [t.clone() for t in d]
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            out = all_of(*static)
+        for turn in range(3):
+            static[0].copy_(d[0] if turn != 1 else d[0] * 2)
+            g.replay()
+            ref = b if turn != 1 else all_of(d[0] * 2, *d[1:])
+            torch.cuda.synchronize()
+            assert all(torch.equal(bits(p), bits(q)) for p, q in zip(out, ref))
+
+
+@pytest.mark.slow
+def test_row_offsets_past_32_bits():
+    cols = 1024
+    store = torch.zeros((1 << 33) + cols, dtype=torch.bfloat16, device="cuda")
+    x = store.as_strided((3, cols), (1 << 32, 1))
+    v = normal(1, 3, cols, dtype="bf16")
+    x.copy_(v)
+    y, rstd = B.rms_norm(x, None, None, EPS, want_stats=True)[::2]
+    assert torch.equal(bits(y), bits(B.rms_norm(v, None, None, EPS)))
+    a, _ = B.rms_norm_backward(x, x, None, rstd, x)
+    b, _ = B.rms_norm_backward(v, v, None, rstd, v)
+    assert torch.equal(bits(a), bits(b))
+
+
+def test_refusals():
+    x = torch.zeros(4, 8, device="cuda")
+    w = torch.ones(8, device="cuda")
+    for call in (lambda: B.rms_norm(x.half()), lambda: B.rms_norm(x, w.half()),
+                 lambda: B.rms_norm(x, w[:4]), lambda: B.rms_norm(x, w, x.bfloat16()),
+                 lambda: B.rms_norm(x, w, x[:2]), lambda: B.rms_norm(x.t(), w),
+                 lambda: B.rms_norm_e4m3(x, Q=torch.zeros(4, 8, device="cuda")),
+                 lambda: B.rms_norm_e4m3(x, scales=torch.zeros(4, 2, device="cuda")),
+                 lambda: B.rms_norm_backward(x, x.bfloat16(), w, x[:, 0].contiguous())):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: B.rms_norm_e4m3(x, block=64), lambda: B.rms_norm(x, H=x.clone()),
+                 lambda: B.rms_norm(x, w.cpu()),
+                 lambda: B.rms_norm_backward(x, x, w, x[:, 0].contiguous(), accumulate=True)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(B.SignMuonError):
+        B.rms_norm(x, eps=-1.0)
+    with pytest.raises(B.SignMuonError):
+        B.rms_norm_e4m3(torch.zeros(1, 16385, device="cuda"))
