@@ -71,45 +71,53 @@ struct EpiLse {
     const int32_t* target;
     float* picked;
   };
-  template <int TI, int TJ>
-  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
-                                             const f32x4_t (&acc)[TI][TJ]) {
+  template <bool WHOLE, int TI, int TJ>
+  static __device__ __forceinline__ void rows(const Args& e, const MmPlace& at,
+                                              const f32x4_t (&acc)[TI][TJ]) {
     const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
-    if (at.m0 >= at.m) return;
     const int64_t strip = at.m0 / (TI * 16);
-    const bool whole = at.m0 + TI * 16 <= at.m;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int n = nc + 16 * j;
-      const int t = n < at.n ? e.target[n] : -1;
-      const bool mine = t >= at.m0 && t < at.m0 + TI * 16 && ((t >> 2) & 3) == at.lane >> 4;
-      float mx = -INFINITY, z = 0.f;
+      float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float v = acc[i][j][k];
-          if (whole || mc + 16 * i + k < at.m) mx = fmaxf(mx, v);
-          z = mc + 16 * i + k == t ? v : z;
-        }
+        for (int k = 0; k < 4; ++k)
+          if (WHOLE || mc + 16 * i + k < at.m) mx = fmaxf(mx, acc[i][j][k]);
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float ref = mx == -INFINITY ? 0.f : mx;
+      // exp(v - ref) as one multiply-add and a power: what the rounding of ref
+      // log2(e) adds is the same for all terms, and below lse's own rounding
+      const float ref = mx == -INFINITY ? 0.f : -mx * kLog2e;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - ref) * kLog2e);
-          s += whole || mc + 16 * i + k < at.m ? p : 0.f;
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], kLog2e, ref));
+          s += WHOLE || mc + 16 * i + k < at.m ? p : 0.f;
         }
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
-      if (n < at.n) {
-        if (at.lane < 16) e.part[strip * e.cap + n] = make_float2(mx, s);
+      const int t = n < at.n ? e.target[n] : -1;
+      const bool mine = t >= at.m0 && t < at.m0 + TI * 16 && ((t >> 2) & 3) == at.lane >> 4;
+      if (__any(mine)) {       // of a vocabulary's strips few have the target
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z = mc + 16 * i + k == t ? acc[i][j][k] : z;
         if (mine) e.picked[n] = z;
       }
+      if (n < at.n && at.lane < 16) e.part[strip * e.cap + n] = make_float2(mx, s);
     }
+  }
+  template <int TI, int TJ>
+  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
+                                             const f32x4_t (&acc)[TI][TJ]) {
+    if (at.m0 + TI * 16 <= at.m) rows<true>(e, at, acc);
+    else if (at.m0 < at.m) rows<false>(e, at, acc);
   }
 };
 
@@ -173,29 +181,49 @@ struct EpiGrad {
     const int32_t* target;
     const float *lse, *scale;
   };
-  template <int TI, int TJ>
-  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
-                                             const f32x4_t (&acc)[TI][TJ]) {
+  template <bool WHOLE, int TI, int TJ>
+  static __device__ __forceinline__ void rows(const Args& e, const MmPlace& at,
+                                              const f32x4_t (&acc)[TI][TJ]) {
     const int mc = at.m0 + 4 * (at.lane >> 4), nc = at.n0 + (at.lane & 15);
     const int cols = ((at.m + 7) & ~7) - at.m0;      // zeros up to a whole piece of 16 bytes
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int n = nc + 16 * j, r = n < at.n ? n : at.n - 1;
       const int t = e.target[r] - e.v0;
-      const float lse = e.lse[r], scale = e.scale[r];
+      const float scale = e.scale[r];
+      // v - lse in powers of two: lse log2(e) in two parts, so that only the
+      // difference is rounded
+      const float hi = e.lse[r] * kLog2e, lo = __builtin_fmaf(e.lse[r], kLog2e, -hi);
       f32x4_t v[TI];
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int m = mc + 16 * i + k;
-          const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * kLog2e);
-          v[i][k] = m < at.m ? (p - (m == t ? 1.f : 0.f)) * scale : 0.f;
+          const float p =
+              __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], kLog2e, -hi) - lo) * scale;
+          v[i][k] = WHOLE || mc + 16 * i + k < at.m ? p : 0.f;
         }
+      if (__any(t >= at.m0 && t < at.m0 + TI * 16)) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (mc + 16 * i + k == t) {
+              const float p =
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], kLog2e, -hi) - lo);
+              v[i][k] = (p - 1.f) * scale;
+            }
+      }
       const int n0 = at.n0 + 16 * j;
       put_planes<P, 16 * TI>(at, v, e.g + (int64_t)n0 * e.ld + at.m0, e.plane, e.ld, at.n - n0,
                              cols);
     }
+  }
+  template <int TI, int TJ>
+  static __device__ __forceinline__ void run(const Args& e, const MmPlace& at,
+                                             const f32x4_t (&acc)[TI][TJ]) {
+    if (at.m0 + TI * 16 <= at.m) rows<true>(e, at, acc);
+    else rows<false>(e, at, acc);
   }
 };
 
