@@ -639,11 +639,11 @@ def _rms_args(X, weight, residual, H, rstd, want_stats, dev):
         wd = _code(weight.dtype, "weight")
         _check_arg(weight, (cols,), weight.dtype, dev, "weight")
     if residual is not None:
-        if residual.dtype != X.dtype or residual.shape != X.shape:
+        if residual.dtype is not X.dtype or residual.shape != X.shape:
             raise TypeError("residual must have X's dtype and shape")
         if residual.get_device() != dev:
             raise ValueError("residual is not on the first tensor's device")
-        rs = _rows(residual, "residual")[2]
+        rs = cols if residual.is_contiguous() else _rows(residual, "residual")[2]
         if H is None:
             H = _dense_like(X)
         else:
@@ -653,7 +653,9 @@ def _rms_args(X, weight, residual, H, rstd, want_stats, dev):
     if rstd is not None:
         _check_arg(rstd, X.shape[:-1], torch.float32, dev, "rstd")
     elif want_stats:
-        rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=X.device)
+        if X.dim() != 2:
+            rstd = rstd.view(X.shape[:-1])
     return rows, cols, xs, rs, xd, wd, H, rstd
 
 

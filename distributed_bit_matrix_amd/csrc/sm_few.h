@@ -5,7 +5,9 @@
 // A wave multiplies 16 rows of W by all rows of x, with the weights' 16-byte
 // pieces going from memory to registers in the layout that the matrix
 // instructions take (lane l holds a piece of row l % 16; which k an instruction
-// sums does not matter as long as x has the same), 8 pieces a matrix in flight.
+// sums does not matter as long as x has the same).  Many waves with 2 pieces a
+// matrix each in flight: 4096 x 16384 bfloat16 27 us (5 TB/s; 8 pieces in half the
+// waves 32, the next pieces fetched ahead in registers 78).
 // WK waves share a group's k and meet in LDS, in a fixed order.
 #pragma once
 
@@ -53,13 +55,13 @@ __device__ __forceinline__ f32x4_t few_multiply(u32x4_t w, u32x4_t x, f32x4_t ac
   }
 }
 
-// Waves of a block, and how many of them share a group's k: as many as make 12
-// waves a CU, each with 8 steps at least.
+// Waves of a block, and how many of them share a group's k: as many as make 24
+// waves a CU, each with 2 steps at least.
 constexpr int few_waves(int wk) { return wk > 8 ? wk : 8; }
 inline int few_share(int64_t m, int64_t k, int step) {
   const int64_t groups = (m + 15) / 16, steps = (k + step - 1) / step;
   int wk = 1;
-  while (wk < 16 && groups * wk < 12 * 256 && steps >= 16 * wk) wk *= 2;
+  while (wk < 16 && groups * wk < 24 * 256 && steps >= 4 * wk) wk *= 2;
   return wk;
 }
 
@@ -70,7 +72,7 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
                                                             int m, const T* x, int64_t xs, int n,
                                                             int k, bool once,
                                                             typename Epi::Args ea) {
-  constexpr int V = 16 / (int)sizeof(T), STEP = 4 * V, U = 8, PER = few_waves(WK) / WK;
+  constexpr int V = 16 / (int)sizeof(T), STEP = 4 * V, U = 2, PER = few_waves(WK) / WK;
   __shared__ f32x4_t sh[WK > 1 ? 2 : 1][WK > 1 ? NA : 1][WK > 1 ? PER * WK : 1][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -173,10 +175,10 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
   if (part == 0) epi.finish(blockIdx.x * PER + mine);
 }
 
-// Blocks of a launch: as many as there are groups for, up to 4096 waves.
+// Blocks of a launch: as many as there are groups for, up to 8192 waves (32 a CU).
 inline int64_t few_blocks(int64_t m, int wk) {
   const int waves = few_waves(wk), per = waves / wk;
-  return std::min<int64_t>(((m + 15) / 16 + per - 1) / per, 4096 / waves);
+  return std::min<int64_t>(((m + 15) / 16 + per - 1) / per, 8192 / waves);
 }
 // Numbers that `finish` gets are below this.
 template <typename T>

@@ -400,7 +400,7 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
   if (!backward && rows <= kFewRows) {
     Places few{static_cast<char*>(ws)};
     p.picked = few.take<float>(kFewRows);
-    p.part = few.take<float2>(4096 * kFewRows);
+    p.part = few.take<float2>(8192 * kFewRows);
     p.bytes = few.used;
     return p;
   }
