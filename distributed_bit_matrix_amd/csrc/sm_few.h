@@ -55,6 +55,57 @@ __device__ __forceinline__ f32x4_t few_multiply(u32x4_t w, u32x4_t x, f32x4_t ac
   }
 }
 
+// A lane's share of one step of x: as many values as a 16-byte piece of W has.
+template <typename T, typename X>
+struct FewX {                  // x in W's type
+  u32x4_t w;
+  __device__ __forceinline__ void zero() { w = u32x4_t{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const X* at) {
+    Piece<X, 16 / (int)sizeof(X)> p;
+    p.load(at);
+    w = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
+  }
+  __device__ __forceinline__ void edge(const X* row, int k, int k_all) {
+    w = few_piece(row, k, k_all);
+  }
+  __device__ __forceinline__ f32x4_t multiply(u32x4_t a, f32x4_t acc) const {
+    return few_multiply<T>(a, w, acc);
+  }
+};
+
+// x in float32 beside bfloat16 weights: x = hi + lo of two bfloat16, which leaves
+// 2^-18 of a value, and two instructions a piece.
+template <>
+struct FewX<bf16_t, float> {
+  u32x4_t w[2];
+  __device__ __forceinline__ void zero() { w[0] = w[1] = u32x4_t{0, 0, 0, 0}; }
+  __device__ __forceinline__ void load(const float* at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Piece<float, 4> p;
+      p.load(at + 4 * i);
+      w[i] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
+    }
+  }
+  __device__ __forceinline__ void edge(const float* row, int k, int k_all) {
+    w[0] = few_piece(row, k, k_all);
+    w[1] = few_piece(row, k + 4, k_all);
+  }
+  __device__ __forceinline__ f32x4_t multiply(u32x4_t a, f32x4_t acc) const {
+    u32x4_t hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v0 = __uint_as_float(w[i / 2][2 * (i & 1)]);
+      const float v1 = __uint_as_float(w[i / 2][2 * (i & 1) + 1]);
+      hi[i] = pack_bf16(v0, v1);
+      const float h0 = __uint_as_float(hi[i] << 16), h1 = __uint_as_float(hi[i] & 0xffff0000u);
+      lo[i] = pack_bf16(__builtin_isfinite(h0) ? v0 - h0 : 0.f,
+                        __builtin_isfinite(h1) ? v1 - h1 : 0.f);
+    }
+    return few_multiply<bf16_t>(a, hi, few_multiply<bf16_t>(a, lo, acc));
+  }
+};
+
 // Waves of a block, and how many of them share a group's k: as many as make 24
 // waves a CU, each with 2 steps at least.
 constexpr int few_waves(int wk) { return wk > 8 ? wk : 8; }
@@ -67,9 +118,9 @@ inline int few_share(int64_t m, int64_t k, int step) {
 
 // NA matrices of the same shape go side by side (w0, w1).  Epi gets, for rows m0 ..
 // m0 + 15 of W, acc[matrix][i] of row m0 + 4 (lane / 16) + i and row lane % 16 of x.
-template <typename T, int NA, int WK, class Epi>
+template <typename T, typename X, int NA, int WK, class Epi>
 __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T* w1, int64_t ldw,
-                                                            int m, const T* x, int64_t xs, int n,
+                                                            int m, const X* x, int64_t xs, int n,
                                                             int k, bool once,
                                                             typename Epi::Args ea) {
   constexpr int V = 16 / (int)sizeof(T), STEP = 4 * V, U = 2, PER = few_waves(WK) / WK;
@@ -78,7 +129,7 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave % WK, mine = wave / WK;
   const int xr = (lane & 15) < n ? lane & 15 : n - 1;
-  const T* xrow = x + (int64_t)xr * xs;
+  const X* xrow = x + (int64_t)xr * xs;
   const int steps = (k + STEP - 1) / STEP, per = (steps + WK - 1) / WK;
   const int s0 = part * per, s1 = s0 + per < steps ? s0 + per : steps;
   const int groups = (m + 15) / 16;
@@ -94,7 +145,8 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
     for (int a = 0; a < NA; ++a) acc[a] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     int s = s0;
     for (; s + U <= s1 && (s + U) * STEP <= k; s += U) {
-      u32x4_t w[NA][U], xv[U];
+      u32x4_t w[NA][U];
+      FewX<T, X> xv[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = (s + u) * STEP + (lane >> 4) * V;
@@ -107,20 +159,17 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        Piece<T, V> p;
-        p.load(xrow + (s + u) * STEP + (lane >> 4) * V);
-        xv[u] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
-      }
+      for (int u = 0; u < U; ++u) xv[u].load(xrow + (s + u) * STEP + (lane >> 4) * V);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int a = 0; a < NA; ++a) acc[a] = few_multiply<T>(w[a][u], xv[u], acc[a]);
+        for (int a = 0; a < NA; ++a) acc[a] = xv[u].multiply(w[a][u], acc[a]);
     }
     if (s < s1) {
       // what is left, in one go: pieces past the end (of the share, or of the row)
       // are loaded from the row's beginning and count as zeros
-      u32x4_t w[NA][U], xv[U];
+      u32x4_t w[NA][U];
+      FewX<T, X> xv[U];
       const u32x4_t zero = {0, 0, 0, 0};
       if (V <= k) {
 #pragma unroll
@@ -133,16 +182,15 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
             p.load((a ? w1 : w0) + at + from);
             w[a][u] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
           }
-          p.load(xrow + from);
-          xv[u] = u32x4_t{p.w[0], p.w[1], p.w[2], p.w[3]};
+          xv[u].load(xrow + from);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = (s + u) * STEP + (lane >> 4) * V;
           const bool in = s + u < s1 && c + V <= k;
+          if (!in) xv[u].zero();
 #pragma unroll
-          for (int a = 0; a < NA; ++a)
-            acc[a] = few_multiply<T>(in ? w[a][u] : zero, in ? xv[u] : zero, acc[a]);
+          for (int a = 0; a < NA; ++a) acc[a] = xv[u].multiply(in ? w[a][u] : zero, acc[a]);
         }
       }
       // a row's last, shorter piece
@@ -150,10 +198,12 @@ __global__ __launch_bounds__(64 * few_waves(WK)) void k_few(const T* w0, const T
         if (s + 1 < steps || k % V == 0) continue;
         const int c = s * STEP + (lane >> 4) * V;
         const bool in = c < k && c + V > k;
-        const u32x4_t xe = in ? few_piece(xrow, c, k) : zero;
+        FewX<T, X> xe;
+        xe.zero();
+        if (in) xe.edge(xrow, c, k);
 #pragma unroll
         for (int a = 0; a < NA; ++a)
-          acc[a] = few_multiply<T>(in ? few_piece((a ? w1 : w0) + at, c, k) : zero, xe, acc[a]);
+          acc[a] = xe.multiply(in ? few_piece((a ? w1 : w0) + at, c, k) : zero, acc[a]);
       }
     }
     if constexpr (WK > 1) {
@@ -187,13 +237,13 @@ int few_strips(int64_t m, int64_t k) {
   return (int)few_blocks(m, wk) * (few_waves(wk) / wk);
 }
 
-template <typename T, int NA, class Epi>
-hipError_t launch_few(const T* w0, const T* w1, int64_t ldw, int64_t m, const T* x, int64_t xs,
+template <typename T, typename X, int NA, class Epi>
+hipError_t launch_few(const T* w0, const T* w1, int64_t ldw, int64_t m, const X* x, int64_t xs,
                       int64_t n, int64_t k, const typename Epi::Args& ea, hipStream_t s) {
   const bool once = NA * m * k * (int64_t)sizeof(T) > kCacheBytes;
   const auto go = [&](auto wk) {
     constexpr int WK = decltype(wk)::value;
-    hipLaunchKernelGGL((k_few<T, NA, WK, Epi>), dim3((unsigned)few_blocks(m, WK)),
+    hipLaunchKernelGGL((k_few<T, X, NA, WK, Epi>), dim3((unsigned)few_blocks(m, WK)),
                        dim3(64 * few_waves(WK)), 0, s, w0, w1, ldw, (int)m, x, xs, (int)n, (int)k,
                        once, ea);
     return hipGetLastError();

@@ -8,8 +8,11 @@
 // bfloat16 they would double it).  Backward, three launches: dh = dy Wd with the
 // activation's derivative in its epilogue, which writes dg, du and h; dx = dg Wg
 // + du Wu, one sum over both; and the three weight gradients.  What is between
-// the products is rounded to the operands' type: for bfloat16 half a step of
-// 2^-8 a value, as much as the rounding of the results.
+// the products is rounded to the operands' type: for bfloat16 half a step of 2^-8
+// a value, as much as the rounding of the results.  Together they leave a result's
+// error at sqrt(2) of its own rounding where errors average; where it comes from few
+// values, or is few values, that can be twice as much: there they have two
+// bfloat16 planes.
 //
 // Up to 16 rows the products are bound by reading the weights once (sm_few.h).
 #include "sm_few.h"
@@ -164,11 +167,11 @@ struct EpiGateGrad {
   }
 };
 
-// The same for few rows: h in the weights' type.
-template <typename T, int ACT>
+// The same for few rows: h of type H.
+template <typename H, int ACT>
 struct FewGate {
   struct Args {
-    T* h;
+    H* h;
     float* pre;
   };
   Args e;
@@ -219,19 +222,6 @@ struct MidArgs {
   float* pre_out;          // forward, or null
   bf16_t* out[3];          // h; or dg, du, h
 };
-template <int P>
-__device__ __forceinline__ void store_mid(bf16_t* p, int64_t plane, f32x4_t v) {
-#pragma unroll
-  for (int q = 0; q < P; ++q) {
-    const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
-    *reinterpret_cast<u32x2_t*>(p + q * plane) = u32x2_t{lo, hi};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float t = bf16_to_f32((bf16_t)((k < 2 ? lo : hi) >> (16 * (k & 1))));
-      v[k] = __builtin_isfinite(t) ? v[k] - t : 0.f;
-    }
-  }
-}
 template <int P, int ACT, bool GRAD>
 __global__ __launch_bounds__(256) void k_mid(MidArgs a) {
   const int hidden = a.hidden, hid4 = (hidden + 3) & ~3, per = ((hidden + 7) & ~7) / 4;
@@ -279,26 +269,20 @@ template <int P, int ACT, bool GRAD>
 hipError_t launch_mid(const MidArgs& a, hipStream_t s) {
   const int64_t work = a.rows * (round_up(a.hidden, 8) / 4);
   hipLaunchKernelGGL((k_mid<P, ACT, GRAD>),
-                     dim3((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16)), dim3(256), 0, s,
-                     a);
+                     dim3((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16)), dim3(256), 0,
+                     s, a);
   return hipGetLastError();
 }
-// A product's sums of splits, for a launch of its own that joins them.
-MmOut sums_out(float* sums, int64_t m, int64_t n) {
-  const int64_t ld = round_up(m, 4);
-  return {sums, ld, n * ld, SM_F32, 0};
-}
-
 struct Operand {
   const char* p;
   int64_t ld, plane;       // elements; bytes from one plane to the next
 };
 
 struct FfnPlan {
-  int planes;
+  int planes, mid_planes;  // of the caller's operands; of what is between the products
   int64_t ld_d, ld_f;
   bf16_t *x, *dy, *wg, *wu, *wd, *h, *dg, *du;
-  void* few_h;
+  void* few_h;             // of few rows: bfloat16, or float32 for more planes
   MmPlan first, out;       // tiles of the first product; of the others (forward: y;
                            // backward: dx, dwg, dwu, dwd)
   float* sums[4];          // of their splits
@@ -307,25 +291,27 @@ struct FfnPlan {
   size_t bytes;
 };
 
+constexpr int64_t kTwoPlanes = 4096;     // values below which there are two planes
+
 FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool backward,
                  void* ws) {
   FfnPlan p{};
   p.planes = dtype == SM_BF16 ? 1 : 3;
+  p.mid_planes = p.planes == 3 ? 3 : rows * std::min(dim, hidden) < kTwoPlanes ? 2 : 1;
   p.ld_d = operand_ld(dim);
   p.ld_f = operand_ld(hidden);
   Places at{static_cast<char*>(ws)};
   if (!backward && rows <= kFewRows) {
-    p.few_h = dtype == SM_BF16 ? (void*)at.take<bf16_t>(rows * hidden)
-                               : (void*)at.take<float>(rows * hidden);
+    p.few_h = at.take<float>(rows * hidden);    // (or half of it in bfloat16)
     p.bytes = at.used;
     return p;
   }
-  const int64_t segs = p.planes == 1 ? 1 : 6;
+  const int64_t segs = p.planes == 1 ? 1 : 6, mid = p.planes == 1 ? p.mid_planes : 6;
   p.x = at.take<bf16_t>(p.planes * rows * p.ld_d);
   p.wg = at.take<bf16_t>(p.planes * hidden * p.ld_d);
   p.wu = at.take<bf16_t>(p.planes * hidden * p.ld_d);
   p.wd = at.take<bf16_t>(p.planes * dim * p.ld_f);
-  p.h = at.take<bf16_t>(p.planes * rows * p.ld_f);
+  p.h = at.take<bf16_t>(p.mid_planes * rows * p.ld_f);
   const auto first = [&](MmSize z, int jobs) {
     const MmSize both[2] = {z, z};
     p.first = plan_products(both, jobs);
@@ -334,6 +320,7 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
       p.mid = at.take<float>(jobs * p.first.splits[0] * rows * round_up(hidden, 4));
   };
   const auto slabs = [&](int64_t k) { return segs * ((k + 63) / 64); };
+  const auto mids = [&](int64_t k) { return mid * ((k + 63) / 64); };
   const auto room = [&](const MmSize* z, int jobs) {
     p.out = plan_products(z, jobs);
     for (int i = 0; i < jobs; ++i)
@@ -341,17 +328,17 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
         p.sums[i] = at.take<float>(p.out.splits[i] * z[i].n * round_up(z[i].m, 4));
   };
   if (!backward) {
-    const MmSize y{dim, rows, slabs(hidden), true};
+    const MmSize y{dim, rows, mids(hidden), true};
     first({hidden, rows, slabs(dim), true}, 2);
     room(&y, 1);
   } else {
     p.dy = at.take<bf16_t>(p.planes * rows * p.ld_d);
-    p.dg = at.take<bf16_t>(p.planes * rows * p.ld_f);
-    p.du = at.take<bf16_t>(p.planes * rows * p.ld_f);
-    const MmSize o[4] = {{dim, rows, 2 * slabs(hidden), true},
-                         {dim, hidden, slabs(rows), true},
-                         {dim, hidden, slabs(rows), true},
-                         {hidden, dim, slabs(rows), true}};
+    p.dg = at.take<bf16_t>(p.mid_planes * rows * p.ld_f);
+    p.du = at.take<bf16_t>(p.mid_planes * rows * p.ld_f);
+    const MmSize o[4] = {{dim, rows, 2 * mids(hidden), true},
+                         {dim, hidden, mids(rows), true},
+                         {dim, hidden, mids(rows), true},
+                         {hidden, dim, mids(rows), true}};
     first({hidden, rows, slabs(dim), true}, 1);
     room(o, 4);
   }
@@ -369,7 +356,8 @@ Operand operand(PlanesJobs& c, const void* src, int32_t dtype, int64_t rows, int
   return {reinterpret_cast<const char*>(copy), ld, rows * ld * 2};
 }
 
-MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t k, int planes) {
+MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t k, int a_planes,
+              int b_planes) {
   MmJob j{};
   j.a = a.p;
   j.b = b.p;
@@ -379,24 +367,22 @@ MmJob product(const Operand& a, const Operand& b, int64_t m, int64_t n, int64_t 
   j.n = (int)n;
   j.k = (int)k;
   j.splits = 1;
-  set_planes(j, planes, a.plane, b.plane);
+  set_planes(j, a_planes, b_planes, a.plane, b.plane);
   return j;
 }
 
-template <typename T, int ACT>
+template <typename T, typename H, int ACT>
 hipError_t ffn_few(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
-  SM_TRY((launch_few<T, 2, FewGate<T, ACT>>((const T*)a.Wg, (const T*)a.Wu, a.dim, a.hidden,
-                                            (const T*)a.X, a.x_stride, a.rows, a.dim,
-                                            {(T*)p.few_h, a.pre}, s)));
-  return launch_few<T, 1, FewStore<T>>((const T*)a.Wd, nullptr, a.hidden, a.dim, (const T*)p.few_h,
-                                       a.hidden, a.rows, a.hidden, {(T*)a.Y}, s);
+  SM_TRY((launch_few<T, T, 2, FewGate<H, ACT>>((const T*)a.Wg, (const T*)a.Wu, a.dim, a.hidden,
+                                               (const T*)a.X, a.x_stride, a.rows, a.dim,
+                                               {(H*)p.few_h, a.pre}, s)));
+  return launch_few<T, H, 1, FewStore<T>>((const T*)a.Wd, nullptr, a.hidden, a.dim,
+                                          (const H*)p.few_h, a.hidden, a.rows, a.hidden,
+                                          {(T*)a.Y}, s);
 }
 
-template <int P, int ACT>
-hipError_t ffn(const FfnArgs& a, hipStream_t s) {
-  const FfnPlan p = ffn_plan(a.rows, a.dim, a.hidden, a.dtype, false, a.ws);
-  if (a.rows <= kFewRows)
-    return ffn_few<std::conditional_t<P == 1, bf16_t, float>, ACT>(a, p, s);
+template <int P, int MP, int ACT>
+hipError_t ffn(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
   // (Wg and Wu lie where they are, or both are copied: they share a row length)
   const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
                       !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
@@ -412,32 +398,31 @@ hipError_t ffn(const FfnArgs& a, hipStream_t s) {
     MmStores z;
     float* sums[2] = {p.mid, p.mid + p.first.splits[0] * a.rows * round_up(a.hidden, 4)};
     for (int i = 0; i < 2; ++i) {
-      z.add(product(i ? wu : wg, x, a.hidden, a.rows, a.dim, P), false, nullptr, SM_F32, 0, sums[i],
-            p.first.splits[0]);
+      z.add(product(i ? wu : wg, x, a.hidden, a.rows, a.dim, P, P), false, nullptr, SM_F32, 0,
+            sums[i], p.first.splits[0]);
       z.e.out[i] = sums_out(sums[i], a.hidden, a.rows);
     }
     SM_TRY((run_mm<false, false, false, EpiStore>(z.a, z.e, p.first.wide, s)));
-    const MidArgs g{{sums[0], sums[1]}, p.first.splits[0], a.rows, (int)a.hidden, (int)p.ld_f, plane,
-                    nullptr, a.pre, {p.h, nullptr, nullptr}};
-    SM_TRY((launch_mid<P, ACT, false>(g, s)));
+    const MidArgs g{{sums[0], sums[1]}, p.first.splits[0], a.rows, (int)a.hidden, (int)p.ld_f,
+                    plane, nullptr, a.pre, {p.h, nullptr, nullptr}};
+    SM_TRY((launch_mid<MP, ACT, false>(g, s)));
   } else {
     MmArgs m{};
     m.jobs = 1;
-    m.job[0] = product(wg, x, a.hidden, a.rows, a.dim, P);
+    m.job[0] = product(wg, x, a.hidden, a.rows, a.dim, P, P);
     m.job[0].a2 = wu.p;
-    SM_TRY((run_mm<false, false, true, EpiGate<P, ACT>>(m, {p.h, p.ld_f, plane, a.pre},
-                                                        p.first.wide, s)));
+    SM_TRY((run_mm<false, false, true, EpiGate<MP, ACT>>(m, {p.h, p.ld_f, plane, a.pre},
+                                                         p.first.wide, s)));
   }
   MmStores out;
-  out.add(product(wd, h, a.dim, a.rows, a.hidden, P), false, a.Y, a.dtype, 0, p.sums[0],
+  out.add(product(wd, h, a.dim, a.rows, a.hidden, P, MP), false, a.Y, a.dtype, 0, p.sums[0],
           p.out.splits[0]);
   SM_TRY((run_mm<false, false, false, EpiStore>(out.a, out.e, p.out.wide, s)));
   return out.joins(s);
 }
 
-template <int P, int ACT>
-hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
-  const FfnPlan p = ffn_plan(a.rows, a.dim, a.hidden, a.dtype, true, a.ws);
+template <int P, int MP, int ACT>
+hipError_t ffn_grad(const FfnGradArgs& a, const FfnPlan& p, hipStream_t s) {
   const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
                       !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
   PlanesJobs c{};
@@ -451,20 +436,20 @@ hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   if (a.dWg || a.dWu) x = operand(c, a.X, a.dtype, a.rows, a.dim, a.x_stride, p.x);
   SM_TRY(launch_planes(c, a.dtype, s));
   const int64_t plane = a.rows * p.ld_f;
-  const MmJob first = product(wd, dy, a.hidden, a.rows, a.dim, P);
+  const MmJob first = product(wd, dy, a.hidden, a.rows, a.dim, P, P);
   if (p.split_first) {
     MmStores z;
     z.add(first, false, nullptr, SM_F32, 0, p.mid, p.first.splits[0]);
     z.e.out[0] = sums_out(p.mid, a.hidden, a.rows);
     SM_TRY((run_mm<true, false, false, EpiStore>(z.a, z.e, p.first.wide, s)));
-    const MidArgs g{{p.mid, nullptr}, p.first.splits[0], a.rows, (int)a.hidden, (int)p.ld_f, plane,
-                    a.pre, nullptr, {p.dg, p.du, p.h}};
-    SM_TRY((launch_mid<P, ACT, true>(g, s)));
+    const MidArgs g{{p.mid, nullptr}, p.first.splits[0], a.rows, (int)a.hidden, (int)p.ld_f,
+                    plane, a.pre, nullptr, {p.dg, p.du, p.h}};
+    SM_TRY((launch_mid<MP, ACT, true>(g, s)));
   } else {
     MmArgs m{};
     m.jobs = 1;
     m.job[0] = first;
-    SM_TRY((run_mm<true, false, false, EpiGateGrad<P, ACT>>(
+    SM_TRY((run_mm<true, false, false, EpiGateGrad<MP, ACT>>(
         m, {p.dg, p.du, p.h, p.ld_f, plane, a.pre}, p.first.wide, s)));
   }
   const Operand dg{(const char*)p.dg, p.ld_f, plane * 2};
@@ -472,7 +457,7 @@ hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   const Operand h{(const char*)p.h, p.ld_f, plane * 2};
   MmStores out;
   if (a.dX) {
-    MmJob j = product(wg, dg, a.dim, a.rows, a.hidden, P);
+    MmJob j = product(wg, dg, a.dim, a.rows, a.hidden, P, MP);
     j.parts = 2;
     j.a_part = wu.p - wg.p;
     j.b_part = du.p - dg.p;
@@ -481,8 +466,8 @@ hipError_t ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   const auto add = [&](int i, const Operand& A, const Operand& B, void* dst, int64_t mm,
                        int64_t nn) {
     if (dst)
-      out.add(product(A, B, mm, nn, a.rows, P), true, dst, a.dw_dtype, a.accumulate, p.sums[i],
-              p.out.splits[i]);
+      out.add(product(A, B, mm, nn, a.rows, i == 3 ? MP : P, i == 3 ? P : MP), true, dst,
+              a.dw_dtype, a.accumulate, p.sums[i], p.out.splits[i]);
   };
   add(1, x, dg, a.dWg, a.dim, a.hidden);
   add(2, x, du, a.dWu, a.dim, a.hidden);
@@ -497,8 +482,19 @@ size_t ffn_workspace(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, b
 }
 
 hipError_t launch_ffn(const FfnArgs& a, hipStream_t s) {
-  if (a.dtype == SM_BF16) return a.act == 0 ? ffn<1, 0>(a, s) : ffn<1, 1>(a, s);
-  return a.act == 0 ? ffn<3, 0>(a, s) : ffn<3, 1>(a, s);
+  const FfnPlan p = ffn_plan(a.rows, a.dim, a.hidden, a.dtype, false, a.ws);
+  const auto go = [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    if (a.rows <= kFewRows)
+      return p.mid_planes == 1   ? ffn_few<bf16_t, bf16_t, ACT>(a, p, s)
+             : p.mid_planes == 2 ? ffn_few<bf16_t, float, ACT>(a, p, s)
+                                 : ffn_few<float, float, ACT>(a, p, s);
+    return p.mid_planes == 1   ? ffn<1, 1, ACT>(a, p, s)
+           : p.mid_planes == 2 ? ffn<1, 2, ACT>(a, p, s)
+                               : ffn<3, 3, ACT>(a, p, s);
+  };
+  return a.act == SM_ACT_SILU ? go(std::integral_constant<int, 0>())
+                              : go(std::integral_constant<int, 1>());
 }
 
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
@@ -508,8 +504,15 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
       if (p) SM_TRY(launch_zero(p, a.dw_dtype, a.dim * a.hidden, s));
     return hipSuccess;
   }
-  if (a.dtype == SM_BF16) return a.act == 0 ? ffn_grad<1, 0>(a, s) : ffn_grad<1, 1>(a, s);
-  return a.act == 0 ? ffn_grad<3, 0>(a, s) : ffn_grad<3, 1>(a, s);
+  const FfnPlan p = ffn_plan(a.rows, a.dim, a.hidden, a.dtype, true, a.ws);
+  const auto go = [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    return p.mid_planes == 1   ? ffn_grad<1, 1, ACT>(a, p, s)
+           : p.mid_planes == 2 ? ffn_grad<1, 2, ACT>(a, p, s)
+                               : ffn_grad<3, 3, ACT>(a, p, s);
+  };
+  return a.act == SM_ACT_SILU ? go(std::integral_constant<int, 0>())
+                              : go(std::integral_constant<int, 1>());
 }
 
 }  // namespace sm

@@ -11,8 +11,15 @@
 // one launch joins them.  Backward, in pieces of the vocabulary: the logits of a
 // piece again, with G = (softmax - onehot) * upstream written by the epilogue
 // (the softmax's statistics are known), then dX += G W and dW = G^T X of it.
+// Where the logits make few tiles (a small vocabulary), their product's k is
+// split, and a launch of its own does what the epilogues do.
+//
 // G is rounded to the operands' precision: for bfloat16 half a step of 2^-8 an
-// entry, as much as the rounding of the gradients themselves.
+// entry, as much as the rounding of the gradients themselves, where errors
+// average.  A row's gradient is mostly its target's entry, so over few rows, or
+// few results, they do not: there G has two bfloat16 planes.  An upstream factor
+// that all rows share would be rounded alike in all of them: it is left out of G
+// and multiplies the results.
 #include <cmath>
 
 #include "sm_few.h"
@@ -275,6 +282,84 @@ __global__ __launch_bounds__(1024) void k_loss_join(const float2* part, int64_t 
   }
 }
 
+// Both, where the logits are sums of splits: [split][rows][vocab rounded up to 4].
+// A wave a row up to kWaveRow logits, a block of 4 waves a row above.
+constexpr int kWaveRow = 512;
+__device__ __forceinline__ float split_sum(const float* p, int splits, int64_t step) {
+  float z = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < splits; ++k) z += p[k * step];
+  return z;
+}
+__global__ __launch_bounds__(256) void k_loss_mid(const float* sums, int splits,
+                                                  const int32_t* count, int rows, int vocab,
+                                                  const int32_t* list, const int32_t* target,
+                                                  float* loss, float* lse) {
+  __shared__ float2 sh[4];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const bool wave_row = vocab <= kWaveRow;
+  const int i = wave_row ? blockIdx.x * 4 + w : blockIdx.x;
+  if (i >= *count) return;       // (of the whole block, or of a wave that meets no other)
+  const int64_t ld = (vocab + 3) & ~3, step = rows * ld;
+  const float* z = sums + i * ld;
+  float m = -INFINITY, s = 0.f;
+  const auto add = [&](float mo, float so) {
+    const float top = fmaxf(m, mo), ref = top == -INFINITY ? 0.f : top;
+    s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) +
+        so * __builtin_amdgcn_exp2f((mo - ref) * kLog2e);
+    m = top;
+  };
+  for (int v = wave_row ? lane : (int)threadIdx.x; v < vocab; v += wave_row ? 64 : 256)
+    add(split_sum(z + v, splits, step), 1.f);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const float mo = __shfl_xor(m, o), so = __shfl_xor(s, o);
+    add(mo, so);
+  }
+  if (!wave_row) {
+    if (lane == 0) sh[w] = make_float2(m, s);
+    __syncthreads();
+    m = -INFINITY, s = 0.f;
+    for (int k = 0; k < 4; ++k) add(sh[k].x, sh[k].y);
+    if (w > 0) return;
+  }
+  if (lane == 0) {
+    const int r = list[i], t = target[i];
+    const float ref = m == -INFINITY ? 0.f : m, ln = logf(s);
+    lse[r] = ref + ln;
+    loss[r] = t < 0 ? NAN : ref - split_sum(z + t, splits, step) + ln;
+  }
+}
+
+// G from such sums; a thread has 4 entries of a row, the last of a row's 8 zero.
+template <int P>
+__global__ __launch_bounds__(256) void k_loss_mid_grad(const float* sums, int splits,
+                                                       const int32_t* count, int rows, int cols,
+                                                       const int32_t* target, int v0,
+                                                       const float* lse, const float* scale,
+                                                       bf16_t* g, int64_t g_ld, int64_t plane) {
+  const int per = ((cols + 7) & ~7) / 4;
+  const int64_t ld = (cols + 3) & ~3, all = (int64_t)*count * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all;
+       i += (int64_t)gridDim.x * 256) {
+    const int r = (int)(i / per), c = (int)(i - (int64_t)r * per) * 4;
+    f32x4_t z = {0.f, 0.f, 0.f, 0.f};
+    if (c < cols) {
+      const float* p = sums + r * ld + c;
+#pragma unroll 4
+      for (int k = 0; k < splits; ++k, p += rows * ld) z += *reinterpret_cast<const f32x4_t*>(p);
+    }
+    const float hi = lse[r] * kLog2e, lo = __builtin_fmaf(lse[r], kLog2e, -hi), by = scale[r];
+    const int t = target[r] - v0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[k], kLog2e, -hi) - lo);
+      z[k] = c + k < cols ? (c + k == t ? p - 1.f : p) * by : 0.f;
+    }
+    store_mid<P>(g + r * g_ld + c, plane, z);
+  }
+}
+
 // All of that for few rows, in one block: a wave a row.
 template <typename I>
 __global__ __launch_bounds__(1024) void k_loss_few(const float2* part, int strips, const I* targets,
@@ -347,25 +432,30 @@ __global__ __launch_bounds__(1024) void k_loss_sum(const int32_t* pos, int rows,
   }
 }
 
-// Backward: what the epilogue needs of each row that counts.
+// Backward: what the epilogue needs of each row that counts, and the factor that
+// they share (where no row counts there is nothing to multiply, whatever dloss is).
 __global__ __launch_bounds__(256) void k_loss_rows(const int32_t* count, const int32_t* list,
                                                    const int32_t* target, const float* lse,
                                                    const float* dloss, int reduction, float* lse_at,
-                                                   float* scale) {
+                                                   float* scale, float* by) {
   const int live = *count, i = blockIdx.x * 256 + threadIdx.x;
+  if (i == 0)
+    *by = live == 0 || reduction == SM_LOSS_ROWS ? 1.f
+          : reduction == SM_LOSS_MEAN            ? *dloss / live
+                                                 : *dloss;
   if (i >= live) return;
   const int r = list[i];
   lse_at[i] = lse[r];
-  const float up = dloss[reduction == 0 ? r : 0];
-  scale[i] = target[i] < 0 ? NAN : reduction == 2 ? up / live : up;
+  scale[i] = target[i] < 0 ? NAN : reduction == SM_LOSS_ROWS ? dloss[r] : 1.f;
 }
 
 namespace {
 
 struct LossPlan {
-  int planes;
+  int planes, g_planes;
   int32_t dim_ld;                 // row length of operand copies
   bool copy_w, wide;
+  int splits;                     // of the logits' k
   int64_t strips;
   // backward
   int64_t piece, g_ld;            // columns of a piece of the vocabulary, G's row length
@@ -373,11 +463,13 @@ struct LossPlan {
   // arrays
   int32_t *list, *target, *pos, *count;
   bf16_t *x, *w, *g;
-  float *picked, *loss, *lse_at, *scale, *dx, *dw;
+  float *picked, *loss, *lse_at, *scale, *by, *dx, *dw;
+  float* sums;                    // of the logits' splits
   float2* part;
   size_t bytes;
 };
 
+constexpr int64_t kTwoRows = 128, kTwoValues = 65536;    // up to which G has two planes
 constexpr int64_t kPieceBytes = (int64_t)1 << 30;
 
 // w_fits: the table is an operand as it lies
@@ -385,11 +477,9 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
                    bool backward, void* ws) {
   LossPlan p{};
   p.planes = dtype == SM_BF16 ? 1 : 3;
+  p.g_planes = p.planes == 3 ? 3 : rows <= kTwoRows || rows * dim <= kTwoValues ? 2 : 1;
   p.dim_ld = (int32_t)operand_ld(dim);
   p.copy_w = !w_fits;
-  const MmSize z{vocab, rows, (p.planes == 1 ? 1 : 6) * ((dim + 63) / 64), false};
-  p.wide = plan_products(&z, 1).wide;
-  p.strips = (vocab + (p.wide ? 127 : 63)) / (p.wide ? 128 : 64);
   Places at{static_cast<char*>(ws)};
   p.list = at.take<int32_t>(rows);
   p.target = at.take<int32_t>(rows);
@@ -404,19 +494,32 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
     p.bytes = few.used;
     return p;
   }
+  const auto logits_of = [&](int64_t cols) {
+    const MmSize z{cols, rows, (p.planes == 1 ? 1 : 6) * ((dim + 63) / 64), true};
+    const MmPlan plan = plan_products(&z, 1);
+    p.wide = plan.wide;
+    p.splits = plan.splits[0];
+    if (p.splits > 1) p.sums = at.take<float>(p.splits * rows * round_up(cols, 4));
+  };
   if (!backward) {
-    p.picked = at.take<float>(rows);
+    logits_of(vocab);
+    p.strips = (vocab + (p.wide ? 127 : 63)) / (p.wide ? 128 : 64);
     p.loss = at.take<float>(rows);
-    p.part = at.take<float2>(p.strips * rows);
+    if (p.splits == 1) {
+      p.picked = at.take<float>(rows);
+      p.part = at.take<float2>(p.strips * rows);
+    }
   } else {
     p.lse_at = at.take<float>(rows);
     p.scale = at.take<float>(rows);
-    const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * p.planes * rows) / 256 * 256);
+    p.by = at.take<float>(1);
+    const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * p.g_planes * rows) / 256 * 256);
     const int64_t pieces = (vocab + most - 1) / most;
     p.piece = std::min(round_up((vocab + pieces - 1) / pieces, 256), round_up(vocab, 8));
     p.g_ld = operand_ld(p.piece);
-    p.g = at.take<bf16_t>(p.planes * rows * p.g_ld);
-    const int segs = p.planes == 1 ? 1 : 6;
+    logits_of(std::min(p.piece, vocab));
+    p.g = at.take<bf16_t>(p.g_planes * rows * p.g_ld);
+    const int segs = p.planes == 1 ? p.g_planes : 6;
     const MmSize sizes[2] = {{dim, rows, segs * ((p.piece + 63) / 64), true},
                              {dim, p.piece, segs * ((rows + 63) / 64), true}};
     p.both = plan_products(sizes, 2);
@@ -458,9 +561,16 @@ MmArgs logits(const LossPlan& p, const void* W, int64_t rows, int64_t dim, int64
   j.m = (int)cols;
   j.n = (int)rows;
   j.k = (int)dim;
-  j.splits = 1;
-  set_planes(j, p.planes, vocab * p.dim_ld * 2, rows * p.dim_ld * 2);
+  j.splits = p.splits;
+  set_planes(j, p.planes, p.planes, vocab * p.dim_ld * 2, rows * p.dim_ld * 2);
   return m;
+}
+
+// Their sums of splits, for a launch of its own.
+hipError_t logit_sums(const LossPlan& p, MmArgs& m, hipStream_t s) {
+  EpiStore::Args e{};
+  e.out[0] = sums_out(p.sums, m.job[0].m, m.job[0].n);
+  return run_mm<false, false, false, EpiStore>(m, e, p.wide, s);
 }
 
 template <int P>
@@ -469,10 +579,18 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
   MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, v0, cols);
   const char* w = m.job[0].a;
   const int64_t ldw = m.job[0].lda;
-  const typename EpiGrad<P>::Args eg{p.g, p.g_ld, plane, (int)v0, p.target, p.lse_at, p.scale};
-  if (hipError_t e = run_mm<false, false, false, EpiGrad<P>>(m, eg, p.wide, s);
-      e != hipSuccess)
-    return e;
+  if (p.splits > 1) {
+    SM_TRY(logit_sums(p, m, s));
+    const int64_t work = a.rows * (round_up(cols, 8) / 4);
+    hipLaunchKernelGGL((k_loss_mid_grad<P>),
+                       dim3((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16)), dim3(256), 0,
+                       s, p.sums, p.splits, p.count, (int)a.rows, (int)cols, p.target, (int)v0,
+                       p.lse_at, p.scale, p.g, p.g_ld, plane);
+    SM_TRY(hipGetLastError());
+  } else {
+    const typename EpiGrad<P>::Args eg{p.g, p.g_ld, plane, (int)v0, p.target, p.lse_at, p.scale};
+    SM_TRY((run_mm<false, false, false, EpiGrad<P>>(m, eg, p.wide, s)));
+  }
   MmStores out;
   if (a.dX) {
     MmJob j{};
@@ -484,11 +602,11 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.m = (int)a.dim;
     j.n = (int)a.rows;
     j.k = (int)cols;
-    set_planes(j, P, a.vocab * p.dim_ld * 2, plane * 2);
+    set_planes(j, p.planes, P, a.vocab * p.dim_ld * 2, plane * 2);
     const int64_t ld = round_up(a.dim, 4);
     out.add(j, false, nullptr, SM_F32, 0, p.dx, 1);
     out.a.job[0].splits = p.both.splits[0];
-    out.e.out[0] = {p.dx, ld, a.rows * ld, SM_F32, v0 > 0};
+    out.e.out[0] = {p.dx, ld, a.rows * ld, SM_F32, v0 > 0, nullptr};
   }
   if (a.dW) {
     MmJob j{};
@@ -500,10 +618,10 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     j.m = (int)a.dim;
     j.n = (int)cols;
     j.k = (int)a.rows;
-    set_planes(j, P, a.rows * p.dim_ld * 2, plane * 2);
+    set_planes(j, p.planes, P, a.rows * p.dim_ld * 2, plane * 2);
     const int64_t size = a.dw_dtype == SM_F32 ? 4 : 2;
     out.add(j, true, static_cast<char*>(a.dW) + v0 * a.dim * size, a.dw_dtype, a.accumulate, p.dw,
-            p.both.splits[1]);
+            p.both.splits[1], p.by);
   }
   return out.run(p.both.wide, s);
 }
@@ -519,9 +637,9 @@ size_t loss_workspace(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, b
 template <typename T>
 static hipError_t loss_few(const LossArgs& a, const LossPlan& p, hipStream_t s) {
   const int strips = few_strips<T>(a.vocab, a.dim);
-  SM_TRY((launch_few<T, 1, FewLse<T>>((const T*)a.W, nullptr, a.dim, a.vocab, (const T*)a.X,
-                                      a.x_stride, a.rows, a.dim,
-                                      {p.part, strips, a.targets, a.target_bits, p.picked}, s)));
+  SM_TRY((launch_few<T, T, 1, FewLse<T>>((const T*)a.W, nullptr, a.dim, a.vocab, (const T*)a.X,
+                                         a.x_stride, a.rows, a.dim,
+                                         {p.part, strips, a.targets, a.target_bits, p.picked}, s)));
   float* loss = a.reduction == SM_LOSS_ROWS ? a.loss : nullptr;
   float* total = a.reduction == SM_LOSS_ROWS ? nullptr : a.loss;
   const auto join = [&](auto* t) {
@@ -543,16 +661,23 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
     return a.dtype == SM_BF16 ? loss_few<bf16_t>(a, p, s) : loss_few<float>(a, p, s);
   if (hipError_t e = gather(p, a, s); e != hipSuccess) return e;
   MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, 0, a.vocab);
-  if (hipError_t e = run_mm<false, false, false, EpiLse>(
-          m, {p.part, a.rows, p.target, p.picked}, p.wide, s);
-      e != hipSuccess)
-    return e;
-  float* loss = a.reduction == 0 ? a.loss : p.loss;
-  hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, p.part,
-                     a.rows, (int)p.strips, p.count, p.list, p.target, p.picked, loss, a.lse);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  float* loss = a.reduction == SM_LOSS_ROWS ? a.loss : p.loss;
+  if (p.splits > 1) {
+    SM_TRY(logit_sums(p, m, s));
+    const int per = a.vocab <= kWaveRow ? 4 : 1;
+    hipLaunchKernelGGL(k_loss_mid, dim3((unsigned)((a.rows + per - 1) / per)), dim3(256), 0, s,
+                       p.sums, p.splits, p.count, (int)a.rows, (int)a.vocab, p.list, p.target,
+                       loss, a.lse);
+  } else {
+    SM_TRY((run_mm<false, false, false, EpiLse>(m, {p.part, a.rows, p.target, p.picked}, p.wide,
+                                                s)));
+    hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, p.part,
+                       a.rows, (int)p.strips, p.count, p.list, p.target, p.picked, loss, a.lse);
+  }
+  SM_TRY(hipGetLastError());
   hipLaunchKernelGGL(k_loss_sum, dim3(1), dim3(1024), 0, s, p.pos, (int)a.rows, p.count, loss,
-                     a.lse, a.reduction == 0 ? nullptr : a.loss, (int)(a.reduction == 2));
+                     a.lse, a.reduction == SM_LOSS_ROWS ? nullptr : a.loss,
+                     (int)(a.reduction == SM_LOSS_MEAN));
   return hipGetLastError();
 }
 
@@ -563,18 +688,19 @@ hipError_t launch_loss_grad(const LossGradArgs& a, hipStream_t s) {
                                operand_fits(a.W, a.dtype, a.dim, a.dim), true, a.ws);
   if (hipError_t e = gather(p, a, s); e != hipSuccess) return e;
   hipLaunchKernelGGL(k_loss_rows, dim3((unsigned)((a.rows + 255) / 256)), dim3(256), 0, s, p.count,
-                     p.list, p.target, a.lse, a.dloss, (int)a.reduction, p.lse_at, p.scale);
+                     p.list, p.target, a.lse, a.dloss, (int)a.reduction, p.lse_at, p.scale, p.by);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
-    const hipError_t e = p.planes == 1 ? loss_grad_piece<1>(p, a, v0, s)
-                                       : loss_grad_piece<3>(p, a, v0, s);
+    const hipError_t e = p.g_planes == 1   ? loss_grad_piece<1>(p, a, v0, s)
+                         : p.g_planes == 2 ? loss_grad_piece<2>(p, a, v0, s)
+                                           : loss_grad_piece<3>(p, a, v0, s);
     if (e != hipSuccess) return e;
   }
   if (!a.dX) return hipSuccess;
   const int64_t ld = round_up(a.dim, 4);
   JoinJobs j{};
   j.job[j.jobs++] = {p.dx, a.rows * ld, ld, p.both.splits[0], p.pos, a.rows, (int)a.dim, a.dtype, 0,
-                     a.dX, a.dim};
+                     a.dX, a.dim, p.by};
   return launch_join(j, s);
 }
 

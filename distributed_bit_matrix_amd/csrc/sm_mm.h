@@ -30,8 +30,10 @@ constexpr int kMaxJobs = 4;
 
 // The pairs of planes of a float32 product: those whose products reach 2^-24 of
 // the largest, the small ones first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0), as
-// codes a + 4 b in four bits each.
+// codes a + 4 b in four bits each.  Products of one plane with two: (0,1) (0,0),
+// or (1,0) (0,0).
 constexpr int kPairCode = 2 | (1 + 4) << 4 | (2 * 4) << 8 | 1 << 12 | 4 << 16;
+constexpr int kPairOneTwo = 4, kPairTwoOne = 1;
 
 // One product of a launch.  Row lengths count elements.
 struct MmJob {
@@ -39,7 +41,7 @@ struct MmJob {
   const int32_t *n_rows, *k_rows;  // where not null, *n_rows replaces n, *k_rows k
   int64_t lda, ldb;
   int32_t m, n, k;
-  int32_t pairs, parts;            // of planes: 1 or 6; products that are summed: 1 or 2
+  int32_t pairs, code, parts;      // of planes, 1, 2 or 6; products that are summed: 1 or 2
   int32_t splits;                  // blocks that share a tile's k
   int32_t m_tiles, n_tiles;
   int32_t block0;                  // its first block
@@ -84,7 +86,8 @@ struct MmSource {
       const int p = lane & 15, kr = lane >> 4;
 #pragma unroll
       for (int v = 0; v < 2; ++v)
-        off[v] = (uint32_t)(kr * row_bytes + ((((p >> 1) ^ km_swz(kr + 8 * v)) << 5) | (p & 1) << 4));
+        off[v] = (uint32_t)(kr * row_bytes +
+                            ((((p >> 1) ^ km_swz(kr + 8 * v)) << 5) | (p & 1) << 4));
     } else {
       const int r = lane >> 3, g = (lane & 7) ^ swz<128>(r);
       chunk = g * 8;
@@ -102,7 +105,8 @@ struct MmSource {
   }
   // load i of the operand's tile
   __device__ __forceinline__ uint32_t at(const uint32_t (&o)[2], int i) const {
-    if constexpr (KM) return o[(i >> 1) & 1] + (uint32_t)(4 * (i & 15) * row_bytes + (i >> 4) * 256);
+    if constexpr (KM)
+      return o[(i >> 1) & 1] + (uint32_t)(4 * (i & 15) * row_bytes + (i >> 4) * 256);
     // 16 rows of a group; paired, groups alternate between two matrices
     return o[i & 1] + (uint32_t)((PAIR ? i >> 2 : i >> 1) * 16 * row_bytes);
   }
@@ -182,7 +186,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& args, const typename Epi::
   MmSource<BKM, false> sb;
   sa.place(lane, job.lda);
   sb.place(lane, job.ldb);
-  const int pairs = job.pairs, per_seg = (k_all + kSlab - 1) / kSlab;
+  const int pairs = job.pairs, code = job.code, per_seg = (k_all + kSlab - 1) / kSlab;
   const int all = per_seg * pairs * job.parts;
   const int per = __builtin_amdgcn_readfirstlane((all + job.splits - 1) / job.splits);
   const int s0 = split * per;
@@ -198,8 +202,7 @@ __device__ __forceinline__ void mm_tile(const MmArgs& args, const typename Epi::
   auto aim = [&]() SM_INLINE {
     const int left = k_all - k0, rows = left < kSlab ? left : kSlab;
     const int part = seg >= pairs ? 1 : 0, pair = seg - part * pairs;
-    // the planes of a pair, in kPairs' order; one plane has one pair (0, 0)
-    const int pl = pairs == 1 ? 0 : kPairCode >> (4 * pair);
+    const int pl = code >> (4 * pair);
     const int64_t a_at = (pl & 3) * a_plane + part * a_part + (AKM ? k0 * lda : (int64_t)k0 * 2);
     const int64_t b_at =
         (pl >> 2 & 3) * b_plane + part * b_part + (BKM ? k0 * ldb : (int64_t)k0 * 2);

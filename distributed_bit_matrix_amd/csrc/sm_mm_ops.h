@@ -7,15 +7,6 @@
 
 namespace sm {
 
-// Three bfloat16 values whose sum is f to 24 bits.  Each is taken of what the
-// others leave, which is exact; a value that is not finite is in the first.
-__device__ __forceinline__ void split3(float f, bf16_t (&p)[3]) {
-  p[0] = f32_to_bf16(f);
-  const float hi = bf16_to_f32(p[0]);
-  const float r = __builtin_isfinite(hi) ? f - hi : 0.f;
-  p[1] = f32_to_bf16(r);
-  p[2] = f32_to_bf16(r - bf16_to_f32(p[1]));
-}
 // 16 rows of an epilogue's F features on their way to memory.  In the accumulators
 // a lane has 4 features of one row: stores from there write 32 bytes of each of 16
 // rows (8 us for a tile of 256 x 256 bfloat16, as long as 5 slabs).  Through LDS
@@ -93,7 +84,7 @@ __device__ __forceinline__ void put_planes(const MmPlace& at, const f32x4_t (&v)
 #pragma unroll
     for (int i = 0; i < F / 16; ++i) left[i] = v[i];
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
+    for (int q = 0; q < P; ++q) {
 #pragma unroll
       for (int i = 0; i < F / 16; ++i) {
         out.put(q & 1, i, left[i]);
@@ -108,6 +99,23 @@ __device__ __forceinline__ void put_planes(const MmPlace& at, const f32x4_t (&v)
   }
 }
 
+// Four neighbouring values to P planes, `plane` entries apart; 8-byte aligned.  Each
+// plane has what the ones before it leave, rounded: three hold float32's 24 bits.  A
+// value that is not finite is in the first.
+template <int P>
+__device__ __forceinline__ void store_mid(bf16_t* p, int64_t plane, f32x4_t v) {
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+    *reinterpret_cast<u32x2_t*>(p + q * plane) = u32x2_t{lo, hi};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float t = bf16_to_f32((bf16_t)((k < 2 ? lo : hi) >> (16 * (k & 1))));
+      v[k] = __builtin_isfinite(t) ? v[k] - t : 0.f;
+    }
+  }
+}
+
 // The product itself: to an array of a caller's type, or (parts) to float32
 // sums of a split, which a later launch joins.
 struct MmOut {
@@ -115,6 +123,7 @@ struct MmOut {
   int64_t ld;
   int64_t split_step;      // elements from one split's sums to the next
   int32_t dtype, add;      // add: to what is there (float32)
+  const float* by;         // a factor, or null
 };
 struct EpiStore {
   struct Args {
@@ -125,10 +134,11 @@ struct EpiStore {
                                                const f32x4_t (&acc)[TI][TJ]) {
     const MmRows<T, 16 * TI> rows{at.lds, at.lane};
     T* p = static_cast<T*>(o.p) + at.split * o.split_step + at.m0;
+    const float by = o.by ? *o.by : 1.f;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
 #pragma unroll
-      for (int i = 0; i < TI; ++i) rows.put(j & 1, i, acc[i][j]);
+      for (int i = 0; i < TI; ++i) rows.put(j & 1, i, acc[i][j] * by);
       const int n = at.n0 + 16 * j;
       rows.template flush<ADD>(j & 1, p + (int64_t)n * o.ld, o.ld, at.n - n, at.m - at.m0);
     }
@@ -162,9 +172,9 @@ struct PlanesJobs {
 };
 hipError_t launch_planes(PlanesJobs& a, int32_t dtype, hipStream_t s);
 
-// Sums of splits joined: out[r][c] = sum over s of part[s][at(r)][c] (plus what
-// is there), at(r) = pos[r], or r where pos is null; a row whose pos is negative
-// is zero.
+// Sums of splits joined: out[r][c] = by * sum over s of part[s][at(r)][c] (plus
+// what is there), at(r) = pos[r], or r where pos is null; a row whose pos is
+// negative is zero.
 struct JoinArgs {
   const float* part;
   int64_t split_step, part_ld;
@@ -174,6 +184,7 @@ struct JoinArgs {
   int32_t cols, dtype, add;
   void* out;
   int64_t ld;
+  const float* by;         // a factor, or null
 };
 struct JoinJobs {
   JoinArgs job[kMaxJobs];
@@ -197,12 +208,23 @@ inline bool operand_fits(const void* p, int32_t dtype, int64_t cols, int64_t str
          stride <= ((int64_t)1 << 21);
 }
 
-// The planes of a job's operands; a_plane and b_plane in bytes.
-inline void set_planes(MmJob& j, int planes, int64_t a_plane, int64_t b_plane) {
-  j.pairs = planes == 1 ? 1 : 6;
+// The planes of a job's operands, (1, 1), (1, 2), (2, 1) or (3, 3); a_plane and
+// b_plane in bytes.
+inline void set_planes(MmJob& j, int a_planes, int b_planes, int64_t a_plane, int64_t b_plane) {
+  j.pairs = a_planes * b_planes == 9 ? 6 : a_planes * b_planes;
+  j.code = a_planes * b_planes == 9 ? kPairCode
+           : b_planes == 2          ? kPairOneTwo
+           : a_planes == 2          ? kPairTwoOne
+                                    : 0;
   j.parts = 1;
   j.a_plane = a_plane;
   j.b_plane = b_plane;
+}
+
+// A product's sums of splits, for a launch of its own that joins them.
+inline MmOut sums_out(float* sums, int64_t m, int64_t n) {
+  const int64_t ld = round_up(m, 4);
+  return {sums, ld, n * ld, SM_F32, 0, nullptr};
 }
 
 // Places in a workspace, each 256-byte aligned.
@@ -272,9 +294,10 @@ struct MmStores {
   MmArgs a{};
   EpiStore::Args e{};
   JoinJobs join{};
-  // job j, whose rows go to dst; sums: where those of its splits go, if it has any
+  // job j, whose rows, times *by, go to dst; sums: where those of its splits go, if
+  // it has any
   void add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t accumulate, float* sums,
-           int splits);
+           int splits, const float* by = nullptr);
   hipError_t run(bool wide, hipStream_t s);
   hipError_t joins(hipStream_t s);
 };

@@ -3,23 +3,6 @@
 
 namespace sm {
 
-// Four neighbouring entries to P planes, `plane` entries apart; 8-byte aligned.
-template <int P>
-__device__ __forceinline__ void store_planes(bf16_t* p, int64_t plane, const float (&v)[4]) {
-  if constexpr (P == 1) {
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-  } else {
-    bf16_t t[4][3];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) split3(v[k], t[k]);
-#pragma unroll
-    for (int q = 0; q < 3; ++q)
-      *reinterpret_cast<u32x2_t*>(p + q * plane) =
-          u32x2_t{(uint32_t)t[0][q] | ((uint32_t)t[1][q] << 16),
-                  (uint32_t)t[2][q] | ((uint32_t)t[3][q] << 16)};
-  }
-}
-
 // The job of a block, and the block's place in it.
 template <int MAX>
 __device__ __forceinline__ int job_of(const int32_t (&block0)[MAX], int jobs, int& block) {
@@ -61,9 +44,8 @@ __global__ __launch_bounds__(256) void k_planes(PlanesJobs all) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = c + k < cols ? to_f32(p[k]) : 0.f;
     }
-    float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-    store_planes<P>(a.dst + r * a.ld + c, plane, lo);
-    store_planes<P>(a.dst + r * a.ld + c + 4, plane, hi);
+    store_mid<P>(a.dst + r * a.ld + c, plane, f32x4_t{v[0], v[1], v[2], v[3]});
+    store_mid<P>(a.dst + r * a.ld + c + 4, plane, f32x4_t{v[4], v[5], v[6], v[7]});
   }
 }
 
@@ -99,6 +81,11 @@ __device__ __forceinline__ void join_rows(const JoinArgs& a, int block, int bloc
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] += t[q];
       }
+    }
+    if (a.by) {
+      const float by = *a.by;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= by;
     }
     T* o = static_cast<T*>(a.out) + r * a.ld + c;
     if (a.add) {
@@ -208,7 +195,7 @@ MmPlan plan_products(const MmSize* sizes, int jobs) {
 }
 
 void MmStores::add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t accumulate,
-                   float* sums, int splits) {
+                   float* sums, int splits, const float* by) {
   const int i = a.jobs++;
   a.job[i] = j;
   a.job[i].b_km = b_km;
@@ -216,10 +203,10 @@ void MmStores::add(const MmJob& j, bool b_km, void* dst, int32_t dtype, int32_t 
   const int64_t ld = round_up(j.m, 4);
   join.job[i] = JoinArgs{};
   if (splits > 1) {
-    e.out[i] = {sums, ld, j.n * ld, SM_F32, 0};
-    join.job[i] = {sums, j.n * ld, ld, splits, nullptr, j.n, j.m, dtype, accumulate, dst, j.m};
+    e.out[i] = sums_out(sums, j.m, j.n);
+    join.job[i] = {sums, j.n * ld, ld, splits, nullptr, j.n, j.m, dtype, accumulate, dst, j.m, by};
   } else {
-    e.out[i] = {dst, j.m, 0, dtype, accumulate};
+    e.out[i] = {dst, j.m, 0, dtype, accumulate, by};
   }
 }
 

@@ -74,6 +74,55 @@ def test_shapes(rows, dim, vocab, dtype):
     check(x, w, t, reduction, torch.float32 if vocab % 2 else None)
 
 
+# long rows against small tables: the logits' sums over k are split
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim,vocab", [(17, 2000, 2), (40, 1203, 91), (300, 2048, 513),
+                                            (100, 1500, 1025), (1, 4096, 3), (2500, 1111, 17)])
+def test_small_tables(rows, dim, vocab, dtype):
+    for reduction in ("mean", "sum", "none"):
+        print(f"loss {rows}x{dim}x{vocab} {dtype} {reduction}", flush=True)
+        x, w, t = inputs(rows, dim, vocab, dtype, rows + vocab, 0.2 if rows > 1 else 0.0)
+        check(x, w, t, reduction)
+
+
+def test_a_small_table_with_rows_and_targets_that_do_not_count():
+    """Where the sums are split: padding of NaN reaches nothing, a target outside the table
+    has NaN for its row alone, and every row may be ignored."""
+    x, w, t = inputs(60, 1500, 70, "bf16", 9, 0.3)
+    drop = t == IGNORE
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    dx, dw = B.linear_cross_entropy_backward(loss, x, w, t, lse, IGNORE, "none")
+    x2 = torch.where(drop[:, None], torch.full_like(x, float("nan")), x)
+    loss2, lse2 = B.linear_cross_entropy(x2, w, t, IGNORE, "none", want_lse=True)
+    dx2, dw2 = B.linear_cross_entropy_backward(loss, x2, w, t, lse2, IGNORE, "none")
+    for a, b in ((loss, loss2), (lse, lse2), (dx, dx2), (dw, dw2)):
+        assert torch.equal(bits(a), bits(b))
+    live = int((~drop).nonzero()[0])
+    t[live] = 70
+    loss = B.linear_cross_entropy(x, w, t, IGNORE, "none")
+    assert loss.isnan().nonzero().flatten().tolist() == [live]
+    t.fill_(IGNORE)
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "mean", want_lse=True)
+    dx, dw = B.linear_cross_entropy_backward(torch.full_like(loss, float("inf")), x, w, t, lse)
+    assert loss == 0 and (lse == 0).all() and (dx == 0).all() and (dw == 0).all()
+
+
+@pytest.mark.parametrize("rows,dim,vocab", [(2000, 96, 300), (20, 1200, 60)])
+def test_a_factor_of_all_rows_is_not_rounded(rows, dim, vocab):
+    """The gradients are the factor times those of the factor 1, though a bfloat16 holds it
+    half a step off: two float32 roundings apart at most, one of each result."""
+    x, w, t = inputs(rows, dim, vocab, "bf16", 3, 0.1)
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "sum", want_lse=True)
+    one = torch.ones((), device="cuda")
+    dw = B.linear_cross_entropy_backward(one, x, w, t, lse, IGNORE, "sum",
+                                         dtype=torch.float32)[1]
+    for c in (1 + 2.0 ** -8, 0.7 * 2.0 ** -12):
+        c = torch.tensor(c, device="cuda")
+        got = B.linear_cross_entropy_backward(c, x, w, t, lse, IGNORE, "sum",
+                                              dtype=torch.float32)[1]
+        within(got, dw.double() * c.double(), 2 * R.U32 * (dw.double() * c.double()).abs(), "dw")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_around_the_form_for_few(dtype):
     """15, 16 and 17 rows, with padding among them, every reduction."""
