@@ -16,6 +16,7 @@
 //
 // Up to 16 rows the products are bound by reading the weights once (sm_few.h).
 #include "sm_few.h"
+#include "sm_thin.h"
 #include "sm_layers.h"
 #include "sm_mm_ops.h"
 
@@ -286,6 +287,7 @@ struct FfnPlan {
   MmPlan first, out;       // tiles of the first product; of the others (forward: y;
                            // backward: dx, dwg, dwu, dwd)
   float* sums[4];          // of their splits
+  int thin[2];             // splits of the thin form's products
   bool split_first;        // the first product's k is split, and what follows it
   float* mid;              // takes a launch of its own: its sums
   size_t bytes;
@@ -306,11 +308,24 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
     p.bytes = at.used;
     return p;
   }
+  const bool thin = thin_form(rows, dim, hidden, 3, dtype, backward);
+  if (!backward && thin) {
+    p.thin[0] = thin_splits(hidden, rows, dim, 2);
+    p.thin[1] = thin_splits(dim, rows, hidden, 1);
+    p.x = at.take<bf16_t>(3 * rows * p.ld_d);
+    p.h = at.take<bf16_t>(3 * rows * p.ld_f);
+    p.mid = at.take<float>(2 * p.thin[0] * rows * round_up(hidden, 4));
+    p.sums[0] = at.take<float>(p.thin[1] * rows * round_up(dim, 4));
+    p.bytes = at.used;
+    return p;
+  }
   const int64_t segs = p.planes == 1 ? 1 : 6, mid = p.planes == 1 ? p.mid_planes : 6;
   p.x = at.take<bf16_t>(p.planes * rows * p.ld_d);
-  p.wg = at.take<bf16_t>(p.planes * hidden * p.ld_d);
-  p.wu = at.take<bf16_t>(p.planes * hidden * p.ld_d);
-  p.wd = at.take<bf16_t>(p.planes * dim * p.ld_f);
+  if (!thin) {
+    p.wg = at.take<bf16_t>(p.planes * hidden * p.ld_d);
+    p.wu = at.take<bf16_t>(p.planes * hidden * p.ld_d);
+    p.wd = at.take<bf16_t>(p.planes * dim * p.ld_f);
+  }
   p.h = at.take<bf16_t>(p.mid_planes * rows * p.ld_f);
   const auto first = [&](MmSize z, int jobs) {
     const MmSize both[2] = {z, z};
@@ -339,8 +354,21 @@ FfnPlan ffn_plan(int64_t rows, int64_t dim, int64_t hidden, int32_t dtype, bool 
                          {dim, hidden, mids(rows), true},
                          {dim, hidden, mids(rows), true},
                          {hidden, dim, mids(rows), true}};
-    first({hidden, rows, slabs(dim), true}, 1);
-    room(o, 4);
+    if (thin) {
+      p.thin[0] = thin_splits(hidden, rows, dim, 1);
+      p.thin[1] = thin_splits(dim, rows, hidden, 2);
+      p.mid = at.take<float>(p.thin[0] * rows * round_up(hidden, 4));
+      p.sums[0] = at.take<float>(2 * p.thin[1] * rows * round_up(dim, 4));
+      p.out = plan_products(o + 1, 3);
+      for (int i = 3; i > 0; --i) {
+        p.out.splits[i] = p.out.splits[i - 1];
+        if (p.out.splits[i] > 1)
+          p.sums[i] = at.take<float>(p.out.splits[i] * o[i].n * round_up(o[i].m, 4));
+      }
+    } else {
+      first({hidden, rows, slabs(dim), true}, 1);
+      room(o, 4);
+    }
   }
   p.bytes = at.used;
   return p;
@@ -381,9 +409,36 @@ hipError_t ffn_few(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
                                           {(T*)a.Y}, s);
 }
 
+// float32 and few rows more (sm_thin.h).
+template <int ACT>
+hipError_t ffn_thin(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
+  PlanesJobs c{};
+  c.job[c.jobs++] = {a.X, a.x_stride, a.rows, (int)a.dim, (int)p.ld_d, nullptr, nullptr, p.x};
+  SM_TRY(launch_planes(c, a.dtype, s));
+  const bool once = 12 * a.dim * a.hidden > kCacheBytes;
+  float* up = p.mid + p.thin[0] * a.rows * round_up(a.hidden, 4);
+  const ThinArgs first{{(const float*)a.Wg, (const float*)a.Wu}, {p.x, p.x}, {p.mid, up}, a.dim,
+                       p.ld_d, a.rows * p.ld_d, (int)a.hidden, (int)a.rows, (int)a.dim, p.thin[0],
+                       2, once};
+  SM_TRY(launch_thin<false>(first, s));
+  const int64_t plane = a.rows * p.ld_f;
+  const MidArgs g{{p.mid, up}, p.thin[0], a.rows, (int)a.hidden, (int)p.ld_f, plane, nullptr, a.pre,
+                  {p.h, nullptr, nullptr}};
+  SM_TRY((launch_mid<3, ACT, false>(g, s)));
+  const ThinArgs out{{(const float*)a.Wd, nullptr}, {p.h, nullptr}, {p.sums[0], nullptr}, a.hidden,
+                     p.ld_f, plane, (int)a.dim, (int)a.rows, (int)a.hidden, p.thin[1], 1, once};
+  SM_TRY(launch_thin<false>(out, s));
+  const int64_t ld = round_up(a.dim, 4);
+  JoinJobs j{};
+  j.job[j.jobs++] = {p.sums[0], a.rows * ld, ld, p.thin[1], nullptr, a.rows, (int)a.dim, a.dtype, 0,
+                     a.Y, a.dim, nullptr};
+  return launch_join(j, s);
+}
+
 template <int P, int MP, int ACT>
 hipError_t ffn(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
   // (Wg and Wu lie where they are, or both are copied: they share a row length)
+  const bool thin = thin_form(a.rows, a.dim, a.hidden, 3, a.dtype, true);
   const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
                       !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
   PlanesJobs c{};
@@ -423,13 +478,14 @@ hipError_t ffn(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
 
 template <int P, int MP, int ACT>
 hipError_t ffn_grad(const FfnGradArgs& a, const FfnPlan& p, hipStream_t s) {
+  const bool thin = thin_form(a.rows, a.dim, a.hidden, 3, a.dtype, true);
   const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
                       !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
   PlanesJobs c{};
   const Operand dy = operand(c, a.dY, a.dtype, a.rows, a.dim, a.dy_stride, p.dy);
-  const Operand wd = operand(c, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, p.wd);
-  Operand x{}, wg{}, wu{};
-  if (a.dX) {
+  Operand x{}, wd{}, wg{}, wu{};
+  if (!thin) wd = operand(c, a.Wd, a.dtype, a.dim, a.hidden, a.hidden, p.wd);
+  if (a.dX && !thin) {
     wg = operand(c, a.Wg, a.dtype, a.hidden, a.dim, a.dim, p.wg, copied);
     wu = operand(c, a.Wu, a.dtype, a.hidden, a.dim, a.dim, p.wu, copied);
   }
@@ -437,7 +493,16 @@ hipError_t ffn_grad(const FfnGradArgs& a, const FfnPlan& p, hipStream_t s) {
   SM_TRY(launch_planes(c, a.dtype, s));
   const int64_t plane = a.rows * p.ld_f;
   const MmJob first = product(wd, dy, a.hidden, a.rows, a.dim, P, P);
-  if (p.split_first) {
+  const bool once = 12 * a.dim * a.hidden > kCacheBytes;
+  if (thin) {
+    const ThinArgs t{{(const float*)a.Wd, nullptr}, {p.dy, nullptr}, {p.mid, nullptr}, a.hidden,
+                     p.ld_d, a.rows * p.ld_d, (int)a.hidden, (int)a.rows, (int)a.dim, p.thin[0], 1,
+                     once};
+    SM_TRY(launch_thin<true>(t, s));
+    const MidArgs g{{p.mid, nullptr}, p.thin[0], a.rows, (int)a.hidden, (int)p.ld_f, plane, a.pre,
+                    nullptr, {p.dg, p.du, p.h}};
+    SM_TRY((launch_mid<MP, ACT, true>(g, s)));
+  } else if (p.split_first) {
     MmStores z;
     z.add(first, false, nullptr, SM_F32, 0, p.mid, p.first.splits[0]);
     z.e.out[0] = sums_out(p.mid, a.hidden, a.rows);
@@ -456,7 +521,17 @@ hipError_t ffn_grad(const FfnGradArgs& a, const FfnPlan& p, hipStream_t s) {
   const Operand du{(const char*)p.du, p.ld_f, plane * 2};
   const Operand h{(const char*)p.h, p.ld_f, plane * 2};
   MmStores out;
-  if (a.dX) {
+  if (a.dX && thin) {
+    const int64_t ld = round_up(a.dim, 4), step = a.rows * ld;
+    const ThinArgs t{{(const float*)a.Wg, (const float*)a.Wu}, {p.dg, p.du},
+                     {p.sums[0], p.sums[0] + p.thin[1] * step}, a.dim, p.ld_f, plane, (int)a.dim,
+                     (int)a.rows, (int)a.hidden, p.thin[1], 2, once};
+    SM_TRY(launch_thin<true>(t, s));
+    JoinJobs j{};
+    j.job[j.jobs++] = {p.sums[0], step, ld, 2 * p.thin[1], nullptr, a.rows, (int)a.dim, a.dtype, 0,
+                       a.dX, a.dim, nullptr};
+    SM_TRY(launch_join(j, s));
+  } else if (a.dX) {
     MmJob j = product(wg, dg, a.dim, a.rows, a.hidden, P, MP);
     j.parts = 2;
     j.a_part = wu.p - wg.p;
@@ -489,6 +564,7 @@ hipError_t launch_ffn(const FfnArgs& a, hipStream_t s) {
       return p.mid_planes == 1   ? ffn_few<bf16_t, bf16_t, ACT>(a, p, s)
              : p.mid_planes == 2 ? ffn_few<bf16_t, float, ACT>(a, p, s)
                                  : ffn_few<float, float, ACT>(a, p, s);
+    if (thin_form(a.rows, a.dim, a.hidden, 3, a.dtype, false)) return ffn_thin<ACT>(a, p, s);
     return p.mid_planes == 1   ? ffn<1, 1, ACT>(a, p, s)
            : p.mid_planes == 2 ? ffn<1, 2, ACT>(a, p, s)
                                : ffn<3, 3, ACT>(a, p, s);

@@ -25,6 +25,7 @@
 #include "sm_few.h"
 #include "sm_layers.h"
 #include "sm_mm_ops.h"
+#include "sm_thin.h"
 
 namespace sm {
 
@@ -234,6 +235,53 @@ struct EpiGrad {
   }
 };
 
+// What EpiLse does, where the logits are sums of splits: [split][rows][vocab rounded
+// up to 4].  A wave has a row's strip of kMidStrip logits.
+constexpr int kMidStrip = 1024;
+__global__ __launch_bounds__(256) void k_loss_mid(const float* sums, int splits,
+                                                  const int32_t* count, int rows, int vocab,
+                                                  int strips, EpiLse::Args e) {
+  constexpr int V = kMidStrip / 256;
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int n = (int)(i / strips), strip = (int)(i - (int64_t)n * strips);
+  if (n >= *count) return;
+  const int64_t ld = (vocab + 3) & ~3;
+  const float* p = sums + n * ld;
+  f32x4_t z[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) z[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < splits; ++k, p += rows * ld) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = strip * kMidStrip + 256 * v + 4 * lane;
+      if (c < vocab) z[v] += *reinterpret_cast<const f32x4_t*>(p + c);
+    }
+  }
+  const int t = e.target[n];
+  float m = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = strip * kMidStrip + 256 * v + 4 * lane + k;
+      if (c < vocab) m = fmaxf(m, z[v][k]);
+      if (c == t) e.picked[n] = z[v][k];
+    }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (strip * kMidStrip + 256 * v + 4 * lane + k < vocab)
+        s += __builtin_amdgcn_exp2f((z[v][k] - ref) * kLog2e);
+  s = lanes_sum<64>(s);
+  if (lane == 0) e.part[strip * e.cap + n] = make_float2(m, s);
+}
+
 // ---------------------------------------------------------------------------
 // Forward: the strips' sums joined, 16 rows by 64 lanes over the strips.
 // loss[r], lse[r] of the caller's rows; a row whose target does not exist has
@@ -279,55 +327,6 @@ __global__ __launch_bounds__(1024) void k_loss_join(const float2* part, int64_t 
     const int r = list[at];
     lse[r] = top + ln;
     loss[r] = target[at] < 0 ? NAN : top - picked[at] + ln;
-  }
-}
-
-// Both, where the logits are sums of splits: [split][rows][vocab rounded up to 4].
-// A wave a row up to kWaveRow logits, a block of 4 waves a row above.
-constexpr int kWaveRow = 512;
-__device__ __forceinline__ float split_sum(const float* p, int splits, int64_t step) {
-  float z = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < splits; ++k) z += p[k * step];
-  return z;
-}
-__global__ __launch_bounds__(256) void k_loss_mid(const float* sums, int splits,
-                                                  const int32_t* count, int rows, int vocab,
-                                                  const int32_t* list, const int32_t* target,
-                                                  float* loss, float* lse) {
-  __shared__ float2 sh[4];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const bool wave_row = vocab <= kWaveRow;
-  const int i = wave_row ? blockIdx.x * 4 + w : blockIdx.x;
-  if (i >= *count) return;       // (of the whole block, or of a wave that meets no other)
-  const int64_t ld = (vocab + 3) & ~3, step = rows * ld;
-  const float* z = sums + i * ld;
-  float m = -INFINITY, s = 0.f;
-  const auto add = [&](float mo, float so) {
-    const float top = fmaxf(m, mo), ref = top == -INFINITY ? 0.f : top;
-    s = s * __builtin_amdgcn_exp2f((m - ref) * kLog2e) +
-        so * __builtin_amdgcn_exp2f((mo - ref) * kLog2e);
-    m = top;
-  };
-  for (int v = wave_row ? lane : (int)threadIdx.x; v < vocab; v += wave_row ? 64 : 256)
-    add(split_sum(z + v, splits, step), 1.f);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const float mo = __shfl_xor(m, o), so = __shfl_xor(s, o);
-    add(mo, so);
-  }
-  if (!wave_row) {
-    if (lane == 0) sh[w] = make_float2(m, s);
-    __syncthreads();
-    m = -INFINITY, s = 0.f;
-    for (int k = 0; k < 4; ++k) add(sh[k].x, sh[k].y);
-    if (w > 0) return;
-  }
-  if (lane == 0) {
-    const int r = list[i], t = target[i];
-    const float ref = m == -INFINITY ? 0.f : m, ln = logf(s);
-    lse[r] = ref + ln;
-    loss[r] = t < 0 ? NAN : ref - split_sum(z + t, splits, step) + ln;
   }
 }
 
@@ -454,7 +453,7 @@ namespace {
 struct LossPlan {
   int planes, g_planes;
   int32_t dim_ld;                 // row length of operand copies
-  bool copy_w, wide;
+  bool copy_w, wide, thin;        // thin: the products with the table (sm_thin.h)
   int splits;                     // of the logits' k
   int64_t strips;
   // backward
@@ -477,9 +476,12 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
                    bool backward, void* ws) {
   LossPlan p{};
   p.planes = dtype == SM_BF16 ? 1 : 3;
-  p.g_planes = p.planes == 3 ? 3 : rows <= kTwoRows || rows * dim <= kTwoValues ? 2 : 1;
   p.dim_ld = (int32_t)operand_ld(dim);
-  p.copy_w = !w_fits;
+  p.g_planes = p.planes == 3 ? 3 : rows <= kTwoRows || rows * dim <= kTwoValues ? 2 : 1;
+  const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * p.g_planes * rows) / 256 * 256);
+  const int64_t pieces = backward ? (vocab + most - 1) / most : 1;
+  p.thin = thin_form(rows, vocab, dim, 1, dtype, backward) && pieces == 1;
+  p.copy_w = !w_fits && !p.thin;
   Places at{static_cast<char*>(ws)};
   p.list = at.take<int32_t>(rows);
   p.target = at.take<int32_t>(rows);
@@ -495,6 +497,11 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
     return p;
   }
   const auto logits_of = [&](int64_t cols) {
+    if (p.thin) {
+      p.splits = thin_splits(cols, rows, dim, 1);
+      p.sums = at.take<float>(p.splits * rows * round_up(cols, 4));
+      return;
+    }
     const MmSize z{cols, rows, (p.planes == 1 ? 1 : 6) * ((dim + 63) / 64), true};
     const MmPlan plan = plan_products(&z, 1);
     p.wide = plan.wide;
@@ -503,18 +510,15 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
   };
   if (!backward) {
     logits_of(vocab);
-    p.strips = (vocab + (p.wide ? 127 : 63)) / (p.wide ? 128 : 64);
+    const int64_t strip = p.thin || p.splits > 1 ? kMidStrip : p.wide ? 128 : 64;
+    p.strips = (vocab + strip - 1) / strip;
     p.loss = at.take<float>(rows);
-    if (p.splits == 1) {
-      p.picked = at.take<float>(rows);
-      p.part = at.take<float2>(p.strips * rows);
-    }
+    p.picked = at.take<float>(rows);
+    p.part = at.take<float2>(p.strips * rows);
   } else {
     p.lse_at = at.take<float>(rows);
     p.scale = at.take<float>(rows);
     p.by = at.take<float>(1);
-    const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * p.g_planes * rows) / 256 * 256);
-    const int64_t pieces = (vocab + most - 1) / most;
     p.piece = std::min(round_up((vocab + pieces - 1) / pieces, 256), round_up(vocab, 8));
     p.g_ld = operand_ld(p.piece);
     logits_of(std::min(p.piece, vocab));
@@ -522,7 +526,13 @@ LossPlan loss_plan(int64_t rows, int64_t dim, int64_t vocab, int32_t dtype, bool
     const int segs = p.planes == 1 ? p.g_planes : 6;
     const MmSize sizes[2] = {{dim, rows, segs * ((p.piece + 63) / 64), true},
                              {dim, p.piece, segs * ((rows + 63) / 64), true}};
-    p.both = plan_products(sizes, 2);
+    if (p.thin) {
+      p.both = plan_products(sizes + 1, 1);
+      p.both.splits[1] = p.both.splits[0];
+      p.both.splits[0] = thin_splits(dim, rows, vocab, 1);
+    } else {
+      p.both = plan_products(sizes, 2);
+    }
     // (dX is summed up over pieces and has its rows to be placed: always in parts)
     p.dx = at.take<float>(p.both.splits[0] * rows * round_up(dim, 4));
     if (p.both.splits[1] > 1) p.dw = at.take<float>(p.both.splits[1] * p.piece * round_up(dim, 4));
@@ -567,7 +577,15 @@ MmArgs logits(const LossPlan& p, const void* W, int64_t rows, int64_t dim, int64
 }
 
 // Their sums of splits, for a launch of its own.
-hipError_t logit_sums(const LossPlan& p, MmArgs& m, hipStream_t s) {
+template <typename A>
+hipError_t logit_sums(const LossPlan& p, MmArgs& m, const A& a, hipStream_t s) {
+  if (p.thin) {
+    // (rows past the count hold whatever there was, and nothing reads their sums)
+    const ThinArgs t{{(const float*)a.W, nullptr}, {p.x, nullptr}, {p.sums, nullptr}, a.dim,
+                     p.dim_ld, a.rows * p.dim_ld, (int)a.vocab, (int)a.rows, (int)a.dim, p.splits,
+                     1, a.vocab * a.dim * 4 > kCacheBytes};
+    return launch_thin<false>(t, s);
+  }
   EpiStore::Args e{};
   e.out[0] = sums_out(p.sums, m.job[0].m, m.job[0].n);
   return run_mm<false, false, false, EpiStore>(m, e, p.wide, s);
@@ -579,8 +597,8 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
   MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, v0, cols);
   const char* w = m.job[0].a;
   const int64_t ldw = m.job[0].lda;
-  if (p.splits > 1) {
-    SM_TRY(logit_sums(p, m, s));
+  if (p.thin || p.splits > 1) {
+    SM_TRY(logit_sums(p, m, a, s));
     const int64_t work = a.rows * (round_up(cols, 8) / 4);
     hipLaunchKernelGGL((k_loss_mid_grad<P>),
                        dim3((unsigned)std::min<int64_t>((work + 255) / 256, 1 << 16)), dim3(256), 0,
@@ -592,7 +610,12 @@ hipError_t loss_grad_piece(const LossPlan& p, const LossGradArgs& a, int64_t v0,
     SM_TRY((run_mm<false, false, false, EpiGrad<P>>(m, eg, p.wide, s)));
   }
   MmStores out;
-  if (a.dX) {
+  if (a.dX && p.thin) {
+    const ThinArgs t{{(const float*)a.W, nullptr}, {p.g, nullptr}, {p.dx, nullptr}, a.dim, p.g_ld,
+                     plane, (int)a.dim, (int)a.rows, (int)a.vocab, p.both.splits[0], 1,
+                     a.vocab * a.dim * 4 > kCacheBytes};
+    SM_TRY(launch_thin<true>(t, s));
+  } else if (a.dX) {
     MmJob j{};
     j.n_rows = p.count;
     j.a = w;
@@ -662,18 +685,17 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
   if (hipError_t e = gather(p, a, s); e != hipSuccess) return e;
   MmArgs m = logits(p, a.W, a.rows, a.dim, a.vocab, 0, a.vocab);
   float* loss = a.reduction == SM_LOSS_ROWS ? a.loss : p.loss;
-  if (p.splits > 1) {
-    SM_TRY(logit_sums(p, m, s));
-    const int per = a.vocab <= kWaveRow ? 4 : 1;
-    hipLaunchKernelGGL(k_loss_mid, dim3((unsigned)((a.rows + per - 1) / per)), dim3(256), 0, s,
-                       p.sums, p.splits, p.count, (int)a.rows, (int)a.vocab, p.list, p.target,
-                       loss, a.lse);
+  const EpiLse::Args e{p.part, a.rows, p.target, p.picked};
+  if (p.thin || p.splits > 1) {
+    SM_TRY(logit_sums(p, m, a, s));
+    hipLaunchKernelGGL(k_loss_mid, dim3((unsigned)((a.rows * p.strips + 3) / 4)), dim3(256), 0, s,
+                       p.sums, p.splits, p.count, (int)a.rows, (int)a.vocab, (int)p.strips, e);
+    SM_TRY(hipGetLastError());
   } else {
-    SM_TRY((run_mm<false, false, false, EpiLse>(m, {p.part, a.rows, p.target, p.picked}, p.wide,
-                                                s)));
-    hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, p.part,
-                       a.rows, (int)p.strips, p.count, p.list, p.target, p.picked, loss, a.lse);
+    SM_TRY((run_mm<false, false, false, EpiLse>(m, e, p.wide, s)));
   }
+  hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.rows + 15) / 16)), dim3(1024), 0, s, p.part,
+                     a.rows, (int)p.strips, p.count, p.list, p.target, p.picked, loss, a.lse);
   SM_TRY(hipGetLastError());
   hipLaunchKernelGGL(k_loss_sum, dim3(1), dim3(1024), 0, s, p.pos, (int)a.rows, p.count, loss,
                      a.lse, a.reduction == SM_LOSS_ROWS ? nullptr : a.loss,

@@ -138,8 +138,8 @@ __device__ __forceinline__ u32x2_t mm_read_tr16(const char* __restrict__ p) {
 // k-major.  PAIR: A's rows alternate in groups of 16 between a and a2 (a tile has
 // TM / 2 features of each).
 template <bool AKM, bool BKM, bool PAIR, class Sh, class Epi>
-__device__ __forceinline__ void mm_tile(const MmArgs& args, const typename Epi::Args& ea, char* smem,
-                                        int ji, int at) {
+__device__ __forceinline__ void mm_tile(const MmArgs& args, const typename Epi::Args& ea,
+                                        char* smem, int ji, int at) {
   constexpr int TM = Sh::TM, TN = Sh::TN, TI = Sh::TI, TJ = Sh::TJ;
   constexpr int QA = Sh::A_BYTES / 1024 / Sh::WAVES, QB = Sh::B_BYTES / 1024 / Sh::WAVES;
   static_assert(!PAIR || (!AKM && QA % 4 == 0), "paired rows");

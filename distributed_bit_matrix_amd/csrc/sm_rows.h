@@ -16,6 +16,7 @@ __device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 // the vector types below carry the element's alignment and rows of every
 // length move in 16-byte pieces.
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 

@@ -85,6 +85,17 @@ def test_small_tables(rows, dim, vocab, dtype):
         check(x, w, t, reduction)
 
 
+# float32 rows that are few for their weights: the weights are read as they lie
+@pytest.mark.parametrize("rows,dim,vocab", [(3, 1030, 2500), (17, 520, 5001), (33, 2049, 1027),
+                                            (100, 1031, 2049), (128, 64, 40000), (129, 1029, 16800),
+                                            (300, 4099, 4100), (512, 260, 66000)])
+def test_few_rows_for_a_large_table(rows, dim, vocab):
+    print(f"loss {rows}x{dim}x{vocab}", flush=True)
+    reduction = ("mean", "sum", "none")[rows % 3]
+    x, w, t = inputs(rows, dim, vocab, "f32", rows, 0.3)
+    check(x, w, t, reduction)
+
+
 def test_a_small_table_with_rows_and_targets_that_do_not_count():
     """Where the sums are split: padding of NaN reaches nothing, a target outside the table
     has NaN for its row alone, and every row may be ignored."""

@@ -73,6 +73,20 @@ def test_shapes(rows, dim, hidden, dtype):
     check_backward(dy, x, wg, wu, wd, pre, kind, DT["f32"] if hidden % 2 else DT[dtype])
 
 
+# float32 rows that are few for their weights: the weights are read as they lie
+@pytest.mark.parametrize("rows,dim,hidden", [(1, 700, 1100), (17, 515, 1400), (33, 1030, 700),
+                                             (64, 64, 11000), (100, 1027, 1029), (128, 4100, 180),
+                                             (129, 2050, 2800), (257, 1300, 4400),
+                                             (512, 5700, 1000)])
+def test_few_rows_for_large_weights(rows, dim, hidden):
+    print(f"mlp {rows}x{dim}x{hidden}", flush=True)
+    kind = "gelu" if rows % 2 else "silu"
+    x, wg, wu, wd = inputs(rows, dim, hidden, "f32", rows * 31 + dim)
+    _, pre = check_forward(x, wg, wu, wd, kind)
+    dy = normal(rows + 5, rows, dim)
+    check_backward(dy, x, wg, wu, wd, pre, kind, DT["f32"])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows", [6, 70])
 @pytest.mark.parametrize("dim,hidden", [(64, 128), (65, 127)])
