@@ -124,7 +124,10 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[j][k] = x[j][k] * rs * (gamma ? g[j][k] : 1.f);
+      for (int k = 0; k < V; ++k) {
+        if constexpr (!CODES) x[j][k] *= rs;
+        if (gamma) x[j][k] *= g[j][k];
+      }
     if constexpr (!CODES) {
       T* Y = (T*)a.Y + r * cols;
 #pragma unroll
@@ -133,7 +136,11 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
         else store_own<V>(Y + last.c, last.skip, x[j]);
       }
     } else {
-      // a block of 128 columns is a piece of W lanes; shorter groups have one
+      // A code is of Y / scale, where rstd cancels: h gamma (448 / max |h gamma|) has
+      // two roundings less than by way of Y, each of which can move a value across the
+      // middle between two codes.  Where that leaves float32's range, or the scale is
+      // the least, by way of Y.
+      // A block of 128 columns is a piece of W lanes; shorter groups have one.
       constexpr int W = 128 / V < LANES ? 128 / V : LANES;
       uint8_t* Y = (uint8_t*)a.Y + r * cols;
       float most[NV];
@@ -156,9 +163,11 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (a.block) most[j] = lanes_max<W>(most[j]);
-        const float scale = fmaxf(most[j] / kE4m3Max, kLeastScale), inv = 1.0f / scale;
+        const float scale = fmaxf(most[j] * rs / kE4m3Max, kLeastScale);
+        const bool direct = scale > kLeastScale && most[j] > 1e-30f && most[j] < INFINITY;
+        const float first = direct ? 1.f : rs, inv = direct ? kE4m3Max / most[j] : 1.f / scale;
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] *= inv;
+        for (int k = 0; k < V; ++k) x[j][k] = x[j][k] * first * inv;
         const int at = (j * LANES + lane) * V;
         if (at < cols && (a.block ? at % 128 == 0 : at == 0))
           a.scales[r * blocks + (a.block ? at / 128 : 0)] = scale;

@@ -207,14 +207,15 @@ __global__ __launch_bounds__(512) void k_thin(ThinArgs a) {
 // tiles and here, forward: 2^20 values (1024 x 1000) 128 rows 34, 40; 2^22 (768 x 2048,
 // three) 128 rows 56, 51, 384 rows 67, 70; 2^25 (768 x 50257) 17 rows 179, 52, 512
 // rows 318, 282; 2^28 (2436 x 126047) 17 rows 1350, 353, 512 rows 2222, 1946.
-// Backward it is the form of the products with the weights, from one row on: 2^25
-// values 17 rows 452, 172, 128 rows 482, 293; 2^28 17 rows 2436, 1068, 128 rows 2871,
-// 1615; 2^22 17 rows 59, 62, 128 rows 61, 89.
+// Backward it is the form of the products with the weights, from one row on: 2^22
+// values 1 row 59, 47, 64 rows 60, 60, 128 rows 61, 76; 2^23 (1000 x 10007) 64 rows 105,
+// 103, 128 rows 112, 134; 2^25 17 rows 452, 172, 128 rows 482, 293; 2^28 17 rows 2436,
+// 1068, 128 rows 2871, 1615.
 inline bool thin_form(int64_t rows, int64_t m, int64_t k, int mats, int32_t dtype,
                       bool backward) {
   const int64_t values = mats * m * k;
   if (dtype != SM_F32 || m < 2 || k < 2) return false;
-  if (backward) return rows <= 128 && values >= 1 << 24;
+  if (backward) return rows <= 128 && values >= (rows <= 64 ? 1 << 22 : 1 << 24);
   return rows > 16 && rows <= 512 && values >= (rows <= 128 ? 1 << 21 : 1 << 24);
 }
 // How many blocks share a tile's k: two blocks a CU, each with two steps at least, and

@@ -169,7 +169,10 @@ sm_status signmuon_rms_norm_backward(
  * all of `dtype`.  Row r of X starts at element r * x_stride (x_stride >= dim).
  * pre: float32[rows x 2 hidden], gate and then up of a row, for the backward pass,
  * or NULL.  0 <= rows <= 2^22, 1 <= dim, hidden <= 2^16.  rows = 0 is a no-op.
- * What lies between the products is rounded to `dtype` once.
+ * What lies between the products is rounded to `dtype` once; in bfloat16, where
+ * rows times the lesser of dim and hidden is below 4096, to a sum of two values.
+ * Products of float32 are sums of products of bfloat16 parts, with float32's
+ * precision; an infinity among their operands makes NaN of what depends on it.
  * ws: signmuon_gated_mlp_workspace() bytes (backward = 1 for the backward call),
  * 256-byte aligned; NULL where that is 0.  Its contents on entry do not matter.
  * The query returns SIZE_MAX for arguments outside the limits.
@@ -234,7 +237,9 @@ sm_status signmuon_linear_cross_entropy(
  *   G[r,v] = (exp(Z[r,v] - lse[r]) - [v = t]) * dloss (/ rows that count),
  *   dX = G W,  dW = G^T X.
  * The logits are computed again, a piece of the vocabulary after the other; a
- * piece of G is held in the workspace, rounded to `dtype`.  lse is what the
+ * piece of G is held in the workspace, rounded to `dtype`; in bfloat16, where
+ * rows are at most 128 or rows times dim at most 2^16, to a sum of two values.
+ * A factor that all rows share multiplies the results instead.  lse is what the
  * forward pass wrote.  dX: contiguous rows x dim of `dtype`, zeros in ignored
  * rows; it may be X itself if X is contiguous.  dW: contiguous vocab x dim of
  * dw_dtype; accumulate = 1 adds to what is there (float32 only).  Either may
