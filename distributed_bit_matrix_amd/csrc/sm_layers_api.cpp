@@ -135,8 +135,10 @@ static sm_status rms_call(const void* X, int64_t x_stride, const void* R, int64_
   if (rows == 0) return SM_OK;
   if (!X || !Y || !stride_ok(x_stride, rows, cols)) return SM_EINVAL;
   if (R && (!H || !stride_ok(r_stride, rows, cols))) return SM_EINVAL;
-  if (codes && (!scales || Y == X)) return SM_EINVAL;
+  if (codes && (!scales || Y == X || scales == Y || scales == X || scales == rstd))
+    return SM_EINVAL;
   if (Y == X && x_stride != cols) return SM_EINVAL;
+  if (rstd && (rstd == X || rstd == Y || rstd == R || (R && rstd == H))) return SM_EINVAL;
   if (R && (Y == R || Y == H || (H == X && x_stride != cols) || (H == R && r_stride != cols)))
     return SM_EINVAL;
   if (!aligned(X, x_dtype) || !aligned(R, x_dtype) || !aligned(gamma, w_dtype) ||
@@ -213,7 +215,9 @@ sm_status signmuon_gated_mlp(const void* X, int64_t x_stride, const void* Wg, co
     return SM_EINVAL;
   if (rows == 0) return SM_OK;
   if (!X || !Wg || !Wu || !Wd || !Y || !stride_ok(x_stride, rows, dim)) return SM_EINVAL;
-  if (Y == X || Y == Wg || Y == Wu || Y == Wd) return SM_EINVAL;
+  for (const void* in : {X, Wg, Wu, Wd})
+    if (Y == in || pre == in) return SM_EINVAL;
+  if (pre == Y) return SM_EINVAL;
   if (!aligned(X, dtype) || !aligned(Wg, dtype) || !aligned(Wu, dtype) || !aligned(Wd, dtype) ||
       !aligned(Y, dtype) || !aligned(pre, SM_F32))
     return SM_EINVAL;
@@ -280,6 +284,9 @@ sm_status signmuon_linear_cross_entropy(const void* X, int64_t x_stride, const v
   if (!loss || !aligned(loss, SM_F32)) return SM_EINVAL;
   if (rows > 0) {
     if (!X || !W || !targets || !lse || !stride_ok(x_stride, rows, dim)) return SM_EINVAL;
+    if (loss == lse) return SM_EINVAL;
+    for (const void* out : {loss, lse})
+      if (out == X || out == W || out == targets) return SM_EINVAL;
     if (!aligned(X, dtype) || !aligned(W, dtype) || !aligned(lse, SM_F32) ||
         (uintptr_t)targets % (target_bits / 8))
       return SM_EINVAL;

@@ -82,7 +82,7 @@ __device__ __forceinline__ void join_rows(const JoinArgs& a, int block, int bloc
         for (int q = 0; q < 4; ++q) v[q] += t[q];
       }
     }
-    if (a.by) {
+    if (a.by && at >= 0) {       // (a factor that is not finite leaves zeros alone)
       const float by = *a.by;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] *= by;

@@ -55,6 +55,19 @@ def _rms_grad(dY=P, dys=8, H=Q, hs=8, dH=None, dhs=8, xd=0, g=None, wd=0, r=S, r
 
 
 @built
+def test_one_array_for_two_outputs_is_refused():
+    for bad in (dict(r=P), dict(r=Q), dict(r=T, R_=T, H=S), dict(r=S, R_=T, H=S)):
+        assert _rms(**bad) == _rms8(**{"sc": U, **bad}) == B.SM_EINVAL, bad
+    for bad in (dict(sc=Q), dict(sc=P), dict(sc=T, r=T)):
+        assert _rms8(**bad) == B.SM_EINVAL, bad
+    for same in (P, Q, S, T, U):
+        assert _mlp(pre=same) == B.SM_EINVAL
+    for bad in (dict(loss=U), dict(loss=P), dict(loss=Q), dict(loss=S), dict(lse=P), dict(lse=Q),
+                dict(lse=S)):
+        assert _loss(**bad) == B.SM_EINVAL, bad
+
+
+@built
 def test_rms_grad_refusals():
     assert _rms_grad(dX=None, dg=None) == B.SM_OK            # nothing is wanted
     for bad in (dict(xd=3), dict(wd=9), dict(dwd=2), dict(rows=-1), dict(cols=0), dict(acc=2),

@@ -134,6 +134,19 @@ def test_a_factor_of_all_rows_is_not_rounded(rows, dim, vocab):
         within(got, dw.double() * c.double(), 2 * R.U32 * (dw.double() * c.double()).abs(), "dw")
 
 
+@pytest.mark.parametrize("rows,dim,vocab", [(9, 64, 200), (300, 96, 300), (40, 1200, 60),
+                                            (40, 260, 70000)])
+@pytest.mark.parametrize("factor", [float("inf"), float("nan")])
+def test_ignored_rows_have_zero_gradients_whatever_the_factor(rows, dim, vocab, factor):
+    x, w, t = inputs(rows, dim, vocab, "f32", 3, 0.4)
+    drop = t == IGNORE
+    assert drop.any() and not drop.all()
+    _, lse = B.linear_cross_entropy(x, w, t, IGNORE, "mean", want_lse=True)
+    dx, _ = B.linear_cross_entropy_backward(torch.tensor(factor, device="cuda"), x, w, t, lse,
+                                            IGNORE, "mean")
+    assert (dx[drop] == 0).all() and not dx[~drop].isfinite().any()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_rows_around_the_form_for_few(dtype):
     """15, 16 and 17 rows, with padding among them, every reduction."""
