@@ -16,6 +16,9 @@
 // bits; the product is the sum over the six pairs of planes that reach float32's
 // precision ("segments" of one long k).  That runs at a sixth of the bfloat16
 // rate, which is above what the float32 matrix instructions reach.
+//
+// Bound by the chip's power: 4096 x 4096 x 16384 463 us (1190 TFLOP/s); 16384 x 8192 x
+// 768 of uniform values 193 us, of zeros 144.
 #pragma once
 
 #include <algorithm>

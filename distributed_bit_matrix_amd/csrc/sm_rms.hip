@@ -1,7 +1,10 @@
 // Root-mean-square norm of a residual stream (signmuon_layers.h), forward and
 // backward, with an 8-bit output too.  Rows live in registers as in the layer
 // norm (sm_norm_rows.h), so each array is read or written once; every sum has an
-// order that the sizes alone decide.  Both passes are bound by HBM.
+// order that the sizes alone decide.  Both passes are bound by HBM: 16384 x 4096
+// bfloat16 with a residual to 8 bits 84 us (470 MB, 5.6 TB/s), its backward pass 96
+// (537 MB, 5.6 TB/s) and 5 for the blocks' sums; 12288 x 768 15 and 4, by a block's
+// start and end; one row of 4096 3.3.
 #include "sm_layers.h"
 #include "sm_norm_rows.h"
 
@@ -136,10 +139,11 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
         else store_own<V>(Y + last.c, last.skip, x[j]);
       }
     } else {
-      // A code is of Y / scale, where rstd cancels: h gamma (448 / max |h gamma|) has
-      // two roundings less than by way of Y, each of which can move a value across the
-      // middle between two codes.  Where that leaves float32's range, or the scale is
-      // the least, by way of Y.
+      // A code is of Y / scale, where rstd cancels: 448 h gamma / max |h gamma|, divided
+      // with a correction, has the division's rounding and that of h gamma, which is
+      // exact of bfloat16; each rounding can move a value across the middle between two
+      // codes (by way of Y there are five).  Where this leaves float32's range, or the
+      // scale is the least, by way of Y.
       // A block of 128 columns is a piece of W lanes; shorter groups have one.
       constexpr int W = 128 / V < LANES ? 128 / V : LANES;
       uint8_t* Y = (uint8_t*)a.Y + r * cols;
@@ -164,10 +168,13 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
       for (int j = 0; j < NV; ++j) {
         if (a.block) most[j] = lanes_max<W>(most[j]);
         const float scale = fmaxf(most[j] * rs / kE4m3Max, kLeastScale);
-        const bool direct = scale > kLeastScale && most[j] > 1e-30f && most[j] < INFINITY;
-        const float first = direct ? 1.f : rs, inv = direct ? kE4m3Max / most[j] : 1.f / scale;
+        const bool direct = scale > kLeastScale && most[j] > 1e-30f && most[j] < 1e30f;
+        const float first = direct ? kE4m3Max : rs, by = direct ? most[j] : scale, inv = 1.f / by;
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[j][k] = x[j][k] * first * inv;
+        for (int k = 0; k < V; ++k) {
+          const float u = x[j][k] * first, q = u * inv;
+          x[j][k] = direct ? __builtin_fmaf(__builtin_fmaf(-q, by, u), inv, q) : q;
+        }
         const int at = (j * LANES + lane) * V;
         if (at < cols && (a.block ? at % 128 == 0 : at == 0))
           a.scales[r * blocks + (a.block ? at / 128 : 0)] = scale;

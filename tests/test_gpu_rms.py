@@ -42,6 +42,21 @@ def check_codes(q, scales, y, e_y, block):
     within(q.float(), v, bound, "codes")
 
 
+@pytest.mark.parametrize("block", [128, None])
+@pytest.mark.parametrize("x_std,w_std", [(1e-18, 1e-14), (1e-18, 1e-25), (1e-3, 1e-36), (1e3, 1e28),
+                                         (1e15, 1e18), (1e15, 1e-33), (1.0, 1e-38)])
+def test_codes_over_float32s_range(x_std, w_std, block):
+    """Products of a row and the weights past what the codes' shorter way takes, and scales
+    at their least."""
+    x = normal(5, 40, 300) * x_std
+    w = normal(6, 300) * w_std
+    q, scales = B.rms_norm_e4m3(x, w, None, EPS, block)
+    want, _ = R.rms(x, w, EPS)
+    e_y, _ = R.rms_bounds(x, w, EPS)
+    # (values below float32's normal range may be flushed: to nothing beside the least scale)
+    check_codes(q, scales, want, e_y + 2.0 ** -126, block)
+
+
 # every boundary of the kernels' row widths, odd ones, one column and many
 SHAPES = [(1, 1), (3, 1), (5, 2), (7, 3), (257, 4), (33, 7), (65, 8), (64, 9), (100, 31),
           (9, 32), (130, 33), (77, 63), (41, 64), (19, 65), (50, 127), (23, 128), (31, 255),
