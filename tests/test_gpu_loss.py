@@ -96,6 +96,21 @@ def test_few_rows_for_a_large_table(rows, dim, vocab):
     check(x, w, t, reduction)
 
 
+@pytest.mark.parametrize("rows,dim,vocab", [(40, 1033, 4500), (20, 1200, 61)])
+def test_strides_and_alignment_beside_large_and_small_tables(rows, dim, vocab):
+    x, w, t = inputs(rows, dim, vocab, "f32", 6, 0.2)
+    gaps = torch.zeros(rows, dim + 7, device="cuda")[:, 3:3 + dim]
+    gaps.copy_(x)
+    w2 = torch.zeros(vocab * dim + 1, device="cuda")[1:].view(vocab, dim)
+    w2.copy_(w)
+    one = torch.ones((), device="cuda")
+    out = []
+    for xs, ws in ((x, w), (gaps, w2)):
+        loss, lse = B.linear_cross_entropy(xs, ws, t, want_lse=True)
+        out.append((loss, lse, *B.linear_cross_entropy_backward(one, xs, ws, t, lse)))
+    assert all(torch.equal(bits(p), bits(q)) for p, q in zip(*out))
+
+
 def test_a_small_table_with_rows_and_targets_that_do_not_count():
     """Where the sums are split: padding of NaN reaches nothing, a target outside the table
     has NaN for its row alone, and every row may be ignored."""
@@ -328,11 +343,14 @@ def test_pieces_of_the_vocabulary(dtype):
     assert (dw.double() - want)[empty].abs().max() <= int(keep.sum()) * 2.0 ** -18
 
 
-def test_streams_and_graphs():
-    """Two calls at once on streams of their own, and a graph replayed between eager
+@pytest.mark.parametrize("shapes", [((300, 64, 1000, "bf16"), (40, 128, 777, "f32"),
+                                     (8, 128, 777, "bf16")),
+                                    ((40, 1200, 60, "bf16"), (40, 1033, 4500, "f32"),
+                                     (150, 515, 33000, "f32"))])
+def test_streams_and_graphs(shapes):
+    """Calls at once on streams of their own, and a graph replayed between eager
     calls with other inputs: the same bits each time."""
-    cases = [inputs(300, 64, 1000, "bf16", 11, 0.2), inputs(40, 128, 777, "f32", 12, 0.2),
-             inputs(8, 128, 777, "bf16", 13)]
+    cases = [inputs(*s, 11 + i, 0.2 if s[0] > 8 else 0.0) for i, s in enumerate(shapes)]
 
     def both(x, w, t):
         loss, lse = B.linear_cross_entropy(x, w, t, want_lse=True)

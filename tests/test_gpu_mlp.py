@@ -205,12 +205,14 @@ def test_sums_that_are_exact(dtype):
         assert torch.equal(dx.double(), (dg @ wg.double() + du @ wu.double()).to(DT[dtype]).double())
 
 
-def test_streams_and_graphs():
+@pytest.mark.parametrize("shapes", [((300, 64, 256, "bf16"), (5, 128, 512, "bf16"),
+                                     (70, 65, 90, "f32")),
+                                    ((40, 1030, 1500, "f32"), (3, 64, 33, "bf16"),
+                                     (20, 40, 90, "bf16"))])
+def test_streams_and_graphs(shapes):
     """Calls at once on streams of their own, and a graph replayed between eager calls
     with other inputs."""
-    cases = [(*inputs(r, d, h, dt, r), normal(7, r, d, dtype=dt))
-             for r, d, h, dt in ((300, 64, 256, "bf16"), (5, 128, 512, "bf16"),
-                                 (70, 65, 90, "f32"))]
+    cases = [(*inputs(r, d, h, dt, r), normal(7, r, d, dtype=dt)) for r, d, h, dt in shapes]
 
     def both(x, wg, wu, wd, dy):
         y, pre = B.gated_mlp(x, wg, wu, wd, "gelu", want_pre=True)
