@@ -21,8 +21,8 @@
 // that all rows share would be rounded alike in all of them: it is left out of G
 // and multiplies the results.
 //
-// 11059 of 12288 rows against 50257 x 768 bfloat16: the logits' launch 853 to 920 us
-// (1000 TFLOP/s; a tile has 12 slabs, and its first loads and epilogue, with nothing
+// 11059 of 12288 rows against 50257 x 768 bfloat16: the logits' launch 903 us (950
+// TFLOP/s; a tile has 12 slabs, and its first loads and epilogue, with nothing
 // beside them in a CU that holds one block, are a third of it); backward 2 pieces,
 // 480 us each for the logits and G, 800 for the two products (1070 TFLOP/s).
 #include <cmath>
