@@ -133,6 +133,22 @@ def test_a_small_table_with_rows_and_targets_that_do_not_count():
     assert loss == 0 and (lse == 0).all() and (dx == 0).all() and (dw == 0).all()
 
 
+@pytest.mark.parametrize("rows,dim,vocab", [(5, 300, 4000), (20, 1200, 60), (128, 700, 900),
+                                            (1500, 40, 300)])
+def test_few_results_keep_two_values_of_g(rows, dim, vocab):
+    """G as a sum of two bfloat16 is off by 2^-18 of an entry at most, its softmax by the
+    logits' float32 errors, under 2^-17 here (lse included, |z| < 16, sums of dim terms of
+    2^-24 each that average): as a whole under 2^-13, where one bfloat16 leaves about 2^-9."""
+    x, w, t = inputs(rows, dim, vocab, "bf16", 21)
+    _, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    dloss = 1 + 0.3 * torch.randn(rows, device="cuda", generator=gen)
+    _, dw = B.linear_cross_entropy_backward(dloss, x, w, t, lse, IGNORE, "none", want_x=False,
+                                            dtype=torch.float32)
+    _, want = R.loss_grad(dloss, x, w, t, lse, IGNORE, "none")
+    assert (dw.double() - want).norm() < 2.0 ** -13 * want.norm()
+
+
 @pytest.mark.parametrize("rows,dim,vocab", [(2000, 96, 300), (20, 1200, 60)])
 def test_a_factor_of_all_rows_is_not_rounded(rows, dim, vocab):
     """The gradients are the factor times those of the factor 1, though a bfloat16 holds it

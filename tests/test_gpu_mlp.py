@@ -205,6 +205,19 @@ def test_sums_that_are_exact(dtype):
         assert torch.equal(dx.double(), (dg @ wg.double() + du @ wu.double()).to(DT[dtype]).double())
 
 
+@pytest.mark.parametrize("rows,dim,hidden", [(3, 200, 900), (16, 65, 700), (40, 90, 1000),
+                                             (20, 2000, 90)])
+def test_few_results_keep_two_values_between_the_products(rows, dim, hidden):
+    """h as a sum of two bfloat16 is off by 2^-18 of a value at most, and its float32 sums
+    by less: y is its own rounding, half a step, and 2^-15 of its terms' sizes."""
+    x, wg, wu, wd = inputs(rows, dim, hidden, "bf16", 23)
+    y, pre = B.gated_mlp(x, wg, wu, wd, want_pre=True)
+    g, u = pre.double().chunk(2, 1)
+    h = g / (1 + torch.exp(-g)) * u
+    want, sizes = h @ wd.double().T, h.abs() @ wd.double().abs().T
+    within(y, want, torch.finfo(torch.bfloat16).eps / 2 * want.abs() + 2.0 ** -15 * sizes, "y")
+
+
 @pytest.mark.parametrize("shapes", [((300, 64, 256, "bf16"), (5, 128, 512, "bf16"),
                                      (70, 65, 90, "f32")),
                                     ((40, 1030, 1500, "f32"), (3, 64, 33, "bf16"),
