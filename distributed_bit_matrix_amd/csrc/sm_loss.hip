@@ -100,15 +100,16 @@ struct EpiLse {
           if (WHOLE || mc + 16 * i + k < at.m) mx = fmaxf(mx, acc[i][j][k]);
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      // exp(v - ref) as one multiply-add and a power: what the rounding of ref
-      // log2(e) adds is the same for all terms, and below lse's own rounding
-      const float ref = mx == -INFINITY ? 0.f : -mx * kLog2e;
+      // The largest logit's own term is 1 to the last bit: where the target has it the
+      // loss is the logarithm of the sum alone, and a rounding of mx log2(e) (one
+      // multiply-add a logit) would be all of it, of either sign.
+      const float ref = mx == -INFINITY ? 0.f : mx;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], kLog2e, ref));
+          const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - ref) * kLog2e);
           s += WHOLE || mc + 16 * i + k < at.m ? p : 0.f;
         }
       s += __shfl_xor(s, 16);

@@ -80,6 +80,28 @@ def loss_bounds(x, w, targets, ignore):
     return torch.where(keep, e_each, zero) + TINY, torch.where(keep, e_lse, zero) + TINY
 
 
+def likely_loss(x, w, targets):
+    """(loss, its bound) of rows whose target's logit is among the largest, where the loss,
+    log(1 + s) of the others' sum s, is far smaller than the logits that it comes from.  A
+    term of s is off by its two logits' errors, three roundings of their distance and 4 u of
+    the power; the sum by one rounding of at most 1 + s for each of 32 terms and 2 steps over
+    lanes, two for each strip that a lane joins (or, of few rows, for each group of 16 that a
+    wave has: at most vocab / 1024 + 4), and 6 more steps over lanes; 6 for the target's
+    own power, the logarithm and the sum."""
+    dtype = x.dtype
+    x, w = x.double(), w.double()
+    dim, vocab = x.shape[1], w.shape[0]
+    z = x @ w.T
+    gap = z.gather(1, targets[:, None]) - z
+    e = product_error(dim, dtype) * (x.abs() @ w.abs().T).amax(1, keepdim=True)
+    terms = torch.exp(-gap).scatter(1, targets[:, None], 0.0)
+    s = terms.sum(1)
+    e_s = (terms * 1.1 * (2 * e + 3 * U32 * gap.abs() + 4 * U32)).sum(1)
+    n = 32 + 2 + 2 * (vocab / 1024 + 4) + 6 + 6
+    want = torch.log1p(s)
+    return want, e_s / (1 + s) + n * U32 * (1 + want)
+
+
 def reduce_loss(each, targets, ignore, reduction):
     if reduction == "none":
         return each

@@ -243,6 +243,30 @@ def test_loss_bounds_take_float32_and_no_mistake(dtype):
     assert not inside(torch.logsumexp(z, 1) - picked, each, e_each)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_likely_loss_takes_float32_and_no_errors_of_the_logits_size(dtype):
+    g = gen(3)
+    w = normal(g, 300, 64)
+    w[:, 0] = 1.0
+    w = w.to(dtype)
+    t = torch.randint(300, (200,), generator=g)
+    x = (0.3 * w[t].float()).to(dtype)
+    x[:, 0] = torch.linspace(-1000, 1000, 200)
+    want, bound = R.likely_loss(x, w, t)
+    z = x.float() @ w.float().T
+    top, at = z.amax(1, keepdim=True), z.gather(1, t[:, None])
+    log2e = torch.tensor(1.4426950408889634)
+
+    def evaluate(power):
+        return ((top - at)[:, 0] + torch.log(torch.exp2(power).sum(1)))
+
+    got = evaluate((z - top) * log2e)
+    assert inside(got, want, bound) and (got >= 0).all()
+    # the largest logit's product with log2(e) rounded, and the difference from it exact
+    got = evaluate((z.double() * log2e.double() - (top * log2e).double()).float())
+    assert not inside(got, want, bound) and (got < 0).any()
+
+
 @pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_loss_grad_bounds_take_float32_and_no_mistake(dtype, reduction):

@@ -429,3 +429,62 @@ def test_offsets_past_32_bits():
     for v in (0, 1, vocab // 2 + 77, vocab - 1):
         row = g[:, v] @ x.float().contiguous()
         assert (dw[v].float() - row).norm() <= 2.0 ** -7 * row.norm() + 1e-6
+
+
+def confident(rows, dim, vocab, dtype, factor, tops, seed):
+    """Rows whose target's logit is the largest: activations along the target's weights, times
+    factor, and a first column that moves all of a row's logits, so that the target's is near
+    tops[row] (None: as it comes).  (x, w, t, logits in 64 bits, the others' distances below
+    the target's)."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    w = torch.randn(vocab, dim, device="cuda", generator=gen)
+    w[:, 0] = 1.0
+    w = w.to(DT[dtype])
+    t = torch.randint(vocab, (rows,), device="cuda", generator=gen)
+    x = (factor * w[t].double()).to(DT[dtype])
+    if tops is not None:
+        x[:, 0] = 0.0
+        x[:, 0] = (tops - (x.double() * w[t].double()).sum(1)).to(DT[dtype])
+    z = x.double() @ w.double().T
+    rest = torch.ones_like(z, dtype=torch.bool)
+    rest[torch.arange(rows, device="cuda"), t] = False
+    gap = (z.gather(1, t[:, None]) - z)[rest].view(rows, vocab - 1)
+    return x, w, t, z, gap
+
+
+# every form of the statistics: few rows; tiles of either size; split sums; float32 weights
+# as they lie
+FORMS = [(12, 64, 300, "f32"), (12, 64, 300, "bf16"), (300, 64, 1000, "f32"),
+         (300, 64, 1000, "bf16"), (2500, 64, 5000, "f32"), (2500, 64, 5000, "bf16"),
+         (40, 1203, 91, "f32"), (40, 1203, 91, "bf16"), (128, 64, 40000, "f32")]
+
+
+@pytest.mark.parametrize("rows,dim,vocab,dtype", FORMS)
+def test_a_certain_target_has_no_loss(rows, dim, vocab, dtype):
+    """Its logit leads by 40 or more, so that all other terms together are below 2^-25: 1 and
+    they are 1, whose logarithm is 0, and the loss is 0 to the last bit in every form,
+    whatever the logits' size.  lse is the target's logit then."""
+    steps = torch.linspace(0, 1, rows, device="cuda", dtype=torch.float64)
+    sizes = 20.0 * 50.0 ** steps
+    for factor, tops in ((12.0, sizes), (12.0, -sizes), (1e3, None), (2e9, None), (1e30, None)):
+        x, w, t, z, gap = confident(rows, dim, vocab, dtype, factor, tops, rows + vocab)
+        assert gap.min() > 40 + torch.log(torch.tensor(float(vocab)))
+        loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+        assert (loss == 0).all(), (factor, loss.min().item(), loss.max().item())
+        e = R.product_error(dim, x.dtype) * (x.double().abs() @ w.double().abs().T)
+        within(lse, z.gather(1, t[:, None])[:, 0], e.gather(1, t[:, None])[:, 0] + R.TINY, "lse")
+        assert B.linear_cross_entropy(x, w, t, IGNORE, "mean") == 0
+
+
+@pytest.mark.parametrize("rows,dim,vocab,dtype", FORMS)
+def test_a_likely_target_has_a_loss_of_its_own_size(rows, dim, vocab, dtype):
+    """The target leads by little, at logits up to 1000: the loss is not negative, and off by
+    errors of its own size, never by one of the logits' (R.likely_loss)."""
+    steps = torch.linspace(0, 1, rows, device="cuda", dtype=torch.float64)
+    sizes = 20.0 * 50.0 ** steps
+    for tops in (sizes, -sizes):
+        x, w, t, _, _ = confident(rows, dim, vocab, dtype, 0.3 if dim < 100 else 0.01, tops,
+                                  rows + vocab)
+        loss = B.linear_cross_entropy(x, w, t, IGNORE, "none")
+        assert (loss >= 0).all(), loss.min().item()
+        within(loss, *R.likely_loss(x, w, t), "loss")
