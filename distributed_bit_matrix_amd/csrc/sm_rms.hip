@@ -124,11 +124,22 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
     }
     group_sums<LANES, 1>(s, turn);
     const float rs = 1.0f / sqrtf(s[0] / cols + a.eps);
+    // For codes only rstd's power of two multiplies the row, which rounds nothing: h
+    // gamma may be past float32's range, or below it, where Y is not.  What is left of
+    // rstd is 1 to 2 (or 1, where rstd is 0 or not finite).
+    float by_row = rs, left = 1.f;
+    if constexpr (CODES) {
+      if (rs > 0.f && rs < INFINITY) {
+        const uint32_t b = __float_as_uint(rs);
+        by_row = __uint_as_float(b & 0x7F800000u);
+        left = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        if constexpr (!CODES) x[j][k] *= rs;
+        x[j][k] *= by_row;
         if (gamma) x[j][k] *= g[j][k];
       }
     if constexpr (!CODES) {
@@ -142,8 +153,8 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
       // A code is of Y / scale, where rstd cancels: 448 h gamma / max |h gamma|, divided
       // with a correction, has the division's rounding and that of h gamma, which is
       // exact of bfloat16; each rounding can move a value across the middle between two
-      // codes (by way of Y there are five).  Where this leaves float32's range, or the
-      // scale is the least, by way of Y.
+      // codes (by way of Y there are five).  Where Y nears the ends of float32's range, or
+      // the scale is the least, by way of Y.
       // A block of 128 columns is a piece of W lanes; shorter groups have one.
       constexpr int W = 128 / V < LANES ? 128 / V : LANES;
       uint8_t* Y = (uint8_t*)a.Y + r * cols;
@@ -167,9 +178,9 @@ __global__ __launch_bounds__(LANES > 64 ? LANES : 256) void k_rms(RmsArgs a, boo
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (a.block) most[j] = lanes_max<W>(most[j]);
-        const float scale = fmaxf(most[j] * rs / kE4m3Max, kLeastScale);
+        const float scale = fmaxf(most[j] * left / kE4m3Max, kLeastScale);
         const bool direct = scale > kLeastScale && most[j] > 1e-30f && most[j] < 1e30f;
-        const float first = direct ? kE4m3Max : rs, by = direct ? most[j] : scale, inv = 1.f / by;
+        const float first = direct ? kE4m3Max : left, by = direct ? most[j] : scale, inv = 1.f / by;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const float u = x[j][k] * first, q = u * inv;

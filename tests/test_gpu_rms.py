@@ -286,3 +286,27 @@ def test_refusals():
         B.rms_norm(x, eps=-1.0)
     with pytest.raises(B.SignMuonError):
         B.rms_norm_e4m3(torch.zeros(1, 16385, device="cuda"))
+
+
+@pytest.mark.parametrize("block", [128, None])
+@pytest.mark.parametrize("x_std,w_std", [(1e-18, 1e-27), (1e-18, 1e-24), (1e17, 1e27), (1e17, 1e22)])
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+def test_codes_where_row_times_weights_leaves_float32(x_std, w_std, x_dtype, block):
+    """Y is an ordinary number though the products of the row as it is and the weights are
+    past float32's largest, or below its least."""
+    x = (normal(5, 40, 300).double() * x_std).to(DT[x_dtype])
+    w = (normal(6, 300).double() * w_std).float()
+    q, scales = B.rms_norm_e4m3(x, w, None, 0.0, block)
+    want, _ = R.rms(x, w, 0.0)
+    e_y, _ = R.rms_bounds(x, w, 0.0)
+    check_codes(q, scales, want, e_y, block)
+
+
+@pytest.mark.parametrize("block", [128, None])
+def test_codes_where_the_squares_sum_past_float32(block):
+    """rstd is 0 then, and so is Y, whatever the weights."""
+    x = torch.full((3, 300), 3e19, device="cuda")
+    w = torch.full((300,), 1e30, device="cuda")
+    assert (B.rms_norm(x, w, None, EPS) == 0).all()
+    q, scales = B.rms_norm_e4m3(x, w, None, EPS, block)
+    assert (q.float() == 0).all() and (scales == 2.0 ** -126).all()
