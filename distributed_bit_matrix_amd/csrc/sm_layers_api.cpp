@@ -1,6 +1,7 @@
 // C ABI of the layer operators (signmuon_layers.h): argument validation.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "sm_layers.h"
 
@@ -25,6 +26,17 @@ bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 // a row stride that memory can hold, and whose last row has a 63-bit byte offset
 bool stride_ok(int64_t stride, int64_t rows, int64_t cols) {
   return in(stride, cols, kMaxStride) && stride <= ((int64_t)1 << 60) / rows;
+}
+// whether none of `out` (null: not wanted) is one of `in`, or another of `out`
+bool apart(std::initializer_list<const void*> out, std::initializer_list<const void*> in) {
+  for (const void* const* o = out.begin(); o != out.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : in)
+      if (*o == i) return false;
+    for (const void* const* p = out.begin(); p != o; ++p)
+      if (*o == *p) return false;
+  }
+  return true;
 }
 bool workspace_ok(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && have >= need && (uintptr_t)ws % 256 == 0);
@@ -135,11 +147,12 @@ static sm_status rms_call(const void* X, int64_t x_stride, const void* R, int64_
   if (rows == 0) return SM_OK;
   if (!X || !Y || !stride_ok(x_stride, rows, cols)) return SM_EINVAL;
   if (R && (!H || !stride_ok(r_stride, rows, cols))) return SM_EINVAL;
-  if (codes && (!scales || Y == X || scales == Y || scales == X || scales == rstd))
-    return SM_EINVAL;
+  if (codes && (!scales || Y == X)) return SM_EINVAL;
   if (Y == X && x_stride != cols) return SM_EINVAL;
-  if (rstd && (rstd == X || rstd == Y || rstd == R || (R && rstd == H))) return SM_EINVAL;
-  if (R && (Y == R || Y == H || (H == X && x_stride != cols) || (H == R && r_stride != cols)))
+  if (R && ((H == X && x_stride != cols) || (H == R && r_stride != cols))) return SM_EINVAL;
+  const void* sum = R ? H : nullptr;
+  if (!apart({Y, sum, rstd, codes ? scales : nullptr}, {gamma}) ||
+      !apart({rstd, codes ? scales : nullptr}, {X, R}) || (R && Y == R))
     return SM_EINVAL;
   if (!aligned(X, x_dtype) || !aligned(R, x_dtype) || !aligned(gamma, w_dtype) ||
       !aligned(rstd, SM_F32) || !aligned(scales, SM_F32) || (R && !aligned(H, x_dtype)) ||
@@ -185,8 +198,10 @@ sm_status signmuon_rms_norm_backward(const void* dY, int64_t dy_stride, const vo
     if (!dY || !H || !rstd) return SM_EINVAL;
     if (!stride_ok(dy_stride, rows, cols) || !stride_ok(h_stride, rows, cols)) return SM_EINVAL;
     if (dH && !stride_ok(dh_stride, rows, cols)) return SM_EINVAL;
-    if (dX && (dX == H || (dX == dY && dy_stride != cols) || (dX == dH && dh_stride != cols)))
+    if (dX && ((dX == dY && dy_stride != cols) || (dX == dH && dh_stride != cols)))
       return SM_EINVAL;
+    // (one launch for few rows reads gamma and writes dgamma)
+    if (!apart({dX, dgamma}, {H, gamma, rstd}) || !apart({dgamma}, {dY, dH})) return SM_EINVAL;
     if (!aligned(dY, x_dtype) || !aligned(H, x_dtype) || !aligned(dH, x_dtype) ||
         !aligned(gamma, w_dtype) || !aligned(rstd, SM_F32) || !aligned(dX, x_dtype))
       return SM_EINVAL;
@@ -313,8 +328,8 @@ sm_status signmuon_linear_cross_entropy_backward(
   if (rows > 0) {
     if (!dloss || !X || !W || !targets || !lse || !stride_ok(x_stride, rows, dim))
       return SM_EINVAL;
-    if (dX && (dX == W || (dX == X && x_stride != dim))) return SM_EINVAL;
-    if (dW && (dW == X || dW == W)) return SM_EINVAL;
+    if (dX == X && x_stride != dim) return SM_EINVAL;
+    if (!apart({dX, dW}, {W, targets, lse, dloss}) || !apart({dW}, {X})) return SM_EINVAL;
     if (!aligned(dloss, SM_F32) || !aligned(X, dtype) || !aligned(W, dtype) ||
         !aligned(lse, SM_F32) || !aligned(dX, dtype) || (uintptr_t)targets % (target_bits / 8))
       return SM_EINVAL;

@@ -88,6 +88,25 @@ def test_rms_grad_refusals():
             B.rms_norm_backward_workspace(*args)
 
 
+@built
+def test_an_output_that_is_an_input_is_refused():
+    """But where a call says that it may be."""
+    gamma = ctypes.c_void_p(9 << 20)
+    for bad in (dict(g=Q), dict(g=S, r=S), dict(g=S, R_=T, H=S)):
+        assert _rms(**bad) == _rms8(**{"sc": U, **bad}) == B.SM_EINVAL, bad
+    for bad in (dict(g=S), dict(R_=S, H=T), dict(sc=T, R_=V, H=T)):
+        assert _rms8(**bad) == B.SM_EINVAL, bad
+    # every size: few rows go in one launch that reads all inputs and writes all outputs
+    big = dict(rows=5000, cols=8, ws=ctypes.c_void_p(11 << 20), nbytes=BIG)
+    for bad in (dict(dg=P), dict(dg=Q), dict(dg=S), dict(dg=T), dict(dg=gamma), dict(dX=S),
+                dict(dX=gamma), dict(dH=V, dg=V)):
+        assert _rms_grad(g=gamma, **bad) == B.SM_EINVAL, bad
+        assert _rms_grad(g=gamma, **big, **bad) == B.SM_EINVAL, bad
+    for bad in (P, Q, S, U, V):
+        assert _loss_grad(dW=bad) == B.SM_EINVAL, bad
+        assert bad is P or _loss_grad(dX=bad) == B.SM_EINVAL, bad
+
+
 BIG = 1 << 34
 
 
