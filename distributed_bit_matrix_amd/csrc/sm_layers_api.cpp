@@ -89,6 +89,10 @@ sm_status signmuon_layer_norm_backward(const void* dY, int64_t dy_stride, const 
   if (!aligned(dgamma, dw_dtype) || !aligned(dbeta, dw_dtype)) return SM_EINVAL;
   if (!workspace_ok(ws, ws_bytes, norm_grad_workspace(rows, cols))) return SM_EWORKSPACE;
   if (dgamma && dgamma == dbeta) return SM_EINVAL;
+  // (one launch for few rows reads gamma and the statistics and writes all results)
+  if (rows > 0 && (!apart({dX, dgamma, dbeta}, {X, gamma, mean, rstd}) ||
+                   !apart({dgamma, dbeta}, {dY})))
+    return SM_EINVAL;
   const NormGradArgs a{dY, X, dy_stride, x_stride, x_dtype, w_dtype, dw_dtype, accumulate,
                        gamma, mean, rstd, rows, cols, dX, dgamma, dbeta, ws};
   return launch_norm_grad(a, stream) == hipSuccess ? SM_OK : SM_EHIP;

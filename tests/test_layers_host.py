@@ -81,6 +81,19 @@ def _embed(W=P, wd=0, vocab=9, dim=8, t=Q, bits=64, n=5, scale=1.0, Y=S, yd=0):
 
 
 @built
+def test_a_norm_gradient_that_is_an_input_is_refused():
+    """But dX, which may be dY."""
+    gamma, dx, dg, db = (ctypes.c_void_p(k << 20) for k in (5, 6, 7, 8))
+    for rows in (4, 5000):
+        full = dict(g=gamma, rows=rows, nbytes=1 << 34)
+        for bad in (P, Q, S, gamma, dx):
+            assert _norm_grad(dX=dx, dg=bad, db=db, **full) == B.SM_EINVAL, bad
+            assert _norm_grad(dX=dx, dg=dg, db=bad, **full) == B.SM_EINVAL, bad
+        for bad in (Q, S, gamma):
+            assert _norm_grad(dX=bad, dg=dg, db=db, **full) == B.SM_EINVAL, bad
+
+
+@built
 def test_embedding_refusals():
     assert _embed(n=0, W=None, t=None, Y=None) == B.SM_OK
     for bad in (dict(wd=2), dict(yd=2), dict(bits=16), dict(n=-1), dict(n=(1 << 30) + 1), dict(vocab=0),
