@@ -99,7 +99,7 @@ struct FewX<bf16_t, float> {
     for (int i = 0; i < 4; ++i) {
       const float v0 = __uint_as_float(w[i / 2][2 * (i & 1)]);
       const float v1 = __uint_as_float(w[i / 2][2 * (i & 1) + 1]);
-      hi[i] = pack_bf16(v0, v1);
+      hi[i] = pack_bf16(first_plane(v0), first_plane(v1));
       const float h0 = __uint_as_float(hi[i] << 16), h1 = __uint_as_float(hi[i] & 0xffff0000u);
       lo[i] = pack_bf16(__builtin_isfinite(h0) ? v0 - h0 : 0.f,
                         __builtin_isfinite(h1) ? v1 - h1 : 0.f);

@@ -87,10 +87,14 @@ __device__ __forceinline__ void put_planes(const MmPlace& at, const f32x4_t (&v)
     for (int q = 0; q < P; ++q) {
 #pragma unroll
       for (int i = 0; i < F / 16; ++i) {
-        out.put(q & 1, i, left[i]);
+        f32x4_t part = left[i];
+        if (q == 0)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) part[k] = first_plane(part[k]);
+        out.put(q & 1, i, part);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float hi = bf16_to_f32(f32_to_bf16(left[i][k]));
+          const float hi = bf16_to_f32(f32_to_bf16(part[k]));
           left[i][k] = __builtin_isfinite(hi) ? left[i][k] - hi : 0.f;
         }
       }
@@ -106,7 +110,11 @@ template <int P>
 __device__ __forceinline__ void store_mid(bf16_t* p, int64_t plane, f32x4_t v) {
 #pragma unroll
   for (int q = 0; q < P; ++q) {
-    const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+    f32x4_t part = v;
+    if (P > 1 && q == 0)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) part[k] = first_plane(part[k]);
+    const uint32_t lo = pack_bf16(part[0], part[1]), hi = pack_bf16(part[2], part[3]);
     *reinterpret_cast<u32x2_t*>(p + q * plane) = u32x2_t{lo, hi};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

@@ -78,6 +78,13 @@ struct Piece<T, 1> {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
 }
+// What the first of several bfloat16 planes of v is rounded from.  A finite v past the
+// largest bfloat16 has that one, and the later planes what is left: nearest rounding
+// would make it an infinity.
+__device__ __forceinline__ float first_plane(float v) {
+  constexpr float kMost = 0x1.FEp127f;
+  return __builtin_isfinite(v) ? __builtin_amdgcn_fmed3f(v, -kMost, kMost) : v;
+}
 template <int V>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
   if constexpr (V == 1) {

@@ -488,3 +488,24 @@ def test_a_likely_target_has_a_loss_of_its_own_size(rows, dim, vocab, dtype):
         loss = B.linear_cross_entropy(x, w, t, IGNORE, "none")
         assert (loss >= 0).all(), loss.min().item()
         within(loss, *R.likely_loss(x, w, t), "loss")
+
+
+@pytest.mark.parametrize("rows,dim,vocab", [(12, 64, 300), (300, 64, 1000), (40, 1203, 91),
+                                            (40, 1033, 4500)])
+def test_finite_float32_activations_up_to_the_largest(rows, dim, vocab):
+    """float32's largest values, a mask's for instance, past the largest bfloat16: beside small
+    weights they are numbers like others."""
+    x, w, t = inputs(rows, dim, vocab, "f32", 31, 0.1)
+    big = torch.finfo(torch.float32).max
+    x[:, 0] = torch.where(torch.arange(rows, device="cuda") % 2 == 0, big, -big)
+    w[:, 0] = torch.where(torch.arange(vocab, device="cuda") % 3 == 0, 2.0 ** -126, -2.0 ** -126)
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    want, want_lse = R.loss(x, w, t, IGNORE)
+    e_each, e_lse = R.loss_bounds(x, w, t, IGNORE)
+    within(lse, want_lse, e_lse, "lse")
+    within(loss, want, e_each, "loss")
+    args = (torch.ones(rows, device="cuda"), x, w, t, lse, IGNORE, "none")
+    dx, _ = B.linear_cross_entropy_backward(*args, want_weight=False)
+    # (but for the column of weights of 2^-126, whose products are below float32's range)
+    within(dx[:, 1:], R.loss_grad(*args)[0][:, 1:],
+           R.loss_grad_bounds(*args, torch.float32)[0][:, 1:], "dx")

@@ -294,3 +294,39 @@ def test_refusals():
             call()
     with pytest.raises(B.SignMuonError):
         B.gated_mlp(x, wg, wu, wd, Y=x)
+
+
+BIG = torch.finfo(torch.float32).max
+
+
+# few rows; tiles with the gate in their epilogue; split sums; weights as they lie
+@pytest.mark.parametrize("rows,dim,hidden", [(9, 96, 200), (300, 64, 1000), (40, 1203, 91),
+                                             (40, 768, 1100)])
+def test_finite_float32_values_up_to_the_largest(rows, dim, hidden):
+    """float32's largest values, past the largest bfloat16, as activations, gradients and
+    what lies between the products: beside small weights they are numbers like others."""
+    sign = torch.where(torch.arange(rows, device="cuda") % 2 == 0, 1.0, -1.0)
+    small = torch.where(torch.arange(hidden, device="cuda") % 3 == 0, 2.0 ** -126, -2.0 ** -126)
+    x, wg, wu, wd = inputs(rows, dim, hidden, "f32", 41)
+    x[:, 0] = sign * BIG
+    wg[:, 0], wu[:, 0] = small, -small
+    _, pre = check_forward(x, wg, wu, wd, "silu")
+    dy = normal(42, rows, dim)
+    dy[:, 0] = sign * BIG
+    wd[0] = small
+    got = B.gated_mlp_backward(dy, x, wg, wu, wd, pre, want=(True, False, False, False))[0]
+    args = (dy, x, wg, wu, wd, pre, "silu")
+    # (but for the column of weights of 2^-126, whose products are below float32's range)
+    within(got[:, 1:], R.mlp_grad(*args)[0][:, 1:],
+           R.mlp_grad_bounds(*args, torch.float32)[0][:, 1:], "dx")
+    # act(gate) * up of a feature is the largest value itself
+    x, wg, wu, wd = inputs(rows, dim, hidden, "f32", 43)
+    x[:, 0] = 1.0
+    wg[0], wu[0] = 0.0, 0.0
+    wg[0, 0], wu[0, 0] = 2.0 ** 64, (1 - 2.0 ** -24) * 2.0 ** 64
+    wd[:, 0] = torch.where(torch.arange(dim, device="cuda") % 3 == 0, 2.0 ** -126, -2.0 ** -126)
+    _, pre = check_forward(x, wg, wu, wd, "silu")
+    dy = 2.0 ** -20 * normal(44, rows, dim)
+    got = B.gated_mlp_backward(dy, x, wg, wu, wd, pre, want=(False, False, False, True))[3]
+    args = (dy, x, wg, wu, wd, pre, "silu")
+    within(got, R.mlp_grad(*args)[3], R.mlp_grad_bounds(*args, torch.float32)[3], "dw_down")
