@@ -205,16 +205,14 @@ struct EpiGrad {
       const int n = nc + 16 * j, r = n < at.n ? n : at.n - 1;
       const int t = e.target[r] - e.v0;
       const float scale = e.scale[r];
-      // v - lse in powers of two: lse log2(e) in two parts, so that only the
-      // difference is rounded
-      const float hi = e.lse[r] * kLog2e, lo = __builtin_fmaf(e.lse[r], kLog2e, -hi);
+      // (the difference first: lse log2(e) may be past float32's range)
+      const float lse = e.lse[r];
       f32x4_t v[TI];
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float p =
-              __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], kLog2e, -hi) - lo) * scale;
+          const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * kLog2e) * scale;
           v[i][k] = WHOLE || mc + 16 * i + k < at.m ? p : 0.f;
         }
       if (__any(t >= at.m0 && t < at.m0 + TI * 16)) {
@@ -223,8 +221,7 @@ struct EpiGrad {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (mc + 16 * i + k == t) {
-              const float p =
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][k], kLog2e, -hi) - lo);
+              const float p = __builtin_amdgcn_exp2f((acc[i][j][k] - lse) * kLog2e);
               v[i][k] = (p - 1.f) * scale;
             }
       }
@@ -354,11 +351,11 @@ __global__ __launch_bounds__(256) void k_loss_mid_grad(const float* sums, int sp
 #pragma unroll 4
       for (int k = 0; k < splits; ++k, p += rows * ld) z += *reinterpret_cast<const f32x4_t*>(p);
     }
-    const float hi = lse[r] * kLog2e, lo = __builtin_fmaf(lse[r], kLog2e, -hi), by = scale[r];
+    const float at = lse[r], by = scale[r];
     const int t = target[r] - v0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[k], kLog2e, -hi) - lo);
+      const float p = __builtin_amdgcn_exp2f((z[k] - at) * kLog2e);
       z[k] = c + k < cols ? (c + k == t ? p - 1.f : p) * by : 0.f;
     }
     store_mid<P>(g + r * g_ld + c, plane, z);

@@ -490,6 +490,39 @@ def test_a_likely_target_has_a_loss_of_its_own_size(rows, dim, vocab, dtype):
         within(loss, *R.likely_loss(x, w, t), "loss")
 
 
+@pytest.mark.parametrize("rows,dim,vocab,dtype", FORMS)
+def test_logits_up_to_the_types_largest(rows, dim, vocab, dtype):
+    """Logits of 1 to 1.75 times 2^127 and their negatives, past 2^128 / log2(e): all sums are
+    exact, probabilities are 0 or 1, and losses, statistics and gradients are finite."""
+    level = torch.tensor([1.0, 1.25, 1.5, -1.5, -1.25, -1.0], device="cuda", dtype=torch.float64)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    a = level[torch.randint(6, (vocab,), device="cuda", generator=gen)]
+    a[7], a[11] = 1.75, -1.75
+    w = torch.zeros(vocab, dim, device="cuda", dtype=DT[dtype])
+    w[:, 0] = (a * 2.0 ** 63).to(DT[dtype])
+    x = torch.zeros(rows, dim, device="cuda", dtype=DT[dtype])
+    sign = torch.where(torch.arange(rows, device="cuda") % 3 == 1, -1.0, 1.0).double()
+    x[:, 0] = (sign * 2.0 ** 64).to(DT[dtype])
+    # targets on the row's own side: the distance from the largest stays in range
+    same = [torch.nonzero(a * s > 0)[:, 0] for s in (1, -1)]
+    pick = torch.randint(1 << 30, (rows,), device="cuda", generator=gen)
+    t = torch.where(sign > 0, same[0][pick % len(same[0])], same[1][pick % len(same[1])])
+    t[:4] = torch.where(sign[:4] > 0, 7, 11)
+    top = torch.where(sign > 0, 7, 11)
+    loss, lse = B.linear_cross_entropy(x, w, t, IGNORE, "none", want_lse=True)
+    assert (lse.double() == 1.75 * 2.0 ** 127).all()
+    assert torch.equal(loss.double(), (a[top] - a[t]).abs() * 2.0 ** 127)
+    one = torch.ones((rows,), device="cuda")
+    dx, dw = B.linear_cross_entropy_backward(one, x, w, t, lse, IGNORE, "none",
+                                             dtype=torch.float32)
+    g = torch.zeros(rows, vocab, device="cuda", dtype=torch.float64)
+    rows_ = torch.arange(rows, device="cuda")
+    g[rows_, top] += 1
+    g[rows_, t] -= 1
+    assert torch.equal(dx.double(), g @ w.double())
+    assert torch.equal(dw.double(), g.T.contiguous() @ x.double())
+
+
 @pytest.mark.parametrize("rows,dim,vocab", [(12, 64, 300), (300, 64, 1000), (40, 1203, 91),
                                             (40, 1033, 4500)])
 def test_finite_float32_activations_up_to_the_largest(rows, dim, vocab):
