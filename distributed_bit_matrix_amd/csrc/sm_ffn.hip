@@ -444,7 +444,6 @@ hipError_t ffn_thin(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
 template <int P, int MP, int ACT>
 hipError_t ffn(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
   // (Wg and Wu lie where they are, or both are copied: they share a row length)
-  const bool thin = thin_form(a.rows, a.dim, a.hidden, 3, a.dtype, true);
   const bool copied = !operand_fits(a.Wg, a.dtype, a.dim, a.dim) ||
                       !operand_fits(a.Wu, a.dtype, a.dim, a.dim);
   PlanesJobs c{};
