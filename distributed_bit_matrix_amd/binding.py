@@ -875,7 +875,7 @@ def gated_mlp_backward(dY, X, w_gate, w_up, w_down, pre, activation: str = "silu
     return (dX, *grads)
 
 
-def _loss_args(X, weight, targets, reduction, dev):
+def _loss_args(X, weight, targets, ignore_index, reduction, dev):
     """(rows, dim, row stride, vocab, dtype code, target bits, reduction code)."""
     rows, dim, xs = _rows(X, "X")
     code = _code(X.dtype, "X")
@@ -889,6 +889,8 @@ def _loss_args(X, weight, targets, reduction, dev):
         raise ValueError("targets are not on the first tensor's device")
     if reduction not in REDUCTIONS:
         raise ValueError("reduction must be none, sum or mean")
+    if not -1 << 63 <= ignore_index < 1 << 63:      # (ctypes would take its low 64 bits)
+        raise ValueError("ignore_index must be a 64-bit integer")
     return rows, dim, xs, weight.shape[0], code, bits, REDUCTIONS[reduction]
 
 
@@ -915,7 +917,8 @@ def linear_cross_entropy(X, weight, targets, ignore_index: int = -100, reduction
         with _placed(X, stream):
             return linear_cross_entropy(X, weight, targets, ignore_index, reduction, want_lse,
                                         loss, lse, ws)
-    rows, dim, xs, vocab, code, bits, red = _loss_args(X, weight, targets, reduction, dev)
+    rows, dim, xs, vocab, code, bits, red = _loss_args(X, weight, targets, ignore_index,
+                                                        reduction, dev)
     shape = targets.shape if red == 0 else targets.shape[:0]
     if loss is None:
         loss = torch.empty(shape, dtype=torch.float32, device=X.device)
@@ -949,7 +952,8 @@ def linear_cross_entropy_backward(dloss, X, weight, targets, lse, ignore_index: 
             return linear_cross_entropy_backward(dloss, X, weight, targets, lse, ignore_index,
                                                  reduction, want_x, want_weight, dX, dweight,
                                                  dtype, accumulate, ws)
-    rows, dim, xs, vocab, code, bits, red = _loss_args(X, weight, targets, reduction, dev)
+    rows, dim, xs, vocab, code, bits, red = _loss_args(X, weight, targets, ignore_index,
+                                                        reduction, dev)
     _check_arg(dloss, targets.shape if red == 0 else targets.shape[:0], torch.float32, dev,
                "dloss")
     _check_arg(lse, targets.shape, torch.float32, dev, "lse")

@@ -217,6 +217,16 @@ def test_cpu_tensors_are_refused():
             call()
 
 
+def test_an_index_to_be_ignored_past_64_bits_is_refused():
+    """Its low 64 bits are another index, the ordinary one for instance."""
+    x, t, w = torch.zeros(3, 4), torch.zeros(3, dtype=torch.int64), torch.zeros(5, 4)
+    for ignore in (-(1 << 63), -100, 4, (1 << 63) - 1):
+        assert B._loss_args(x, w, t, ignore, "mean", -1)[:4] == (3, 4, 4, 5)
+    for ignore in ((1 << 64) - 100, 1 << 63, -(1 << 63) - 1):
+        with pytest.raises(ValueError, match="ignore_index"):
+            B._loss_args(x, w, t, ignore, "mean", -1)
+
+
 # --- the reference and its bounds ------------------------------------------
 
 DTYPES = [torch.float32, torch.bfloat16]
