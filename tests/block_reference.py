@@ -188,6 +188,26 @@ def e4m3_half_step(v):
     return torch.exp2(e.double() - 5)
 
 
+def e4m3_nearest(v):
+    """The e4m3 value nearest to float64 v, |v| <= 448, halves to the even one."""
+    step = 2 * e4m3_half_step(v)
+    return torch.round(v / step) * step        # (torch.round: halves to even)
+
+
+def rows_with_ties(device=None):
+    """(x, v): 128 rows whose largest values are the integers of 8 bits, one in front of
+    every 128 columns, among them all values of 8 bits down to 2^-20 of it; and v = 448 x /
+    max.  Many of v are middles between two e4m3 values, also where the maximum's
+    reciprocal is inexact (odd multiples of 7)."""
+    most = torch.arange(128, 256, device=device, dtype=torch.float64)
+    h = (most * torch.exp2(-torch.arange(20, device=device, dtype=torch.float64))[:, None]).ravel()
+    h[1::2] *= -1
+    x = torch.where(h.abs() <= most[:, None], h, 0.0)
+    x = torch.nn.functional.pad(x, (0, 21 * 127 - x.shape[1])).view(128, 21, 127)
+    x = torch.cat([most[:, None, None].expand(128, 21, 1), x], 2).reshape(128, 21 * 128)
+    return x, 448 * x / most[:, None]
+
+
 def e4m3_scales(y, block):
     """max |y| / 448 of a row's blocks, at least 2^-126."""
     parts = [y] if block is None else y.split(block, -1)

@@ -365,6 +365,23 @@ def test_rms_bounds_take_float32_and_no_mistake(dtype):
                                             2.0 ** -10]
 
 
+def test_nearest_codes_take_a_rounded_quotient_and_no_other():
+    x, v = R.rows_with_ties()
+    k = v / R.e4m3_half_step(v)
+    tie = (k % 2 == 1) & (v != 0)
+    assert tie.sum() > 1000 and tie.any(1).all()
+    off = ((k - 1) % 2 - 1).abs()                # 1 on a middle
+    assert (1 - off[~tie]).min() >= 2.0 ** -11
+    code = lambda q: q.to(torch.float8_e4m3fn).double()  # noqa: E731
+    want = R.e4m3_nearest(v)
+    assert torch.equal(code(v.float()), want)
+    # the maximum's reciprocal rounded first; halves away from zero
+    most = x.float().amax(1, keepdim=True)
+    assert not torch.equal(code(x.float() * (448 / most)), want)
+    step = 2 * R.e4m3_half_step(v)
+    assert not torch.equal(torch.sign(v) * torch.floor(v.abs() / step + 0.5) * step, want)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_rms_grad_bounds_take_float32_and_no_mistake(dtype):
     g = gen()

@@ -310,3 +310,20 @@ def test_codes_where_the_squares_sum_past_float32(block):
     assert (B.rms_norm(x, w, None, EPS) == 0).all()
     q, scales = B.rms_norm_e4m3(x, w, None, EPS, block)
     assert (q.float() == 0).all() and (scales == 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("block", [128, None])
+@pytest.mark.parametrize("x_dtype", ["f32", "bf16"])
+def test_codes_are_the_nearest_values_and_ties_stay_ties(x_dtype, block):
+    """Of rows of 8-bit values without weights a code stands for 448 h / max |h|.  In units
+    of half a code's step that is a multiple of 2^-3 / max, max an integer of 8 bits: 2^-11
+    from a middle between two codes, an odd number, at least, unless it is one.  The
+    quotient's rounding to float32 is 2^-19 of half a step at most.  So the code is the exact
+    quotient's, and a tie stays one."""
+    x, v = R.rows_with_ties(torch.device("cuda"))
+    for power in (0, -7, 40):
+        q, _ = B.rms_norm_e4m3((x * 2.0 ** power).to(DT[x_dtype]), None, None, EPS, block)
+        want = R.e4m3_nearest(v)
+        bad = q.float().double() != want
+        assert not bad.any(), (int(bad.sum()), x[bad][:4].tolist(), want[bad][:4].tolist(),
+                               q.float()[bad][:4].tolist())
