@@ -172,7 +172,8 @@ sm_status signmuon_rms_norm_backward(
  * What lies between the products is rounded to `dtype` once; in bfloat16, where
  * rows times the lesser of dim and hidden is below 4096, to a sum of two values.
  * Products of float32 are sums of products of bfloat16 parts, with float32's
- * precision; an infinity among their operands makes NaN of what depends on it.
+ * precision for operands of 2^-109 and more (smaller ones are held to 2^-133); an
+ * infinity among their operands makes NaN of what depends on it.
  * ws: signmuon_gated_mlp_workspace() bytes (backward = 1 for the backward call),
  * 256-byte aligned; NULL where that is 0.  Its contents on entry do not matter.
  * The query returns SIZE_MAX for arguments outside the limits.
@@ -206,7 +207,7 @@ sm_status signmuon_gated_mlp_backward(
 /*
  * Softmax cross entropy of a linear output layer, whose logits Z = X W^T
  * (rows x vocab) are not kept: with t = targets[r],
- *   lse[r] = log(sum_v exp(Z[r,v])),  loss_r = lse[r] - Z[r,t].
+ *   lse[r] = log(sum_v exp(Z[r,v])),  loss_r = lse[r] - Z[r,t] >= 0.
  * Row r of X starts at element r * x_stride (x_stride >= dim); W: contiguous
  * vocab x dim; both of `dtype`.  targets: rows integers of target_bits (32 or
  * 64) bits.  A row whose target is `ignore` (any integer) counts nowhere,

@@ -330,3 +330,24 @@ def test_finite_float32_values_up_to_the_largest(rows, dim, hidden):
     got = B.gated_mlp_backward(dy, x, wg, wu, wd, pre, want=(False, False, False, True))[3]
     args = (dy, x, wg, wu, wd, pre, "silu")
     within(got, R.mlp_grad(*args)[3], R.mlp_grad_bounds(*args, torch.float32)[3], "dw_down")
+
+
+@pytest.mark.parametrize("rows,dim,hidden", [(9, 96, 200), (300, 64, 1000), (40, 1203, 91),
+                                             (40, 768, 1100)])
+def test_small_float32_operands(rows, dim, hidden):
+    """An operand is held to 2^-133 at least, below float32's normal range too: from 2^-109 on
+    that is all of its 24 bits.  (Products with 1 and sums with 0 are exact.)"""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    part = 1 + torch.randint(1 << 23, (hidden,), device="cuda", generator=gen).double() * 2.0 ** -23
+    wd = torch.zeros(dim, hidden, device="cuda")
+    for power in (-100, -109, -110, -118, -126, -130, -140):
+        small = (part * 2.0 ** power).float()
+        x = torch.zeros(rows, dim, device="cuda")
+        w = torch.zeros(hidden, dim, device="cuda")
+        x[:, 0], w[:, 0] = 1, small
+        want = small.double().repeat(2)
+        off = (B.gated_mlp(x, w, w, wd, want_pre=True)[1].double() - want).abs().max()
+        assert off == 0 if power >= -109 else off <= 2.0 ** -133
+        x[:, 0], w[:, 0] = small[0], 1
+        off = (B.gated_mlp(x, w, w, wd, want_pre=True)[1].double() - want[0]).abs().max()
+        assert off == 0 if power >= -109 else off <= 2.0 ** -133
