@@ -7,7 +7,10 @@
 // instructions take (lane l holds a piece of row l % 16; which k an instruction
 // sums does not matter as long as x has the same).  Many waves with 2 pieces a
 // matrix each in flight: 4096 x 16384 bfloat16 27 us (5 TB/s; 8 pieces in half the
-// waves 32, the next pieces fetched ahead in registers 78).
+// waves 32, the next pieces fetched ahead in registers 78).  float32 goes through the
+// float32 matrix instructions (busy for a quarter of the time): one row of a block of 4096 x
+// 16384 108 + 68 us, 4.9 and 3.9 TB/s, which is slower as a call (184 us, 16 rows 217)
+// than elementary operations (168, 172).
 // WK waves share a group's k and meet in LDS, in a fixed order.
 #pragma once
 

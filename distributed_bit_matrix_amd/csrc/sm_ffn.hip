@@ -15,11 +15,12 @@
 // bfloat16 planes.
 //
 // Up to 16 rows the products are bound by reading the weights once (sm_few.h): one
-// row, 4096 x 16384, 47 + 27 us.  4096 rows of it: 1056 us for gate and up with
-// their epilogue (1040 TFLOP/s, and 0.7 GB written), 458 for the last product (1200);
-// the chip's power bounds both.  Backward, 12288 rows of 768 x 2048: 161 us
+// row, 4096 x 16384, 47 + 26 us.  4096 rows of it: 1037 us for gate and up with
+// their epilogue (1060 TFLOP/s, and 0.7 GB written), 465 for the last product (1180);
+// the chip's power bounds both.  Backward, 12288 rows of 768 x 2048: 163 us
 // for dh with its epilogue, which reads 201 MB of pre and writes 151 MB beside 39
-// GFLOP, and 267 for the rest in one launch (193 GFLOP).
+// GFLOP and runs beside no product, and 270 for the rest in one launch (193 GFLOP in
+// 864 unsplit tiles of 128 x 128).
 #include "sm_few.h"
 #include "sm_thin.h"
 #include "sm_layers.h"

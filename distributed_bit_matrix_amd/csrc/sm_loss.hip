@@ -21,10 +21,11 @@
 // that all rows share would be rounded alike in all of them: it is left out of G
 // and multiplies the results.
 //
-// 11059 of 12288 rows against 50257 x 768 bfloat16: the logits' launch 903 us (950
+// 11059 of 12288 rows against 50257 x 768 bfloat16: the logits' launch 912 us (940
 // TFLOP/s; a tile has 12 slabs, and its first loads and epilogue, with nothing
 // beside them in a CU that holds one block, are a third of it); backward 2 pieces,
-// 480 us each for the logits and G, 800 for the two products (1070 TFLOP/s).
+// 502 and 475 us for the logits and G, 806 and 827 for the two products (1060
+// TFLOP/s).
 #include <cmath>
 
 #include "sm_few.h"
@@ -102,7 +103,8 @@ struct EpiLse {
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       // The largest logit's own term is 1 to the last bit: where the target has it the
       // loss is the logarithm of the sum alone, and a rounding of mx log2(e) (one
-      // multiply-add a logit) would be all of it, of either sign.
+      // multiply-add a logit, 821 us a call of the size above instead of 832) would be
+      // all of it, of either sign.
       const float ref = mx == -INFINITY ? 0.f : mx;
       float s = 0.f;
 #pragma unroll

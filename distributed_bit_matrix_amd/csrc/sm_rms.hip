@@ -2,9 +2,9 @@
 // backward, with an 8-bit output too.  Rows live in registers as in the layer
 // norm (sm_norm_rows.h), so each array is read or written once; every sum has an
 // order that the sizes alone decide.  Both passes are bound by HBM: 16384 x 4096
-// bfloat16 with a residual to 8 bits 84 us (470 MB, 5.6 TB/s), its backward pass 96
-// (537 MB, 5.6 TB/s) and 5 for the blocks' sums; 12288 x 768 15 and 4, by a block's
-// start and end; one row of 4096 3.3.
+// bfloat16 with a residual 94 us (537 MB, 5.7 TB/s), to 8 bits 84 (470 MB, 5.6 TB/s),
+// its backward pass 96 (537 MB, 5.6 TB/s) and 5 for the blocks' sums; 12288 x 768 15 and
+// 4, by a block's start and end; one row of 4096 3.
 #include "sm_layers.h"
 #include "sm_norm_rows.h"
 

@@ -8,10 +8,11 @@
 // splits them into three bfloat16 planes there (truncated, so that their sum is W
 // itself); x has its planes in memory, and a block's 8 waves share a step of them in
 // LDS, in two turns.  The six products of planes are those of sm_mm.h.  Bound by
-// reading W: 17 rows, two matrices of 16384 x 4096 with m along rows 124 us (4.3
-// TB/s), 126047 x 2436 with k along rows 390 us (3.2 TB/s); 128 rows by the matrix
-// units as well.  (Each wave loading x for itself from the caches: 17 rows of that
-// block 296 us instead of 220, 128 rows 861 instead of 331.)
+// reading W, one step in flight: 17 rows, two matrices of 16384 x 4096 with k along rows
+// 132 us (4.1 TB/s), with m along rows 116 (4.6); 126047 x 2436 with k along rows 331,
+// and 381 in the backward pass (3.7, 3.2), with m 281 (4.4); 128 rows by the matrix units
+// as well.  (Each wave loading x for itself from the caches: 17 rows of the first's block
+// 296 us instead of 220, 128 rows 861 instead of 331.)
 #pragma once
 
 #include "sm_mm_ops.h"
@@ -210,7 +211,11 @@ __global__ __launch_bounds__(512) void k_thin(ThinArgs a) {
 // Backward it is the form of the products with the weights, from one row on: 2^22
 // values 1 row 59, 47, 64 rows 60, 60, 128 rows 61, 76; 2^23 (1000 x 10007) 64 rows 105,
 // 103, 128 rows 112, 134; 2^25 17 rows 452, 172, 128 rows 482, 293; 2^28 17 rows 2436,
-// 1068, 128 rows 2871, 1615.
+// 1068, 128 rows 2871, 1615.  Elementary operations (float32 library products, and h
+// through memory) are faster where a block's weights are large and its rows few: 4096 x
+// 16384, 17 rows 179 us and here 216, 64 rows 260 and 261, 128 rows 470 and 353; 2048 x
+// 8192, 128 rows 131 and 157; gradients of the first, 1 row 477 and 506, 17 rows 548 and
+// 525.
 inline bool thin_form(int64_t rows, int64_t m, int64_t k, int mats, int32_t dtype,
                       bool backward) {
   const int64_t values = mats * m * k;
